@@ -38,17 +38,18 @@ enum {
     TG_ERR_ALIGN = 3,              /* pointer not 16-byte aligned or ld*2 not a multiple of 16 (tg_gemm),
                                       or a pointer not 2-byte aligned (every call) */
     TG_ERR_OVERLAP = 4,            /* output bytes intersect an input's bytes */
-    TG_ERR_DTYPE = 5,              /* dtype not TG_F16 / TG_BF16 */
+    TG_ERR_DTYPE = 5,              /* dtype not TG_F16 / TG_BF16 (tg_adamw: nor TG_F32) */
     TG_ERR_UNSUPPORTED_DEVICE = 6, /* no CUDA device, or not compute capability 10.x with tcgen05 */
     TG_ERR_CUDA = 7,               /* a CUDA runtime/driver call or the launch failed */
     TG_ERR_TIMEOUT = 8,            /* a bounded device wait expired (reported by tg_debug_status) */
     TG_ERR_POINTER = 9,            /* a pointer is not device memory of the current device, or the
                                       bytes the call touches run past the end of its allocation */
     TG_ERR_LAYOUT = 10,            /* layout arguments violate a layout invariant */
-    TG_ERR_BUFFER = 11             /* caller's output buffer too small */
+    TG_ERR_BUFFER = 11             /* caller's output buffer or workspace too small */
 };
 
-typedef enum { TG_F16 = 0, TG_BF16 = 1 } tg_dtype;
+/* TG_F32 is a type of tg_adamw's parameters and gradients only. */
+typedef enum { TG_F16 = 0, TG_BF16 = 1, TG_F32 = 2 } tg_dtype;
 
 /* Explicit permute of an operand's storage.  A transposed input must say so;
  * a matching size never stands in for a transpose (ninetoothed.org "Named
@@ -261,6 +262,145 @@ int tg_gemm_host_workspace_size(int64_t M, int64_t N, int64_t K, tg_dtype dtype,
 int tg_pointwise(int64_t M, int64_t N, const void* X, int64_t ldx, tg_perm permX,
                  void* C, int64_t ldc, tg_dtype dtype, const tg_epilogue* epi,
                  cudaStream_t stream);
+
+/* ------------------------------------------------------------------------
+ * The training step of a model's output head: layer norm, linear cross
+ * entropy (projection onto a vocabulary and softmax cross entropy of its
+ * logits, which are never kept), their gradients, and the AdamW update.
+ *
+ * As for the GEMM: device pointers, row strides in elements with inner stride
+ * 1, every check before any device work, launches on `stream` only, nothing
+ * allocated, no synchronisation, results that repeat bit for bit.  Rows may
+ * start at any 2-byte-aligned address and strides may be any value that is at
+ * least the row width; 16-byte-aligned rows are faster.  Every output's bytes
+ * are disjoint from every other operand's.  Statistics, sums and products are
+ * fp32.  Workspaces need no initialisation; calls that share one must not
+ * overlap on the GPU.
+ * ---------------------------------------------------------------------- */
+
+/*
+ * Layer norm over the `cols` columns of each row:
+ *
+ *     mean = sum(x) / cols;  rstd = 1 / sqrt(sum((x - mean)^2) / cols + eps)
+ *     Y[r, c] = (X[r, c] - mean[r]) * rstd[r] * weight[c] + bias[c]
+ *
+ * X, weight, bias and Y have type `dtype`; mean and rstd are fp32 [rows] and
+ * are what tg_layernorm_grad needs.  bias may be NULL (no shift).  eps >= 0.
+ * One kernel launch.  Errors as tg_pointwise's checks.
+ */
+int tg_layernorm(int64_t rows, int64_t cols, const void* X, int64_t ldx, const void* weight,
+                 const void* bias, float eps, void* Y, int64_t ldy, float* mean, float* rstd,
+                 tg_dtype dtype, cudaStream_t stream);
+
+/*
+ * Gradient of tg_layernorm, with xh = (X - mean) * rstd and g = dY * weight:
+ *
+ *     dX[r, c]   = rstd[r] * (g - sum(g) / cols - xh * sum(g xh) / cols)
+ *     dweight[c] = sum over rows of dY xh        dbias[c] = sum over rows of dY
+ *
+ * dweight and dbias have type `dtype`, are summed in fp32 and rounded once;
+ * dbias may be NULL.  workspace: 256-byte aligned, at least
+ * tg_layernorm_grad_workspace_size() bytes (else TG_ERR_BUFFER).  Two kernel
+ * launches (three for rows too wide for a block's registers).
+ */
+int tg_layernorm_grad(int64_t rows, int64_t cols, const void* dY, int64_t lddy, const void* X,
+                      int64_t ldx, const void* weight, const float* mean, const float* rstd,
+                      void* dX, int64_t lddx, void* dweight, void* dbias, tg_dtype dtype,
+                      void* workspace, size_t workspace_bytes, cudaStream_t stream);
+int tg_layernorm_grad_workspace_size(int64_t rows, int64_t cols, tg_dtype dtype, size_t* bytes);
+
+/*
+ * Softmax cross entropy of the logits l = H W^T without keeping them:
+ *
+ *     lse[t]  = log(sum over v < V of exp(l[t, v]))
+ *     loss[t] = lse[t] - l[t, target[t]]     if 0 <= target[t] < V
+ *             = 0                            otherwise (an ignored token)
+ *
+ * H is T x D (row stride ldh), W is V x D (row stride ldw), both of type
+ * `dtype`; target is [T]; loss and lse are fp32 [T].  The logits are fp32 and
+ * stay on chip; the workspace holds 8 bytes per token and 128 or 256 columns
+ * of the vocabulary.  Two kernel launches.
+ * workspace: 256-byte aligned, at least tg_linear_ce_workspace_size() bytes
+ * (else TG_ERR_BUFFER).  An H or W whose rows are not 16-byte aligned is
+ * copied into the workspace first.  A row whose logits hold a NaN or +inf
+ * has lse = NaN.  Device waits are bounded; see tg_debug_status().
+ */
+int tg_linear_ce(int64_t T, int64_t V, int64_t D, const void* H, int64_t ldh, const void* W,
+                 int64_t ldw, const int64_t* target, float* loss, float* lse, tg_dtype dtype,
+                 void* workspace, size_t workspace_bytes, cudaStream_t stream);
+int tg_linear_ce_workspace_size(int64_t T, int64_t V, int64_t D, const void* H, int64_t ldh,
+                                const void* W, int64_t ldw, tg_dtype dtype, size_t* bytes);
+
+/*
+ * Gradient of sum over t of dloss[t] * loss[t]:
+ *
+ *     G[t, v] = dloss[t] * (exp(l[t, v] - lse[t]) - [v = target[t]])
+ *     dH = G W  (T x D)        dW = G^T H  (V x D)
+ *
+ * with the lse that tg_linear_ce returned.  The logits are computed again, in
+ * pieces of the vocabulary; a piece of G is rounded to `dtype` (scaled so
+ * that fp16 does not underflow), both products accumulate in fp32 and are
+ * rounded once.  Ignored tokens contribute nothing whatever their rows of H
+ * hold, and their rows of dH are zeros.  dH or dW may be NULL (not both): it
+ * is then not computed.  workspace as above, of
+ * tg_linear_ce_grad_workspace_size() bytes: a piece of G of at most 512 MiB
+ * (one 256-column strip of it at least), a dense copy of H, dH in fp32.
+ */
+int tg_linear_ce_grad(int64_t T, int64_t V, int64_t D, const void* H, int64_t ldh, const void* W,
+                      int64_t ldw, const int64_t* target, const float* lse, const float* dloss,
+                      void* dH, int64_t lddh, void* dW, int64_t lddw, tg_dtype dtype,
+                      void* workspace, size_t workspace_bytes, cudaStream_t stream);
+int tg_linear_ce_grad_workspace_size(int64_t T, int64_t V, int64_t D, const void* H, int64_t ldh,
+                                     const void* W, int64_t ldw, const void* dH, int64_t lddh,
+                                     const void* dW, int64_t lddw, tg_dtype dtype, size_t* bytes);
+
+/*
+ * One AdamW step over `count` tensors, in place, with gradients g scaled by
+ * *grad_scale (a clipping or unscaling factor computed on the device; NULL: 1):
+ *
+ *     m = beta1 m + (1 - beta1) g        v = beta2 v + (1 - beta2) g^2
+ *     p = p (1 - lr weight_decay)
+ *         - lr / (1 - beta1^step) * m / (sqrt(v) / sqrt(1 - beta2^step) + eps)
+ *
+ * in fp32.  With a master copy, p is the master copy and `param` receives it
+ * rounded to its type.  state_bits = 32: m and v are fp32 [numel].
+ * state_bits = 8: m and v are e4m3 bytes [numel], m_scale and v_scale fp32
+ * [ceil(numel / 256)]; a block of 256 elements of m stands for code *
+ * m_scale, of v for (code * v_scale)^2.  After the step the scales are a
+ * 448th of the block's largest |m| and sqrt(v); m is rounded to nearest even,
+ * sqrt(v) stochastically (up with the probability of the part cut off, by
+ * bits mixed from the element's index and `seed`: pass another seed each
+ * step), and a root above zero never becomes zero.
+ * `tensors` is a host array, read during the call; a tensor of no elements is
+ * skipped.  One kernel launch per 256 tensors.
+ * Errors: TG_ERR_INVALID_ARG for a null pointer, a master copy of an fp32
+ * parameter, numel < 0, step < 1, betas outside [0, 1), eps < 0 or another
+ * state_bits; TG_ERR_DTYPE if grad_dtype is neither dtype nor TG_F32;
+ * TG_ERR_ALIGN for a pointer that is not a multiple of its element size;
+ * TG_ERR_OVERLAP if two operands share bytes and either is written.
+ */
+typedef struct {
+    void* param;      /* [numel] of type dtype */
+    float* master;    /* [numel] or NULL */
+    const void* grad; /* [numel] of type grad_dtype */
+    void* m;          /* first state */
+    void* v;          /* second state */
+    float* m_scale;   /* 8-bit states only */
+    float* v_scale;   /* 8-bit states only */
+    int64_t numel;
+} tg_adamw_tensor;
+
+typedef struct {
+    double lr, beta1, beta2, eps, weight_decay;
+    int64_t step; /* 1 for the first step */
+    tg_dtype dtype, grad_dtype;
+    int state_bits;          /* 32 or 8 */
+    uint32_t seed;           /* of the 8-bit states' rounding */
+    const float* grad_scale; /* device pointer or NULL */
+} tg_adamw_options;
+
+int tg_adamw(int64_t count, const tg_adamw_tensor* tensors, const tg_adamw_options* options,
+             cudaStream_t stream);
 
 /* Static name of a status code ("TG_OK", "TG_ERR_ALIGN", ...). */
 const char* tg_status_string(int status);

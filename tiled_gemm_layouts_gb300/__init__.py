@@ -38,7 +38,7 @@ TG_ERR_POINTER = 9
 TG_ERR_LAYOUT = 10
 TG_ERR_BUFFER = 11
 
-TG_F16, TG_BF16 = 0, 1
+TG_F16, TG_BF16, TG_F32 = 0, 1, 2  # TG_F32: tg_adamw only
 TG_OP_N, TG_OP_T = 0, 1
 
 _i64, _int, _vp, _cp = ctypes.c_int64, ctypes.c_int, ctypes.c_void_p, ctypes.c_char_p
@@ -47,6 +47,18 @@ _i64, _int, _vp, _cp = ctypes.c_int64, ctypes.c_int, ctypes.c_void_p, ctypes.c_c
 class tg_epilogue(ctypes.Structure):
     _fields_ = [("bias_n", _vp), ("scale_m", _vp), ("relu", _int), ("residual", _vp),
                 ("ldr", _i64)]
+
+
+class tg_adamw_tensor(ctypes.Structure):
+    _fields_ = [("param", _vp), ("master", _vp), ("grad", _vp), ("m", _vp), ("v", _vp),
+                ("m_scale", _vp), ("v_scale", _vp), ("numel", _i64)]
+
+
+class tg_adamw_options(ctypes.Structure):
+    _fields_ = [("lr", ctypes.c_double), ("beta1", ctypes.c_double), ("beta2", ctypes.c_double),
+                ("eps", ctypes.c_double), ("weight_decay", ctypes.c_double), ("step", _i64),
+                ("dtype", _int), ("grad_dtype", _int), ("state_bits", _int),
+                ("seed", ctypes.c_uint32), ("grad_scale", _vp)]
 
 
 def _sig(name, res, *args):
@@ -79,6 +91,20 @@ _sig("tg_gemm_host", _int, _i64, _i64, _i64, _vp, _i64, _int, _vp, _i64, _int, _
      ctypes.POINTER(tg_epilogue), _vp, ctypes.c_size_t, _vp)
 _sig("tg_gemm_host_workspace_size", _int, _i64, _i64, _i64, _int, _int, _int,
      ctypes.POINTER(tg_epilogue), ctypes.POINTER(ctypes.c_size_t))
+_size_p = ctypes.POINTER(ctypes.c_size_t)
+_sig("tg_layernorm", _int, _i64, _i64, _vp, _i64, _vp, _vp, ctypes.c_float, _vp, _i64, _vp, _vp, _int,
+     _vp)
+_sig("tg_layernorm_grad", _int, _i64, _i64, _vp, _i64, _vp, _i64, _vp, _vp, _vp, _vp, _i64, _vp, _vp,
+     _int, _vp, ctypes.c_size_t, _vp)
+_sig("tg_layernorm_grad_workspace_size", _int, _i64, _i64, _int, _size_p)
+_sig("tg_linear_ce", _int, _i64, _i64, _i64, _vp, _i64, _vp, _i64, _vp, _vp, _vp, _int, _vp,
+     ctypes.c_size_t, _vp)
+_sig("tg_linear_ce_workspace_size", _int, _i64, _i64, _i64, _vp, _i64, _vp, _i64, _int, _size_p)
+_sig("tg_linear_ce_grad", _int, _i64, _i64, _i64, _vp, _i64, _vp, _i64, _vp, _vp, _vp, _vp, _i64, _vp,
+     _i64, _int, _vp, ctypes.c_size_t, _vp)
+_sig("tg_linear_ce_grad_workspace_size", _int, _i64, _i64, _i64, _vp, _i64, _vp, _i64, _vp, _i64, _vp,
+     _i64, _int, _size_p)
+_sig("tg_adamw", _int, _i64, ctypes.POINTER(tg_adamw_tensor), ctypes.POINTER(tg_adamw_options), _vp)
 _sig("tg_debug_status", _int, ctypes.POINTER(_int))
 _sig("tg_debug_configure", _int, _i64, _i64)
 _sig("tg_probe_swizzle128", _int, _vp, _int, _i64, _vp, _vp, _vp)
@@ -132,6 +158,9 @@ _sig("tg_layout_tmem_32x32b", _int, _int, _PP)
 EXPORTED = [
     "tg_gemm", "tg_gemm_ws", "tg_gemm_workspace_size", "tg_gemm_workspace_size_ex",
     "tg_pointwise",
+    "tg_layernorm", "tg_layernorm_grad", "tg_layernorm_grad_workspace_size",
+    "tg_linear_ce", "tg_linear_ce_workspace_size",
+    "tg_linear_ce_grad", "tg_linear_ce_grad_workspace_size", "tg_adamw",
     "tg_gemm_static_ws", "tg_gemm_host", "tg_gemm_host_workspace_size",
     "tg_status_string", "tg_query_config",
     "tg_query_config_ws", "tg_query_config_for_sms",
@@ -261,6 +290,124 @@ def tg_gemm_host_workspace_size(M, N, K, dtype, permA=TG_OP_N, permB=TG_OP_N, ep
 def tg_pointwise(M, N, X, ldx, permX, C, ldc, dtype, epi=None, stream=None) -> int:
     return _lib.tg_pointwise(M, N, _addr(X), ldx, permX, _addr(C), ldc, dtype,
                              ctypes.byref(epi) if epi is not None else None, _stream(stream))
+
+
+# ------------------------------------------- an output head's training step
+# The tg_* functions return a status and never raise; those without the prefix
+# raise TileGemmError on a nonzero one (the workspace sizes always raise).
+
+def tg_layernorm(rows, cols, X, ldx, weight, bias, eps, Y, ldy, mean, rstd, dtype,
+                 stream=None) -> int:
+    return _lib.tg_layernorm(rows, cols, _addr(X), ldx, _addr(weight), _addr(bias), eps, _addr(Y),
+                             ldy, _addr(mean), _addr(rstd), dtype, _stream(stream))
+
+
+def layernorm(rows, cols, X, ldx, weight, bias, eps, Y, ldy, mean, rstd, dtype, stream=None) -> None:
+    rc = tg_layernorm(rows, cols, X, ldx, weight, bias, eps, Y, ldy, mean, rstd, dtype, stream)
+    if rc != TG_OK:
+        raise TileGemmError(rc, "tg_layernorm")
+
+
+def tg_layernorm_grad_workspace_size(rows, cols, dtype) -> int:
+    n = ctypes.c_size_t(0)
+    rc = _lib.tg_layernorm_grad_workspace_size(rows, cols, dtype, ctypes.byref(n))
+    if rc != TG_OK:
+        raise TileGemmError(rc, "tg_layernorm_grad_workspace_size")
+    return n.value
+
+
+def tg_layernorm_grad(rows, cols, dY, lddy, X, ldx, weight, mean, rstd, dX, lddx, dweight, dbias,
+                      dtype, workspace, workspace_bytes, stream=None) -> int:
+    return _lib.tg_layernorm_grad(rows, cols, _addr(dY), lddy, _addr(X), ldx, _addr(weight),
+                                  _addr(mean), _addr(rstd), _addr(dX), lddx, _addr(dweight),
+                                  _addr(dbias), dtype, _addr(workspace), workspace_bytes,
+                                  _stream(stream))
+
+
+def layernorm_grad(rows, cols, dY, lddy, X, ldx, weight, mean, rstd, dX, lddx, dweight, dbias,
+                   dtype, workspace, workspace_bytes, stream=None) -> None:
+    rc = tg_layernorm_grad(rows, cols, dY, lddy, X, ldx, weight, mean, rstd, dX, lddx, dweight,
+                           dbias, dtype, workspace, workspace_bytes, stream)
+    if rc != TG_OK:
+        raise TileGemmError(rc, "tg_layernorm_grad")
+
+
+def tg_linear_ce_workspace_size(T, V, D, H, ldh, W, ldw, dtype) -> int:
+    n = ctypes.c_size_t(0)
+    rc = _lib.tg_linear_ce_workspace_size(T, V, D, _addr(H), ldh, _addr(W), ldw, dtype,
+                                          ctypes.byref(n))
+    if rc != TG_OK:
+        raise TileGemmError(rc, "tg_linear_ce_workspace_size")
+    return n.value
+
+
+def tg_linear_ce(T, V, D, H, ldh, W, ldw, target, loss, lse, dtype, workspace, workspace_bytes,
+                 stream=None) -> int:
+    return _lib.tg_linear_ce(T, V, D, _addr(H), ldh, _addr(W), ldw, _addr(target), _addr(loss),
+                             _addr(lse), dtype, _addr(workspace), workspace_bytes, _stream(stream))
+
+
+def linear_ce(T, V, D, H, ldh, W, ldw, target, loss, lse, dtype, workspace, workspace_bytes,
+              stream=None) -> None:
+    rc = tg_linear_ce(T, V, D, H, ldh, W, ldw, target, loss, lse, dtype, workspace,
+                      workspace_bytes, stream)
+    if rc != TG_OK:
+        raise TileGemmError(rc, "tg_linear_ce")
+
+
+def tg_linear_ce_grad_workspace_size(T, V, D, H, ldh, W, ldw, dH, lddh, dW, lddw, dtype) -> int:
+    n = ctypes.c_size_t(0)
+    rc = _lib.tg_linear_ce_grad_workspace_size(T, V, D, _addr(H), ldh, _addr(W), ldw, _addr(dH),
+                                               lddh, _addr(dW), lddw, dtype, ctypes.byref(n))
+    if rc != TG_OK:
+        raise TileGemmError(rc, "tg_linear_ce_grad_workspace_size")
+    return n.value
+
+
+def tg_linear_ce_grad(T, V, D, H, ldh, W, ldw, target, lse, dloss, dH, lddh, dW, lddw, dtype,
+                      workspace, workspace_bytes, stream=None) -> int:
+    return _lib.tg_linear_ce_grad(T, V, D, _addr(H), ldh, _addr(W), ldw, _addr(target), _addr(lse),
+                                  _addr(dloss), _addr(dH), lddh, _addr(dW), lddw, dtype,
+                                  _addr(workspace), workspace_bytes, _stream(stream))
+
+
+def linear_ce_grad(T, V, D, H, ldh, W, ldw, target, lse, dloss, dH, lddh, dW, lddw, dtype,
+                   workspace, workspace_bytes, stream=None) -> None:
+    rc = tg_linear_ce_grad(T, V, D, H, ldh, W, ldw, target, lse, dloss, dH, lddh, dW, lddw, dtype,
+                           workspace, workspace_bytes, stream)
+    if rc != TG_OK:
+        raise TileGemmError(rc, "tg_linear_ce_grad")
+
+
+def make_adamw_tensors(params, grads, m, v, master=None, m_scale=None, v_scale=None, numel=None):
+    """The tensor array of tg_adamw, from lists of pointers or tensors (numel:
+    the params' own, where they have it).  It holds addresses only: keep the
+    tensors alive, and make it again when one of them moves."""
+    n = len(params)
+    lists = [params, master or [None] * n, grads, m, v, m_scale or [None] * n, v_scale or [None] * n]
+    sizes = numel if numel is not None else [p.numel() for p in params]
+    if any(len(x) != n for x in lists) or len(sizes) != n:
+        raise TileGemmError(TG_ERR_INVALID_ARG, "make_adamw_tensors")
+    return (tg_adamw_tensor * n)(*[tg_adamw_tensor(*map(_addr, row), size)
+                                   for *row, size in zip(*lists, sizes)])
+
+
+def make_adamw_options(lr, beta1, beta2, eps, weight_decay, step, dtype, grad_dtype=None,
+                       state_bits=32, seed=0, grad_scale=None):
+    return tg_adamw_options(lr, beta1, beta2, eps, weight_decay, step, dtype,
+                            dtype if grad_dtype is None else grad_dtype, state_bits, seed,
+                            _addr(grad_scale))
+
+
+def tg_adamw(tensors, options, stream=None) -> int:
+    """Status of one AdamW step over an array made by make_adamw_tensors."""
+    return _lib.tg_adamw(len(tensors), tensors, ctypes.byref(options), _stream(stream))
+
+
+def adamw(tensors, options, stream=None) -> None:
+    rc = tg_adamw(tensors, options, stream)
+    if rc != TG_OK:
+        raise TileGemmError(rc, "tg_adamw")
 
 
 def tg_gemm_workspace_size_ex(M, N, K, A, lda, permA, B, ldb, permB, C, ldc, dtype,

@@ -18,6 +18,7 @@
 
 #include "../../include/tilegemm.h"
 #include "gemm_params.h"
+#include "host_common.h"
 #include "pointwise.h"
 #include "select.h"
 
@@ -29,18 +30,11 @@ __device__ int g_device_status;
 namespace {
 
 constexpr int kMaxDevices = 64;
-constexpr int64_t kMaxDim = 2147483647LL;
 constexpr long long kDefaultTimeout = 4000000000LL;
 
 std::atomic<long long> g_timeout{kDefaultTimeout};
 std::atomic<long long> g_skip_kblock{-1};
 
-struct DeviceInfo {
-    bool ready = false;
-    bool supported = false;
-    int sms = 0;
-    int* status = nullptr;  // device address of g_device_status
-};
 DeviceInfo g_dev[kMaxDevices];
 std::mutex g_dev_mu;
 
@@ -53,7 +47,12 @@ EncodeTiledFn g_encode = nullptr;
 AddressRangeFn g_range = nullptr;
 std::once_flag g_driver_once;
 
-void load_driver_entry_points() {
+}  // namespace
+
+long long watchdog_timeout() { return g_timeout.load(); }
+int watchdog_skip_kblock() { return (int)g_skip_kblock.load(); }
+
+bool load_driver_entry_points() {
     std::call_once(g_driver_once, [] {
         cudaDriverEntryPointQueryResult q;
         void* fn = nullptr;
@@ -67,6 +66,7 @@ void load_driver_entry_points() {
             q == cudaDriverEntryPointSuccess)
             g_range = reinterpret_cast<AddressRangeFn>(fn);
     });
+    return g_encode != nullptr;
 }
 
 // Current device, checked for tcgen05 (compute capability 10.x) once.
@@ -104,15 +104,6 @@ int current_device(int* dev_out, DeviceInfo** info_out) {
     return TG_OK;
 }
 
-typedef unsigned __int128 u128;
-
-struct Span {
-    uintptr_t lo = 0;
-    u128 hi = 0;  // exclusive
-    bool present = false;
-};
-
-// Bytes [p, p + ((rows-1)*ld + width) * 2) of a row-strided 16-bit matrix.
 Span span_of(const void* p, int64_t rows, int64_t width, int64_t ld) {
     Span s;
     if (!p) return s;
@@ -122,12 +113,21 @@ Span span_of(const void* p, int64_t rows, int64_t width, int64_t ld) {
     return s;
 }
 
+Span span_bytes(const void* p, u128 bytes) {
+    Span s;
+    if (!p) return s;
+    s.present = true;
+    s.lo = reinterpret_cast<uintptr_t>(p);
+    s.hi = (u128)s.lo + bytes;
+    return s;
+}
+
 bool intersects(const Span& a, const Span& b) {
     if (!a.present || !b.present) return false;
     return (u128)a.lo < b.hi && (u128)b.lo < a.hi;
 }
 
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+namespace {
 
 struct Args {
     int64_t M, N, K;
@@ -161,9 +161,7 @@ int check_args(const Args& a) {
     if (!a.A || !a.B || !a.C) return TG_ERR_INVALID_ARG;
     const int64_t a_rows = a.permA == TG_OP_N ? a.M : a.K, a_w = a.permA == TG_OP_N ? a.K : a.M;
     const int64_t b_rows = a.permB == TG_OP_N ? a.K : a.N, b_w = a.permB == TG_OP_N ? a.N : a.K;
-    // Leading dimensions: >= row width (so rows never overlap), and below the
-    // tensor-map stride limit of 2^40 bytes.
-    constexpr int64_t kMaxLd = (1LL << 39) - 8;
+    // Leading dimensions: >= row width (so rows never overlap) and encodable.
     if (a.lda < a_w || a.ldb < b_w || a.ldc < a.N || a.lda > kMaxLd || a.ldb > kMaxLd ||
         a.ldc > kMaxLd)
         return TG_ERR_STRIDE;
@@ -180,6 +178,8 @@ int check_args(const Args& a) {
         if (intersects(c, s)) return TG_ERR_OVERLAP;
     return TG_OK;
 }
+
+}  // namespace
 
 // The touched bytes of every operand must lie inside one allocation of the
 // current device (proves the kernel cannot read or write outside caller memory).
@@ -201,6 +201,8 @@ int check_pointer(const void* p, const Span& s, int dev) {
     return TG_OK;
 }
 
+namespace {
+
 int check_pointers(const Args& a, int dev) {
     const int64_t a_rows = a.permA == TG_OP_N ? a.M : a.K, a_w = a.permA == TG_OP_N ? a.K : a.M;
     const int64_t b_rows = a.permB == TG_OP_N ? a.K : a.N, b_w = a.permB == TG_OP_N ? a.N : a.K;
@@ -214,9 +216,10 @@ int check_pointers(const Args& a, int dev) {
     return TG_OK;
 }
 
+}  // namespace
+
 bool encode_2d(CUtensorMap* map, int dtype, const void* base, uint64_t inner, uint64_t outer,
-               int64_t ld, uint32_t box_inner, uint32_t box_outer,
-               CUtensorMapSwizzle swizzle = CU_TENSOR_MAP_SWIZZLE_128B) {
+               int64_t ld, uint32_t box_inner, uint32_t box_outer, CUtensorMapSwizzle swizzle) {
     const cuuint64_t dims[2] = {inner, outer};
     const cuuint64_t strides[1] = {(cuuint64_t)ld * 2};
     const cuuint32_t box[2] = {box_inner, box_outer};
@@ -228,6 +231,8 @@ bool encode_2d(CUtensorMap* map, int dtype, const void* base, uint64_t inner, ui
                     CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+namespace {
+
 // Operand tensor map.  `rows` x `k` operand; if mn_major the storage has the
 // rows dimension contiguous (dims {rows, K}), else K contiguous (dims {K, rows}).
 bool encode_operand(CUtensorMap* map, int dtype, const void* base, int64_t rows, int64_t k,
@@ -235,6 +240,8 @@ bool encode_operand(CUtensorMap* map, int dtype, const void* base, int64_t rows,
     if (mn_major) return encode_2d(map, dtype, base, rows, k, ld, 64, 64);
     return encode_2d(map, dtype, base, k, rows, ld, 64, box_rows);
 }
+
+}  // namespace
 
 // An MN-major operand whose per-CTA stage is `atoms` 64-wide swizzle atoms,
 // as one 3-D box: dims {64 contiguous elements, K, rows / 64} with strides
@@ -298,6 +305,18 @@ bool encode_mn_atom_pairs(CUtensorMap* map, int dtype, const void* base, int64_t
                     CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+bool encode_f32_planes(CUtensorMap* map, const void* base, uint64_t cols, uint64_t rows,
+                       uint64_t planes, int64_t ld) {
+    const cuuint64_t dims[3] = {cols, rows, planes};
+    const cuuint64_t strides[2] = {(cuuint64_t)ld * 4, (cuuint64_t)ld * 4 * rows};
+    const cuuint32_t box[3] = {32, 32, 1};
+    const cuuint32_t estr[3] = {1, 1, 1};
+    return g_encode(map, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 3, const_cast<void*>(base), dims, strides,
+                    box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                    CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                    CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 uint32_t make_idesc(int dtype, bool p_mn, bool q_mn, int n, int m) {
     const uint32_t fmt = dtype == TG_BF16 ? 1u : 0u;
     return (1u << 4)                   // accumulator format: fp32
@@ -305,11 +324,6 @@ uint32_t make_idesc(int dtype, bool p_mn, bool q_mn, int n, int m) {
            | ((p_mn ? 1u : 0u) << 15) | ((q_mn ? 1u : 0u) << 16) |
            ((uint32_t)(n >> 3) << 17) | ((uint32_t)(m >> 4) << 24);
 }
-
-}  // namespace
-
-cudaError_t launch_copy_rows(const void* src, long long lds, void* dst, long long ldd,
-                             long long rows, long long cols, cudaStream_t stream);
 
 // Operands a tensor map cannot describe (base not 16-byte aligned, or a row
 // stride that is not a whole number of 16-byte units) are staged through the
@@ -577,7 +591,6 @@ extern "C" int tg_pointwise(int64_t M, int64_t N, const void* X, int64_t ldx, tg
     const void* resid = epi ? epi->residual : nullptr;
     const int64_t ldr = resid ? (epi->ldr ? epi->ldr : ldc) : 0;
     const int64_t x_rows = permX == TG_OP_N ? M : N, x_w = permX == TG_OP_N ? N : M;
-    constexpr int64_t kMaxLd = (1LL << 39) - 8;
     if (ldx < x_w || ldc < N || ldx > kMaxLd || ldc > kMaxLd) return TG_ERR_STRIDE;
     if (resid && (ldr < N || ldr > kMaxLd)) return TG_ERR_STRIDE;
     auto odd = [](const void* p) { return (reinterpret_cast<uintptr_t>(p) & 1u) != 0; };

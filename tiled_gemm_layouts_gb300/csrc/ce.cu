@@ -1,0 +1,621 @@
+// ce.cu -- linear cross entropy (tg_linear_ce, tg_linear_ce_grad): argument
+// checks, the plan of pieces, tiles and workspace, the launches, and the
+// small kernels around the tensor-core products of ce_kernel.cuh.
+//
+// Forward: one product kernel (CE_LSE) and a combination of its partial sums.
+// Backward: the tokens whose target lies in the vocabulary are gathered into
+// a dense copy of H first.  The others have no gradient, and a batch of
+// prompts or padded texts has many; their rows of H may hold anything, and an
+// infinity times G = 0 would put a NaN into dW.  Then, for each piece of the
+// vocabulary, CE_GRAD, CE_DH and CE_DW; at the end dH's fp32 planes are
+// summed, scaled and scattered back to the tokens' rows.
+#include <climits>
+#include <cstring>
+
+#include "../../include/tilegemm.h"
+#include "ce_launch.cuh"
+#include "host_common.h"
+
+namespace tg {
+
+template <>
+cudaError_t launch_ce_mode<CE_LSE>(const CeParams&, CeTile, int, cudaStream_t);
+template <>
+cudaError_t launch_ce_mode<CE_GRAD>(const CeParams&, CeTile, int, cudaStream_t);
+template <>
+cudaError_t launch_ce_mode<CE_DH>(const CeParams&, CeTile, int, cudaStream_t);
+template <>
+cudaError_t launch_ce_mode<CE_DW>(const CeParams&, CeTile, int, cudaStream_t);
+
+cudaError_t launch_ce(int mode, const CeParams& p, CeTile tile, int sms, cudaStream_t stream) {
+    switch (mode) {
+        case CE_LSE: return launch_ce_mode<CE_LSE>(p, tile, sms, stream);
+        case CE_GRAD: return launch_ce_mode<CE_GRAD>(p, tile, sms, stream);
+        case CE_DH: return launch_ce_mode<CE_DH>(p, tile, sms, stream);
+        default: return launch_ce_mode<CE_DW>(p, tile, sms, stream);
+    }
+}
+
+namespace {
+
+int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
+int64_t up(int64_t a, int64_t b) { return cdiv(a, b) * b; }
+
+// ------------------------------------------------------ small kernels
+
+// loss and lse of one token per warp, from its tiles' (max, sum).
+__global__ void ce_combine_kernel(const float2* __restrict__ part, const float* __restrict__ hit,
+                                  const long long* __restrict__ target, int T, long long V,
+                                  int tiles, float* __restrict__ loss, float* __restrict__ lse) {
+    const int t = (int)(blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5));
+    const int lane = threadIdx.x & 31;
+    if (t >= T) return;
+    const float2* row = part + (long long)t * tiles;
+    float m = -INFINITY, s = 0.0f;
+    auto merge = [&](float m2, float s2) {
+        const float mn = fmaxf(m, m2), base = mn == -INFINITY ? 0.0f : mn;
+        s = s * pow2(m - base) + s2 * pow2(m2 - base);
+        m = mn;
+    };
+#pragma unroll 4
+    for (int i = lane; i < tiles; i += 32) {
+        const float2 u = __ldg(row + i);
+        merge(u.x, u.y);
+    }
+#pragma unroll
+    for (int o = 16; o; o >>= 1) {
+        const float m2 = __shfl_xor_sync(0xffffffffu, m, o), s2 = __shfl_xor_sync(0xffffffffu, s, o);
+        merge(m2, s2);
+    }
+    if (lane == 0) {
+        const float l = m * 0.6931471805599453f + logf(s);
+        lse[t] = l;
+        const long long y = target[t];
+        loss[t] = y >= 0 && y < V ? l - hit[t] : 0.0f;
+    }
+}
+
+// What the backward pass keeps per token and per compacted row.
+struct CeRows {
+    int* live;          // number of tokens whose target lies in the vocabulary
+    float* alpha;       // factor that the products of the scaled G still need
+    int* token;         // [T] compacted row -> token
+    int* target;        // [T] compacted row -> target
+    float2* scale;      // [T] compacted row -> (lse in log2 units, factor of G)
+    int* place;         // [T] token -> compacted row, or -1
+};
+
+constexpr int kCompactThreads = 1024;
+
+// One block: the largest |dloss|, then a stable compaction in steps of 1024
+// tokens.  G is scaled by 2^shift / max|dloss|: with one dloss for all tokens
+// its factor is then a power of two, and rounding G to 16 bits rounds
+// (p - [hit]) itself instead of repeating one rounding of dloss in every row.
+__global__ void __launch_bounds__(kCompactThreads)
+ce_compact_kernel(const long long* __restrict__ target, const float* __restrict__ lse,
+                  const float* __restrict__ dloss, int T, long long V, float scale2, CeRows r) {
+    __shared__ float wmax[32];
+    __shared__ int wsum[33];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    float top = 0.0f;
+    for (int t = threadIdx.x; t < T; t += kCompactThreads) {
+        const long long y = target[t];
+        if (y >= 0 && y < V) top = fmaxf(top, fabsf(dloss[t]));
+    }
+#pragma unroll
+    for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+    if (lane == 0) wmax[warp] = top;
+    __syncthreads();
+    top = wmax[lane];
+#pragma unroll
+    for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+    const float ref = top > 0.0f && top < INFINITY ? top : 1.0f;
+    int total = 0;
+    for (int base = 0; base < T; base += kCompactThreads) {
+        const int t = base + threadIdx.x;
+        const long long y = t < T ? target[t] : -1;
+        const bool counts = y >= 0 && y < V;
+        const unsigned votes = __ballot_sync(0xffffffffu, counts);
+        if (lane == 0) wsum[warp] = __popc(votes);
+        __syncthreads();
+        if (warp == 0) {
+            int v = wsum[lane], x = v;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int u = __shfl_up_sync(0xffffffffu, x, o);
+                if (lane >= o) x += u;
+            }
+            wsum[lane] = x - v;
+            if (lane == 31) wsum[32] = x;
+        }
+        __syncthreads();
+        if (t < T) {
+            const int j = total + wsum[warp] + __popc(votes & ((1u << lane) - 1));
+            r.place[t] = counts ? j : -1;
+            if (counts) {
+                r.token[j] = t;
+                r.target[j] = (int)y;
+                r.scale[j] = make_float2(lse[t] * kLog2e, dloss[t] / ref * scale2);
+            }
+        }
+        total += wsum[32];
+        __syncthreads();
+    }
+    if (threadIdx.x == 0) {
+        *r.live = total;
+        *r.alpha = ref / scale2;
+    }
+}
+
+// Dense rows of H for the tokens that count: out[j] = H[token[j]], columns
+// [D, ldo) and the rows up to the next multiple of 256 filled with zeros.
+__global__ void ce_gather_kernel(const uint16_t* __restrict__ H, long long ldh, int D, CeRows r,
+                                 uint16_t* __restrict__ out, int ldo, long long max_rows) {
+    const int live = *r.live;
+    const long long rows = min(max_rows, (long long)max(256, (live + 255) / 256 * 256));
+    const int vecs = ldo / 8;
+    for (long long i = blockIdx.x * (long long)blockDim.x + threadIdx.x; i < rows * vecs;
+         i += (long long)gridDim.x * blockDim.x) {
+        const long long j = i / vecs;
+        const int c = (int)(i - j * vecs) * 8;
+        uint4 v = make_uint4(0, 0, 0, 0);
+        if (j < live && c < D) {
+            const uint16_t* s = H + (long long)__ldg(r.token + j) * ldh + c;
+            if (c + 8 <= D && (reinterpret_cast<uintptr_t>(s) & 15u) == 0) {
+                v = *reinterpret_cast<const uint4*>(s);
+            } else {
+                uint32_t e[4] = {0, 0, 0, 0};
+#pragma unroll
+                for (int k = 0; k < 8; ++k)
+                    if (c + k < D) e[k >> 1] |= (uint32_t)s[k] << (16 * (k & 1));
+                v = make_uint4(e[0], e[1], e[2], e[3]);
+            }
+        }
+        *reinterpret_cast<uint4*>(out + j * ldo + c) = v;
+    }
+}
+
+// dH rows: the sum of the fp32 planes' rows, scaled and rounded once; zeros
+// for tokens without a gradient.
+template <bool BF>
+__global__ void ce_scatter_kernel(const float* __restrict__ planes, int splits, long long plane,
+                                  int ldp, CeRows r, int T, int D, uint16_t* __restrict__ dH,
+                                  long long ldd) {
+    const float alpha = *r.alpha;
+    const int vecs = (D + 7) / 8;
+    for (long long i = blockIdx.x * (long long)blockDim.x + threadIdx.x; i < (long long)T * vecs;
+         i += (long long)gridDim.x * blockDim.x) {
+        const long long t = i / vecs;
+        const int c = (int)(i - t * vecs) * 8;
+        const int j = __ldg(r.place + t);
+        float y[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+        if (j >= 0) {
+            const float* s = planes + (long long)j * ldp + c;
+            for (int k = 0; k < splits; ++k, s += plane) {
+                const float4 a = *reinterpret_cast<const float4*>(s);
+                const float4 b = *reinterpret_cast<const float4*>(s + 4);
+                y[0] += a.x; y[1] += a.y; y[2] += a.z; y[3] += a.w;
+                y[4] += b.x; y[5] += b.y; y[6] += b.z; y[7] += b.w;
+            }
+#pragma unroll
+            for (int k = 0; k < 8; ++k) y[k] *= alpha;
+        }
+        uint16_t* o = dH + t * ldd + c;
+        if (c + 8 <= D && (reinterpret_cast<uintptr_t>(o) & 15u) == 0) {
+            *reinterpret_cast<uint4*>(o) = make_uint4(pack2t<BF>(y[0], y[1]), pack2t<BF>(y[2], y[3]),
+                                                      pack2t<BF>(y[4], y[5]), pack2t<BF>(y[6], y[7]));
+        } else {
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+                if (c + k < D) o[k] = from_f32(y[k], BF);
+        }
+    }
+}
+
+unsigned blocks_for(int64_t threads, int sms) {
+    const int64_t blocks = cdiv(threads, 256), most = (int64_t)sms * 8;
+    return (unsigned)(blocks < most ? blocks : most);
+}
+
+// --------------------------------------------------------------- plans
+
+bool tma_rows(const void* p, int64_t ld) { return aligned16(p) && (ld * 2) % 16 == 0; }
+
+// Places regions one after another, 256-byte aligned.
+struct Cursor {
+    size_t at = 0;
+    size_t take(u128 bytes) {
+        const size_t here = at;
+        at += ((size_t)bytes + 255) / 256 * 256;
+        return here;
+    }
+};
+
+// Tile of the logits' products: CTA pairs from 129 tokens on.  For fewer, a
+// pair's second half would multiply rows that do not exist, and reading W
+// bounds the time: 128-column tiles of single CTAs deal V out more evenly.
+CeTile logits_tile(int64_t T) { return T > 128 ? CeTile{256, 1} : CeTile{128, 0}; }
+
+struct FwdPlan {
+    bool copy_h, copy_w;
+    CeTile tile;
+    int64_t tiles_n;
+    size_t part, hit, h, w, bytes;
+};
+
+FwdPlan forward_plan(int64_t T, int64_t V, int64_t D, const void* H, int64_t ldh, const void* W,
+                     int64_t ldw) {
+    FwdPlan f;
+    f.copy_h = !tma_rows(H, ldh);
+    f.copy_w = !tma_rows(W, ldw);
+    f.tile = logits_tile(T);
+    f.tiles_n = cdiv(V, f.tile.bn);
+    Cursor c;
+    f.part = c.take((u128)T * f.tiles_n * sizeof(float2));
+    f.hit = c.take((u128)T * sizeof(float));
+    f.h = c.take(f.copy_h ? (u128)T * up(D, 8) * 2 : 0);
+    f.w = c.take(f.copy_w ? (u128)V * up(D, 8) * 2 : 0);
+    f.bytes = c.at;
+    return f;
+}
+
+// Bytes that a piece of G may take.  Each piece costs three launches, whose
+// first and last tiles leave SMs idle; a larger one costs memory only.
+constexpr int64_t kPieceBytes = 512LL << 20;
+
+struct BwdPlan {
+    bool copy_w;
+    int64_t rows;        // T rounded up to whole 256-row tiles
+    int64_t ldh;         // columns of the gathered H: D rounded up to whole K-blocks
+    int64_t piece;       // columns of a piece of G, a multiple of 256
+    int64_t pieces;
+    int64_t ldp;         // columns of dH's planes
+    CeTile grad, dh, dw;
+    int64_t dh_kb;       // K-blocks of one split of dH's contraction
+    int splits;
+    size_t live, token, target, scale, place, h, g, planes, w, bytes;
+};
+
+BwdPlan backward_plan(int64_t T, int64_t V, int64_t D, const void* W, int64_t ldw, int sms) {
+    BwdPlan b;
+    b.copy_w = !tma_rows(W, ldw);
+    b.rows = up(T, 256);
+    b.ldh = up(D, 64);
+    const int64_t tiles_v = cdiv(V, 256);
+    int64_t most = kPieceBytes / (b.rows * 512);
+    if (most < 1) most = 1;
+    b.pieces = cdiv(tiles_v, most);
+    b.piece = cdiv(tiles_v, b.pieces) * 256;
+    b.pieces = cdiv(V, b.piece);
+    b.ldp = up(D, 8);
+    b.grad = logits_tile(T);
+    b.dh = T > 128 ? CeTile{D > 128 ? 256 : 128, 1} : CeTile{128, 0};
+    b.dw = CeTile{D > 128 ? 256 : 128, 1};
+    // dH's tiles alone often leave SMs idle while its contraction over the
+    // piece is long: split that into planes, each at least 8 K-blocks deep
+    const int64_t tiles = cdiv(T, b.dh.pair ? 256 : 128) * cdiv(D, b.dh.bn);
+    const int64_t kb = cdiv(V < b.piece ? V : b.piece, 64), workers = b.dh.pair ? sms / 2 : sms;
+    int64_t splits = workers / tiles;
+    if (splits > kb / 8) splits = kb / 8;
+    if (splits < 1) splits = 1;
+    b.dh_kb = up(cdiv(kb, splits), 2);
+    b.splits = (int)cdiv(kb, b.dh_kb);
+    Cursor c;
+    b.live = c.take(8);
+    b.token = c.take((u128)T * 4);
+    b.target = c.take((u128)T * 4);
+    b.scale = c.take((u128)T * 8);
+    b.place = c.take((u128)T * 4);
+    b.h = c.take((u128)b.rows * b.ldh * 2);
+    b.g = c.take((u128)b.rows * b.piece * 2);
+    b.planes = c.take((u128)b.splits * T * b.ldp * 4);
+    b.w = c.take(b.copy_w ? (u128)V * up(D, 8) * 2 : 0);
+    b.bytes = c.at;
+    return b;
+}
+
+// ------------------------------------------------------ argument checks
+
+int check_sizes(int64_t T, int64_t V, int64_t D, int dtype) {
+    if (T <= 0 || V <= 0 || D <= 0 || T > kMaxDim || V > kMaxDim || D > kMaxDim)
+        return TG_ERR_INVALID_ARG;
+    // tiles are counted in 32 bits
+    if (cdiv(T, 128) * cdiv(V, 64) > INT_MAX || cdiv(T, 128) * cdiv(D, 64) > INT_MAX ||
+        cdiv(V, 128) * cdiv(D, 64) > INT_MAX)
+        return TG_ERR_INVALID_ARG;
+    if (dtype != TG_F16 && dtype != TG_BF16) return TG_ERR_DTYPE;
+    return TG_OK;
+}
+
+bool off(const void* p, unsigned bytes) { return (reinterpret_cast<uintptr_t>(p) & (bytes - 1)) != 0; }
+
+// Every output (and the workspace) disjoint from every other operand.
+template <int N>
+int check_disjoint(const Span (&s)[N], int outputs) {
+    for (int i = 0; i < outputs; ++i)
+        for (int j = i + 1; j < N; ++j)
+            if (intersects(s[i], s[j])) return TG_ERR_OVERLAP;
+    return TG_OK;
+}
+
+void common_params(CeParams* p, int dtype, const DeviceInfo* info) {
+    std::memset(p, 0, sizeof(*p));
+    p->bf16 = dtype == TG_BF16;
+    p->splits = 1;
+    p->timeout_cycles = watchdog_timeout();
+    p->status = info->status;
+}
+
+// K-major operand: `rows` x `k`, `box` rows of it per CTA.
+bool k_major(CUtensorMap* one, CUtensorMap* two, int* use_two, int dtype, const void* base,
+             int64_t rows, int64_t k, int64_t ld, int box) {
+    *use_two = two && encode_k_pairs(two, dtype, base, rows, k, ld, (uint32_t)box);
+    return encode_2d(one, dtype, base, k, rows, ld, 64, (uint32_t)box);
+}
+
+// Q = W^T or H'^T of the logits: K-major, and P = H or H', K-major.
+bool logits_maps(CeParams* p, int dtype, CeTile tile, const void* H, int64_t h_rows, int64_t h_cols,
+                 int64_t ldh, const void* W, int64_t V, int64_t D, int64_t ldw) {
+    // For few tokens the box holds only the rows there are, in whole groups of
+    // 8: one token's K-block is then 1 KB of copies instead of 16.  (The rest
+    // of the stage keeps old bytes, which reach only accumulator rows that
+    // nobody reads.)
+    const int64_t box = h_rows >= 128 ? 128 : up(h_rows, 8);
+    p->p_bytes = (uint32_t)box * 128;
+    int unused;
+    if (!k_major(&p->map_p, box == 128 ? &p->map_p2 : nullptr, box == 128 ? &p->p_2k : &unused, dtype,
+                 H, h_rows, h_cols, ldh, (int)box) ||
+        !k_major(&p->map_q, &p->map_q2, &p->q_2k, dtype, W, V, D, ldw,
+                 tile.pair ? tile.bn / 2 : tile.bn))
+        return false;
+    p->num_kb = p->kb_per_split = (int)cdiv(D, 64);
+    p->idesc = make_idesc(dtype, false, false, tile.bn, tile.pair ? 256 : 128);
+    return true;
+}
+
+// MN-major Q: `cols` columns contiguous, `k` rows of them.
+bool mn_major_q(CeParams* p, int dtype, CeTile tile, const void* base, int64_t cols, int64_t k,
+                int64_t ld) {
+    const int atoms = (tile.pair ? tile.bn / 2 : tile.bn) / 64;
+    p->q_3d = encode_mn_atoms(&p->map_q, dtype, base, cols, k, ld, (uint32_t)atoms);
+    p->q_2k = p->q_3d && encode_mn_atom_pairs(&p->map_q2, dtype, base, cols, k, ld, (uint32_t)atoms);
+    return p->q_3d || encode_2d(&p->map_q, dtype, base, cols, k, ld, 64, 64);
+}
+
+// Tile rows of a raster group: enough for a wave of tiles to share panels of
+// both operands (the GEMM kernel's value).
+int raster(int64_t tiles_m) { return (int)(tiles_m < 16 ? tiles_m : 16); }
+
+}  // namespace
+}  // namespace tg
+
+using namespace tg;
+
+extern "C" int tg_linear_ce_workspace_size(int64_t T, int64_t V, int64_t D, const void* H,
+                                           int64_t ldh, const void* W, int64_t ldw, tg_dtype dtype,
+                                           size_t* bytes) {
+    const int rc = check_sizes(T, V, D, (int)dtype);
+    if (rc) return rc;
+    if (!bytes) return TG_ERR_INVALID_ARG;
+    if (ldh < D || ldw < D || ldh > kMaxLd || ldw > kMaxLd) return TG_ERR_STRIDE;
+    *bytes = forward_plan(T, V, D, H, ldh, W, ldw).bytes;
+    return TG_OK;
+}
+
+extern "C" int tg_linear_ce(int64_t T, int64_t V, int64_t D, const void* H, int64_t ldh,
+                            const void* W, int64_t ldw, const int64_t* target, float* loss,
+                            float* lse, tg_dtype dtype, void* workspace, size_t workspace_bytes,
+                            cudaStream_t stream) {
+    int rc = check_sizes(T, V, D, (int)dtype);
+    if (rc) return rc;
+    if (!H || !W || !target || !loss || !lse || !workspace) return TG_ERR_INVALID_ARG;
+    if (ldh < D || ldw < D || ldh > kMaxLd || ldw > kMaxLd) return TG_ERR_STRIDE;
+    if (off(H, 2) || off(W, 2) || off(target, 8) || off(loss, 4) || off(lse, 4) || off(workspace, 256))
+        return TG_ERR_ALIGN;
+    const FwdPlan f = forward_plan(T, V, D, H, ldh, W, ldw);
+    if (workspace_bytes < f.bytes) return TG_ERR_BUFFER;
+    const Span spans[6] = {span_bytes(loss, (u128)T * 4), span_bytes(lse, (u128)T * 4),
+                           span_bytes(workspace, f.bytes), span_of(H, T, D, ldh),
+                           span_of(W, V, D, ldw), span_bytes(target, (u128)T * 8)};
+    if ((rc = check_disjoint(spans, 3))) return rc;
+    int dev;
+    DeviceInfo* info;
+    if ((rc = current_device(&dev, &info))) return rc;
+    if (!load_driver_entry_points()) return TG_ERR_CUDA;
+    const void* ptrs[6] = {loss, lse, workspace, H, W, target};
+    for (int i = 0; i < 6; ++i)
+        if ((rc = check_pointer(ptrs[i], spans[i], dev))) return rc;
+
+    char* ws = static_cast<char*>(workspace);
+    bool ok = true;
+    if (f.copy_h) {
+        ok = ok && launch_copy_rows(H, ldh, ws + f.h, up(D, 8), T, D, stream) == cudaSuccess;
+        H = ws + f.h;
+        ldh = up(D, 8);
+    }
+    if (f.copy_w) {
+        ok = ok && launch_copy_rows(W, ldw, ws + f.w, up(D, 8), V, D, stream) == cudaSuccess;
+        W = ws + f.w;
+        ldw = up(D, 8);
+    }
+    CeParams p;
+    common_params(&p, (int)dtype, info);
+    ok = ok && logits_maps(&p, (int)dtype, f.tile, H, T, D, ldh, W, V, D, ldw);
+    p.tiles_m = (int)cdiv(T, f.tile.pair ? 256 : 128);
+    p.tiles_n = (int)f.tiles_n;
+    p.group_m = raster(p.tiles_m);
+    p.rows = (int)T;
+    p.cols = (int)V;
+    p.target = reinterpret_cast<const long long*>(target);
+    p.part = reinterpret_cast<float2*>(ws + f.part);
+    p.hit = reinterpret_cast<float*>(ws + f.hit);
+    ok = ok && launch_ce(CE_LSE, p, f.tile, info->sms, stream) == cudaSuccess;
+    if (ok) {
+        ce_combine_kernel<<<(unsigned)cdiv(T, 8), 256, 0, stream>>>(p.part, p.hit, p.target, (int)T, V,
+                                                                    p.tiles_n, loss, lse);
+        ok = cudaGetLastError() == cudaSuccess;
+    }
+    if (!ok) {
+        cudaGetLastError();
+        return TG_ERR_CUDA;
+    }
+    return TG_OK;
+}
+
+extern "C" int tg_linear_ce_grad_workspace_size(int64_t T, int64_t V, int64_t D, const void* H,
+                                                int64_t ldh, const void* W, int64_t ldw,
+                                                const void* dH, int64_t lddh, const void* dW,
+                                                int64_t lddw, tg_dtype dtype, size_t* bytes) {
+    int rc = check_sizes(T, V, D, (int)dtype);
+    if (rc) return rc;
+    if (!bytes || (!dH && !dW)) return TG_ERR_INVALID_ARG;
+    if (ldh < D || ldw < D || ldh > kMaxLd || ldw > kMaxLd) return TG_ERR_STRIDE;
+    if ((dH && (lddh < D || lddh > kMaxLd)) || (dW && (lddw < D || lddw > kMaxLd))) return TG_ERR_STRIDE;
+    (void)H;
+    int dev;
+    DeviceInfo* info;
+    if ((rc = current_device(&dev, &info))) return rc;
+    *bytes = backward_plan(T, V, D, W, ldw, info->sms).bytes;
+    return TG_OK;
+}
+
+extern "C" int tg_linear_ce_grad(int64_t T, int64_t V, int64_t D, const void* H, int64_t ldh,
+                                 const void* W, int64_t ldw, const int64_t* target,
+                                 const float* lse, const float* dloss, void* dH, int64_t lddh,
+                                 void* dW, int64_t lddw, tg_dtype dtype, void* workspace,
+                                 size_t workspace_bytes, cudaStream_t stream) {
+    int rc = check_sizes(T, V, D, (int)dtype);
+    if (rc) return rc;
+    if (!H || !W || !target || !lse || !dloss || (!dH && !dW) || !workspace) return TG_ERR_INVALID_ARG;
+    if (ldh < D || ldw < D || ldh > kMaxLd || ldw > kMaxLd) return TG_ERR_STRIDE;
+    if ((dH && (lddh < D || lddh > kMaxLd)) || (dW && (lddw < D || lddw > kMaxLd))) return TG_ERR_STRIDE;
+    if (off(H, 2) || off(W, 2) || off(dH, 2) || off(dW, 2) || off(target, 8) || off(lse, 4) ||
+        off(dloss, 4) || off(workspace, 256))
+        return TG_ERR_ALIGN;
+    const Span outs[2] = {span_of(dH, T, D, lddh), span_of(dW, V, D, lddw)};
+    const Span ins[5] = {span_of(H, T, D, ldh), span_of(W, V, D, ldw), span_bytes(target, (u128)T * 8),
+                         span_bytes(lse, (u128)T * 4), span_bytes(dloss, (u128)T * 4)};
+    {
+        const Span all[7] = {outs[0], outs[1], ins[0], ins[1], ins[2], ins[3], ins[4]};
+        if ((rc = check_disjoint(all, 2))) return rc;
+    }
+    int dev;
+    DeviceInfo* info;
+    if ((rc = current_device(&dev, &info))) return rc;
+    if (!load_driver_entry_points()) return TG_ERR_CUDA;
+    const BwdPlan b = backward_plan(T, V, D, W, ldw, info->sms);
+    if (workspace_bytes < b.bytes) return TG_ERR_BUFFER;
+    const Span work = span_bytes(workspace, b.bytes);
+    for (const Span& s : outs)
+        if (intersects(work, s)) return TG_ERR_OVERLAP;
+    for (const Span& s : ins)
+        if (intersects(work, s)) return TG_ERR_OVERLAP;
+    if ((rc = check_pointer(workspace, work, dev)) || (rc = check_pointer(dH, outs[0], dev)) ||
+        (rc = check_pointer(dW, outs[1], dev)) || (rc = check_pointer(H, ins[0], dev)) ||
+        (rc = check_pointer(W, ins[1], dev)) || (rc = check_pointer(target, ins[2], dev)) ||
+        (rc = check_pointer(lse, ins[3], dev)) || (rc = check_pointer(dloss, ins[4], dev)))
+        return rc;
+
+    char* ws = static_cast<char*>(workspace);
+    const int dt = (int)dtype, sms = info->sms;
+    bool ok = true;
+    if (b.copy_w) {
+        ok = launch_copy_rows(W, ldw, ws + b.w, up(D, 8), V, D, stream) == cudaSuccess;
+        W = ws + b.w;
+        ldw = up(D, 8);
+    }
+    CeRows rows;
+    rows.live = reinterpret_cast<int*>(ws + b.live);
+    rows.alpha = reinterpret_cast<float*>(ws + b.live) + 1;
+    rows.token = reinterpret_cast<int*>(ws + b.token);
+    rows.target = reinterpret_cast<int*>(ws + b.target);
+    rows.scale = reinterpret_cast<float2*>(ws + b.scale);
+    rows.place = reinterpret_cast<int*>(ws + b.place);
+    uint16_t* h = reinterpret_cast<uint16_t*>(ws + b.h);
+    uint16_t* g = reinterpret_cast<uint16_t*>(ws + b.g);
+    float* planes = reinterpret_cast<float*>(ws + b.planes);
+    ce_compact_kernel<<<1, kCompactThreads, 0, stream>>>(reinterpret_cast<const long long*>(target), lse,
+                                                         dloss, (int)T, V, dt == TG_F16 ? 1024.0f : 1.0f,
+                                                         rows);
+    ce_gather_kernel<<<blocks_for(b.rows * (b.ldh / 8), sms), 256, 0, stream>>>(
+        static_cast<const uint16_t*>(H), ldh, (int)D, rows, h, (int)b.ldh, b.rows);
+    ok = ok && cudaGetLastError() == cudaSuccess;
+
+    for (int64_t i = 0; ok && i < b.pieces; ++i) {
+        const int64_t v0 = i * b.piece, cols = V - v0 < b.piece ? V - v0 : b.piece;
+        const uint16_t* w = static_cast<const uint16_t*>(W) + v0 * ldw;
+        CeParams p;
+        // G, scaled: T x cols logits from the gathered rows
+        common_params(&p, dt, info);
+        ok = logits_maps(&p, dt, b.grad, h, b.rows, b.ldh, b.ldh, w, cols, D, ldw) &&
+             encode_2d(&p.map_c, dt, g, b.piece, b.rows, b.piece, 32, 32, CU_TENSOR_MAP_SWIZZLE_64B);
+        p.live = rows.live;
+        p.tiles_m = (int)cdiv(T, b.grad.pair ? 256 : 128);
+        p.tiles_n = (int)cdiv(cols, b.grad.bn);
+        p.group_m = raster(p.tiles_m);
+        p.rows = (int)T;
+        p.cols = (int)cols;
+        p.col0 = v0;
+        p.row_target = rows.target;
+        p.row_scale = rows.scale;
+        ok = ok && launch_ce(CE_GRAD, p, b.grad, sms, stream) == cudaSuccess;
+        if (ok && dH) {
+            const int64_t kb = cdiv(cols, 64);
+            common_params(&p, dt, info);
+            // a K-block past `cols` meets G's zero columns and W rows that the
+            // map fills with zeros
+            ok = k_major(&p.map_p, &p.map_p2, &p.p_2k, dt, g, b.rows, kb * 64, b.piece, 128) &&
+                 mn_major_q(&p, dt, b.dh, w, D, cols, ldw) &&
+                 encode_f32_planes(&p.map_c, planes, b.ldp, T, b.splits, b.ldp);
+            p.p_bytes = 128 * 128;
+            p.live = rows.live;
+            p.num_kb = (int)kb;
+            p.kb_per_split = (int)b.dh_kb;
+            p.splits = (int)cdiv(kb, b.dh_kb);
+            p.tiles_m = (int)cdiv(T, b.dh.pair ? 256 : 128);
+            p.tiles_n = (int)cdiv(D, b.dh.bn);
+            p.group_m = raster(p.tiles_m);
+            p.idesc = make_idesc(dt, false, true, b.dh.bn, b.dh.pair ? 256 : 128);
+            p.out_rows = (int)T;
+            p.out_cols = (int)D;
+            p.accumulate = i > 0;
+            ok = ok && launch_ce(CE_DH, p, b.dh, sms, stream) == cudaSuccess;
+        }
+        if (ok && dW) {
+            common_params(&p, dt, info);
+            uint16_t* out = static_cast<uint16_t*>(dW) + v0 * lddw;
+            const bool tensor = tma_rows(dW, lddw) && D >= 8;
+            p.n_tma = tensor ? (int)(D & ~int64_t(7)) : 0;
+            ok = encode_mn_atoms(&p.map_p, dt, g, b.piece, b.rows, b.piece, 2) &&
+                 mn_major_q(&p, dt, b.dw, h, b.ldh, b.rows, b.ldh) &&
+                 encode_2d(&p.map_c, dt, tensor ? out : g, tensor ? p.n_tma : 8, cols,
+                           tensor ? lddw : b.piece, 32, 32, CU_TENSOR_MAP_SWIZZLE_64B);
+            p.p_2k = encode_mn_atom_pairs(&p.map_p2, dt, g, b.piece, b.rows, b.piece, 2);
+            p.p_bytes = 128 * 128;
+            p.live = rows.live;
+            p.num_kb = p.kb_per_split = (int)(b.rows / 64);
+            p.tiles_m = (int)cdiv(cols, 256);
+            p.tiles_n = (int)cdiv(D, b.dw.bn);
+            p.group_m = raster(p.tiles_m);
+            p.idesc = make_idesc(dt, true, true, b.dw.bn, 256);
+            p.out = out;
+            p.ldo = lddw;
+            p.out_rows = (int)cols;
+            p.out_cols = (int)D;
+            p.alpha = rows.alpha;
+            ok = ok && launch_ce(CE_DW, p, b.dw, sms, stream) == cudaSuccess;
+        }
+    }
+    if (ok && dH) {
+        const unsigned blocks = blocks_for(T * ((D + 7) / 8), sms);
+        auto kern = dt == TG_BF16 ? ce_scatter_kernel<true> : ce_scatter_kernel<false>;
+        kern<<<blocks, 256, 0, stream>>>(planes, b.splits, (long long)T * b.ldp, (int)b.ldp, rows, (int)T,
+                                         (int)D, static_cast<uint16_t*>(dH), lddh);
+        ok = cudaGetLastError() == cudaSuccess;
+    }
+    if (!ok) {
+        cudaGetLastError();
+        return TG_ERR_CUDA;
+    }
+    return TG_OK;
+}

@@ -1,0 +1,11 @@
+// Instantiations of the linear cross entropy kernel: CE_DW.
+#include "ce_launch.cuh"
+
+namespace tg {
+template <>
+cudaError_t launch_ce_mode<CE_DW>(const CeParams& p, CeTile tile, int sms, cudaStream_t stream) {
+    if (tile.pair && tile.bn == 256) return launch_ce_tile<CE_DW, 256, true>(p, sms, stream);
+    if (tile.pair && tile.bn == 128) return launch_ce_tile<CE_DW, 128, true>(p, sms, stream);
+    return cudaErrorInvalidValue;
+}
+}  // namespace tg

@@ -1,0 +1,570 @@
+// ce_kernel.cuh -- the tensor-core products of linear cross entropy on
+// sm_103a: softmax cross entropy of the logits l = H W^T (H: T x D, W: V x D)
+// whose T x V logits never reach memory, and its gradients.
+//
+//   lse_t = log sum_v exp l_tv          loss_t = lse_t - l_t,target
+//   G_tv  = g_t (exp(l_tv - lse_t) - [v = target_t])
+//   dH    = G W                         dW = G^T H
+//
+// The forward pass is one GEMM whose epilogue keeps a running maximum and sum
+// of powers of two per accumulator row: in TMEM a tile's row is one lane, so
+// the thread that reads it reduces its 256 columns without talking to any
+// other, and only 8 bytes per row and tile leave the SM.  The backward pass
+// recomputes the logits piece by piece of the vocabulary (2TVD operations,
+// where keeping them would take 2TV or 4TV bytes), writes each piece of G in
+// 16 bits, and multiplies it twice.  G is scaled so that its largest possible
+// entry is 1 (bf16) or 1024 (fp16, whose smallest normal number is 6e-5 while
+// a probability is about 1/V); the factor is applied to the fp32 products.
+//
+// The main loop is that of the GEMM kernel: two TMA producer warps fill a
+// ring of 128B-swizzled stages, one thread issues tcgen05.mma into a
+// double-buffered fp32 accumulator in TMEM, four epilogue warps drain it
+// while the next tile's products run; tiles of 256 x BN on a CTA pair, or
+// 128 x BN on one CTA for few tokens.  Every wait is bounded; on a timeout
+// the status word is set, copies and MMAs in flight are drained, TMEM is
+// freed and the kernel returns.
+//
+// What bounds it: at T = 8192, D = 4096 the tensor pipe; the epilogue's
+// 128 x 256 exponentials per tile and SM take 2048 cycles of the special
+// function unit against 16384 cycles of products, beside them.  For a few
+// tokens, reading W.
+#pragma once
+
+#include "ce_params.h"
+#include "gemm_kernel.cuh"
+
+namespace tg {
+
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr int kCeThreads = 32 * (3 + kEpiWarps);  // producers (warps 0 and 6), MMA (1), epilogue (2..5)
+constexpr int kCeBlocksPerStage = 2;              // K-blocks per barrier transaction
+
+// 2^x; results below the normal range become 0 (for sums of at least 1).
+__device__ __forceinline__ float pow2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// 2^x with gradual underflow, for probabilities that are results themselves.
+__device__ __forceinline__ float pow2_gradual(float x) {
+    float y;
+    asm("ex2.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// (a, b) * s + (t, t), as one packed operation.
+__device__ __forceinline__ void fma2(float a, float b, float s, float t, float& x, float& y) {
+    unsigned long long ab, ss, tt;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(ab) : "f"(a), "f"(b));
+    asm("mov.b64 %0, {%1, %1};" : "=l"(ss) : "f"(s));
+    asm("mov.b64 %0, {%1, %1};" : "=l"(tt) : "f"(t));
+    asm("fma.rn.f32x2 %0, %0, %1, %2;" : "+l"(ab) : "l"(ss), "l"(tt));
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(x), "=f"(y) : "l"(ab));
+}
+
+// Waits for this thread's TMEM loads; the loaded registers pass through, so
+// no use of them is scheduled before it.
+__device__ __forceinline__ void tmem_wait_ld_regs(uint32_t (&r)[32]) {
+    tmem_wait_ld();
+#pragma unroll
+    for (int j = 0; j < 32; ++j) asm volatile("" : "+r"(r[j]));
+}
+
+// 3-D tensor store and tensor add, shared -> global, fp32.
+__device__ __forceinline__ void tma_store_3d(const CUtensorMap* map, uint32_t src, int c0, int c1,
+                                             int c2) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.global.shared::cta.tile.bulk_group [%0, {%2, %3, %4}], [%1];" ::"l"(
+            reinterpret_cast<uint64_t>(map)),
+        "r"(src), "r"(c0), "r"(c1), "r"(c2)
+        : "memory");
+}
+__device__ __forceinline__ void tma_add_3d(const CUtensorMap* map, uint32_t src, int c0, int c1,
+                                           int c2) {
+    asm volatile(
+        "cp.reduce.async.bulk.tensor.3d.global.shared::cta.add.tile.bulk_group"
+        " [%0, {%2, %3, %4}], [%1];" ::"l"(reinterpret_cast<uint64_t>(map)),
+        "r"(src), "r"(c0), "r"(c1), "r"(c2)
+        : "memory");
+}
+
+// The work items of one persistent worker: (tile, split of the contraction),
+// every `workers`-th.  `live` shrinks the row tiles or the K-blocks to those
+// that hold a row that counts; one is always left, so that every output is
+// written (its rows are zeros).
+template <int MODE>
+struct CeItems {
+    int tiles_m, tiles_n, num_kb, kb_per, group_m, step;
+    long long at, end;
+
+    __device__ __forceinline__ CeItems(const CeParams& p, int worker, int workers, int bm)
+        : tiles_m(p.tiles_m), tiles_n(p.tiles_n), num_kb(p.num_kb), kb_per(p.kb_per_split),
+          group_m(p.group_m), step(workers), at(worker) {
+        if (p.live) {
+            const int n = max(1, __ldg(p.live));
+            if (MODE == CE_DW)
+                num_kb = kb_per = min(num_kb, (n + kBK - 1) / kBK);
+            else
+                tiles_m = min(tiles_m, (n + bm - 1) / bm);
+        }
+        end = (long long)tiles_m * tiles_n * p.splits;
+    }
+    __device__ __forceinline__ bool next(int& tm, int& tn, int& split, int& kb0, int& kb1) {
+        if (at >= end) return false;
+        const long long tiles = (long long)tiles_m * tiles_n;
+        split = (int)(at / tiles);
+        const int t = (int)(at - split * tiles);
+        const int group = group_m * tiles_n, g = t / group, first = g * group_m;
+        const int gm = min(tiles_m - first, group_m), r = t - g * group;
+        tm = first + r % gm;
+        tn = r / gm;
+        kb0 = split * kb_per;
+        kb1 = min(num_kb, kb0 + kb_per);
+        at += step;
+        return true;
+    }
+};
+
+// ------------------------------------------------------------ epilogues
+//
+// Each holds what one thread keeps for its accumulator row and takes the
+// tile's columns in chunks of 32, in order.
+
+// The row's running (max, sum): m in log2 units, s the sum of 2^(l - m).
+struct CeRowStats {
+    float m, s, hit;
+    int target;  // column of the tile's row of logits, or negative
+
+    __device__ __forceinline__ void chunk(const uint32_t (&v)[32], int c0, int cols) {
+        if (c0 >= cols) return;
+        float x[32];
+#pragma unroll
+        for (int j = 0; j < 32; ++j) x[j] = __uint_as_float(v[j]);
+        if (c0 + 32 > cols) {
+#pragma unroll
+            for (int j = 0; j < 32; ++j)
+                if (c0 + j >= cols) x[j] = -INFINITY;
+        }
+        const unsigned d = (unsigned)(target - c0);
+        if (d < 32u) {
+#pragma unroll
+            for (int j = 0; j < 32; ++j) hit = d == (unsigned)j ? x[j] : hit;
+        }
+        float top[4] = {x[0], x[1], x[2], x[3]};
+#pragma unroll
+        for (int j = 4; j < 32; ++j) top[j & 3] = fmaxf(top[j & 3], x[j]);
+        const float mc = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * kLog2e;
+        const float mn = fmaxf(m, mc);
+        const float base = mn == -INFINITY ? 0.0f : mn;  // a row of -inf so far: every term is 0
+        float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+        for (int j = 0; j < 32; j += 2) {
+            float a, b;
+            fma2(x[j], x[j + 1], kLog2e, -base, a, b);
+            add2(&sum[j & 2], pow2(a), pow2(b));
+        }
+        s = s * pow2(m - base) + ((sum[0] + sum[1]) + (sum[2] + sum[3]));
+        m = mn;
+    }
+};
+
+// One kernel for the four products.  PAIR: a CTA pair works on 256 x BN tiles.
+template <int MODE, int BN, bool PAIR>
+__global__ void __launch_bounds__(kCeThreads, 1) ce_kernel(const __grid_constant__ CeParams p) {
+    using TS = TileShape<BN, PAIR>;
+    constexpr bool P_MN = MODE == CE_DW;                    // P's rows contiguous in memory
+    constexpr bool Q_MN = MODE == CE_DH || MODE == CE_DW;   // Q's columns contiguous
+    constexpr int STAGES = TS::kStages;
+    constexpr int GROUPS = STAGES / kCeBlocksPerStage;
+    constexpr int CG = PAIR ? 2 : 1;
+    constexpr uint32_t kQBytes = Q_MN ? (uint32_t)TS::kBStage : (uint32_t)TS::kBNC * 128u;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                               ~uintptr_t(1023));
+    uint8_t* sA = smem;
+    uint8_t* sB = smem + STAGES * TS::kAStage;
+    uint8_t* staging = sB + STAGES * TS::kBStage;
+    uint64_t* full = reinterpret_cast<uint64_t*>(staging + TS::kStaging);
+    uint64_t* empty = full + GROUPS;
+    uint64_t* tfull = empty + GROUPS;
+    uint64_t* tempty = tfull + 2;
+    uint64_t* drain = tempty + 2;
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+
+    const int warp = threadIdx.x >> 5;
+    const int lane = threadIdx.x & 31;
+    const uint32_t rank = PAIR ? cluster_ctarank() : 0;
+    const bool leader = rank == 0;
+    const int worker = PAIR ? (int)(blockIdx.x >> 1) : (int)blockIdx.x;
+    const int workers = PAIR ? (int)(gridDim.x >> 1) : (int)gridDim.x;
+    const Watch w{abort_flag,
+                  PAIR ? mapa_shared(smem_addr((const void*)abort_flag), rank ^ 1u) : 0u, PAIR,
+                  p.status, p.timeout_cycles};
+
+    if (threadIdx.x == 0) {
+        prefetch_tensormap(&p.map_p);
+        prefetch_tensormap(&p.map_q);
+        for (int s = 0; s < GROUPS; ++s) {
+            mbar_init(smem_addr(&full[s]), 1);
+            mbar_init(smem_addr(&empty[s]), 1);
+        }
+        for (int b = 0; b < 2; ++b) {
+            mbar_init(smem_addr(&tfull[b]), 1);
+            mbar_init(smem_addr(&tempty[b]), (PAIR ? 2 : 1) * kEpiWarps);
+        }
+        mbar_init(smem_addr(drain), 1);
+        *abort_flag = 0;
+        fence_barrier_init();
+    }
+    if (warp == 1) {
+        tmem_alloc<CG>(smem_addr(tmem_slot), TS::kTmemCols);
+        tmem_relinquish<CG>();
+    }
+    tc_fence_before();
+    if constexpr (PAIR)
+        cluster_sync();
+    else
+        __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem_base = *tmem_slot;
+
+    // ------------------------------------------------------ TMA producers
+    // Role 1 arms each transaction and loads P, role 2 loads Q into it.
+    auto run_producer = [&](auto role) {
+        constexpr int ROLE = decltype(role)::value;
+        int grp = 0;
+        uint32_t phase = 0, armed = 0, armed_parity = 0;
+        const uint32_t stage_tx = (p.p_bytes + kQBytes) * (PAIR ? 2u : 1u);
+        CeItems<MODE> items(p, worker, workers, TS::kBM);
+        int tm, tn, split, kb0, kb1;
+        bool ok = true;
+        while (ok && items.next(tm, tn, split, kb0, kb1)) {
+            const int m0 = tm * TS::kBM + (int)rank * 128;
+            const int n0 = tn * BN + (int)rank * TS::kBNC;
+            for (int kb = kb0; kb < kb1; kb += kCeBlocksPerStage) {
+                const int n = min(kb1 - kb, kCeBlocksPerStage);
+                if (!wait_bar(smem_addr(&empty[grp]), phase ^ 1, w, DEV_TIMEOUT_PRODUCER + 1)) {
+                    ok = false;
+                    break;
+                }
+                const uint32_t fb_local = smem_addr(&full[grp]);
+                if (ROLE == 1 && leader) {
+                    mbar_arrive_expect_tx(fb_local, stage_tx * (uint32_t)n);
+                    armed |= 1u << grp;
+                    armed_parity = (armed_parity & ~(1u << grp)) | (phase << grp);
+                }
+                const uint32_t fb = PAIR ? mapa_shared(fb_local, 0) : fb_local;
+                auto load2 = [&](uint32_t dst, const CUtensorMap* map, int x, int y) {
+                    if constexpr (PAIR)
+                        tma_load_2d_pair(dst, map, fb, x, y);
+                    else
+                        tma_load_2d(dst, map, fb, x, y);
+                };
+                auto load3 = [&](uint32_t dst, const CUtensorMap* map, int x, int y, int z) {
+                    if constexpr (PAIR)
+                        tma_load_3d_pair(dst, map, fb, x, y, z);
+                    else
+                        tma_load_3d(dst, map, fb, x, y, z);
+                };
+                auto load4 = [&](uint32_t dst, const CUtensorMap* map, int y, int z) {
+                    if constexpr (PAIR)
+                        tma_load_4d_pair(dst, map, fb, 0, 0, y, z);
+                    else
+                        tma_load_4d(dst, map, fb, 0, 0, y, z);
+                };
+                const int slot0 = grp * kCeBlocksPerStage;
+                const uint32_t dst0 = ROLE == 1 ? smem_addr(sA + slot0 * TS::kAStage)
+                                                : smem_addr(sB + slot0 * TS::kBStage);
+                constexpr uint32_t kStep = ROLE == 1 ? TS::kAStage : TS::kBStage;
+                if (n == 2 && (ROLE == 1 ? p.p_2k : p.q_2k)) {  // both K-blocks as one box
+                    if constexpr (ROLE == 1 && P_MN)
+                        load4(dst0, &p.map_p2, m0 >> 6, kb);
+                    else if constexpr (ROLE == 1)
+                        load3(dst0, &p.map_p2, 0, m0, kb);
+                    else if constexpr (Q_MN)
+                        load4(dst0, &p.map_q2, n0 >> 6, kb);
+                    else
+                        load3(dst0, &p.map_q2, 0, n0, kb);
+                } else {
+                    for (int j = 0; j < n; ++j) {
+                        const uint32_t dst = dst0 + j * kStep;
+                        const int k0 = (kb + j) * kBK;
+                        if constexpr (ROLE == 1 && P_MN) {
+                            load3(dst, &p.map_p, 0, k0, m0 >> 6);
+                        } else if constexpr (ROLE == 1) {
+                            load2(dst, &p.map_p, k0, m0);
+                        } else if constexpr (Q_MN) {
+                            if (p.q_3d) {
+                                load3(dst, &p.map_q, 0, k0, n0 >> 6);
+                            } else {
+#pragma unroll
+                                for (int h = 0; h < TS::kBBoxes; ++h)
+                                    load2(dst + h * 8192, &p.map_q, n0 + 64 * h, k0);
+                            }
+                        } else {
+                            load2(dst, &p.map_q, k0, n0);
+                        }
+                    }
+                }
+                if (++grp == GROUPS) {
+                    grp = 0;
+                    phase ^= 1;
+                }
+            }
+        }
+        if (*abort_flag) {  // no TMA write may land after the CTA exits
+            for (int q = 0; q < GROUPS; ++q)
+                if (armed & (1u << q)) drain_bar(smem_addr(&full[q]), (armed_parity >> q) & 1, w);
+        }
+    };
+
+    if (warp == 0 && lane == 0) {
+        run_producer(RoleTag<1>{});
+    } else if (warp == 2 + kEpiWarps && lane == 0) {
+        run_producer(RoleTag<2>{});
+    } else if (warp == 1 && lane == 0 && leader) {
+        // ---------------------------------------------------- MMA issuer
+        int grp = 0, i = 0;
+        uint32_t phase = 0;
+        bool ok = true;
+        const uint32_t idesc = p.idesc;
+        const uint32_t d_hi = smem_desc_hi_sw128(1024);
+        const uint32_t a_lo0 = smem_desc_lo(smem_addr(sA), P_MN ? 8192u : 16u);
+        const uint32_t b_lo0 = smem_desc_lo(smem_addr(sB), Q_MN ? 8192u : 16u);
+        constexpr uint32_t a_kstep = P_MN ? (2048u >> 4) : (32u >> 4);
+        constexpr uint32_t b_kstep = Q_MN ? (2048u >> 4) : (32u >> 4);
+        CeItems<MODE> items(p, worker, workers, TS::kBM);
+        int tm, tn, split, kb0, kb1;
+        for (; ok && items.next(tm, tn, split, kb0, kb1); ++i) {
+            const int buf = i & 1;
+            if (!wait_bar(smem_addr(&tempty[buf]), ((i >> 1) & 1) ^ 1, w, DEV_TIMEOUT_MMA + 3)) break;
+            tc_fence_after();
+            const uint32_t d_tmem = tmem_base + buf * BN;
+            for (int kb = kb0; kb < kb1; kb += kCeBlocksPerStage) {
+                const int n = min(kb1 - kb, kCeBlocksPerStage);
+                if (!wait_bar(smem_addr(&full[grp]), phase, w, DEV_TIMEOUT_MMA + 4)) {
+                    ok = false;
+                    break;
+                }
+                tc_fence_after();
+#pragma unroll
+                for (int j = 0; j < kCeBlocksPerStage; ++j) {
+                    if (j >= n) break;
+                    const uint32_t slot = (uint32_t)(grp * kCeBlocksPerStage + j);
+                    const uint32_t a_lo = a_lo0 + slot * (TS::kAStage >> 4);
+                    const uint32_t b_lo = b_lo0 + slot * (TS::kBStage >> 4);
+#pragma unroll
+                    for (int kk = 0; kk < kBK / kUmmaK; ++kk)
+                        mma_f16<CG>(d_tmem, smem_desc_join(a_lo + kk * a_kstep, d_hi),
+                                    smem_desc_join(b_lo + kk * b_kstep, d_hi), idesc,
+                                    (kb + j != kb0) || (kk != 0));
+                }
+                if constexpr (PAIR)
+                    mma_commit_pair(smem_addr(&empty[grp]), 0x3);
+                else
+                    mma_commit(smem_addr(&empty[grp]));
+                if (++grp == GROUPS) {
+                    grp = 0;
+                    phase ^= 1;
+                }
+            }
+            if (!ok) break;
+            if constexpr (PAIR)
+                mma_commit_pair(smem_addr(&tfull[buf]), 0x3);
+            else
+                mma_commit(smem_addr(&tfull[buf]));
+        }
+        // nothing may still write TMEM when it is released
+        if constexpr (PAIR)
+            mma_commit_pair_local(smem_addr(drain));
+        else
+            mma_commit(smem_addr(drain));
+        drain_bar(smem_addr(drain), 0, w);
+    } else if (warp >= 2 && warp < 2 + kEpiWarps) {
+        // ------------------------------------------------------ epilogue
+        // Warp q of a quadrant reads TMEM lanes 32q..32q+31; thread = row.
+        constexpr int kChunks = BN / 32;
+        static_assert(kChunks % 2 == 0, "chunks are taken in pairs");
+        const int q = warp & 3;
+        uint8_t* stage = staging + (warp - 2) * kStageBufs * 2048;
+        uint32_t stored = 0;  // output chunks stored so far
+        float alpha = 1.0f;
+        if constexpr (MODE == CE_DW) alpha = __ldg(p.alpha);
+        int live = 0;
+        if constexpr (MODE == CE_GRAD) live = p.live ? __ldg(p.live) : p.rows;
+        CeItems<MODE> items(p, worker, workers, TS::kBM);
+        int tm, tn, split, kb0, kb1;
+        for (int i = 0; items.next(tm, tn, split, kb0, kb1); ++i) {
+            const int buf = i & 1;
+            const int row0 = tm * TS::kBM + (int)rank * 128 + q * 32;  // this warp's first row
+            const int row = row0 + lane;
+            const int n0 = tn * BN;
+            // what the row's epilogue needs, loaded while the products run
+            CeRowStats st{-INFINITY, 0.0f, 0.0f, -1};
+            float2 rs = make_float2(0.0f, 0.0f);
+            int target = -1;
+            if constexpr (MODE == CE_LSE) {
+                if (row < p.rows) {
+                    const long long t = __ldg(p.target + row);
+                    if (t >= p.col0 && t < p.col0 + p.cols) st.target = (int)(t - p.col0);
+                }
+            } else if constexpr (MODE == CE_GRAD) {
+                if (row < live) {
+                    rs = __ldg(p.row_scale + row);
+                    const long long t = __ldg(p.row_target + row);
+                    if (t >= p.col0 && t < p.col0 + p.cols) target = (int)(t - p.col0);
+                }
+            }
+            const bool got = wait_bar(smem_addr(&tfull[buf]), (i >> 1) & 1, w, DEV_TIMEOUT_EPILOGUE + 4);
+            if (!__all_sync(0xffffffffu, got)) break;
+            tc_fence_after();
+            const uint32_t t_row = tmem_base + ((uint32_t)(q * 32) << 16) + buf * BN;
+
+            auto finish = [&](uint32_t (&v)[32], int c) {
+                const int c0 = n0 + c * 32;
+                if constexpr (MODE == CE_LSE) {
+                    st.chunk(v, c0, p.cols);
+                } else {
+                    float y[32];
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) y[j] = __uint_as_float(v[j]);
+                    if constexpr (MODE == CE_GRAD) {
+#pragma unroll
+                        for (int j = 0; j < 32; j += 2) {
+                            fma2(y[j], y[j + 1], kLog2e, -rs.x, y[j], y[j + 1]);
+                            y[j] = pow2_gradual(y[j]);
+                            y[j + 1] = pow2_gradual(y[j + 1]);
+                        }
+                        const unsigned d = (unsigned)(target - c0);
+                        if (__any_sync(0xffffffffu, d < 32u)) {
+#pragma unroll
+                            for (int j = 0; j < 32; ++j)
+                                if (d == (unsigned)j) y[j] -= 1.0f;
+                        }
+#pragma unroll
+                        for (int j = 0; j < 32; j += 2) mul2(y + j, rs.y);
+                        if (c0 + 32 > p.cols) {  // the piece's padding columns hold zeros
+#pragma unroll
+                            for (int j = 0; j < 32; ++j)
+                                if (c0 + j >= p.cols) y[j] = 0.0f;
+                        }
+                    } else if constexpr (MODE == CE_DW) {
+#pragma unroll
+                        for (int j = 0; j < 32; j += 2) mul2(y + j, alpha);
+                    }
+                    // stage the 32 x 32 chunk in swizzled shared memory and store
+                    // it with one tensor copy, clipped by the map
+                    constexpr int kBufs = MODE == CE_DH ? kStageBufs / 2 : kStageBufs;
+                    constexpr int kBufBytes = MODE == CE_DH ? 4096 : 2048;
+                    uint8_t* b = stage + (stored % kBufs) * kBufBytes;
+                    if (stored >= kBufs && lane == 0) bulk_wait_group_read<kBufs - 1>();
+                    __syncwarp();
+                    if constexpr (MODE == CE_DH) {
+#pragma unroll
+                        for (int k = 0; k < 8; ++k)
+                            *reinterpret_cast<float4*>(b + lane * 128 + ((k ^ (lane & 7)) << 4)) =
+                                make_float4(y[4 * k], y[4 * k + 1], y[4 * k + 2], y[4 * k + 3]);
+                    } else {
+                        if (p.bf16)
+                            stage_row<true>(b, lane, y);
+                        else
+                            stage_row<false>(b, lane, y);
+                    }
+                    fence_proxy_async_shared();
+                    __syncwarp();
+                    if (lane == 0) {
+                        if constexpr (MODE == CE_DH) {
+                            if (row0 < p.out_rows && c0 < p.out_cols) {
+                                if (p.accumulate)
+                                    tma_add_3d(&p.map_c, smem_addr(b), c0, row0, split);
+                                else
+                                    tma_store_3d(&p.map_c, smem_addr(b), c0, row0, split);
+                            }
+                        } else if constexpr (MODE == CE_DW) {
+                            // dW is not read again: its lines leave L2 first
+                            if (row0 < p.out_rows && c0 < p.n_tma)
+                                tma_store_2d_hint(&p.map_c, smem_addr(b), c0, row0, l2_policy_evict_first());
+                        } else {
+                            tma_store_2d(&p.map_c, smem_addr(b), c0, row0);
+                        }
+                        bulk_commit_group();
+                    }
+                    if constexpr (MODE == CE_DW) {
+                        // columns the map cannot hold (all of them for an unaligned
+                        // dW): a row of the chunk per store, lane = column
+                        if (c0 + 32 > p.n_tma && c0 < p.out_cols) {
+                            const int col = c0 + lane;
+                            const bool mine = col >= p.n_tma && col < p.out_cols;
+                            uint16_t* o = static_cast<uint16_t*>(p.out) + (long long)row0 * p.ldo + col;
+#pragma unroll 4
+                            for (int r = 0; r < 32; ++r)
+                                if (mine && row0 + r < p.out_rows)
+                                    o[(long long)r * p.ldo] = *reinterpret_cast<const uint16_t*>(
+                                        b + r * 64 + (((lane >> 3) ^ ((r >> 1) & 3)) << 4) + (lane & 7) * 2);
+                        }
+                    }
+++stored;
+                }
+            };
+            auto release = [&]() {  // every column of this buffer is in registers
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) {
+                    if constexpr (PAIR)
+                        mbar_arrive_cluster(smem_addr(&tempty[buf]), 0);
+                    else
+                        mbar_arrive(smem_addr(&tempty[buf]));
+                }
+            };
+            // the next chunk's TMEM load runs beside this chunk's arithmetic
+            uint32_t va[32], vb[32];
+            __syncwarp();
+            tmem_ld_32x32b_x32(t_row, va);
+#pragma unroll 1
+            for (int c = 0; c < kChunks; c += 2) {
+                tmem_wait_ld_regs(va);
+                __syncwarp();
+                tmem_ld_32x32b_x32(t_row + (c + 1) * 32, vb);
+                finish(va, c);
+                tmem_wait_ld_regs(vb);
+                if (c + 2 < kChunks) {
+                    __syncwarp();
+                    tmem_ld_32x32b_x32(t_row + (c + 2) * 32, va);
+                } else {
+                    release();
+                }
+                finish(vb, c + 1);
+            }
+            if constexpr (MODE == CE_LSE) {
+                if (row < p.rows) {
+                    p.part[(long long)row * p.tiles_n + tn] = make_float2(st.m, st.s);
+                    const int t = st.target - n0;
+                    if (t >= 0 && t < BN) p.hit[row] = st.hit;
+                }
+            }
+        }
+        if (lane == 0) bulk_wait_group<0>();  // every output chunk has reached global memory
+    }
+
+    tc_fence_before();
+    __syncwarp();
+    if (*abort_flag) {
+        // copies for phases that were never armed cannot be observed: give
+        // them ample time to land
+        const long long t0 = clock64();
+        while (clock64() - t0 < 2000000) {
+        }
+    }
+    if constexpr (PAIR)
+        cluster_sync();  // no CTA leaves while its peer may still signal it
+    else
+        __syncthreads();
+    if (warp == 1) {
+        tc_fence_after();
+        tmem_dealloc<CG>(tmem_base, TS::kTmemCols);
+    }
+}
+
+}  // namespace tg
