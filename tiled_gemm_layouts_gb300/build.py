@@ -21,7 +21,7 @@ LIB = os.path.join(HERE, "libtilegemm.so")
 
 CUDA_SOURCES = ["api.cu", "gemm_sm103.cu", "probes.cu", "noalloc.cu", "stage.cu", "pointwise.cu",
                 "layernorm.cu", "adamw.cu", "ce.cu", "ce_inst_lse.cu", "ce_inst_grad.cu",
-                "ce_inst_dh.cu", "ce_inst_dw.cu"] + [f"gemm_inst_{i}.cu" for i in range(1, 37)]
+                "ce_inst_products.cu"] + [f"gemm_inst_{i}.cu" for i in range(1, 37)]
 CXX_SOURCES = ["layout.cpp", "select.cpp", "host_pipeline.cpp"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 

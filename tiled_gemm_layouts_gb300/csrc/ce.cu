@@ -7,7 +7,7 @@
 // a dense copy of H first.  The others have no gradient, and a batch of
 // prompts or padded texts has many; their rows of H may hold anything, and an
 // infinity times G = 0 would put a NaN into dW.  Then, for each piece of the
-// vocabulary, CE_GRAD, CE_DH and CE_DW; at the end dH's fp32 planes are
+// vocabulary, CE_GRAD and CE_PRODUCTS; at the end dH's fp32 planes are
 // summed, scaled and scattered back to the tokens' rows.
 #include <climits>
 #include <cstring>
@@ -19,20 +19,18 @@
 namespace tg {
 
 template <>
-cudaError_t launch_ce_mode<CE_LSE>(const CeParams&, CeTile, int, cudaStream_t);
+cudaError_t launch_ce_mode<CE_LSE>(const CeParams&, CeTile, int, bool, cudaStream_t);
 template <>
-cudaError_t launch_ce_mode<CE_GRAD>(const CeParams&, CeTile, int, cudaStream_t);
+cudaError_t launch_ce_mode<CE_GRAD>(const CeParams&, CeTile, int, bool, cudaStream_t);
 template <>
-cudaError_t launch_ce_mode<CE_DH>(const CeParams&, CeTile, int, cudaStream_t);
-template <>
-cudaError_t launch_ce_mode<CE_DW>(const CeParams&, CeTile, int, cudaStream_t);
+cudaError_t launch_ce_mode<CE_PRODUCTS>(const CeParams&, CeTile, int, bool, cudaStream_t);
 
-cudaError_t launch_ce(int mode, const CeParams& p, CeTile tile, int sms, cudaStream_t stream) {
+cudaError_t launch_ce(int mode, const CeParams& p, CeTile tile, int sms, bool chained,
+                      cudaStream_t stream) {
     switch (mode) {
-        case CE_LSE: return launch_ce_mode<CE_LSE>(p, tile, sms, stream);
-        case CE_GRAD: return launch_ce_mode<CE_GRAD>(p, tile, sms, stream);
-        case CE_DH: return launch_ce_mode<CE_DH>(p, tile, sms, stream);
-        default: return launch_ce_mode<CE_DW>(p, tile, sms, stream);
+        case CE_LSE: return launch_ce_mode<CE_LSE>(p, tile, sms, chained, stream);
+        case CE_GRAD: return launch_ce_mode<CE_GRAD>(p, tile, sms, chained, stream);
+        default: return launch_ce_mode<CE_PRODUCTS>(p, tile, sms, chained, stream);
     }
 }
 
@@ -41,37 +39,60 @@ namespace {
 int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
 int64_t up(int64_t a, int64_t b) { return cdiv(a, b) * b; }
 
+constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
+
 // ------------------------------------------------------ small kernels
 
-// loss and lse of one token per warp, from its tiles' (max, sum).
-__global__ void ce_combine_kernel(const float2* __restrict__ part, const float* __restrict__ hit,
-                                  const long long* __restrict__ target, int T, long long V,
-                                  int tiles, float* __restrict__ loss, float* __restrict__ lse) {
-    const int t = (int)(blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5));
-    const int lane = threadIdx.x & 31;
-    if (t >= T) return;
-    const float2* row = part + (long long)t * tiles;
-    float m = -INFINITY, s = 0.0f;
-    auto merge = [&](float m2, float s2) {
+// (max in log2 units, sum of 2^(l - max)) of a set of logits.
+struct LogSum {
+    float m, s;
+    __device__ __forceinline__ void merge(float m2, float s2) {
         const float mn = fmaxf(m, m2), base = mn == -INFINITY ? 0.0f : mn;
         s = s * pow2(m - base) + s2 * pow2(m2 - base);
         m = mn;
-    };
-#pragma unroll 4
-    for (int i = lane; i < tiles; i += 32) {
-        const float2 u = __ldg(row + i);
-        merge(u.x, u.y);
     }
+    __device__ __forceinline__ void merge_warp() {
 #pragma unroll
-    for (int o = 16; o; o >>= 1) {
-        const float m2 = __shfl_xor_sync(0xffffffffu, m, o), s2 = __shfl_xor_sync(0xffffffffu, s, o);
-        merge(m2, s2);
+        for (int o = 16; o; o >>= 1) {
+            const float m2 = __shfl_xor_sync(0xffffffffu, m, o);
+            const float s2 = __shfl_xor_sync(0xffffffffu, s, o);
+            merge(m2, s2);
+        }
+    }
+};
+
+// loss and lse of a token from its tiles' partial sums: WARPS warps per token,
+// 8 warps per block.
+template <int WARPS>
+__global__ void __launch_bounds__(256)
+ce_combine_kernel(const float2* __restrict__ part, const float* __restrict__ hit,
+                  const long long* __restrict__ target, int T, long long V, int tiles,
+                  float* __restrict__ loss, float* __restrict__ lse) {
+    wait_for_previous_kernel();
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int t = WARPS == 1 ? (int)(blockIdx.x * 8 + warp) : (int)blockIdx.x;
+    if (t >= T) return;
+    const float2* row = part + (long long)t * tiles;
+    LogSum a{-INFINITY, 0.0f};
+#pragma unroll 4
+    for (int i = (WARPS == 1 ? lane : (int)threadIdx.x); i < tiles; i += 32 * WARPS) {
+        const float2 u = row[i];
+        a.merge(u.x, u.y);
+    }
+    a.merge_warp();
+    if constexpr (WARPS > 1) {
+        __shared__ float2 all[WARPS];
+        if (lane == 0) all[warp] = make_float2(a.m, a.s);
+        __syncthreads();
+        if (warp) return;
+        a = lane < WARPS ? LogSum{all[lane].x, all[lane].y} : LogSum{-INFINITY, 0.0f};
+        a.merge_warp();
     }
     if (lane == 0) {
-        const float l = m * 0.6931471805599453f + logf(s);
-        lse[t] = l;
+        const float tail = logf(a.s);
+        lse[t] = a.m * kLn2 + tail;
         const long long y = target[t];
-        loss[t] = y >= 0 && y < V ? l - hit[t] : 0.0f;
+        loss[t] = y >= 0 && y < V ? (a.m - hit[t]) * kLn2 + tail : 0.0f;
     }
 }
 
@@ -96,6 +117,8 @@ ce_compact_kernel(const long long* __restrict__ target, const float* __restrict_
                   const float* __restrict__ dloss, int T, long long V, float scale2, CeRows r) {
     __shared__ float wmax[32];
     __shared__ int wsum[33];
+    allow_next_kernel();
+    wait_for_previous_kernel();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     float top = 0.0f;
     for (int t = threadIdx.x; t < T; t += kCompactThreads) {
@@ -151,6 +174,8 @@ ce_compact_kernel(const long long* __restrict__ target, const float* __restrict_
 // [D, ldo) and the rows up to the next multiple of 256 filled with zeros.
 __global__ void ce_gather_kernel(const uint16_t* __restrict__ H, long long ldh, int D, CeRows r,
                                  uint16_t* __restrict__ out, int ldo, long long max_rows) {
+    allow_next_kernel();
+    wait_for_previous_kernel();
     const int live = *r.live;
     const long long rows = min(max_rows, (long long)max(256, (live + 255) / 256 * 256));
     const int vecs = ldo / 8;
@@ -160,7 +185,7 @@ __global__ void ce_gather_kernel(const uint16_t* __restrict__ H, long long ldh, 
         const int c = (int)(i - j * vecs) * 8;
         uint4 v = make_uint4(0, 0, 0, 0);
         if (j < live && c < D) {
-            const uint16_t* s = H + (long long)__ldg(r.token + j) * ldh + c;
+            const uint16_t* s = H + (long long)r.token[j] * ldh + c;
             if (c + 8 <= D && (reinterpret_cast<uintptr_t>(s) & 15u) == 0) {
                 v = *reinterpret_cast<const uint4*>(s);
             } else {
@@ -181,13 +206,14 @@ template <bool BF>
 __global__ void ce_scatter_kernel(const float* __restrict__ planes, int splits, long long plane,
                                   int ldp, CeRows r, int T, int D, uint16_t* __restrict__ dH,
                                   long long ldd) {
+    wait_for_previous_kernel();
     const float alpha = *r.alpha;
     const int vecs = (D + 7) / 8;
     for (long long i = blockIdx.x * (long long)blockDim.x + threadIdx.x; i < (long long)T * vecs;
          i += (long long)gridDim.x * blockDim.x) {
         const long long t = i / vecs;
         const int c = (int)(i - t * vecs) * 8;
-        const int j = __ldg(r.place + t);
+        const int j = r.place[t];
         float y[8] = {0, 0, 0, 0, 0, 0, 0, 0};
         if (j >= 0) {
             const float* s = planes + (long long)j * ldp + c;
@@ -270,7 +296,7 @@ struct BwdPlan {
     int64_t piece;       // columns of a piece of G, a multiple of 256
     int64_t pieces;
     int64_t ldp;         // columns of dH's planes
-    CeTile grad, dh, dw;
+    CeTile grad, products;
     int64_t dh_kb;       // K-blocks of one split of dH's contraction
     int splits;
     size_t live, token, target, scale, place, h, g, planes, w, bytes;
@@ -289,13 +315,15 @@ BwdPlan backward_plan(int64_t T, int64_t V, int64_t D, const void* W, int64_t ld
     b.pieces = cdiv(V, b.piece);
     b.ldp = up(D, 8);
     b.grad = logits_tile(T);
-    b.dh = T > 128 ? CeTile{D > 128 ? 256 : 128, 1} : CeTile{128, 0};
-    b.dw = CeTile{D > 128 ? 256 : 128, 1};
-    // dH's tiles alone often leave SMs idle while its contraction over the
-    // piece is long: split that into planes, each at least 8 K-blocks deep
-    const int64_t tiles = cdiv(T, b.dh.pair ? 256 : 128) * cdiv(D, b.dh.bn);
-    const int64_t kb = cdiv(V < b.piece ? V : b.piece, 64), workers = b.dh.pair ? sms / 2 : sms;
-    int64_t splits = workers / tiles;
+    b.products = CeTile{D > 128 ? 256 : 128, 1};
+    // A tile of dH contracts over the whole piece.  Where that is longer than
+    // an equal share of all the products, split it into fp32 planes that the
+    // last kernel adds, each at least 8 K-blocks deep.
+    const int64_t cols = V < b.piece ? V : b.piece, kb = cdiv(cols, 64), workers = sms / 2;
+    const int64_t n = cdiv(T, 256) * cdiv(D, b.products.bn);
+    const int64_t n_dw = cdiv(cols, 256) * cdiv(D, b.products.bn);
+    const int64_t share = (n * kb + n_dw * cdiv(T, 64)) / workers + 1;
+    int64_t splits = cdiv(kb, share);
     if (splits > kb / 8) splits = kb / 8;
     if (splits < 1) splits = 1;
     b.dh_kb = up(cdiv(kb, splits), 2);
@@ -342,6 +370,7 @@ void common_params(CeParams* p, int dtype, const DeviceInfo* info) {
     std::memset(p, 0, sizeof(*p));
     p->bf16 = dtype == TG_BF16;
     p->splits = 1;
+    p->p_bytes = 128 * 128;
     p->timeout_cycles = watchdog_timeout();
     p->status = info->status;
 }
@@ -353,9 +382,10 @@ bool k_major(CUtensorMap* one, CUtensorMap* two, int* use_two, int dtype, const 
     return encode_2d(one, dtype, base, k, rows, ld, 64, (uint32_t)box);
 }
 
-// Q = W^T or H'^T of the logits: K-major, and P = H or H', K-major.
-bool logits_maps(CeParams* p, int dtype, CeTile tile, const void* H, int64_t h_rows, int64_t h_cols,
-                 int64_t ldh, const void* W, int64_t V, int64_t D, int64_t ldw) {
+// The logits' product: P = H (or its gathered rows) and Q = W^T, both K-major.
+bool logits_side(CeParams* p, int dtype, CeTile tile, int64_t T, const void* H, int64_t h_rows,
+                 int64_t h_cols, int64_t ldh, const void* W, int64_t V, int64_t D, int64_t ldw) {
+    CeSide& s = p->side[0];
     // For few tokens the box holds only the rows there are, in whole groups of
     // 8: one token's K-block is then 1 KB of copies instead of 16.  (The rest
     // of the stage keeps old bytes, which reach only accumulator rows that
@@ -363,28 +393,36 @@ bool logits_maps(CeParams* p, int dtype, CeTile tile, const void* H, int64_t h_r
     const int64_t box = h_rows >= 128 ? 128 : up(h_rows, 8);
     p->p_bytes = (uint32_t)box * 128;
     int unused;
-    if (!k_major(&p->map_p, box == 128 ? &p->map_p2 : nullptr, box == 128 ? &p->p_2k : &unused, dtype,
+    if (!k_major(&s.map_p, box == 128 ? &s.map_p2 : nullptr, box == 128 ? &s.p_2k : &unused, dtype,
                  H, h_rows, h_cols, ldh, (int)box) ||
-        !k_major(&p->map_q, &p->map_q2, &p->q_2k, dtype, W, V, D, ldw,
+        !k_major(&s.map_q, &s.map_q2, &s.q_2k, dtype, W, V, D, ldw,
                  tile.pair ? tile.bn / 2 : tile.bn))
         return false;
-    p->num_kb = p->kb_per_split = (int)cdiv(D, 64);
-    p->idesc = make_idesc(dtype, false, false, tile.bn, tile.pair ? 256 : 128);
+    s.num_kb = (int)cdiv(D, 64);
+    s.tiles_m = (int)cdiv(T, tile.pair ? 256 : 128);
+    s.tiles_n = (int)cdiv(V, tile.bn);
+    s.group_m = s.tiles_m < 16 ? s.tiles_m : 16;
+    s.idesc = make_idesc(dtype, false, false, tile.bn, tile.pair ? 256 : 128);
+    // Each tcgen05.mma adds 16 products to the fp32 accumulator and truncates
+    // the sum: for sums of products of either sign a logit comes out smaller
+    // by a quarter of 2^-24 per addition, measured at D = 64 to 8192 in both
+    // types (0.20 to 0.36; products of one sign lose up to 1.6).  lse and the
+    // probabilities see that as a common factor, so the factor that turns
+    // logits into log2 units takes it back; at D = 4096 it is 3.8e-6.
+    p->to_log2 = (float)(1.4426950408889634 * (1.0 + 0.25 * 0x1p-24 * 4.0 * s.num_kb));
+    p->rows = (int)T;
+    p->cols = (int)V;
     return true;
 }
 
 // MN-major Q: `cols` columns contiguous, `k` rows of them.
-bool mn_major_q(CeParams* p, int dtype, CeTile tile, const void* base, int64_t cols, int64_t k,
+bool mn_major_q(CeSide* s, int dtype, CeTile tile, const void* base, int64_t cols, int64_t k,
                 int64_t ld) {
     const int atoms = (tile.pair ? tile.bn / 2 : tile.bn) / 64;
-    p->q_3d = encode_mn_atoms(&p->map_q, dtype, base, cols, k, ld, (uint32_t)atoms);
-    p->q_2k = p->q_3d && encode_mn_atom_pairs(&p->map_q2, dtype, base, cols, k, ld, (uint32_t)atoms);
-    return p->q_3d || encode_2d(&p->map_q, dtype, base, cols, k, ld, 64, 64);
+    s->q_3d = encode_mn_atoms(&s->map_q, dtype, base, cols, k, ld, (uint32_t)atoms);
+    s->q_2k = s->q_3d && encode_mn_atom_pairs(&s->map_q2, dtype, base, cols, k, ld, (uint32_t)atoms);
+    return s->q_3d || encode_2d(&s->map_q, dtype, base, cols, k, ld, 64, 64);
 }
-
-// Tile rows of a raster group: enough for a wave of tiles to share panels of
-// both operands (the GEMM kernel's value).
-int raster(int64_t tiles_m) { return (int)(tiles_m < 16 ? tiles_m : 16); }
 
 }  // namespace
 }  // namespace tg
@@ -440,20 +478,18 @@ extern "C" int tg_linear_ce(int64_t T, int64_t V, int64_t D, const void* H, int6
     }
     CeParams p;
     common_params(&p, (int)dtype, info);
-    ok = ok && logits_maps(&p, (int)dtype, f.tile, H, T, D, ldh, W, V, D, ldw);
-    p.tiles_m = (int)cdiv(T, f.tile.pair ? 256 : 128);
-    p.tiles_n = (int)f.tiles_n;
-    p.group_m = raster(p.tiles_m);
-    p.rows = (int)T;
-    p.cols = (int)V;
+    ok = ok && logits_side(&p, (int)dtype, f.tile, T, H, T, D, ldh, W, V, D, ldw);
     p.target = reinterpret_cast<const long long*>(target);
     p.part = reinterpret_cast<float2*>(ws + f.part);
     p.hit = reinterpret_cast<float*>(ws + f.hit);
-    ok = ok && launch_ce(CE_LSE, p, f.tile, info->sms, stream) == cudaSuccess;
+    ok = ok && launch_ce(CE_LSE, p, f.tile, info->sms, false, stream) == cudaSuccess;
     if (ok) {
-        ce_combine_kernel<<<(unsigned)cdiv(T, 8), 256, 0, stream>>>(p.part, p.hit, p.target, (int)T, V,
-                                                                    p.tiles_n, loss, lse);
-        ok = cudaGetLastError() == cudaSuccess;
+        // few tokens: a block for each, so that hundreds of partial sums are
+        // not one warp's serial chain (1024 of them: 6.9 us by one warp)
+        const bool few = T <= info->sms;
+        ok = launch_chained(few ? ce_combine_kernel<8> : ce_combine_kernel<1>,
+                            dim3((unsigned)(few ? T : cdiv(T, 8))), 256, stream, p.part, p.hit, p.target,
+                            (int)T, (long long)V, (int)f.tiles_n, loss, lse) == cudaSuccess;
     }
     if (!ok) {
         cudaGetLastError();
@@ -537,82 +573,74 @@ extern "C" int tg_linear_ce_grad(int64_t T, int64_t V, int64_t D, const void* H,
     ce_compact_kernel<<<1, kCompactThreads, 0, stream>>>(reinterpret_cast<const long long*>(target), lse,
                                                          dloss, (int)T, V, dt == TG_F16 ? 1024.0f : 1.0f,
                                                          rows);
-    ce_gather_kernel<<<blocks_for(b.rows * (b.ldh / 8), sms), 256, 0, stream>>>(
-        static_cast<const uint16_t*>(H), ldh, (int)D, rows, h, (int)b.ldh, b.rows);
-    ok = ok && cudaGetLastError() == cudaSuccess;
+    ok = ok && cudaGetLastError() == cudaSuccess &&
+         launch_chained(ce_gather_kernel, dim3(blocks_for(b.rows * (b.ldh / 8), sms)), 256, stream,
+                        static_cast<const uint16_t*>(H), (long long)ldh, (int)D, rows, h, (int)b.ldh,
+                        (long long)b.rows) == cudaSuccess;
 
     for (int64_t i = 0; ok && i < b.pieces; ++i) {
         const int64_t v0 = i * b.piece, cols = V - v0 < b.piece ? V - v0 : b.piece;
         const uint16_t* w = static_cast<const uint16_t*>(W) + v0 * ldw;
         CeParams p;
-        // G, scaled: T x cols logits from the gathered rows
+        // a piece of G, scaled, from the gathered rows
         common_params(&p, dt, info);
-        ok = logits_maps(&p, dt, b.grad, h, b.rows, b.ldh, b.ldh, w, cols, D, ldw) &&
-             encode_2d(&p.map_c, dt, g, b.piece, b.rows, b.piece, 32, 32, CU_TENSOR_MAP_SWIZZLE_64B);
+        ok = logits_side(&p, dt, b.grad, T, h, b.rows, b.ldh, b.ldh, w, cols, D, ldw) &&
+             encode_2d(&p.side[0].map_c, dt, g, b.piece, b.rows, b.piece, 32, 32,
+                       CU_TENSOR_MAP_SWIZZLE_64B);
         p.live = rows.live;
-        p.tiles_m = (int)cdiv(T, b.grad.pair ? 256 : 128);
-        p.tiles_n = (int)cdiv(cols, b.grad.bn);
-        p.group_m = raster(p.tiles_m);
-        p.rows = (int)T;
-        p.cols = (int)cols;
         p.col0 = v0;
         p.row_target = rows.target;
         p.row_scale = rows.scale;
-        ok = ok && launch_ce(CE_GRAD, p, b.grad, sms, stream) == cudaSuccess;
-        if (ok && dH) {
-            const int64_t kb = cdiv(cols, 64);
-            common_params(&p, dt, info);
+        ok = ok && launch_ce(CE_GRAD, p, b.grad, sms, true, stream) == cudaSuccess;
+        if (!ok) break;
+        common_params(&p, dt, info);
+        p.live = rows.live;
+        p.alpha = rows.alpha;
+        if (dH) {
+            CeSide& s = p.side[0];
+            p.all_kb = (int)cdiv(cols, 64);
+            p.splits = (int)cdiv(p.all_kb, b.dh_kb);
+            p.accumulate = i > 0;
             // a K-block past `cols` meets G's zero columns and W rows that the
             // map fills with zeros
-            ok = k_major(&p.map_p, &p.map_p2, &p.p_2k, dt, g, b.rows, kb * 64, b.piece, 128) &&
-                 mn_major_q(&p, dt, b.dh, w, D, cols, ldw) &&
-                 encode_f32_planes(&p.map_c, planes, b.ldp, T, b.splits, b.ldp);
-            p.p_bytes = 128 * 128;
-            p.live = rows.live;
-            p.num_kb = (int)kb;
-            p.kb_per_split = (int)b.dh_kb;
-            p.splits = (int)cdiv(kb, b.dh_kb);
-            p.tiles_m = (int)cdiv(T, b.dh.pair ? 256 : 128);
-            p.tiles_n = (int)cdiv(D, b.dh.bn);
-            p.group_m = raster(p.tiles_m);
-            p.idesc = make_idesc(dt, false, true, b.dh.bn, b.dh.pair ? 256 : 128);
-            p.out_rows = (int)T;
-            p.out_cols = (int)D;
-            p.accumulate = i > 0;
-            ok = ok && launch_ce(CE_DH, p, b.dh, sms, stream) == cudaSuccess;
+            ok = k_major(&s.map_p, &s.map_p2, &s.p_2k, dt, g, b.rows, (int64_t)p.all_kb * 64, b.piece, 128) &&
+                 mn_major_q(&s, dt, b.products, w, D, cols, ldw) &&
+                 encode_f32_planes(&s.map_c, planes, b.ldp, T, b.splits, b.ldp);
+            s.num_kb = (int)b.dh_kb;
+            s.tiles_m = (int)cdiv(T, 256);
+            s.tiles_n = (int)cdiv(D, b.products.bn);
+            s.group_m = s.tiles_m < 16 ? s.tiles_m : 16;
+            s.idesc = make_idesc(dt, false, true, b.products.bn, 256);
+            s.out_rows = (int)T;
+            s.out_cols = (int)D;
         }
         if (ok && dW) {
-            common_params(&p, dt, info);
+            CeSide& s = p.side[1];
             uint16_t* out = static_cast<uint16_t*>(dW) + v0 * lddw;
             const bool tensor = tma_rows(dW, lddw) && D >= 8;
             p.n_tma = tensor ? (int)(D & ~int64_t(7)) : 0;
-            ok = encode_mn_atoms(&p.map_p, dt, g, b.piece, b.rows, b.piece, 2) &&
-                 mn_major_q(&p, dt, b.dw, h, b.ldh, b.rows, b.ldh) &&
-                 encode_2d(&p.map_c, dt, tensor ? out : g, tensor ? p.n_tma : 8, cols,
+            ok = encode_mn_atoms(&s.map_p, dt, g, b.piece, b.rows, b.piece, 2) &&
+                 mn_major_q(&s, dt, b.products, h, b.ldh, b.rows, b.ldh) &&
+                 encode_2d(&s.map_c, dt, tensor ? out : g, tensor ? p.n_tma : 8, cols,
                            tensor ? lddw : b.piece, 32, 32, CU_TENSOR_MAP_SWIZZLE_64B);
-            p.p_2k = encode_mn_atom_pairs(&p.map_p2, dt, g, b.piece, b.rows, b.piece, 2);
-            p.p_bytes = 128 * 128;
-            p.live = rows.live;
-            p.num_kb = p.kb_per_split = (int)(b.rows / 64);
-            p.tiles_m = (int)cdiv(cols, 256);
-            p.tiles_n = (int)cdiv(D, b.dw.bn);
-            p.group_m = raster(p.tiles_m);
-            p.idesc = make_idesc(dt, true, true, b.dw.bn, 256);
+            s.p_2k = encode_mn_atom_pairs(&s.map_p2, dt, g, b.piece, b.rows, b.piece, 2);
+            s.num_kb = (int)(b.rows / 64);
+            s.tiles_m = (int)cdiv(cols, 256);
+            s.tiles_n = (int)cdiv(D, b.products.bn);
+            s.group_m = s.tiles_m < 16 ? s.tiles_m : 16;
+            s.idesc = make_idesc(dt, true, true, b.products.bn, 256);
+            s.out_rows = (int)cols;
+            s.out_cols = (int)D;
             p.out = out;
             p.ldo = lddw;
-            p.out_rows = (int)cols;
-            p.out_cols = (int)D;
-            p.alpha = rows.alpha;
-            ok = ok && launch_ce(CE_DW, p, b.dw, sms, stream) == cudaSuccess;
         }
+        ok = ok && launch_ce(CE_PRODUCTS, p, b.products, sms, true, stream) == cudaSuccess;
     }
-    if (ok && dH) {
-        const unsigned blocks = blocks_for(T * ((D + 7) / 8), sms);
-        auto kern = dt == TG_BF16 ? ce_scatter_kernel<true> : ce_scatter_kernel<false>;
-        kern<<<blocks, 256, 0, stream>>>(planes, b.splits, (long long)T * b.ldp, (int)b.ldp, rows, (int)T,
-                                         (int)D, static_cast<uint16_t*>(dH), lddh);
-        ok = cudaGetLastError() == cudaSuccess;
-    }
+    if (ok && dH)
+        ok = launch_chained(dt == TG_BF16 ? ce_scatter_kernel<true> : ce_scatter_kernel<false>,
+                            dim3(blocks_for(T * ((D + 7) / 8), sms)), 256, stream, planes, b.splits,
+                            (long long)T * b.ldp, (int)b.ldp, rows, (int)T, (int)D,
+                            static_cast<uint16_t*>(dH), (long long)lddh) == cudaSuccess;
     if (!ok) {
         cudaGetLastError();
         return TG_ERR_CUDA;

@@ -31,11 +31,11 @@
 #pragma once
 
 #include "ce_params.h"
+#include "chained.cuh"
 #include "gemm_kernel.cuh"
 
 namespace tg {
 
-constexpr float kLog2e = 1.4426950408889634f;
 constexpr int kCeThreads = 32 * (3 + kEpiWarps);  // producers (warps 0 and 6), MMA (1), epilogue (2..5)
 constexpr int kCeBlocksPerStage = 2;              // K-blocks per barrier transaction
 
@@ -89,40 +89,96 @@ __device__ __forceinline__ void tma_add_3d(const CUtensorMap* map, uint32_t src,
         : "memory");
 }
 
-// The work items of one persistent worker: (tile, split of the contraction),
-// every `workers`-th.  `live` shrinks the row tiles or the K-blocks to those
-// that hold a row that counts; one is always left, so that every output is
-// written (its rows are zeros).
+struct CeItem {
+    int side, tm, tn, split, kb0, kb1;
+};
+
+// The work items of one persistent worker.  `live` shrinks the row tiles or
+// the K-blocks to those that hold a row that counts; one is always left, so
+// that every output is written (its rows are zeros).
+//
+// CE_LSE, CE_GRAD: every `workers`-th tile.  CE_PRODUCTS: first every
+// `workers`-th (tile, split) of dH; the last round of those leaves some
+// workers idle for as long as it takes (at 4096 tokens and columns, 256 tiles
+// on 76 pairs: 48 of 76 for a quarter of the time), so these take tiles of dW
+// meanwhile; then all share dW's remaining tiles.  The order within a side
+// stays a raster, for L2.
 template <int MODE>
 struct CeItems {
-    int tiles_m, tiles_n, num_kb, kb_per, group_m, step;
-    long long at, end;
+    int tiles_m[2], tiles_n[2], num_kb[2], group_m[2];
+    int all_kb, step, stride;
+    long long at[2], end[2];  // next and last item of each side
+    long long tail, tail_at;  // first item of dW's common part, and this worker's next there
 
     __device__ __forceinline__ CeItems(const CeParams& p, int worker, int workers, int bm)
-        : tiles_m(p.tiles_m), tiles_n(p.tiles_n), num_kb(p.num_kb), kb_per(p.kb_per_split),
-          group_m(p.group_m), step(workers), at(worker) {
+        : all_kb(p.all_kb), step(workers) {
+#pragma unroll
+        for (int s = 0; s < 2; ++s) {
+            tiles_m[s] = p.side[s].tiles_m;
+            tiles_n[s] = p.side[s].tiles_n;
+            num_kb[s] = p.side[s].num_kb;
+            group_m[s] = p.side[s].group_m;
+        }
         if (p.live) {
             const int n = max(1, __ldg(p.live));
-            if (MODE == CE_DW)
-                num_kb = kb_per = min(num_kb, (n + kBK - 1) / kBK);
-            else
-                tiles_m = min(tiles_m, (n + bm - 1) / bm);
+            tiles_m[0] = min(tiles_m[0], (n + bm - 1) / bm);
+            num_kb[1] = min(num_kb[1], (n + kBK - 1) / kBK);
         }
-        end = (long long)tiles_m * tiles_n * p.splits;
+        end[0] = (long long)tiles_m[0] * tiles_n[0] * (MODE == CE_PRODUCTS ? p.splits : 1);
+        at[0] = worker;
+        if constexpr (MODE == CE_PRODUCTS) {
+            const long long all = (long long)tiles_m[1] * tiles_n[1];
+            const int busy = (int)(end[0] % workers);  // workers with one more item of dH
+            stride = workers - busy;
+            const long long rounds = busy && all ? num_kb[0] / num_kb[1] : 0;
+            tail = min(all, rounds * stride);
+            at[1] = worker >= busy ? worker - busy : tail;
+            tail_at = tail + worker;
+            end[1] = all;
+        }
     }
-    __device__ __forceinline__ bool next(int& tm, int& tn, int& split, int& kb0, int& kb1) {
-        if (at >= end) return false;
-        const long long tiles = (long long)tiles_m * tiles_n;
-        split = (int)(at / tiles);
-        const int t = (int)(at - split * tiles);
-        const int group = group_m * tiles_n, g = t / group, first = g * group_m;
-        const int gm = min(tiles_m - first, group_m), r = t - g * group;
-        tm = first + r % gm;
-        tn = r / gm;
-        kb0 = split * kb_per;
-        kb1 = min(num_kb, kb0 + kb_per);
-        at += step;
-        return true;
+    __device__ __forceinline__ void place(CeItem& it, long long t) const {
+        const int s = it.side, group = group_m[s] * tiles_n[s];
+        const int i = (int)t, g = i / group, first = g * group_m[s];
+        const int gm = min(tiles_m[s] - first, group_m[s]), r = i - g * group;
+        it.tm = first + r % gm;
+        it.tn = r / gm;
+    }
+    __device__ __forceinline__ bool next(CeItem& it) {
+        if (at[0] < end[0]) {
+            it.side = 0;
+            if constexpr (MODE == CE_PRODUCTS) {
+                const long long tiles = (long long)tiles_m[0] * tiles_n[0];
+                it.split = (int)(at[0] / tiles);
+                place(it, at[0] - it.split * tiles);
+                it.kb0 = it.split * num_kb[0];
+                it.kb1 = min(all_kb, it.kb0 + num_kb[0]);
+            } else {
+                it.split = 0;
+                place(it, at[0]);
+                it.kb0 = 0;
+                it.kb1 = num_kb[0];
+            }
+            at[0] += step;
+            return true;
+        }
+        if constexpr (MODE == CE_PRODUCTS) {
+            it.side = 1;
+            it.split = 0;
+            it.kb0 = 0;
+            it.kb1 = num_kb[1];
+            if (at[1] < tail) {
+                place(it, at[1]);
+                at[1] += stride;
+                return true;
+            }
+            if (tail_at < end[1]) {
+                place(it, tail_at);
+                tail_at += step;
+                return true;
+            }
+        }
+        return false;
     }
 };
 
@@ -134,7 +190,8 @@ struct CeItems {
 // The row's running (max, sum): m in log2 units, s the sum of 2^(l - m).
 struct CeRowStats {
     float m, s, hit;
-    int target;  // column of the tile's row of logits, or negative
+    int target;     // column of the target in this launch, or negative
+    float to_log2;
 
     __device__ __forceinline__ void chunk(const uint32_t (&v)[32], int c0, int cols) {
         if (c0 >= cols) return;
@@ -149,19 +206,19 @@ struct CeRowStats {
         const unsigned d = (unsigned)(target - c0);
         if (d < 32u) {
 #pragma unroll
-            for (int j = 0; j < 32; ++j) hit = d == (unsigned)j ? x[j] : hit;
+            for (int j = 0; j < 32; ++j) hit = d == (unsigned)j ? x[j] * to_log2 : hit;
         }
         float top[4] = {x[0], x[1], x[2], x[3]};
 #pragma unroll
         for (int j = 4; j < 32; ++j) top[j & 3] = fmaxf(top[j & 3], x[j]);
-        const float mc = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * kLog2e;
+        const float mc = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * to_log2;
         const float mn = fmaxf(m, mc);
         const float base = mn == -INFINITY ? 0.0f : mn;  // a row of -inf so far: every term is 0
         float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
         for (int j = 0; j < 32; j += 2) {
             float a, b;
-            fma2(x[j], x[j + 1], kLog2e, -base, a, b);
+            fma2(x[j], x[j + 1], to_log2, -base, a, b);
             add2(&sum[j & 2], pow2(a), pow2(b));
         }
         s = s * pow2(m - base) + ((sum[0] + sum[1]) + (sum[2] + sum[3]));
@@ -169,12 +226,12 @@ struct CeRowStats {
     }
 };
 
-// One kernel for the four products.  PAIR: a CTA pair works on 256 x BN tiles.
+// One kernel for all products.  PAIR: a CTA pair works on 256 x BN tiles.
 template <int MODE, int BN, bool PAIR>
 __global__ void __launch_bounds__(kCeThreads, 1) ce_kernel(const __grid_constant__ CeParams p) {
     using TS = TileShape<BN, PAIR>;
-    constexpr bool P_MN = MODE == CE_DW;                    // P's rows contiguous in memory
-    constexpr bool Q_MN = MODE == CE_DH || MODE == CE_DW;   // Q's columns contiguous
+    constexpr bool Q_MN = MODE == CE_PRODUCTS;  // Q's columns contiguous in memory
+    constexpr bool BOTH = MODE == CE_PRODUCTS;  // side 1's P (G^T) has its rows contiguous
     constexpr int STAGES = TS::kStages;
     constexpr int GROUPS = STAGES / kCeBlocksPerStage;
     constexpr int CG = PAIR ? 2 : 1;
@@ -203,9 +260,10 @@ __global__ void __launch_bounds__(kCeThreads, 1) ce_kernel(const __grid_constant
                   PAIR ? mapa_shared(smem_addr((const void*)abort_flag), rank ^ 1u) : 0u, PAIR,
                   p.status, p.timeout_cycles};
 
+    allow_next_kernel();
     if (threadIdx.x == 0) {
-        prefetch_tensormap(&p.map_p);
-        prefetch_tensormap(&p.map_q);
+        prefetch_tensormap(&p.side[0].map_p);
+        prefetch_tensormap(&p.side[0].map_q);
         for (int s = 0; s < GROUPS; ++s) {
             mbar_init(smem_addr(&full[s]), 1);
             mbar_init(smem_addr(&empty[s]), 1);
@@ -229,6 +287,7 @@ __global__ void __launch_bounds__(kCeThreads, 1) ce_kernel(const __grid_constant
         __syncthreads();
     tc_fence_after();
     const uint32_t tmem_base = *tmem_slot;
+    wait_for_previous_kernel();
 
     // ------------------------------------------------------ TMA producers
     // Role 1 arms each transaction and loads P, role 2 loads Q into it.
@@ -238,13 +297,15 @@ __global__ void __launch_bounds__(kCeThreads, 1) ce_kernel(const __grid_constant
         uint32_t phase = 0, armed = 0, armed_parity = 0;
         const uint32_t stage_tx = (p.p_bytes + kQBytes) * (PAIR ? 2u : 1u);
         CeItems<MODE> items(p, worker, workers, TS::kBM);
-        int tm, tn, split, kb0, kb1;
+        CeItem it;
         bool ok = true;
-        while (ok && items.next(tm, tn, split, kb0, kb1)) {
-            const int m0 = tm * TS::kBM + (int)rank * 128;
-            const int n0 = tn * BN + (int)rank * TS::kBNC;
-            for (int kb = kb0; kb < kb1; kb += kCeBlocksPerStage) {
-                const int n = min(kb1 - kb, kCeBlocksPerStage);
+        while (ok && items.next(it)) {
+            const CeSide& sd = p.side[BOTH ? it.side : 0];
+            const bool p_mn = BOTH && it.side == 1;
+            const int m0 = it.tm * TS::kBM + (int)rank * 128;
+            const int n0 = it.tn * BN + (int)rank * TS::kBNC;
+            for (int kb = it.kb0; kb < it.kb1; kb += kCeBlocksPerStage) {
+                const int n = min(it.kb1 - kb, kCeBlocksPerStage);
                 if (!wait_bar(smem_addr(&empty[grp]), phase ^ 1, w, DEV_TIMEOUT_PRODUCER + 1)) {
                     ok = false;
                     break;
@@ -278,33 +339,36 @@ __global__ void __launch_bounds__(kCeThreads, 1) ce_kernel(const __grid_constant
                 const uint32_t dst0 = ROLE == 1 ? smem_addr(sA + slot0 * TS::kAStage)
                                                 : smem_addr(sB + slot0 * TS::kBStage);
                 constexpr uint32_t kStep = ROLE == 1 ? TS::kAStage : TS::kBStage;
-                if (n == 2 && (ROLE == 1 ? p.p_2k : p.q_2k)) {  // both K-blocks as one box
-                    if constexpr (ROLE == 1 && P_MN)
-                        load4(dst0, &p.map_p2, m0 >> 6, kb);
-                    else if constexpr (ROLE == 1)
-                        load3(dst0, &p.map_p2, 0, m0, kb);
-                    else if constexpr (Q_MN)
-                        load4(dst0, &p.map_q2, n0 >> 6, kb);
-                    else
-                        load3(dst0, &p.map_q2, 0, n0, kb);
+                if (n == 2 && (ROLE == 1 ? sd.p_2k : sd.q_2k)) {  // both K-blocks as one box
+                    if constexpr (ROLE == 1) {
+                        if (p_mn)
+                            load4(dst0, &sd.map_p2, m0 >> 6, kb);
+                        else
+                            load3(dst0, &sd.map_p2, 0, m0, kb);
+                    } else if constexpr (Q_MN) {
+                        load4(dst0, &sd.map_q2, n0 >> 6, kb);
+                    } else {
+                        load3(dst0, &sd.map_q2, 0, n0, kb);
+                    }
                 } else {
                     for (int j = 0; j < n; ++j) {
                         const uint32_t dst = dst0 + j * kStep;
                         const int k0 = (kb + j) * kBK;
-                        if constexpr (ROLE == 1 && P_MN) {
-                            load3(dst, &p.map_p, 0, k0, m0 >> 6);
-                        } else if constexpr (ROLE == 1) {
-                            load2(dst, &p.map_p, k0, m0);
+                        if constexpr (ROLE == 1) {
+                            if (p_mn)
+                                load3(dst, &sd.map_p, 0, k0, m0 >> 6);
+                            else
+                                load2(dst, &sd.map_p, k0, m0);
                         } else if constexpr (Q_MN) {
-                            if (p.q_3d) {
-                                load3(dst, &p.map_q, 0, k0, n0 >> 6);
+                            if (sd.q_3d) {
+                                load3(dst, &sd.map_q, 0, k0, n0 >> 6);
                             } else {
 #pragma unroll
                                 for (int h = 0; h < TS::kBBoxes; ++h)
-                                    load2(dst + h * 8192, &p.map_q, n0 + 64 * h, k0);
+                                    load2(dst + h * 8192, &sd.map_q, n0 + 64 * h, k0);
                             }
                         } else {
-                            load2(dst, &p.map_q, k0, n0);
+                            load2(dst, &sd.map_q, k0, n0);
                         }
                     }
                 }
@@ -329,21 +393,22 @@ __global__ void __launch_bounds__(kCeThreads, 1) ce_kernel(const __grid_constant
         int grp = 0, i = 0;
         uint32_t phase = 0;
         bool ok = true;
-        const uint32_t idesc = p.idesc;
         const uint32_t d_hi = smem_desc_hi_sw128(1024);
-        const uint32_t a_lo0 = smem_desc_lo(smem_addr(sA), P_MN ? 8192u : 16u);
         const uint32_t b_lo0 = smem_desc_lo(smem_addr(sB), Q_MN ? 8192u : 16u);
-        constexpr uint32_t a_kstep = P_MN ? (2048u >> 4) : (32u >> 4);
         constexpr uint32_t b_kstep = Q_MN ? (2048u >> 4) : (32u >> 4);
         CeItems<MODE> items(p, worker, workers, TS::kBM);
-        int tm, tn, split, kb0, kb1;
-        for (; ok && items.next(tm, tn, split, kb0, kb1); ++i) {
+        CeItem it;
+        for (; ok && items.next(it); ++i) {
             const int buf = i & 1;
+            const bool p_mn = BOTH && it.side == 1;
+            const uint32_t idesc = p.side[BOTH ? it.side : 0].idesc;
+            const uint32_t a_lo0 = smem_desc_lo(smem_addr(sA), p_mn ? 8192u : 16u);
+            const uint32_t a_kstep = p_mn ? (2048u >> 4) : (32u >> 4);
             if (!wait_bar(smem_addr(&tempty[buf]), ((i >> 1) & 1) ^ 1, w, DEV_TIMEOUT_MMA + 3)) break;
             tc_fence_after();
             const uint32_t d_tmem = tmem_base + buf * BN;
-            for (int kb = kb0; kb < kb1; kb += kCeBlocksPerStage) {
-                const int n = min(kb1 - kb, kCeBlocksPerStage);
+            for (int kb = it.kb0; kb < it.kb1; kb += kCeBlocksPerStage) {
+                const int n = min(it.kb1 - kb, kCeBlocksPerStage);
                 if (!wait_bar(smem_addr(&full[grp]), phase, w, DEV_TIMEOUT_MMA + 4)) {
                     ok = false;
                     break;
@@ -359,7 +424,7 @@ __global__ void __launch_bounds__(kCeThreads, 1) ce_kernel(const __grid_constant
                     for (int kk = 0; kk < kBK / kUmmaK; ++kk)
                         mma_f16<CG>(d_tmem, smem_desc_join(a_lo + kk * a_kstep, d_hi),
                                     smem_desc_join(b_lo + kk * b_kstep, d_hi), idesc,
-                                    (kb + j != kb0) || (kk != 0));
+                                    (kb + j != it.kb0) || (kk != 0));
                 }
                 if constexpr (PAIR)
                     mma_commit_pair(smem_addr(&empty[grp]), 0x3);
@@ -391,18 +456,27 @@ __global__ void __launch_bounds__(kCeThreads, 1) ce_kernel(const __grid_constant
         uint8_t* stage = staging + (warp - 2) * kStageBufs * 2048;
         uint32_t stored = 0;  // output chunks stored so far
         float alpha = 1.0f;
-        if constexpr (MODE == CE_DW) alpha = __ldg(p.alpha);
+        if constexpr (MODE == CE_PRODUCTS) alpha = __ldg(p.alpha);
+        int last_side = 0;
         int live = 0;
         if constexpr (MODE == CE_GRAD) live = p.live ? __ldg(p.live) : p.rows;
         CeItems<MODE> items(p, worker, workers, TS::kBM);
-        int tm, tn, split, kb0, kb1;
-        for (int i = 0; items.next(tm, tn, split, kb0, kb1); ++i) {
+        CeItem it;
+        for (int i = 0; items.next(it); ++i) {
             const int buf = i & 1;
-            const int row0 = tm * TS::kBM + (int)rank * 128 + q * 32;  // this warp's first row
+            const CeSide& sd = p.side[BOTH ? it.side : 0];
+            const int row0 = it.tm * TS::kBM + (int)rank * 128 + q * 32;  // this warp's first row
             const int row = row0 + lane;
-            const int n0 = tn * BN;
+            const int n0 = it.tn * BN;
+            const bool planes = BOTH && it.side == 0;  // fp32 output
+            if (BOTH && it.side != last_side) {
+                // the two sides cut the staging area differently
+                if (lane == 0) bulk_wait_group_read<0>();
+                last_side = it.side;
+                stored = 0;
+            }
             // what the row's epilogue needs, loaded while the products run
-            CeRowStats st{-INFINITY, 0.0f, 0.0f, -1};
+            CeRowStats st{-INFINITY, 0.0f, 0.0f, -1, p.to_log2};
             float2 rs = make_float2(0.0f, 0.0f);
             int target = -1;
             if constexpr (MODE == CE_LSE) {
@@ -433,7 +507,7 @@ __global__ void __launch_bounds__(kCeThreads, 1) ce_kernel(const __grid_constant
                     if constexpr (MODE == CE_GRAD) {
 #pragma unroll
                         for (int j = 0; j < 32; j += 2) {
-                            fma2(y[j], y[j + 1], kLog2e, -rs.x, y[j], y[j + 1]);
+                            fma2(y[j], y[j + 1], p.to_log2, -rs.x, y[j], y[j + 1]);
                             y[j] = pow2_gradual(y[j]);
                             y[j + 1] = pow2_gradual(y[j + 1]);
                         }
@@ -450,62 +524,66 @@ __global__ void __launch_bounds__(kCeThreads, 1) ce_kernel(const __grid_constant
                             for (int j = 0; j < 32; ++j)
                                 if (c0 + j >= p.cols) y[j] = 0.0f;
                         }
-                    } else if constexpr (MODE == CE_DW) {
+                    } else if (!planes) {
 #pragma unroll
                         for (int j = 0; j < 32; j += 2) mul2(y + j, alpha);
                     }
                     // stage the 32 x 32 chunk in swizzled shared memory and store
                     // it with one tensor copy, clipped by the map
-                    constexpr int kBufs = MODE == CE_DH ? kStageBufs / 2 : kStageBufs;
-                    constexpr int kBufBytes = MODE == CE_DH ? 4096 : 2048;
-                    uint8_t* b = stage + (stored % kBufs) * kBufBytes;
-                    if (stored >= kBufs && lane == 0) bulk_wait_group_read<kBufs - 1>();
-                    __syncwarp();
-                    if constexpr (MODE == CE_DH) {
+                    if (planes) {
+                        uint8_t* b = stage + (stored & 1) * 4096;
+                        if (stored >= 2 && lane == 0) bulk_wait_group_read<1>();
+                        __syncwarp();
 #pragma unroll
                         for (int k = 0; k < 8; ++k)
                             *reinterpret_cast<float4*>(b + lane * 128 + ((k ^ (lane & 7)) << 4)) =
                                 make_float4(y[4 * k], y[4 * k + 1], y[4 * k + 2], y[4 * k + 3]);
+                        fence_proxy_async_shared();
+                        __syncwarp();
+                        if (lane == 0) {
+                            if (row0 < sd.out_rows && c0 < sd.out_cols) {
+                                if (p.accumulate)
+                                    tma_add_3d(&sd.map_c, smem_addr(b), c0, row0, it.split);
+                                else
+                                    tma_store_3d(&sd.map_c, smem_addr(b), c0, row0, it.split);
+                            }
+                            bulk_commit_group();
+                        }
                     } else {
+                        uint8_t* b = stage + (stored % kStageBufs) * 2048;
+                        if (stored >= kStageBufs && lane == 0) bulk_wait_group_read<kStageBufs - 1>();
+                        __syncwarp();
                         if (p.bf16)
                             stage_row<true>(b, lane, y);
                         else
                             stage_row<false>(b, lane, y);
-                    }
-                    fence_proxy_async_shared();
-                    __syncwarp();
-                    if (lane == 0) {
-                        if constexpr (MODE == CE_DH) {
-                            if (row0 < p.out_rows && c0 < p.out_cols) {
-                                if (p.accumulate)
-                                    tma_add_3d(&p.map_c, smem_addr(b), c0, row0, split);
-                                else
-                                    tma_store_3d(&p.map_c, smem_addr(b), c0, row0, split);
+                        fence_proxy_async_shared();
+                        __syncwarp();
+                        if (lane == 0) {
+                            if constexpr (BOTH) {
+                                // dW is not read again: its lines leave L2 first
+                                if (row0 < sd.out_rows && c0 < p.n_tma)
+                                    tma_store_2d_hint(&sd.map_c, smem_addr(b), c0, row0,
+                                                      l2_policy_evict_first());
+                            } else {
+                                tma_store_2d(&sd.map_c, smem_addr(b), c0, row0);
                             }
-                        } else if constexpr (MODE == CE_DW) {
-                            // dW is not read again: its lines leave L2 first
-                            if (row0 < p.out_rows && c0 < p.n_tma)
-                                tma_store_2d_hint(&p.map_c, smem_addr(b), c0, row0, l2_policy_evict_first());
-                        } else {
-                            tma_store_2d(&p.map_c, smem_addr(b), c0, row0);
+                            bulk_commit_group();
                         }
-                        bulk_commit_group();
-                    }
-                    if constexpr (MODE == CE_DW) {
                         // columns the map cannot hold (all of them for an unaligned
                         // dW): a row of the chunk per store, lane = column
-                        if (c0 + 32 > p.n_tma && c0 < p.out_cols) {
+                        if (BOTH && c0 + 32 > p.n_tma && c0 < sd.out_cols) {
                             const int col = c0 + lane;
-                            const bool mine = col >= p.n_tma && col < p.out_cols;
+                            const bool mine = col >= p.n_tma && col < sd.out_cols;
                             uint16_t* o = static_cast<uint16_t*>(p.out) + (long long)row0 * p.ldo + col;
 #pragma unroll 4
                             for (int r = 0; r < 32; ++r)
-                                if (mine && row0 + r < p.out_rows)
+                                if (mine && row0 + r < sd.out_rows)
                                     o[(long long)r * p.ldo] = *reinterpret_cast<const uint16_t*>(
                                         b + r * 64 + (((lane >> 3) ^ ((r >> 1) & 3)) << 4) + (lane & 7) * 2);
                         }
                     }
-++stored;
+                    ++stored;
                 }
             };
             auto release = [&]() {  // every column of this buffer is in registers
@@ -539,7 +617,7 @@ __global__ void __launch_bounds__(kCeThreads, 1) ce_kernel(const __grid_constant
             }
             if constexpr (MODE == CE_LSE) {
                 if (row < p.rows) {
-                    p.part[(long long)row * p.tiles_n + tn] = make_float2(st.m, st.s);
+                    p.part[(long long)row * sd.tiles_n + it.tn] = make_float2(st.m, st.s);
                     const int t = st.target - n0;
                     if (t >= 0 && t < BN) p.hit[row] = st.hit;
                 }

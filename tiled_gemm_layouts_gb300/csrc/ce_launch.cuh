@@ -10,7 +10,7 @@
 namespace tg {
 
 template <int MODE, int BN, bool PAIR>
-cudaError_t launch_ce_tile(const CeParams& p, int sms, cudaStream_t stream) {
+cudaError_t launch_ce_tile(const CeParams& p, int sms, bool chained, cudaStream_t stream) {
     using TS = TileShape<BN, PAIR>;
     auto kern = ce_kernel<MODE, BN, PAIR>;
     static std::atomic<unsigned long long> attr_set{0};  // one bit per device
@@ -23,27 +23,35 @@ cudaError_t launch_ce_tile(const CeParams& p, int sms, cudaStream_t stream) {
         if (e != cudaSuccess) return e;
         attr_set.fetch_or(bit, std::memory_order_release);
     }
-    const long long items = (long long)p.tiles_m * p.tiles_n * p.splits;
+    long long items = 0;
+    for (const CeSide& s : p.side)
+        items += (long long)s.tiles_m * s.tiles_n * (&s == p.side ? p.splits : 1);
     const long long slots = PAIR ? sms / 2 : sms;
     const int workers = (int)(items < slots ? items : slots);
     cudaLaunchConfig_t lc = {};
-    cudaLaunchAttribute attr[1];
+    cudaLaunchAttribute attr[2];
     lc.gridDim = dim3(PAIR ? 2 * workers : workers, 1, 1);
     lc.blockDim = dim3(kCeThreads, 1, 1);
     lc.dynamicSmemBytes = TS::kSmemBytes;
     lc.stream = stream;
     if (PAIR) {
-        attr[0].id = cudaLaunchAttributeClusterDimension;
-        attr[0].val.clusterDim.x = 2;
-        attr[0].val.clusterDim.y = 1;
-        attr[0].val.clusterDim.z = 1;
-        lc.attrs = attr;
-        lc.numAttrs = 1;
+        attr[lc.numAttrs].id = cudaLaunchAttributeClusterDimension;
+        attr[lc.numAttrs].val.clusterDim.x = 2;
+        attr[lc.numAttrs].val.clusterDim.y = 1;
+        attr[lc.numAttrs].val.clusterDim.z = 1;
+        ++lc.numAttrs;
     }
+    if (chained) {
+        attr[lc.numAttrs].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attr[lc.numAttrs].val.programmaticStreamSerializationAllowed = 1;
+        ++lc.numAttrs;
+    }
+    lc.attrs = attr;
     return cudaLaunchKernelEx(&lc, kern, p);
 }
 
 template <int MODE>
-cudaError_t launch_ce_mode(const CeParams& p, CeTile tile, int sms, cudaStream_t stream);
+cudaError_t launch_ce_mode(const CeParams& p, CeTile tile, int sms, bool chained,
+                           cudaStream_t stream);
 
 }  // namespace tg
