@@ -183,7 +183,7 @@ int check_args(const Args& a) {
 
 // The touched bytes of every operand must lie inside one allocation of the
 // current device (proves the kernel cannot read or write outside caller memory).
-int check_pointer(const void* p, const Span& s, int dev) {
+int check_pointer(const void* p, const Span& s, int dev, Span* inside) {
     if (!p) return TG_OK;
     cudaPointerAttributes at;
     if (cudaPointerGetAttributes(&at, p) != cudaSuccess) {
@@ -198,6 +198,11 @@ int check_pointer(const void* p, const Span& s, int dev) {
     if (g_range(&base, &size, reinterpret_cast<CUdeviceptr>(p)) != CUDA_SUCCESS)
         return TG_ERR_POINTER;
     if ((u128)s.lo < (u128)base || s.hi > (u128)base + size) return TG_ERR_POINTER;
+    if (inside) {
+        inside->present = true;
+        inside->lo = (uintptr_t)base;
+        inside->hi = (u128)base + size;
+    }
     return TG_OK;
 }
 

@@ -461,8 +461,9 @@ extern "C" int tg_linear_ce(int64_t T, int64_t V, int64_t D, const void* H, int6
     if ((rc = current_device(&dev, &info))) return rc;
     if (!load_driver_entry_points()) return TG_ERR_CUDA;
     const void* ptrs[6] = {loss, lse, workspace, H, W, target};
+    PointerChecks check{dev};
     for (int i = 0; i < 6; ++i)
-        if ((rc = check_pointer(ptrs[i], spans[i], dev))) return rc;
+        if ((rc = check(ptrs[i], spans[i]))) return rc;
 
     char* ws = static_cast<char*>(workspace);
     bool ok = true;
@@ -546,10 +547,10 @@ extern "C" int tg_linear_ce_grad(int64_t T, int64_t V, int64_t D, const void* H,
         if (intersects(work, s)) return TG_ERR_OVERLAP;
     for (const Span& s : ins)
         if (intersects(work, s)) return TG_ERR_OVERLAP;
-    if ((rc = check_pointer(workspace, work, dev)) || (rc = check_pointer(dH, outs[0], dev)) ||
-        (rc = check_pointer(dW, outs[1], dev)) || (rc = check_pointer(H, ins[0], dev)) ||
-        (rc = check_pointer(W, ins[1], dev)) || (rc = check_pointer(target, ins[2], dev)) ||
-        (rc = check_pointer(lse, ins[3], dev)) || (rc = check_pointer(dloss, ins[4], dev)))
+    PointerChecks check{dev};
+    if ((rc = check(workspace, work)) || (rc = check(dH, outs[0])) || (rc = check(dW, outs[1])) ||
+        (rc = check(H, ins[0])) || (rc = check(W, ins[1])) || (rc = check(target, ins[2])) ||
+        (rc = check(lse, ins[3])) || (rc = check(dloss, ins[4])))
         return rc;
 
     char* ws = static_cast<char*>(workspace);

@@ -48,8 +48,20 @@ Span span_bytes(const void* p, u128 bytes);
 bool intersects(const Span& a, const Span& b);
 inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
-// TG_OK if the span is absent or lies inside one allocation of device `dev`.
-int check_pointer(const void* p, const Span& s, int dev);
+// TG_OK if the span is absent or lies inside one allocation of device `dev`
+// (whose bytes then are *inside, if given).
+int check_pointer(const void* p, const Span& s, int dev, Span* inside = nullptr);
+
+// The same for the many operands of one call: tensors often lie in one
+// allocation after another, and what was proven for it is asked for once.
+struct PointerChecks {
+    int dev;
+    Span last = {};
+    int operator()(const void* p, const Span& s) {
+        if (s.present && last.present && last.lo <= s.lo && s.hi <= last.hi) return 0;
+        return check_pointer(p, s, dev, &last);
+    }
+};
 
 // Tensor maps of a 16-bit matrix (see the definitions for the box shapes).
 bool encode_2d(CUtensorMap* map, int dtype, const void* base, uint64_t inner, uint64_t outer,

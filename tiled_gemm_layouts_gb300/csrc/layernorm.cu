@@ -15,11 +15,16 @@
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
+#include <atomic>
 #include <cstring>
 #include <initializer_list>
 
 #include "../../include/tilegemm.h"
+#include "chained.cuh"
+#include "gemm_params.h"
 #include "host_common.h"
+#include "packed.cuh"
+#include "ptx.cuh"
 
 namespace tg {
 namespace {
@@ -49,16 +54,33 @@ struct alignas(4) Pack<2> {
     uint16_t e[2];
 };
 
-template <int VEC>
-__device__ __forceinline__ Pack<VEC> load(const uint16_t* p) {
-    Pack<VEC> v;
-    if constexpr (VEC == 8)
-        *reinterpret_cast<uint4*>(&v) = __ldg(reinterpret_cast<const uint4*>(p));
-    else if constexpr (VEC == 2)
-        *reinterpret_cast<uint32_t*>(&v) = __ldg(reinterpret_cast<const uint32_t*>(p));
-    else
-        v.e[0] = __ldg(p);
+// A pack from p; `left` elements of the row start there.  Packs of rows that
+// are not aligned to them (WHOLE = false) are read element by element, zeros
+// past the end; whole packs lie inside the row or outside.
+template <int VEC, bool WHOLE>
+__device__ __forceinline__ Pack<VEC> load(const uint16_t* p, int left) {
+    Pack<VEC> v{};
+    if constexpr (!WHOLE) {
+#pragma unroll
+        for (int k = 0; k < VEC; ++k)
+            if (k < left) v.e[k] = __ldg(p + k);
+    } else if (left > 0) {
+        if constexpr (VEC == 8)
+            *reinterpret_cast<uint4*>(&v) = __ldg(reinterpret_cast<const uint4*>(p));
+        else
+            *reinterpret_cast<uint32_t*>(&v) = __ldg(reinterpret_cast<const uint32_t*>(p));
+    }
     return v;
+}
+template <int VEC, bool WHOLE>
+__device__ __forceinline__ void store(uint16_t* p, int left, const Pack<VEC>& v) {
+    if constexpr (!WHOLE) {
+#pragma unroll
+        for (int k = 0; k < VEC; ++k)
+            if (k < left) p[k] = v.e[k];
+    } else if (left > 0) {
+        *reinterpret_cast<Pack<VEC>*>(p) = v;
+    }
 }
 
 // Sums of N values over the WARPS warps that share a row; every thread gets
@@ -97,164 +119,543 @@ struct LnParams {
     long long ldo;
     float *mean, *rstd;
     float* part;  // gradient: [blocks][2][cols]
+    int stages;   // ring: rows in flight per team
+    long long timeout_cycles;
+    int* status;
 };
+
+template <bool BF>
+__device__ __forceinline__ f2 widen2(const uint16_t* e) {
+    const uint32_t w = *reinterpret_cast<const uint32_t*>(e);
+    if constexpr (BF) return pair(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
+    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w));
+    return pair(f.x, f.y);
+}
+template <bool BF>
+__device__ __forceinline__ uint32_t narrow2(f2 a) {
+    const float2 f = split(a);
+    uint32_t w;
+    if constexpr (BF) {
+        const __nv_bfloat162 h = __floats2bfloat162_rn(f.x, f.y);
+        w = *reinterpret_cast<const uint32_t*>(&h);
+    } else {
+        const __half2 h = __floats2half2_rn(f.x, f.y);
+        w = *reinterpret_cast<const uint32_t*>(&h);
+    }
+    return w;
+}
+
+// ------------------------------------------------------------- row ring
+//
+// Rows of whole 16-byte packs travel through shared memory: each team of
+// warps (one row at a time) keeps `stages` rows in flight as bulk copies,
+// counted on one mbarrier per stage.  Loads into registers keep at most 32 KB
+// per SM in flight here, since a thread's columns also hold its weights and
+// sums, and memory's latency times its rate is about 50 KB per SM.
+constexpr int kMaxStages = 8;
+
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
+    asm volatile(
+        "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
+        "l"(src), "r"(bytes), "r"(bar)
+        : "memory");
+}
+
+// Bounded wait for a stage; on a timeout the status word is set, and copies
+// in flight get ample time to land before the block may end.
+__device__ __forceinline__ bool stage_ready(uint32_t bar, uint32_t parity, const LnParams& p) {
+    if (mbar_try_wait(bar, parity)) return true;
+    const long long t0 = clock64();
+    while (!mbar_try_wait_suspend(bar, parity, 200000)) {
+        if (clock64() - t0 > p.timeout_cycles) {
+            atomicCAS(p.status, 0, DEV_TIMEOUT_PRODUCER + 2);
+            const long long t1 = clock64();
+            while (clock64() - t1 < 2000000) {
+            }
+            return false;
+        }
+    }
+    return true;
+}
 
 // WARPS warps per row, NV packs of VEC elements per thread.  Rows wider than
 // that (WIDE) are read again from memory, which finds most of them in L2.
 constexpr int kRowsPerBlock = 4;  // rows of a block whose rows take one warp each
+constexpr int row_threads(int warps) { return 32 * (warps == 1 ? kRowsPerBlock : warps); }
 
-template <bool BF, int VEC, int WARPS, int NV, bool WIDE>
-__global__ void __launch_bounds__(WARPS == 1 ? 32 * kRowsPerBlock : 32 * WARPS)
+template <bool BF, int VEC, bool WHOLE, int WARPS, int NV, bool WIDE>
+__global__ void __launch_bounds__(row_threads(WARPS))
 ln_forward_kernel(const LnParams p) {
     __shared__ float buf[2][WARPS == 1 ? 1 : WARPS];
     const int tid = WARPS == 1 ? threadIdx.x & 31 : threadIdx.x;
-    constexpr int kThreads = 32 * WARPS, kStep = kThreads * VEC;
+    constexpr int kThreads = 32 * WARPS, kStep = kThreads * VEC, PAIRS = VEC / 2;
     const long long row = WARPS == 1 ? (long long)blockIdx.x * kRowsPerBlock + (threadIdx.x >> 5)
                                      : (long long)blockIdx.x;
     if (row >= p.rows) return;
     const uint16_t* x = p.x + row * p.ldx;
     uint16_t* y = p.out + row * p.ldo;
     const int chunks = WIDE ? (p.cols + kStep * NV - 1) / (kStep * NV) : 1;
+    auto column = [&](int chunk, int i) { return (chunk * NV + i) * kStep + tid * VEC; };
     Pack<VEC> v[NV];
     auto fetch = [&](int chunk) {
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
-            const int c = (chunk * NV + i) * kStep + tid * VEC;
-            if (c < p.cols) v[i] = load<VEC>(x + c);
+            const int c = column(chunk, i);
+            v[i] = load<VEC, WHOLE>(x + c, p.cols - c);
         }
     };
-    float sum[1] = {0.0f};
+    f2 acc = pair(0.0f, 0.0f);
     for (int k = 0; k < chunks; ++k) {
         fetch(k);
 #pragma unroll
-        for (int i = 0; i < NV; ++i)
-            if ((k * NV + i) * kStep + tid * VEC < p.cols)
+        for (int i = 0; i < NV; ++i)  // zeros past the row's end
 #pragma unroll
-                for (int j = 0; j < VEC; ++j) sum[0] += widen<BF>(v[i].e[j]);
+            for (int j = 0; j < PAIRS; ++j) acc = add(acc, widen2<BF>(v[i].e + 2 * j));
     }
+    float2 a = split(acc);
+    float sum[1] = {a.x + a.y};
     row_sum<1, WARPS>(sum, buf[0]);
     const float mean = sum[0] / (float)p.cols;
-    float sq[1] = {0.0f};
+    const f2 minus = pair(-mean, -mean);
+    acc = pair(0.0f, 0.0f);
     for (int k = 0; k < chunks; ++k) {
         if (WIDE) fetch(k);
 #pragma unroll
-        for (int i = 0; i < NV; ++i)
-            if ((k * NV + i) * kStep + tid * VEC < p.cols)
+        for (int i = 0; i < NV; ++i) {
+            const int left = p.cols - column(k, i);
+            if (WHOLE && left <= 0) continue;
 #pragma unroll
-                for (int j = 0; j < VEC; ++j) {
-                    const float d = widen<BF>(v[i].e[j]) - mean;
-                    sq[0] = fmaf(d, d, sq[0]);
-                }
+            for (int j = 0; j < PAIRS; ++j) {
+                f2 d = add(widen2<BF>(v[i].e + 2 * j), minus);
+                if (!WHOLE && 2 * j + 1 >= left)
+                    d = pair(2 * j < left ? split(d).x : 0.0f, 0.0f);
+                acc = fma(d, d, acc);
+            }
+        }
     }
+    a = split(acc);
+    float sq[1] = {a.x + a.y};
     row_sum<1, WARPS>(sq, buf[1]);
     const float rstd = 1.0f / sqrtf(sq[0] / (float)p.cols + p.eps);
     if (tid == 0) {
         p.mean[row] = mean;
         p.rstd[row] = rstd;
     }
+    const f2 scale = pair(rstd, rstd);
     for (int k = 0; k < chunks; ++k) {
         if (WIDE) fetch(k);
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
-            const int c = (k * NV + i) * kStep + tid * VEC;
-            if (c >= p.cols) continue;
-            const Pack<VEC> w = load<VEC>(p.weight + c);
-            Pack<VEC> b = {}, o;
-            if (p.bias) b = load<VEC>(p.bias + c);
+            const int c = column(k, i), left = p.cols - c;
+            if (left <= 0) continue;
+            const Pack<VEC> w = load<VEC, WHOLE>(p.weight + c, left);
+            Pack<VEC> b{};
+            if (p.bias) b = load<VEC, WHOLE>(p.bias + c, left);
+            Pack<VEC> o;
 #pragma unroll
-            for (int j = 0; j < VEC; ++j) {
-                const float xh = (widen<BF>(v[i].e[j]) - mean) * rstd;
-                o.e[j] = narrow<BF>(fmaf(xh, widen<BF>(w.e[j]), widen<BF>(b.e[j])));
+            for (int j = 0; j < PAIRS; ++j) {
+                const f2 xh = mul(add(widen2<BF>(v[i].e + 2 * j), minus), scale);
+                const uint32_t word =
+                    narrow2<BF>(fma(xh, widen2<BF>(w.e + 2 * j), widen2<BF>(b.e + 2 * j)));
+                *reinterpret_cast<uint32_t*>(o.e + 2 * j) = word;
             }
-            *reinterpret_cast<Pack<VEC>*>(y + c) = o;
+            store<VEC, WHOLE>(y + c, left, o);
         }
     }
 }
 
-// dx, and this block's partial sums of dw and db.
-template <bool BF, int VEC, int WARPS, int NV>
-__global__ void __launch_bounds__(WARPS == 1 ? 32 * kRowsPerBlock : 32 * WARPS)
-ln_backward_kernel(const LnParams p) {
-    constexpr int kThreads = 32 * WARPS, kStep = kThreads * VEC;
-    constexpr int kGroups = WARPS == 1 ? kRowsPerBlock : 1;  // rows in work at once
-    __shared__ float buf[2][WARPS == 1 ? 1 : 2 * WARPS];
+// The forward pass through the ring: teams walk over rows.
+// (1024 threads per SM with 64 registers each: 49.5 us against 47.6.)
+constexpr int kForwardThreadsPerSm = 768;  // 85 registers each
+constexpr int forward_blocks_per_sm(int warps) {
+    return row_threads(warps) >= 512 ? 1 : kForwardThreadsPerSm / row_threads(warps);
+}
+
+template <bool BF, int WARPS, int NV>
+__global__ void __launch_bounds__(row_threads(WARPS), forward_blocks_per_sm(WARPS))
+ln_forward_ring_kernel(const LnParams p) {
+    constexpr int VEC = 8, kStep = 32 * WARPS * VEC, PAIRS = VEC / 2;
+    constexpr int kTeams = WARPS == 1 ? kRowsPerBlock : 1;
+    extern __shared__ __align__(128) uint8_t ring[];
+    __shared__ float buf[2][WARPS == 1 ? 1 : WARPS];
+    __shared__ uint64_t full[kTeams][kMaxStages];
     const int tid = WARPS == 1 ? threadIdx.x & 31 : threadIdx.x;
-    const int group = WARPS == 1 ? threadIdx.x >> 5 : 0;
-    float dw[NV][VEC], db[NV][VEC];
-    Pack<VEC> w[NV];
+    const int team = WARPS == 1 ? threadIdx.x >> 5 : 0;
+    const uint32_t bytes = (uint32_t)p.cols * 2;
+    uint8_t* stages = ring + (size_t)team * p.stages * bytes;
+    if (threadIdx.x < kTeams * kMaxStages) mbar_init(smem_addr(&full[0][0] + threadIdx.x), 1);
+    if (threadIdx.x == 0) fence_barrier_init();
+    __syncthreads();
+    const long long first = (long long)blockIdx.x * kTeams + team, step = (long long)gridDim.x * kTeams;
+    auto issue = [&](long long row, int st) {
+        const uint32_t bar = smem_addr(&full[team][st]);
+        mbar_arrive_expect_tx(bar, bytes);
+        bulk_load(smem_addr(stages + st * bytes), p.x + row * p.ldx, bytes, bar);
+    };
+    if (tid == 0)
+        for (int st = 0; st < p.stages && first + st * step < p.rows; ++st) issue(first + st * step, st);
+    Pack<VEC> w[NV], b[NV];
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
         const int c = i * kStep + tid * VEC;
-        w[i] = Pack<VEC>{};
-        if (c < p.cols) w[i] = load<VEC>(p.weight + c);
-#pragma unroll
-        for (int j = 0; j < VEC; ++j) dw[i][j] = db[i][j] = 0.0f;
+        w[i] = load<VEC, true>(p.weight + c, p.cols - c);
+        b[i] = Pack<VEC>{};
+        if (p.bias) b[i] = load<VEC, true>(p.bias + c, p.cols - c);
     }
-    const float inv = 1.0f / (float)p.cols;
-    int flip = 0;
-    for (long long row = (long long)blockIdx.x * kGroups + group; row < p.rows;
-         row += (long long)gridDim.x * kGroups) {
-        const uint16_t* x = p.x + row * p.ldx;
-        const uint16_t* dy = p.dy + row * p.lddy;
-        Pack<VEC> vx[NV], vd[NV];
+    int st = 0;
+    uint32_t phase = 0;
+    for (long long row = first; row < p.rows; row += step) {
+        if (!stage_ready(smem_addr(&full[team][st]), phase, p)) return;
+        f2 v[NV][PAIRS], acc = pair(0.0f, 0.0f);
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
             const int c = i * kStep + tid * VEC;
-            if (c < p.cols) {
-                vx[i] = load<VEC>(x + c);
-                vd[i] = load<VEC>(dy + c);
+            Pack<VEC> x{};
+            if (c < p.cols) x = *reinterpret_cast<const Pack<VEC>*>(stages + st * bytes + c * 2);
+#pragma unroll
+            for (int j = 0; j < PAIRS; ++j) {
+                v[i][j] = widen2<BF>(x.e + 2 * j);
+                acc = add(acc, v[i][j]);
             }
         }
-        const float mean = __ldg(p.mean + row), rstd = __ldg(p.rstd + row);
-        float s[2] = {0.0f, 0.0f};  // sums of g and of g xh
+        float2 a = split(acc);
+        float sum[1] = {a.x + a.y};
+        row_sum<1, WARPS>(sum, buf[0]);
+        // everyone has read the stage
+        if constexpr (WARPS == 1) __syncwarp();
+        if (tid == 0 && row + p.stages * step < p.rows) issue(row + p.stages * step, st);
+        const float mean = sum[0] / (float)p.cols;
+        const f2 minus = pair(-mean, -mean);
+        acc = pair(0.0f, 0.0f);
 #pragma unroll
         for (int i = 0; i < NV; ++i)
             if (i * kStep + tid * VEC < p.cols)
 #pragma unroll
-                for (int j = 0; j < VEC; ++j) {
-                    const float xh = (widen<BF>(vx[i].e[j]) - mean) * rstd;
-                    const float d = widen<BF>(vd[i].e[j]), g = d * widen<BF>(w[i].e[j]);
-                    s[0] += g;
-                    s[1] = fmaf(g, xh, s[1]);
-                    dw[i][j] = fmaf(d, xh, dw[i][j]);
-                    db[i][j] += d;
+                for (int j = 0; j < PAIRS; ++j) {
+                    v[i][j] = add(v[i][j], minus);
+                    acc = fma(v[i][j], v[i][j], acc);
                 }
-        row_sum<2, WARPS>(s, buf[flip]);
-        flip ^= 1;
-        const float c1 = s[0] * inv, c2 = s[1] * inv;
-        uint16_t* dx = p.out + row * p.ldo;
+        a = split(acc);
+        float sq[1] = {a.x + a.y};
+        row_sum<1, WARPS>(sq, buf[1]);
+        const float rstd = 1.0f / sqrtf(sq[0] / (float)p.cols + p.eps);
+        if (tid == 0) {
+            p.mean[row] = mean;
+            p.rstd[row] = rstd;
+        }
+        const f2 scale = pair(rstd, rstd);
+        uint16_t* y = p.out + row * p.ldo;
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
             const int c = i * kStep + tid * VEC;
             if (c >= p.cols) continue;
             Pack<VEC> o;
 #pragma unroll
-            for (int j = 0; j < VEC; ++j) {
-                const float xh = (widen<BF>(vx[i].e[j]) - mean) * rstd;
-                const float g = widen<BF>(vd[i].e[j]) * widen<BF>(w[i].e[j]);
-                o.e[j] = narrow<BF>(rstd * (g - c1 - xh * c2));
+            for (int j = 0; j < PAIRS; ++j) {
+                const uint32_t word = narrow2<BF>(fma(mul(v[i][j], scale), widen2<BF>(w[i].e + 2 * j),
+                                                      widen2<BF>(b[i].e + 2 * j)));
+                *reinterpret_cast<uint32_t*>(o.e + 2 * j) = word;
             }
-            *reinterpret_cast<Pack<VEC>*>(dx + c) = o;
+            store<VEC, true>(y + c, p.cols - c, o);
+        }
+        if (++st == p.stages) {
+            st = 0;
+            phase ^= 1;
         }
     }
-    // one partial row per row group: [block * kGroups + group][2][cols]
-    float* part = p.part + ((long long)blockIdx.x * kGroups + group) * 2 * p.cols;
+}
+
+// One partial row per block: [block][2][cols]; rows that a block's warps took
+// side by side are added in the order of the warps.
+template <int VEC, int WARPS, int NV>
+__device__ __forceinline__ void write_partials(const LnParams& p, const f2 (&dw)[NV][VEC / 2],
+                                               const f2 (&db)[NV][VEC / 2]) {
+    constexpr int kStep = 32 * WARPS * VEC, PAIRS = VEC / 2;
+    const int tid = WARPS == 1 ? threadIdx.x & 31 : threadIdx.x;
+    const int group = WARPS == 1 ? threadIdx.x >> 5 : 0;
+    if constexpr (WARPS == 1) {
+        __shared__ float2 part[kRowsPerBlock][32 * NV * PAIRS];
+        for (int what = 0; what < 2; ++what) {
+#pragma unroll
+            for (int i = 0; i < NV; ++i)
+#pragma unroll
+                for (int j = 0; j < PAIRS; ++j)
+                    part[group][(i * PAIRS + j) * 32 + tid] = split(what ? db[i][j] : dw[i][j]);
+            __syncthreads();
+            float* out = p.part + ((long long)blockIdx.x * 2 + what) * p.cols;
+            for (int k = threadIdx.x; k < 32 * NV * PAIRS; k += 32 * kRowsPerBlock) {
+                const int i = k / (32 * PAIRS), j = k / 32 % PAIRS, lane = k % 32;
+                const int c = i * kStep + lane * VEC + 2 * j;
+                float2 s = part[0][k];
+#pragma unroll
+                for (int y = 1; y < kRowsPerBlock; ++y) {
+                    s.x += part[y][k].x;
+                    s.y += part[y][k].y;
+                }
+                if (c < p.cols) out[c] = s.x;
+                if (c + 1 < p.cols) out[c + 1] = s.y;
+            }
+            __syncthreads();
+        }
+    } else {
+        float* out = p.part + (long long)blockIdx.x * 2 * p.cols;
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const int c = i * kStep + tid * VEC;
+#pragma unroll
+            for (int j = 0; j < PAIRS; ++j) {
+                const float2 a = split(dw[i][j]), b = split(db[i][j]);
+                if (c + 2 * j < p.cols) {
+                    out[c + 2 * j] = a.x;
+                    out[p.cols + c + 2 * j] = b.x;
+                }
+                if (c + 2 * j + 1 < p.cols) {
+                    out[c + 2 * j + 1] = a.y;
+                    out[p.cols + c + 2 * j + 1] = b.y;
+                }
+            }
+        }
+    }
+}
+
+// dx, and this block's partial sums of dw and db; 16 elements per thread.  Up
+// to 8192 columns (512 threads, 128 registers each) the next row's loads are
+// in flight while this row is reduced and written, and xh and g stay in
+// registers between the reduction and dx; 1024 threads have 64 registers and
+// compute those two again, with the weights from L1.
+constexpr int kGradThreadsPerSm = 512;
+constexpr int grad_blocks_per_sm(int warps) {
+    return row_threads(warps) >= kGradThreadsPerSm ? 1 : kGradThreadsPerSm / row_threads(warps);
+}
+
+template <bool BF, int VEC, bool WHOLE, int WARPS, int NV>
+__global__ void __launch_bounds__(row_threads(WARPS), grad_blocks_per_sm(WARPS))
+ln_backward_kernel(const LnParams p) {
+    constexpr bool AHEAD = WARPS < 32;
+    constexpr int kThreads = 32 * WARPS, kStep = kThreads * VEC, PAIRS = VEC / 2;
+    constexpr int kGroups = WARPS == 1 ? kRowsPerBlock : 1;  // rows in work at once
+    __shared__ float buf[2][WARPS == 1 ? 1 : 2 * WARPS];
+    const int tid = WARPS == 1 ? threadIdx.x & 31 : threadIdx.x;
+    const int group = WARPS == 1 ? threadIdx.x >> 5 : 0;
+    f2 dw[NV][PAIRS], db[NV][PAIRS];
+    Pack<VEC> w[NV];
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
         const int c = i * kStep + tid * VEC;
-        if (c < p.cols)
+        if (AHEAD) w[i] = load<VEC, WHOLE>(p.weight + c, p.cols - c);
 #pragma unroll
-            for (int j = 0; j < VEC; ++j) {
-                part[c + j] = dw[i][j];
-                part[p.cols + c + j] = db[i][j];
-            }
+        for (int j = 0; j < PAIRS; ++j) dw[i][j] = db[i][j] = pair(0.0f, 0.0f);
     }
+    allow_next_kernel();
+    const float inv = 1.0f / (float)p.cols;
+    const long long step = (long long)gridDim.x * kGroups;
+    Pack<VEC> vx[NV], vd[NV], nx[NV], nd[NV];
+    float mean = 0.0f, rstd = 0.0f;
+    auto fetch = [&](long long row, Pack<VEC>(&x)[NV], Pack<VEC>(&d)[NV]) {
+        const uint16_t* px = p.x + row * p.ldx;
+        const uint16_t* pd = p.dy + row * p.lddy;
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const int c = i * kStep + tid * VEC;
+            x[i] = load<VEC, WHOLE>(px + c, p.cols - c);
+            d[i] = load<VEC, WHOLE>(pd + c, p.cols - c);
+        }
+        mean = __ldg(p.mean + row);
+        rstd = __ldg(p.rstd + row);
+    };
+    long long row = (long long)blockIdx.x * kGroups + group;
+    if (AHEAD && row < p.rows) fetch(row, nx, nd);
+    int flip = 0;
+    for (; row < p.rows; row += step) {
+        if (!AHEAD) fetch(row, vx, vd);
+        const float r = rstd;
+        // x - mean first: scaled apart, the two would cancel with their roundings
+        const f2 scale = pair(r, r), minus = pair(-mean, -mean);
+        if (AHEAD) {
+#pragma unroll
+            for (int i = 0; i < NV; ++i) {
+                vx[i] = nx[i];
+                vd[i] = nd[i];
+            }
+            if (row + step < p.rows) fetch(row + step, nx, nd);
+        }
+        f2 s0 = pair(0.0f, 0.0f), s1 = s0;  // sums of g and of g xh
+        f2 g[AHEAD ? NV : 1][PAIRS], xh[AHEAD ? NV : 1][PAIRS];
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            if (!AHEAD) {
+                const int c = i * kStep + tid * VEC;
+                w[i] = load<VEC, WHOLE>(p.weight + c, p.cols - c);
+            }
+#pragma unroll
+            for (int j = 0; j < PAIRS; ++j) {
+                // columns past the row's end hold zeros in dy and w: they add nothing
+                const f2 d = widen2<BF>(vd[i].e + 2 * j);
+                const f2 x = mul(add(widen2<BF>(vx[i].e + 2 * j), minus), scale);
+                const f2 gg = mul(d, widen2<BF>(w[i].e + 2 * j));
+                s0 = add(s0, gg);
+                s1 = fma(gg, x, s1);
+                dw[i][j] = fma(d, x, dw[i][j]);
+                db[i][j] = add(db[i][j], d);
+                if (AHEAD) {
+                    xh[i][j] = x;
+                    g[i][j] = gg;
+                }
+            }
+        }
+        const float2 a = split(s0), b = split(s1);
+        float s[2] = {a.x + a.y, b.x + b.y};
+        row_sum<2, WARPS>(s, buf[flip]);
+        flip ^= 1;
+        const float c1 = -r * s[0] * inv, c2 = -r * s[1] * inv;
+        const f2 k1 = pair(c1, c1), k2 = pair(c2, c2);
+        uint16_t* dx = p.out + row * p.ldo;
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const int c = i * kStep + tid * VEC;
+            if (c >= p.cols) continue;
+            if (!AHEAD) w[i] = load<VEC, WHOLE>(p.weight + c, p.cols - c);
+            Pack<VEC> o;
+#pragma unroll
+            for (int j = 0; j < PAIRS; ++j) {
+                const f2 x = AHEAD ? xh[i][j] : mul(add(widen2<BF>(vx[i].e + 2 * j), minus), scale);
+                const f2 gg = AHEAD ? g[i][j]
+                                    : mul(widen2<BF>(vd[i].e + 2 * j), widen2<BF>(w[i].e + 2 * j));
+                const uint32_t word = narrow2<BF>(fma(x, k2, fma(gg, scale, k1)));
+                *reinterpret_cast<uint32_t*>(o.e + 2 * j) = word;
+            }
+            store<VEC, WHOLE>(dx + c, p.cols - c, o);
+        }
+    }
+    write_partials<VEC, WARPS, NV>(p, dw, db);
+}
+
+// The same through the ring.  A row's stage is read twice, before and after
+// its reduction, by 1024 threads, whose registers hold neither the row nor xh
+// and g; it is filled again after the next row's barrier.
+template <bool BF, int WARPS, int NV>
+__global__ void __launch_bounds__(row_threads(WARPS), grad_blocks_per_sm(WARPS))
+ln_backward_ring_kernel(const LnParams p) {
+    constexpr bool KEEP = WARPS < 32;
+    constexpr int VEC = 8, kStep = 32 * WARPS * VEC, PAIRS = VEC / 2;
+    constexpr int kTeams = WARPS == 1 ? kRowsPerBlock : 1;
+    extern __shared__ __align__(128) uint8_t ring[];
+    __shared__ float buf[2][WARPS == 1 ? 1 : 2 * WARPS];
+    __shared__ uint64_t full[kTeams][kMaxStages];
+    const int tid = WARPS == 1 ? threadIdx.x & 31 : threadIdx.x;
+    const int team = WARPS == 1 ? threadIdx.x >> 5 : 0;
+    const uint32_t bytes = (uint32_t)p.cols * 2;
+    uint8_t* stages = ring + (size_t)team * p.stages * 2 * bytes;
+    allow_next_kernel();
+    if (threadIdx.x < kTeams * kMaxStages) mbar_init(smem_addr(&full[0][0] + threadIdx.x), 1);
+    if (threadIdx.x == 0) fence_barrier_init();
+    __syncthreads();
+    const long long first = (long long)blockIdx.x * kTeams + team, step = (long long)gridDim.x * kTeams;
+    auto issue = [&](long long row, int st) {
+        const uint32_t bar = smem_addr(&full[team][st]), dst = smem_addr(stages + st * 2 * bytes);
+        mbar_arrive_expect_tx(bar, 2 * bytes);
+        bulk_load(dst, p.x + row * p.ldx, bytes, bar);
+        bulk_load(dst + bytes, p.dy + row * p.lddy, bytes, bar);
+    };
+    if (tid == 0)
+        for (int st = 0; st < p.stages && first + st * step < p.rows; ++st) issue(first + st * step, st);
+    f2 dw[NV][PAIRS], db[NV][PAIRS];
+    Pack<VEC> w[NV];
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+        const int c = i * kStep + tid * VEC;
+        w[i] = load<VEC, true>(p.weight + c, p.cols - c);
+#pragma unroll
+        for (int j = 0; j < PAIRS; ++j) dw[i][j] = db[i][j] = pair(0.0f, 0.0f);
+    }
+    const float inv = 1.0f / (float)p.cols;
+    float next_mean = 0.0f, next_rstd = 0.0f;
+    if (first < p.rows) {
+        next_mean = __ldg(p.mean + first);
+        next_rstd = __ldg(p.rstd + first);
+    }
+    int st = 0, flip = 0;
+    uint32_t phase = 0;
+    for (long long row = first; row < p.rows; row += step) {
+        const float r = next_rstd, mean = next_mean;
+        if (row + step < p.rows) {
+            next_mean = __ldg(p.mean + row + step);
+            next_rstd = __ldg(p.rstd + row + step);
+        }
+        // x - mean first: scaled apart, the two would cancel with their roundings
+        const f2 scale = pair(r, r), minus = pair(-mean, -mean);
+        if (!stage_ready(smem_addr(&full[team][st]), phase, p)) return;
+        const uint8_t* sx = stages + st * 2 * bytes;
+        f2 s0 = pair(0.0f, 0.0f), s1 = s0;  // sums of g and of g xh
+        f2 g[KEEP ? NV : 1][PAIRS], xh[KEEP ? NV : 1][PAIRS];
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const int c = i * kStep + tid * VEC;
+            Pack<VEC> vx{}, vd{};  // columns past the row's end add nothing
+            if (c < p.cols) {
+                vx = *reinterpret_cast<const Pack<VEC>*>(sx + c * 2);
+                vd = *reinterpret_cast<const Pack<VEC>*>(sx + bytes + c * 2);
+            }
+#pragma unroll
+            for (int j = 0; j < PAIRS; ++j) {
+                const f2 d = widen2<BF>(vd.e + 2 * j);
+                const f2 x = mul(add(widen2<BF>(vx.e + 2 * j), minus), scale);
+                const f2 gg = mul(d, widen2<BF>(w[i].e + 2 * j));
+                s0 = add(s0, gg);
+                s1 = fma(gg, x, s1);
+                dw[i][j] = fma(d, x, dw[i][j]);
+                db[i][j] = add(db[i][j], d);
+                if (KEEP) {
+                    xh[i][j] = x;
+                    g[i][j] = gg;
+                }
+            }
+        }
+        const float2 a = split(s0), b = split(s1);
+        float s[2] = {a.x + a.y, b.x + b.y};
+        row_sum<2, WARPS>(s, buf[flip]);
+        flip ^= 1;
+        if constexpr (WARPS == 1) __syncwarp();
+        if (tid == 0) {
+            // KEEP: everyone has read this row's stage; else the one before's
+            const long long done = KEEP ? row : row - step;
+            const int slot = KEEP ? st : (st ? st - 1 : p.stages - 1);
+            if (done >= first && done + p.stages * step < p.rows) issue(done + p.stages * step, slot);
+        }
+        const float c1 = -r * s[0] * inv, c2 = -r * s[1] * inv;
+        const f2 k1 = pair(c1, c1), k2 = pair(c2, c2);
+        uint16_t* dx = p.out + row * p.ldo;
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const int c = i * kStep + tid * VEC;
+            if (c >= p.cols) continue;
+            Pack<VEC> o, vx, vd;
+            if (!KEEP) {
+                vx = *reinterpret_cast<const Pack<VEC>*>(sx + c * 2);
+                vd = *reinterpret_cast<const Pack<VEC>*>(sx + bytes + c * 2);
+            }
+#pragma unroll
+            for (int j = 0; j < PAIRS; ++j) {
+                const f2 x = KEEP ? xh[i][j] : mul(add(widen2<BF>(vx.e + 2 * j), minus), scale);
+                const f2 gg = KEEP ? g[i][j] : mul(widen2<BF>(vd.e + 2 * j), widen2<BF>(w[i].e + 2 * j));
+                const uint32_t word = narrow2<BF>(fma(x, k2, fma(gg, scale, k1)));
+                *reinterpret_cast<uint32_t*>(o.e + 2 * j) = word;
+            }
+            store<VEC, true>(dx + c, p.cols - c, o);
+        }
+        if (++st == p.stages) {
+            st = 0;
+            phase ^= 1;
+        }
+    }
+    write_partials<VEC, WARPS, NV>(p, dw, db);
 }
 
 // Rows too wide for registers: dx alone, one block per row.
 template <bool BF>
 __global__ void __launch_bounds__(1024) ln_backward_wide_kernel(const LnParams p) {
     __shared__ float buf[2 * 32];
+    allow_next_kernel();
     const long long row = blockIdx.x;
     const uint16_t* x = p.x + row * p.ldx;
     const uint16_t* dy = p.dy + row * p.lddy;
@@ -277,6 +678,8 @@ __global__ void __launch_bounds__(1024) ln_backward_wide_kernel(const LnParams p
 // Their partial dw and db: block (column group, row group), thread = column.
 template <bool BF>
 __global__ void __launch_bounds__(256) ln_backward_wide_columns_kernel(const LnParams p) {
+    allow_next_kernel();
+    wait_for_previous_kernel();  // so that the end of this kernel is the end of both
     const int c = blockIdx.x * 256 + threadIdx.x;
     if (c >= p.cols) return;
     float dw = 0.0f, db = 0.0f;
@@ -298,6 +701,7 @@ __global__ void __launch_bounds__(1024)
 ln_reduce_kernel(const float* __restrict__ part, int parts, int cols, uint16_t* __restrict__ dw,
                  uint16_t* __restrict__ db) {
     __shared__ float s[2][32][33];
+    wait_for_previous_kernel();
     const int lane = threadIdx.x & 31, y = threadIdx.x >> 5;
     const int c = blockIdx.x * 32 + lane;
     float a = 0.0f, b = 0.0f;
@@ -324,8 +728,8 @@ ln_reduce_kernel(const float* __restrict__ part, int parts, int cols, uint16_t* 
     }
 }
 
-// Widest pack that every row, weight and output allows: whole packs per row
-// and aligned row starts.
+// Widest aligned pack that every row, weight and output allows: whole packs
+// per row and aligned row starts.  0: none, rows are read by elements.
 int pack_of(int64_t cols, std::initializer_list<const void*> ptrs, std::initializer_list<int64_t> lds) {
     for (int vec : {8, 2}) {
         bool ok = cols % vec == 0;
@@ -333,115 +737,158 @@ int pack_of(int64_t cols, std::initializer_list<const void*> ptrs, std::initiali
         for (int64_t ld : lds) ok = ok && ld % vec == 0;
         if (ok) return vec;
     }
-    return 1;
+    return 0;
 }
 
-// Calls f with the row shape (warps per row, packs per thread) for `cols`;
-// packs in registers up to the last one's width.
-#define TG_LN_SHAPES(F, VEC)          \
-    if (cols <= 32 * 1 * VEC) F(1, 1) \
-    if (cols <= 32 * 2 * VEC) F(1, 2) \
-    if (cols <= 32 * 4 * VEC) F(1, 4) \
-    if (cols <= 128 * 2 * VEC) F(4, 2) \
-    if (cols <= 128 * 4 * VEC) F(4, 4) \
-    if (cols <= 256 * 4 * VEC) F(8, 4) \
-    if (cols <= 512 * 4 * VEC) F(16, 4)
-// Narrow packs (rows of odd addresses): more of them per thread.
-#define TG_LN_NARROW_SHAPES(F, VEC)   \
-    if (cols <= 32 * 4 * VEC) F(1, 4) \
-    if (cols <= 32 * 8 * VEC) F(1, 8) \
-    if (cols <= 128 * 8 * VEC) F(4, 8) \
-    if (cols <= 256 * 8 * VEC) F(8, 8) \
-    if (cols <= 512 * 8 * VEC) F(16, 8) \
-    if (cols <= 1024 * 8 * VEC) F(32, 8)
+// Row shapes: F(warps per row, packs per thread) for the first that holds
+// `cols`: up to 16 elements per thread, in packs of 8 or of 2.
+#define TG_LN_SHAPES_8(F)        \
+    if (cols <= 256) F(1, 1)     \
+    if (cols <= 512) F(1, 2)     \
+    if (cols <= 1024) F(2, 2)    \
+    if (cols <= 2048) F(4, 2)    \
+    if (cols <= 4096) F(8, 2)    \
+    if (cols <= 8192) F(16, 2)   \
+    if (cols <= 16384) F(32, 2)
+#define TG_LN_SHAPES_2(F)        \
+    if (cols <= 256) F(1, 4)     \
+    if (cols <= 512) F(1, 8)     \
+    if (cols <= 1024) F(2, 8)    \
+    if (cols <= 2048) F(4, 8)    \
+    if (cols <= 4096) F(8, 8)    \
+    if (cols <= 8192) F(16, 8)   \
+    if (cols <= 16384) F(32, 8)
+
+// Launches a ring kernel: `operands` rows per stage, `per_sm` blocks on an SM.
+template <auto Kern>
+cudaError_t launch_ring(LnParams p, int warps, int operands, int per_sm, int64_t blocks,
+                        cudaStream_t stream) {
+    constexpr size_t kRoom = 224 * 1024;  // of an SM's shared memory
+    // a block's own part: its static shared memory and the 1 KB it reserves
+    const size_t fixed = warps == 1 ? 10240 : 2048;
+    static std::atomic<unsigned long long> attr_set{0};  // one bit per device
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    const unsigned long long bit = dev < 64 ? 1ull << dev : 0ull;
+    if (!(attr_set.load(std::memory_order_acquire) & bit)) {
+        e = cudaFuncSetAttribute(Kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 (int)(kRoom - fixed));
+        if (e != cudaSuccess) return e;
+        attr_set.fetch_or(bit, std::memory_order_release);
+    }
+    const size_t stage = (size_t)(warps == 1 ? kRowsPerBlock : 1) * operands * p.cols * 2;
+    size_t stages = (kRoom / per_sm - fixed) / stage;
+    if (stages > kMaxStages) stages = kMaxStages;
+    p.stages = (int)stages;
+    Kern<<<(unsigned)blocks, row_threads(warps), stages * stage, stream>>>(p);
+    return cudaGetLastError();
+}
 
 template <bool BF>
-cudaError_t launch_forward(const LnParams& p, int vec, cudaStream_t stream) {
+cudaError_t launch_forward(const LnParams& p, int vec, int sms, cudaStream_t stream) {
     const int cols = p.cols;
-#define TG_LAUNCH(WARPS, NV, VEC, WIDE)                                                            \
+#define TG_LAUNCH(WARPS, NV, VEC, WHOLE, WIDE)                                                       \
     {                                                                                              \
         const long long blocks = WARPS == 1 ? cdiv(p.rows, kRowsPerBlock) : p.rows;                \
-        ln_forward_kernel<BF, VEC, WARPS, NV, WIDE>                                                \
-            <<<(unsigned)blocks, WARPS == 1 ? 32 * kRowsPerBlock : 32 * WARPS, 0, stream>>>(p);    \
+        ln_forward_kernel<BF, VEC, WHOLE, WARPS, NV, WIDE>                                         \
+            <<<(unsigned)blocks, row_threads(WARPS), 0, stream>>>(p);                              \
         return cudaGetLastError();                                                                 \
     }
-#define TG_F8(WARPS, NV) TG_LAUNCH(WARPS, NV, 8, false)
-#define TG_F2(WARPS, NV) TG_LAUNCH(WARPS, NV, 2, false)
-#define TG_F1(WARPS, NV) TG_LAUNCH(WARPS, NV, 1, false)
+#define TG_FR(WARPS, NV)                                                                       \
+    {                                                                                          \
+        const int64_t need = cdiv(p.rows, WARPS == 1 ? kRowsPerBlock : 1);                     \
+        const int64_t most = (int64_t)sms * forward_blocks_per_sm(WARPS);                      \
+        return launch_ring<ln_forward_ring_kernel<BF, WARPS, NV>>(                             \
+            p, WARPS, 1, forward_blocks_per_sm(WARPS), need < most ? need : most, stream);     \
+    }
+#define TG_F2(WARPS, NV) TG_LAUNCH(WARPS, NV, 2, true, false)
+#define TG_F0(WARPS, NV) TG_LAUNCH(WARPS, NV, 2, false, false)
     if (vec == 8) {
-        TG_LN_SHAPES(TG_F8, 8)
-        TG_LAUNCH(16, 4, 8, true)
+        TG_LN_SHAPES_8(TG_FR)
+        TG_LAUNCH(32, 2, 8, true, true)
     }
     if (vec == 2) {
-        TG_LN_NARROW_SHAPES(TG_F2, 2)
-        TG_LAUNCH(32, 8, 2, true)
+        TG_LN_SHAPES_2(TG_F2)
+        TG_LAUNCH(32, 8, 2, true, true)
     }
-    TG_LN_NARROW_SHAPES(TG_F1, 1)
-    TG_LAUNCH(32, 8, 1, true)
-#undef TG_F8
+    TG_LN_SHAPES_2(TG_F0)
+    TG_LAUNCH(32, 8, 2, false, true)
+#undef TG_FR
 #undef TG_F2
-#undef TG_F1
+#undef TG_F0
 #undef TG_LAUNCH
 }
 
-// Partial rows of dw and db for a row shape: enough blocks to fill the GPU.
+// Blocks of the gradient's kernel, each of which leaves one partial row of dw
+// and db: what the SMs hold, but at least four rows each once every SM has
+// two blocks (the partial rows are 8 bytes per column against 6 per element).
 struct GradShape {
     int warps, packs, vec;  // warps 0: the wide kernels
-    int blocks, parts;
+    int parts;
 };
 
 GradShape grad_shape(int64_t rows, int64_t cols, int vec, int sms) {
-    GradShape s{0, 0, vec, 0, 0};
-#define TG_SET(WARPS, NV)                  \
-    {                                      \
-        if (!s.warps) s.warps = WARPS, s.packs = NV; \
+    GradShape s{0, 0, vec, 0};
+#define TG_SET(WARPS, NV)              \
+    {                                  \
+        if (!s.warps) {                \
+            s.warps = WARPS;           \
+            s.packs = NV;              \
+        }                              \
     }
     if (vec == 8) {
-        TG_LN_SHAPES(TG_SET, 8)
-    } else if (vec == 2) {
-        TG_LN_NARROW_SHAPES(TG_SET, 2)
+        TG_LN_SHAPES_8(TG_SET)
     } else {
-        TG_LN_NARROW_SHAPES(TG_SET, 1)
+        TG_LN_SHAPES_2(TG_SET)
     }
 #undef TG_SET
-    const int groups = s.warps == 1 ? kRowsPerBlock : 1;
-    const int threads = s.warps == 1 ? 32 * kRowsPerBlock : 32 * s.warps;
-    int64_t most;
-    if (s.warps) {
-        most = (int64_t)sms * (threads >= 1024 ? 1 : threads >= 512 ? 1 : threads >= 256 ? 2 : 4);
-        const int64_t need = cdiv(rows, groups);
-        s.blocks = (int)(need < most ? need : most);
-        s.parts = s.blocks * groups;
-    } else {
-        s.blocks = s.parts = (int)(rows < 64 ? rows : 64);
+    if (!s.warps) {
+        s.parts = (int)(rows < 64 ? rows : 64);
+        return s;
     }
+    const int groups = s.warps == 1 ? kRowsPerBlock : 1;
+    const int64_t steps = cdiv(rows, groups);
+    int64_t blocks = steps / 4;
+    if (blocks < 2 * sms) blocks = 2 * sms;
+    const int64_t most = (int64_t)sms * grad_blocks_per_sm(s.warps);
+    if (blocks > most) blocks = most;
+    if (blocks > steps) blocks = steps;
+    s.parts = (int)blocks;
     return s;
 }
 
 template <bool BF>
 cudaError_t launch_backward(const LnParams& p, const GradShape& s, cudaStream_t stream) {
-#define TG_LAUNCH(WARPS, NV, VEC)                                                                     \
+#define TG_LAUNCH(WARPS, NV, VEC, WHOLE)                                                              \
     if (s.warps == WARPS && s.packs == NV) {                                                          \
-        ln_backward_kernel<BF, VEC, WARPS, NV>                                                        \
-            <<<s.blocks, WARPS == 1 ? 32 * kRowsPerBlock : 32 * WARPS, 0, stream>>>(p);               \
+        ln_backward_kernel<BF, VEC, WHOLE, WARPS, NV>                                                 \
+            <<<s.parts, row_threads(WARPS), 0, stream>>>(p);                                          \
         return cudaGetLastError();                                                                    \
     }
+#define TG_BR(WARPS, NV)                                                                              \
+    return launch_ring<ln_backward_ring_kernel<BF, WARPS, NV>>(p, WARPS, 2, grad_blocks_per_sm(WARPS), \
+                                                               s.parts, stream);
+#define TG_B2(WARPS, NV) TG_LAUNCH(WARPS, NV, 2, true)
+#define TG_B0(WARPS, NV) TG_LAUNCH(WARPS, NV, 2, false)
+    const int cols = p.cols;
     if (s.warps == 0) {
         ln_backward_wide_kernel<BF><<<(unsigned)p.rows, 1024, 0, stream>>>(p);
-        ln_backward_wide_columns_kernel<BF>
-            <<<dim3((unsigned)cdiv(p.cols, 256), s.blocks), 256, 0, stream>>>(p);
-        return cudaGetLastError();
+        const cudaError_t e = cudaGetLastError();
+        return e != cudaSuccess ? e
+                                : launch_chained(ln_backward_wide_columns_kernel<BF>,
+                                                 dim3((unsigned)cdiv(cols, 256), s.parts), 256, stream, p);
     }
     if (s.vec == 8) {
-        TG_LAUNCH(1, 1, 8) TG_LAUNCH(1, 2, 8) TG_LAUNCH(1, 4, 8) TG_LAUNCH(4, 2, 8)
-        TG_LAUNCH(4, 4, 8) TG_LAUNCH(8, 4, 8) TG_LAUNCH(16, 4, 8)
+        TG_LN_SHAPES_8(TG_BR)
     } else if (s.vec == 2) {
-        TG_LAUNCH(1, 4, 2) TG_LAUNCH(1, 8, 2) TG_LAUNCH(4, 8, 2) TG_LAUNCH(8, 8, 2)
-        TG_LAUNCH(16, 8, 2) TG_LAUNCH(32, 8, 2)
+        TG_LN_SHAPES_2(TG_B2)
     } else {
-        TG_LAUNCH(1, 4, 1) TG_LAUNCH(1, 8, 1) TG_LAUNCH(4, 8, 1) TG_LAUNCH(8, 8, 1)
-        TG_LAUNCH(16, 8, 1) TG_LAUNCH(32, 8, 1)
+        TG_LN_SHAPES_2(TG_B0)
     }
+#undef TG_BR
+#undef TG_B2
+#undef TG_B0
 #undef TG_LAUNCH
     return cudaErrorInvalidValue;
 }
@@ -479,8 +926,9 @@ extern "C" int tg_layernorm(int64_t rows, int64_t cols, const void* X, int64_t l
     if ((rc = current_device(&dev, &info))) return rc;
     load_driver_entry_points();  // the allocation-range query of check_pointer
     const void* ptrs[6] = {Y, mean, rstd, X, weight, bias};
+    PointerChecks check{dev};
     for (int i = 0; i < 6; ++i)
-        if ((rc = check_pointer(ptrs[i], spans[i], dev))) return rc;
+        if ((rc = check(ptrs[i], spans[i]))) return rc;
     LnParams p;
     std::memset(&p, 0, sizeof(p));
     p.rows = rows;
@@ -495,8 +943,10 @@ extern "C" int tg_layernorm(int64_t rows, int64_t cols, const void* X, int64_t l
     p.mean = mean;
     p.rstd = rstd;
     const int vec = pack_of(cols, {X, weight, bias, Y}, {ldx, ldy});
-    if ((dtype == TG_BF16 ? launch_forward<true>(p, vec, stream)
-                          : launch_forward<false>(p, vec, stream)) != cudaSuccess) {
+    p.timeout_cycles = watchdog_timeout();
+    p.status = info->status;
+    if ((dtype == TG_BF16 ? launch_forward<true>(p, vec, info->sms, stream)
+                          : launch_forward<false>(p, vec, info->sms, stream)) != cudaSuccess) {
         cudaGetLastError();
         return TG_ERR_CUDA;
     }
@@ -513,7 +963,7 @@ extern "C" int tg_layernorm_grad_workspace_size(int64_t rows, int64_t cols, tg_d
     DeviceInfo* info;
     if ((rc = current_device(&dev, &info))) return rc;
     int64_t parts = 0;
-    for (int vec : {8, 2, 1}) {
+    for (int vec : {8, 2}) {
         const GradShape s = grad_shape(rows, cols, vec, info->sms);
         if (s.parts > parts) parts = s.parts;
     }
@@ -561,11 +1011,12 @@ extern "C" int tg_layernorm_grad(int64_t rows, int64_t cols, const void* dY, int
         if (intersects(work, o)) return TG_ERR_OVERLAP;
     const void* outp[3] = {dX, dweight, dbias};
     const void* inp[5] = {dY, X, weight, mean, rstd};
+    PointerChecks check{dev};
     for (int i = 0; i < 3; ++i)
-        if ((rc = check_pointer(outp[i], outs[i], dev))) return rc;
+        if ((rc = check(outp[i], outs[i]))) return rc;
     for (int i = 0; i < 5; ++i)
-        if ((rc = check_pointer(inp[i], ins[i], dev))) return rc;
-    if ((rc = check_pointer(workspace, work, dev))) return rc;
+        if ((rc = check(inp[i], ins[i]))) return rc;
+    if ((rc = check(workspace, work))) return rc;
     LnParams p;
     std::memset(&p, 0, sizeof(p));
     p.rows = rows;
@@ -580,14 +1031,14 @@ extern "C" int tg_layernorm_grad(int64_t rows, int64_t cols, const void* dY, int
     p.mean = const_cast<float*>(mean);
     p.rstd = const_cast<float*>(rstd);
     p.part = static_cast<float*>(workspace);
+    p.timeout_cycles = watchdog_timeout();
+    p.status = info->status;
     cudaError_t e = dtype == TG_BF16 ? launch_backward<true>(p, s, stream)
                                      : launch_backward<false>(p, s, stream);
     if (e == cudaSuccess) {
         auto reduce = dtype == TG_BF16 ? ln_reduce_kernel<true> : ln_reduce_kernel<false>;
-        reduce<<<(unsigned)cdiv(cols, 32), 1024, 0, stream>>>(p.part, s.parts, p.cols,
-                                                              static_cast<uint16_t*>(dweight),
-                                                              static_cast<uint16_t*>(dbias));
-        e = cudaGetLastError();
+        e = launch_chained(reduce, dim3((unsigned)cdiv(cols, 32)), 1024, stream, p.part, s.parts, p.cols,
+                           static_cast<uint16_t*>(dweight), static_cast<uint16_t*>(dbias));
     }
     if (e != cudaSuccess) {
         cudaGetLastError();
