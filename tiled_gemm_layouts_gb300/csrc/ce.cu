@@ -9,6 +9,7 @@
 // infinity times G = 0 would put a NaN into dW.  Then, for each piece of the
 // vocabulary, CE_GRAD and CE_PRODUCTS; at the end dH's fp32 planes are
 // summed, scaled and scattered back to the tokens' rows.
+#include <algorithm>
 #include <climits>
 #include <cstring>
 
@@ -107,18 +108,21 @@ struct CeRows {
 };
 
 constexpr int kCompactThreads = 1024;
+// Up to this many tokens every block of the gather does the compaction for
+// itself (two passes over 12 bytes per token), which saves a launch.
+constexpr int kCompactEverywhere = 2048;
 
-// One block: the largest |dloss|, then a stable compaction in steps of 1024
-// tokens.  G is scaled by 2^shift / max|dloss|: with one dloss for all tokens
+// Stable compaction by one block: the largest |dloss|, then steps of 1024
+// tokens; returns the number of tokens that count and, to every thread, the
+// factors.  G is scaled by 2^shift / max|dloss|: with one dloss for all tokens
 // its factor is then a power of two, and rounding G to 16 bits rounds
 // (p - [hit]) itself instead of repeating one rounding of dloss in every row.
-__global__ void __launch_bounds__(kCompactThreads)
-ce_compact_kernel(const long long* __restrict__ target, const float* __restrict__ lse,
-                  const float* __restrict__ dloss, int T, long long V, float scale2, CeRows r) {
+// `keep(row, token, target)` is called for each token that counts.
+template <class Keep, class Drop>
+__device__ __forceinline__ int compact(const long long* __restrict__ target, const float* __restrict__ dloss,
+                                       int T, long long V, float& ref, Keep keep, Drop drop) {
     __shared__ float wmax[32];
     __shared__ int wsum[33];
-    allow_next_kernel();
-    wait_for_previous_kernel();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     float top = 0.0f;
     for (int t = threadIdx.x; t < T; t += kCompactThreads) {
@@ -132,7 +136,7 @@ ce_compact_kernel(const long long* __restrict__ target, const float* __restrict_
     top = wmax[lane];
 #pragma unroll
     for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-    const float ref = top > 0.0f && top < INFINITY ? top : 1.0f;
+    ref = top > 0.0f && top < INFINITY ? top : 1.0f;
     int total = 0;
     for (int base = 0; base < T; base += kCompactThreads) {
         const int t = base + threadIdx.x;
@@ -152,31 +156,76 @@ ce_compact_kernel(const long long* __restrict__ target, const float* __restrict_
             if (lane == 31) wsum[32] = x;
         }
         __syncthreads();
-        if (t < T) {
-            const int j = total + wsum[warp] + __popc(votes & ((1u << lane) - 1));
-            r.place[t] = counts ? j : -1;
-            if (counts) {
-                r.token[j] = t;
-                r.target[j] = (int)y;
-                r.scale[j] = make_float2(lse[t] * kLog2e, dloss[t] / ref * scale2);
-            }
-        }
+        if (counts)
+            keep(total + wsum[warp] + __popc(votes & ((1u << lane) - 1)), t, (int)y);
+        else if (t < T)
+            drop(t);
         total += wsum[32];
         __syncthreads();
     }
+    return total;
+}
+
+// Writes a compaction down.
+struct CeKeep {
+    CeRows r;
+    const float *lse, *dloss;
+    float scale2;
+    const float* ref;
+    __device__ __forceinline__ void operator()(int j, int t, int y) const {
+        r.place[t] = j;
+        r.token[j] = t;
+        r.target[j] = y;
+        r.scale[j] = make_float2(lse[t] * kLog2e, dloss[t] / *ref * scale2);
+    }
+};
+
+__global__ void __launch_bounds__(kCompactThreads)
+ce_compact_kernel(const long long* __restrict__ target, const float* __restrict__ lse,
+                  const float* __restrict__ dloss, int T, long long V, float scale2, CeRows r) {
+    allow_next_kernel();
+    float ref;
+    const CeKeep keep{r, lse, dloss, scale2, &ref};
+    const int live = compact(target, dloss, T, V, ref, keep, [&](int t) { r.place[t] = -1; });
     if (threadIdx.x == 0) {
-        *r.live = total;
+        *r.live = live;
         *r.alpha = ref / scale2;
     }
 }
 
 // Dense rows of H for the tokens that count: out[j] = H[token[j]], columns
 // [D, ldo) and the rows up to the next multiple of 256 filled with zeros.
-__global__ void ce_gather_kernel(const uint16_t* __restrict__ H, long long ldh, int D, CeRows r,
-                                 uint16_t* __restrict__ out, int ldo, long long max_rows) {
+// HERE: the blocks compact for themselves, and the first one writes it down.
+template <bool HERE>
+__global__ void __launch_bounds__(kCompactThreads)
+ce_gather_kernel(const uint16_t* __restrict__ H, long long ldh, int D, CeRows r,
+                 uint16_t* __restrict__ out, int ldo, long long max_rows,
+                 const long long* __restrict__ target, const float* __restrict__ lse,
+                 const float* __restrict__ dloss, int T, long long V, float scale2) {
+    __shared__ int tokens[HERE ? kCompactEverywhere : 1];
     allow_next_kernel();
-    wait_for_previous_kernel();
-    const int live = *r.live;
+    int live;
+    if constexpr (HERE) {
+        float ref;
+        const bool first = blockIdx.x == 0;
+        const CeKeep keep{r, lse, dloss, scale2, &ref};
+        live = compact(
+            target, dloss, T, V, ref,
+            [&](int j, int t, int y) {
+                tokens[j] = t;
+                if (first) keep(j, t, y);
+            },
+            [&](int t) {
+                if (first) r.place[t] = -1;
+            });
+        if (first && threadIdx.x == 0) {
+            *r.live = live;
+            *r.alpha = ref / scale2;
+        }
+    } else {
+        wait_for_previous_kernel();
+        live = *r.live;
+    }
     const long long rows = min(max_rows, (long long)max(256, (live + 255) / 256 * 256));
     const int vecs = ldo / 8;
     for (long long i = blockIdx.x * (long long)blockDim.x + threadIdx.x; i < rows * vecs;
@@ -185,7 +234,8 @@ __global__ void ce_gather_kernel(const uint16_t* __restrict__ H, long long ldh, 
         const int c = (int)(i - j * vecs) * 8;
         uint4 v = make_uint4(0, 0, 0, 0);
         if (j < live && c < D) {
-            const uint16_t* s = H + (long long)r.token[j] * ldh + c;
+            const long long t = HERE ? tokens[j] : r.token[j];
+            const uint16_t* s = H + t * ldh + c;
             if (c + 8 <= D && (reinterpret_cast<uintptr_t>(s) & 15u) == 0) {
                 v = *reinterpret_cast<const uint4*>(s);
             } else {
@@ -277,7 +327,7 @@ FwdPlan forward_plan(int64_t T, int64_t V, int64_t D, const void* H, int64_t ldh
     f.tile = logits_tile(T);
     f.tiles_n = cdiv(V, f.tile.bn);
     Cursor c;
-    f.part = c.take((u128)T * f.tiles_n * sizeof(float2));
+    f.part = c.take((u128)T * f.tiles_n * 2 * sizeof(float2));
     f.hit = c.take((u128)T * sizeof(float));
     f.h = c.take(f.copy_h ? (u128)T * up(D, 8) * 2 : 0);
     f.w = c.take(f.copy_w ? (u128)V * up(D, 8) * 2 : 0);
@@ -322,7 +372,9 @@ BwdPlan backward_plan(int64_t T, int64_t V, int64_t D, const void* W, int64_t ld
     const int64_t cols = V < b.piece ? V : b.piece, kb = cdiv(cols, 64), workers = sms / 2;
     const int64_t n = cdiv(T, 256) * cdiv(D, b.products.bn);
     const int64_t n_dw = cdiv(cols, 256) * cdiv(D, b.products.bn);
-    const int64_t share = (n * kb + n_dw * cdiv(T, 64)) / workers + 1;
+    const int64_t share = (n * (kb > kCeTileBlocks ? kb : kCeTileBlocks) +
+                           n_dw * (cdiv(T, 64) > kCeTileBlocks ? cdiv(T, 64) : kCeTileBlocks)) /
+                              workers + 1;
     int64_t splits = cdiv(kb, share);
     if (splits > kb / 8) splits = kb / 8;
     if (splits < 1) splits = 1;
@@ -490,7 +542,7 @@ extern "C" int tg_linear_ce(int64_t T, int64_t V, int64_t D, const void* H, int6
         const bool few = T <= info->sms;
         ok = launch_chained(few ? ce_combine_kernel<8> : ce_combine_kernel<1>,
                             dim3((unsigned)(few ? T : cdiv(T, 8))), 256, stream, p.part, p.hit, p.target,
-                            (int)T, (long long)V, (int)f.tiles_n, loss, lse) == cudaSuccess;
+                            (int)T, (long long)V, (int)f.tiles_n * 2, loss, lse) == cudaSuccess;
     }
     if (!ok) {
         cudaGetLastError();
@@ -571,13 +623,22 @@ extern "C" int tg_linear_ce_grad(int64_t T, int64_t V, int64_t D, const void* H,
     uint16_t* h = reinterpret_cast<uint16_t*>(ws + b.h);
     uint16_t* g = reinterpret_cast<uint16_t*>(ws + b.g);
     float* planes = reinterpret_cast<float*>(ws + b.planes);
-    ce_compact_kernel<<<1, kCompactThreads, 0, stream>>>(reinterpret_cast<const long long*>(target), lse,
-                                                         dloss, (int)T, V, dt == TG_F16 ? 1024.0f : 1.0f,
-                                                         rows);
-    ok = ok && cudaGetLastError() == cudaSuccess &&
-         launch_chained(ce_gather_kernel, dim3(blocks_for(b.rows * (b.ldh / 8), sms)), 256, stream,
-                        static_cast<const uint16_t*>(H), (long long)ldh, (int)D, rows, h, (int)b.ldh,
-                        (long long)b.rows) == cudaSuccess;
+    const float scale2 = dt == TG_F16 ? 1024.0f : 1.0f;
+    const long long* tgt = reinterpret_cast<const long long*>(target);
+    const bool here = T <= kCompactEverywhere;
+    const unsigned gather_blocks = (unsigned)std::min<int64_t>(cdiv(b.rows * (b.ldh / 8), kCompactThreads), sms * 2);
+    if (here) {
+        ce_gather_kernel<true><<<gather_blocks, kCompactThreads, 0, stream>>>(
+            static_cast<const uint16_t*>(H), ldh, (int)D, rows, h, (int)b.ldh, b.rows, tgt, lse, dloss,
+            (int)T, V, scale2);
+        ok = ok && cudaGetLastError() == cudaSuccess;
+    } else {
+        ce_compact_kernel<<<1, kCompactThreads, 0, stream>>>(tgt, lse, dloss, (int)T, V, scale2, rows);
+        ok = ok && cudaGetLastError() == cudaSuccess &&
+             launch_chained(ce_gather_kernel<false>, dim3(gather_blocks), kCompactThreads, stream,
+                            static_cast<const uint16_t*>(H), (long long)ldh, (int)D, rows, h, (int)b.ldh,
+                            (long long)b.rows, tgt, lse, dloss, (int)T, (long long)V, scale2) == cudaSuccess;
+    }
 
     for (int64_t i = 0; ok && i < b.pieces; ++i) {
         const int64_t v0 = i * b.piece, cols = V - v0 < b.piece ? V - v0 : b.piece;

@@ -8,8 +8,8 @@
 //
 // The forward pass is one GEMM whose epilogue keeps a running maximum and sum
 // of powers of two per accumulator row: in TMEM a tile's row is one lane, so
-// the thread that reads it reduces its 256 columns without talking to any
-// other, and only 8 bytes per row and tile leave the SM.  The backward pass
+// the thread that reads it reduces its 128 columns without talking to any
+// other, and only 8 bytes per row and half tile leave the SM.  The backward pass
 // recomputes the logits piece by piece of the vocabulary (2TVD operations,
 // where keeping them would take 2TV or 4TV bytes), writes each piece of G in
 // 16 bits, and multiplies it twice.  G is scaled so that its largest possible
@@ -18,7 +18,7 @@
 //
 // The main loop is that of the GEMM kernel: two TMA producer warps fill a
 // ring of 128B-swizzled stages, one thread issues tcgen05.mma into a
-// double-buffered fp32 accumulator in TMEM, four epilogue warps drain it
+// double-buffered fp32 accumulator in TMEM, eight epilogue warps drain it
 // while the next tile's products run; tiles of 256 x BN on a CTA pair, or
 // 128 x BN on one CTA for few tokens.  Every wait is bounded; on a timeout
 // the status word is set, copies and MMAs in flight are drained, TMEM is
@@ -36,7 +36,16 @@
 
 namespace tg {
 
-constexpr int kCeThreads = 32 * (3 + kEpiWarps);  // producers (warps 0 and 6), MMA (1), epilogue (2..5)
+// Two epilogue warps per TMEM lane quadrant, each with half of a tile's
+// columns: one warp's chain of maximum, exponentials and sum leaves its
+// scheduler idle half of the time, which shows where a tile's contraction is
+// short (D below about 500).
+constexpr int kCeEpiWarps = 8;
+constexpr int kCeThreads = 32 * (3 + kCeEpiWarps);  // producers (warps 0 and 10), MMA (1), epilogue (2..9)
+constexpr int kCeBufs = 2;                          // staging buffers of 2 KB per epilogue warp
+// Time of an output tile's epilogue in K-blocks: 128 KB of stores at an SM
+// pair's share of the memory bandwidth.
+constexpr int kCeTileBlocks = 6;
 constexpr int kCeBlocksPerStage = 2;              // K-blocks per barrier transaction
 
 // 2^x; results below the normal range become 0 (for sums of at least 1).
@@ -130,7 +139,8 @@ struct CeItems {
             const long long all = (long long)tiles_m[1] * tiles_n[1];
             const int busy = (int)(end[0] % workers);  // workers with one more item of dH
             stride = workers - busy;
-            const long long rounds = busy && all ? num_kb[0] / num_kb[1] : 0;
+            const long long rounds =
+                busy && all ? max(num_kb[0], kCeTileBlocks) / max(num_kb[1], kCeTileBlocks) : 0;
             tail = min(all, rounds * stride);
             at[1] = worker >= busy ? worker - busy : tail;
             tail_at = tail + worker;
@@ -270,7 +280,7 @@ __global__ void __launch_bounds__(kCeThreads, 1) ce_kernel(const __grid_constant
         }
         for (int b = 0; b < 2; ++b) {
             mbar_init(smem_addr(&tfull[b]), 1);
-            mbar_init(smem_addr(&tempty[b]), (PAIR ? 2 : 1) * kEpiWarps);
+            mbar_init(smem_addr(&tempty[b]), (PAIR ? 2 : 1) * kCeEpiWarps);
         }
         mbar_init(smem_addr(drain), 1);
         *abort_flag = 0;
@@ -386,7 +396,7 @@ __global__ void __launch_bounds__(kCeThreads, 1) ce_kernel(const __grid_constant
 
     if (warp == 0 && lane == 0) {
         run_producer(RoleTag<1>{});
-    } else if (warp == 2 + kEpiWarps && lane == 0) {
+    } else if (warp == 2 + kCeEpiWarps && lane == 0) {
         run_producer(RoleTag<2>{});
     } else if (warp == 1 && lane == 0 && leader) {
         // ---------------------------------------------------- MMA issuer
@@ -447,17 +457,16 @@ __global__ void __launch_bounds__(kCeThreads, 1) ce_kernel(const __grid_constant
         else
             mma_commit(smem_addr(drain));
         drain_bar(smem_addr(drain), 0, w);
-    } else if (warp >= 2 && warp < 2 + kEpiWarps) {
+    } else if (warp >= 2 && warp < 2 + kCeEpiWarps) {
         // ------------------------------------------------------ epilogue
-        // Warp q of a quadrant reads TMEM lanes 32q..32q+31; thread = row.
-        constexpr int kChunks = BN / 32;
+        // A warp of quadrant q reads TMEM lanes 32q..32q+31; thread = row.
+        constexpr int kChunks = BN / 64;  // of 32 columns, per warp
         static_assert(kChunks % 2 == 0, "chunks are taken in pairs");
-        const int q = warp & 3;
-        uint8_t* stage = staging + (warp - 2) * kStageBufs * 2048;
+        const int q = warp & 3, half = (warp - 2) / 4;
+        uint8_t* stage = staging + (warp - 2) * kCeBufs * 2048;
         uint32_t stored = 0;  // output chunks stored so far
         float alpha = 1.0f;
         if constexpr (MODE == CE_PRODUCTS) alpha = __ldg(p.alpha);
-        int last_side = 0;
         int live = 0;
         if constexpr (MODE == CE_GRAD) live = p.live ? __ldg(p.live) : p.rows;
         CeItems<MODE> items(p, worker, workers, TS::kBM);
@@ -467,14 +476,8 @@ __global__ void __launch_bounds__(kCeThreads, 1) ce_kernel(const __grid_constant
             const CeSide& sd = p.side[BOTH ? it.side : 0];
             const int row0 = it.tm * TS::kBM + (int)rank * 128 + q * 32;  // this warp's first row
             const int row = row0 + lane;
-            const int n0 = it.tn * BN;
+            const int n0 = it.tn * BN + half * (BN / 2);  // and first column
             const bool planes = BOTH && it.side == 0;  // fp32 output
-            if (BOTH && it.side != last_side) {
-                // the two sides cut the staging area differently
-                if (lane == 0) bulk_wait_group_read<0>();
-                last_side = it.side;
-                stored = 0;
-            }
             // what the row's epilogue needs, loaded while the products run
             CeRowStats st{-INFINITY, 0.0f, 0.0f, -1, p.to_log2};
             float2 rs = make_float2(0.0f, 0.0f);
@@ -494,7 +497,8 @@ __global__ void __launch_bounds__(kCeThreads, 1) ce_kernel(const __grid_constant
             const bool got = wait_bar(smem_addr(&tfull[buf]), (i >> 1) & 1, w, DEV_TIMEOUT_EPILOGUE + 4);
             if (!__all_sync(0xffffffffu, got)) break;
             tc_fence_after();
-            const uint32_t t_row = tmem_base + ((uint32_t)(q * 32) << 16) + buf * BN;
+            const uint32_t t_row =
+                tmem_base + ((uint32_t)(q * 32) << 16) + buf * BN + half * (BN / 2);
 
             auto finish = [&](uint32_t (&v)[32], int c) {
                 const int c0 = n0 + c * 32;
@@ -530,28 +534,35 @@ __global__ void __launch_bounds__(kCeThreads, 1) ce_kernel(const __grid_constant
                     }
                     // stage the 32 x 32 chunk in swizzled shared memory and store
                     // it with one tensor copy, clipped by the map
+                    // (fp32: two of 16 columns, so that both kinds fill a buffer)
                     if (planes) {
-                        uint8_t* b = stage + (stored & 1) * 4096;
-                        if (stored >= 2 && lane == 0) bulk_wait_group_read<1>();
-                        __syncwarp();
 #pragma unroll
-                        for (int k = 0; k < 8; ++k)
-                            *reinterpret_cast<float4*>(b + lane * 128 + ((k ^ (lane & 7)) << 4)) =
-                                make_float4(y[4 * k], y[4 * k + 1], y[4 * k + 2], y[4 * k + 3]);
-                        fence_proxy_async_shared();
-                        __syncwarp();
-                        if (lane == 0) {
-                            if (row0 < sd.out_rows && c0 < sd.out_cols) {
-                                if (p.accumulate)
-                                    tma_add_3d(&sd.map_c, smem_addr(b), c0, row0, it.split);
-                                else
-                                    tma_store_3d(&sd.map_c, smem_addr(b), c0, row0, it.split);
+                        for (int h = 0; h < 2; ++h) {
+                            uint8_t* b = stage + (stored % kCeBufs) * 2048;
+                            if (stored >= kCeBufs && lane == 0) bulk_wait_group_read<kCeBufs - 1>();
+                            __syncwarp();
+#pragma unroll
+                            for (int k = 0; k < 4; ++k)
+                                *reinterpret_cast<float4*>(b + lane * 64 + ((k ^ ((lane >> 1) & 3)) << 4)) =
+                                    make_float4(y[16 * h + 4 * k], y[16 * h + 4 * k + 1],
+                                                y[16 * h + 4 * k + 2], y[16 * h + 4 * k + 3]);
+                            fence_proxy_async_shared();
+                            __syncwarp();
+                            if (lane == 0) {
+                                const int c1 = c0 + 16 * h;
+                                if (row0 < sd.out_rows && c1 < sd.out_cols) {
+                                    if (p.accumulate)
+                                        tma_add_3d(&sd.map_c, smem_addr(b), c1, row0, it.split);
+                                    else
+                                        tma_store_3d(&sd.map_c, smem_addr(b), c1, row0, it.split);
+                                }
+                                bulk_commit_group();
                             }
-                            bulk_commit_group();
+                            ++stored;
                         }
                     } else {
-                        uint8_t* b = stage + (stored % kStageBufs) * 2048;
-                        if (stored >= kStageBufs && lane == 0) bulk_wait_group_read<kStageBufs - 1>();
+                        uint8_t* b = stage + (stored % kCeBufs) * 2048;
+                        if (stored >= kCeBufs && lane == 0) bulk_wait_group_read<kCeBufs - 1>();
                         __syncwarp();
                         if (p.bf16)
                             stage_row<true>(b, lane, y);
@@ -582,8 +593,8 @@ __global__ void __launch_bounds__(kCeThreads, 1) ce_kernel(const __grid_constant
                                     o[(long long)r * p.ldo] = *reinterpret_cast<const uint16_t*>(
                                         b + r * 64 + (((lane >> 3) ^ ((r >> 1) & 3)) << 4) + (lane & 7) * 2);
                         }
+                        ++stored;
                     }
-                    ++stored;
                 }
             };
             auto release = [&]() {  // every column of this buffer is in registers
@@ -617,9 +628,9 @@ __global__ void __launch_bounds__(kCeThreads, 1) ce_kernel(const __grid_constant
             }
             if constexpr (MODE == CE_LSE) {
                 if (row < p.rows) {
-                    p.part[(long long)row * sd.tiles_n + it.tn] = make_float2(st.m, st.s);
+                    p.part[((long long)row * sd.tiles_n + it.tn) * 2 + half] = make_float2(st.m, st.s);
                     const int t = st.target - n0;
-                    if (t >= 0 && t < BN) p.hit[row] = st.hit;
+                    if (t >= 0 && t < BN / 2) p.hit[row] = st.hit;
                 }
             }
         }

@@ -42,7 +42,7 @@ struct alignas(128) CeParams {
     int cols;                // columns of the logits in this launch (a piece of V)
     long long col0;          // first of them in the vocabulary
     const long long* target; // CE_LSE: [T] as the caller gave it
-    float2* part;            // CE_LSE: [T][tiles_n] (max in log2 units, sum of powers of two)
+    float2* part;            // CE_LSE: [T][tiles_n][2 halves] (max in log2 units, sum of powers of two)
     float* hit;              // CE_LSE: [T] logit of the target, in log2 units
     const int* row_target;   // CE_GRAD: per compacted row, its target
     const float2* row_scale; // CE_GRAD: per compacted row, lse in log2 units and factor of G

@@ -184,7 +184,7 @@ constexpr int kRowsPerBlock = 4;  // rows of a block whose rows take one warp ea
 constexpr int row_threads(int warps) { return 32 * (warps == 1 ? kRowsPerBlock : warps); }
 
 template <bool BF, int VEC, bool WHOLE, int WARPS, int NV, bool WIDE>
-__global__ void __launch_bounds__(row_threads(WARPS))
+__global__ void __launch_bounds__(row_threads(WARPS), WARPS == 16 ? 2 : 1)
 ln_forward_kernel(const LnParams p) {
     __shared__ float buf[2][WARPS == 1 ? 1 : WARPS];
     const int tid = WARPS == 1 ? threadIdx.x & 31 : threadIdx.x;
@@ -694,38 +694,32 @@ __global__ void __launch_bounds__(256) ln_backward_wide_columns_kernel(const LnP
     part[p.cols + c] = db;
 }
 
-// Adds the partial rows: 32 columns per block, 32 threads along the rows of
-// each, then across those in a fixed order.
-template <bool BF>
-__global__ void __launch_bounds__(1024)
+// Adds the partial rows in a fixed order: 32 columns per block, Y threads
+// along the rows of each, then one over those.
+template <bool BF, int Y>
+__global__ void __launch_bounds__(32 * Y)
 ln_reduce_kernel(const float* __restrict__ part, int parts, int cols, uint16_t* __restrict__ dw,
                  uint16_t* __restrict__ db) {
-    __shared__ float s[2][32][33];
+    __shared__ float s[2][Y][32];
     wait_for_previous_kernel();
     const int lane = threadIdx.x & 31, y = threadIdx.x >> 5;
     const int c = blockIdx.x * 32 + lane;
     float a = 0.0f, b = 0.0f;
     if (c < cols)
 #pragma unroll 4
-        for (int r = y; r < parts; r += 32) {
+        for (int r = y; r < parts; r += Y) {
             a += part[(long long)r * 2 * cols + c];
             b += part[((long long)r * 2 + 1) * cols + c];
         }
     s[0][y][lane] = a;
     s[1][y][lane] = b;
     __syncthreads();
-    a = s[0][lane][y];
-    b = s[1][lane][y];
+    if (y > 1 || c >= cols) return;
+    float sum = 0.0f;
 #pragma unroll
-    for (int o = 16; o; o >>= 1) {
-        a += __shfl_xor_sync(0xffffffffu, a, o);
-        b += __shfl_xor_sync(0xffffffffu, b, o);
-    }
-    const int out = blockIdx.x * 32 + y;
-    if (lane == 0 && out < cols) {
-        dw[out] = narrow<BF>(a);
-        if (db) db[out] = narrow<BF>(b);
-    }
+    for (int k = 0; k < Y; ++k) sum += s[y][k][lane];
+    uint16_t* out = y == 0 ? dw : db;
+    if (out) out[c] = narrow<BF>(sum);
 }
 
 // Widest aligned pack that every row, weight and output allows: whole packs
@@ -756,8 +750,7 @@ int pack_of(int64_t cols, std::initializer_list<const void*> ptrs, std::initiali
     if (cols <= 1024) F(2, 8)    \
     if (cols <= 2048) F(4, 8)    \
     if (cols <= 4096) F(8, 8)    \
-    if (cols <= 8192) F(16, 8)   \
-    if (cols <= 16384) F(32, 8)
+    if (cols <= 8192) F(16, 8)
 
 // Launches a ring kernel: `operands` rows per stage, `per_sm` blocks on an SM.
 template <auto Kern>
@@ -810,9 +803,11 @@ cudaError_t launch_forward(const LnParams& p, int vec, int sms, cudaStream_t str
     }
     if (vec == 2) {
         TG_LN_SHAPES_2(TG_F2)
+        if (cols <= 16384) TG_F2(16, 16)  // two rows per SM at a time
         TG_LAUNCH(32, 8, 2, true, true)
     }
     TG_LN_SHAPES_2(TG_F0)
+    if (cols <= 16384) TG_F0(16, 16)
     TG_LAUNCH(32, 8, 2, false, true)
 #undef TG_FR
 #undef TG_F2
@@ -841,6 +836,7 @@ GradShape grad_shape(int64_t rows, int64_t cols, int vec, int sms) {
         TG_LN_SHAPES_8(TG_SET)
     } else {
         TG_LN_SHAPES_2(TG_SET)
+        if (cols <= 16384) TG_SET(32, 8)
     }
 #undef TG_SET
     if (!s.warps) {
@@ -883,8 +879,10 @@ cudaError_t launch_backward(const LnParams& p, const GradShape& s, cudaStream_t 
         TG_LN_SHAPES_8(TG_BR)
     } else if (s.vec == 2) {
         TG_LN_SHAPES_2(TG_B2)
+        TG_B2(32, 8)
     } else {
         TG_LN_SHAPES_2(TG_B0)
+        TG_B0(32, 8)
     }
 #undef TG_BR
 #undef TG_B2
@@ -1036,9 +1034,11 @@ extern "C" int tg_layernorm_grad(int64_t rows, int64_t cols, const void* dY, int
     cudaError_t e = dtype == TG_BF16 ? launch_backward<true>(p, s, stream)
                                      : launch_backward<false>(p, s, stream);
     if (e == cudaSuccess) {
-        auto reduce = dtype == TG_BF16 ? ln_reduce_kernel<true> : ln_reduce_kernel<false>;
-        e = launch_chained(reduce, dim3((unsigned)cdiv(cols, 32)), 1024, stream, p.part, s.parts, p.cols,
-                           static_cast<uint16_t*>(dweight), static_cast<uint16_t*>(dbias));
+        const bool bf = dtype == TG_BF16, few = s.parts <= 16;
+        auto reduce = few ? (bf ? ln_reduce_kernel<true, 4> : ln_reduce_kernel<false, 4>)
+                          : (bf ? ln_reduce_kernel<true, 32> : ln_reduce_kernel<false, 32>);
+        e = launch_chained(reduce, dim3((unsigned)cdiv(cols, 32)), few ? 128 : 1024, stream, p.part, s.parts,
+                           p.cols, static_cast<uint16_t*>(dweight), static_cast<uint16_t*>(dbias));
     }
     if (e != cudaSuccess) {
         cudaGetLastError();
