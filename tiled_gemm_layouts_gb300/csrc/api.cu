@@ -314,10 +314,10 @@ bool encode_f32_planes(CUtensorMap* map, const void* base, uint64_t cols, uint64
                        uint64_t planes, int64_t ld) {
     const cuuint64_t dims[3] = {cols, rows, planes};
     const cuuint64_t strides[2] = {(cuuint64_t)ld * 4, (cuuint64_t)ld * 4 * rows};
-    const cuuint32_t box[3] = {16, 32, 1};
+    const cuuint32_t box[3] = {32, 32, 1};
     const cuuint32_t estr[3] = {1, 1, 1};
     return g_encode(map, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 3, const_cast<void*>(base), dims, strides,
-                    box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_64B,
+                    box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
                     CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                     CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }

@@ -307,10 +307,24 @@ struct Cursor {
     }
 };
 
-// Tile of the logits' products: CTA pairs from 129 tokens on.  For fewer, a
-// pair's second half would multiply rows that do not exist, and reading W
-// bounds the time: 128-column tiles of single CTAs deal V out more evenly.
-CeTile logits_tile(int64_t T) { return T > 128 ? CeTile{256, 1} : CeTile{128, 0}; }
+// Tile of the logits' products.  CTA pairs' 256 x 256 tiles feed the tensor
+// cores best.  For up to 128 tokens a pair's second half would multiply rows
+// that do not exist, and reading W bounds the time; and where such tiles are
+// fewer than the pairs, 128 x 128 tiles of single CTAs keep more SMs busy.
+constexpr int kPairs = 76;  // of a GB300's 152 SMs (only the choice of a tile depends on it)
+
+CeTile logits_tile(int64_t T, int64_t V) {
+    return T > 128 && cdiv(T, 256) * cdiv(V, 256) >= kPairs ? CeTile{256, 1} : CeTile{128, 0};
+}
+
+// Tile of the gradients' products: the same rule on the tiles of dH and dW
+// together (128 x 512 x 4096: 25.2 us with pairs, 23.1 with single CTAs; 64 x
+// 1024 x 65536: 110 and 112).  A narrow D does not fill 256 columns.
+CeTile products_tile(int64_t T, int64_t cols, int64_t D) {
+    const int bn = D > 128 ? 256 : 128;
+    const int64_t tiles = (cdiv(T, 256) + cdiv(cols, 256)) * cdiv(D, bn);
+    return tiles >= kPairs ? CeTile{bn, 1} : CeTile{128, 0};
+}
 
 struct FwdPlan {
     bool copy_h, copy_w;
@@ -324,7 +338,7 @@ FwdPlan forward_plan(int64_t T, int64_t V, int64_t D, const void* H, int64_t ldh
     FwdPlan f;
     f.copy_h = !tma_rows(H, ldh);
     f.copy_w = !tma_rows(W, ldw);
-    f.tile = logits_tile(T);
+    f.tile = logits_tile(T, V);
     f.tiles_n = cdiv(V, f.tile.bn);
     Cursor c;
     f.part = c.take((u128)T * f.tiles_n * 2 * sizeof(float2));
@@ -364,17 +378,17 @@ BwdPlan backward_plan(int64_t T, int64_t V, int64_t D, const void* W, int64_t ld
     b.piece = cdiv(tiles_v, b.pieces) * 256;
     b.pieces = cdiv(V, b.piece);
     b.ldp = up(D, 8);
-    b.grad = logits_tile(T);
-    b.products = CeTile{D > 128 ? 256 : 128, 1};
+    b.grad = logits_tile(T, V < b.piece ? V : b.piece);
     // A tile of dH contracts over the whole piece.  Where that is longer than
     // an equal share of all the products, split it into fp32 planes that the
     // last kernel adds, each at least 8 K-blocks deep.
-    const int64_t cols = V < b.piece ? V : b.piece, kb = cdiv(cols, 64), workers = sms / 2;
-    const int64_t n = cdiv(T, 256) * cdiv(D, b.products.bn);
-    const int64_t n_dw = cdiv(cols, 256) * cdiv(D, b.products.bn);
-    const int64_t share = (n * (kb > kCeTileBlocks ? kb : kCeTileBlocks) +
-                           n_dw * (cdiv(T, 64) > kCeTileBlocks ? cdiv(T, 64) : kCeTileBlocks)) /
-                              workers + 1;
+    const int64_t cols = V < b.piece ? V : b.piece, kb = cdiv(cols, 64);
+    b.products = products_tile(T, cols, D);
+    const int64_t workers = b.products.pair ? sms / 2 : sms, bm = b.products.rows();
+    const int64_t n = cdiv(T, bm) * cdiv(D, b.products.bn);
+    const int64_t n_dw = cdiv(cols, bm) * cdiv(D, b.products.bn);
+    const int64_t share = (n * std::max<int64_t>(kb, kCeTileBlocks) +
+                           n_dw * std::max<int64_t>(cdiv(T, 64), kCeTileBlocks)) / workers + 1;
     int64_t splits = cdiv(kb, share);
     if (splits > kb / 8) splits = kb / 8;
     if (splits < 1) splits = 1;
@@ -422,7 +436,6 @@ void common_params(CeParams* p, int dtype, const DeviceInfo* info) {
     std::memset(p, 0, sizeof(*p));
     p->bf16 = dtype == TG_BF16;
     p->splits = 1;
-    p->p_bytes = 128 * 128;
     p->timeout_cycles = watchdog_timeout();
     p->status = info->status;
 }
@@ -443,7 +456,7 @@ bool logits_side(CeParams* p, int dtype, CeTile tile, int64_t T, const void* H, 
     // of the stage keeps old bytes, which reach only accumulator rows that
     // nobody reads.)
     const int64_t box = h_rows >= 128 ? 128 : up(h_rows, 8);
-    p->p_bytes = (uint32_t)box * 128;
+    s.p_bytes = (uint32_t)box * 128;
     int unused;
     if (!k_major(&s.map_p, box == 128 ? &s.map_p2 : nullptr, box == 128 ? &s.p_2k : &unused, dtype,
                  H, h_rows, h_cols, ldh, (int)box) ||
@@ -451,10 +464,10 @@ bool logits_side(CeParams* p, int dtype, CeTile tile, int64_t T, const void* H, 
                  tile.pair ? tile.bn / 2 : tile.bn))
         return false;
     s.num_kb = (int)cdiv(D, 64);
-    s.tiles_m = (int)cdiv(T, tile.pair ? 256 : 128);
+    s.tiles_m = (int)cdiv(T, tile.rows());
     s.tiles_n = (int)cdiv(V, tile.bn);
     s.group_m = s.tiles_m < 16 ? s.tiles_m : 16;
-    s.idesc = make_idesc(dtype, false, false, tile.bn, tile.pair ? 256 : 128);
+    s.idesc = make_idesc(dtype, false, false, tile.bn, tile.rows());
     // Each tcgen05.mma adds 16 products to the fp32 accumulator and truncates
     // the sum: for sums of products of either sign a logit comes out smaller
     // by a quarter of 2^-24 per addition, measured at D = 64 to 8192 in both
@@ -504,15 +517,15 @@ extern "C" int tg_linear_ce(int64_t T, int64_t V, int64_t D, const void* H, int6
         return TG_ERR_ALIGN;
     const FwdPlan f = forward_plan(T, V, D, H, ldh, W, ldw);
     if (workspace_bytes < f.bytes) return TG_ERR_BUFFER;
-    const Span spans[6] = {span_bytes(loss, (u128)T * 4), span_bytes(lse, (u128)T * 4),
-                           span_bytes(workspace, f.bytes), span_of(H, T, D, ldh),
+    const Span spans[6] = {span_bytes(workspace, f.bytes), span_bytes(loss, (u128)T * 4),
+                           span_bytes(lse, (u128)T * 4), span_of(H, T, D, ldh),
                            span_of(W, V, D, ldw), span_bytes(target, (u128)T * 8)};
     if ((rc = check_disjoint(spans, 3))) return rc;
     int dev;
     DeviceInfo* info;
     if ((rc = current_device(&dev, &info))) return rc;
     if (!load_driver_entry_points()) return TG_ERR_CUDA;
-    const void* ptrs[6] = {loss, lse, workspace, H, W, target};
+    const void* ptrs[6] = {workspace, loss, lse, H, W, target};
     PointerChecks check{dev};
     for (int i = 0; i < 6; ++i)
         if ((rc = check(ptrs[i], spans[i]))) return rc;
@@ -560,7 +573,7 @@ extern "C" int tg_linear_ce_grad_workspace_size(int64_t T, int64_t V, int64_t D,
     if (!bytes || (!dH && !dW)) return TG_ERR_INVALID_ARG;
     if (ldh < D || ldw < D || ldh > kMaxLd || ldw > kMaxLd) return TG_ERR_STRIDE;
     if ((dH && (lddh < D || lddh > kMaxLd)) || (dW && (lddw < D || lddw > kMaxLd))) return TG_ERR_STRIDE;
-    (void)H;
+    (void)H;  // copied in any case
     int dev;
     DeviceInfo* info;
     if ((rc = current_device(&dev, &info))) return rc;
@@ -640,6 +653,7 @@ extern "C" int tg_linear_ce_grad(int64_t T, int64_t V, int64_t D, const void* H,
                             (long long)b.rows, tgt, lse, dloss, (int)T, (long long)V, scale2) == cudaSuccess;
     }
 
+    const int bm = b.products.rows();
     for (int64_t i = 0; ok && i < b.pieces; ++i) {
         const int64_t v0 = i * b.piece, cols = V - v0 < b.piece ? V - v0 : b.piece;
         const uint16_t* w = static_cast<const uint16_t*>(W) + v0 * ldw;
@@ -647,8 +661,7 @@ extern "C" int tg_linear_ce_grad(int64_t T, int64_t V, int64_t D, const void* H,
         // a piece of G, scaled, from the gathered rows
         common_params(&p, dt, info);
         ok = logits_side(&p, dt, b.grad, T, h, b.rows, b.ldh, b.ldh, w, cols, D, ldw) &&
-             encode_2d(&p.side[0].map_c, dt, g, b.piece, b.rows, b.piece, 32, 32,
-                       CU_TENSOR_MAP_SWIZZLE_64B);
+             encode_2d(&p.side[0].map_c, dt, g, b.piece, b.rows, b.piece, 64, 32);
         p.live = rows.live;
         p.col0 = v0;
         p.row_target = rows.target;
@@ -665,14 +678,19 @@ extern "C" int tg_linear_ce_grad(int64_t T, int64_t V, int64_t D, const void* H,
             p.accumulate = i > 0;
             // a K-block past `cols` meets G's zero columns and W rows that the
             // map fills with zeros
-            ok = k_major(&s.map_p, &s.map_p2, &s.p_2k, dt, g, b.rows, (int64_t)p.all_kb * 64, b.piece, 128) &&
+            // one CTA's tiles need only the rows of G that there are
+            const int64_t box = b.products.pair || T >= 128 ? 128 : up(T, 8);
+            int unused;
+            s.p_bytes = (uint32_t)box * 128;
+            ok = k_major(&s.map_p, box == 128 ? &s.map_p2 : nullptr, box == 128 ? &s.p_2k : &unused, dt, g,
+                         b.rows, (int64_t)p.all_kb * 64, b.piece, (int)box) &&
                  mn_major_q(&s, dt, b.products, w, D, cols, ldw) &&
                  encode_f32_planes(&s.map_c, planes, b.ldp, T, b.splits, b.ldp);
             s.num_kb = (int)b.dh_kb;
-            s.tiles_m = (int)cdiv(T, 256);
+            s.tiles_m = (int)cdiv(T, bm);
             s.tiles_n = (int)cdiv(D, b.products.bn);
             s.group_m = s.tiles_m < 16 ? s.tiles_m : 16;
-            s.idesc = make_idesc(dt, false, true, b.products.bn, 256);
+            s.idesc = make_idesc(dt, false, true, b.products.bn, bm);
             s.out_rows = (int)T;
             s.out_cols = (int)D;
         }
@@ -684,13 +702,14 @@ extern "C" int tg_linear_ce_grad(int64_t T, int64_t V, int64_t D, const void* H,
             ok = encode_mn_atoms(&s.map_p, dt, g, b.piece, b.rows, b.piece, 2) &&
                  mn_major_q(&s, dt, b.products, h, b.ldh, b.rows, b.ldh) &&
                  encode_2d(&s.map_c, dt, tensor ? out : g, tensor ? p.n_tma : 8, cols,
-                           tensor ? lddw : b.piece, 32, 32, CU_TENSOR_MAP_SWIZZLE_64B);
+                           tensor ? lddw : b.piece, 64, 32);
             s.p_2k = encode_mn_atom_pairs(&s.map_p2, dt, g, b.piece, b.rows, b.piece, 2);
             s.num_kb = (int)(b.rows / 64);
-            s.tiles_m = (int)cdiv(cols, 256);
+            s.p_bytes = 128 * 128;
+            s.tiles_m = (int)cdiv(cols, bm);
             s.tiles_n = (int)cdiv(D, b.products.bn);
             s.group_m = s.tiles_m < 16 ? s.tiles_m : 16;
-            s.idesc = make_idesc(dt, true, true, b.products.bn, 256);
+            s.idesc = make_idesc(dt, true, true, b.products.bn, bm);
             s.out_rows = (int)cols;
             s.out_cols = (int)D;
             p.out = out;

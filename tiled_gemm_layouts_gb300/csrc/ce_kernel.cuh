@@ -42,7 +42,6 @@ namespace tg {
 // short (D below about 500).
 constexpr int kCeEpiWarps = 8;
 constexpr int kCeThreads = 32 * (3 + kCeEpiWarps);  // producers (warps 0 and 10), MMA (1), epilogue (2..9)
-constexpr int kCeBufs = 2;                          // staging buffers of 2 KB per epilogue warp
 // Time of an output tile's epilogue in K-blocks: 128 KB of stores at an SM
 // pair's share of the memory bandwidth.
 constexpr int kCeTileBlocks = 6;
@@ -112,6 +111,22 @@ __device__ __forceinline__ void tma_add_3d(const CUtensorMap* map, uint32_t src,
         : "memory");
 }
 
+// Shared memory of a launch: the ring, and 4 KB of staging per epilogue warp
+// (32 rows of 128 bytes: 64 columns of 16 bits or 32 of fp32).  More staging
+// at the price of ring slots was slower: 4 slots and 12 KB per warp took 108
+// us for 8 x 856 x 54155, 6 slots 92.
+template <int BN, bool PAIR>
+struct CeShape : TileShape<BN, PAIR> {
+    using TS = TileShape<BN, PAIR>;
+    static constexpr int kSlots = 6;
+    static constexpr int kGroups = kSlots / kCeBlocksPerStage;
+    static constexpr int kUnit = 4096;
+    static constexpr int kCeSmemBytes =
+        1024 + kSlots * TS::kStage + kCeEpiWarps * kUnit + (2 * kGroups + 5) * 8 + 16;
+    static_assert(kSlots % kCeBlocksPerStage == 0, "whole groups");
+    static_assert(kCeSmemBytes <= TS::kSmemLimit, "shared memory budget");
+};
+
 struct CeItem {
     int side, tm, tn, split, kb0, kb1;
 };
@@ -130,8 +145,8 @@ template <int MODE>
 struct CeItems {
     int tiles_m[2], tiles_n[2], num_kb[2], group_m[2];
     int all_kb, step, stride;
-    long long at[2], end[2];  // next and last item of each side
-    long long tail, tail_at;  // first item of dW's common part, and this worker's next there
+    int at[2], end[2];  // next item of each side, and their numbers
+    int tail, tail_at;  // first item of dW's common part, and this worker's next there
 
     __device__ __forceinline__ CeItems(const CeParams& p, int worker, int workers, int bm)
         : all_kb(p.all_kb), step(workers) {
@@ -147,23 +162,23 @@ struct CeItems {
             tiles_m[0] = min(tiles_m[0], (n + bm - 1) / bm);
             num_kb[1] = min(num_kb[1], (n + kBK - 1) / kBK);
         }
-        end[0] = (long long)tiles_m[0] * tiles_n[0] * (MODE == CE_PRODUCTS ? p.splits : 1);
+        end[0] = tiles_m[0] * tiles_n[0] * (MODE == CE_PRODUCTS ? p.splits : 1);
         at[0] = worker;
         if constexpr (MODE == CE_PRODUCTS) {
-            const long long all = (long long)tiles_m[1] * tiles_n[1];
-            const int busy = (int)(end[0] % workers);  // workers with one more item of dH
+            const int all = tiles_m[1] * tiles_n[1];
+            const int busy = end[0] % workers;  // workers with one more item of dH
             stride = workers - busy;
             const long long rounds =
                 busy && all ? max(num_kb[0], kCeTileBlocks) / max(num_kb[1], kCeTileBlocks) : 0;
-            tail = min(all, rounds * stride);
+            tail = (int)min((long long)all, rounds * stride);
             at[1] = worker >= busy ? worker - busy : tail;
             tail_at = tail + worker;
             end[1] = all;
         }
     }
-    __device__ __forceinline__ void place(CeItem& it, long long t) const {
+    __device__ __forceinline__ void place(CeItem& it, int i) const {
         const int s = it.side, group = group_m[s] * tiles_n[s];
-        const int i = (int)t, g = i / group, first = g * group_m[s];
+        const int g = i / group, first = g * group_m[s];
         const int gm = min(tiles_m[s] - first, group_m[s]), r = i - g * group;
         it.tm = first + r % gm;
         it.tn = r / gm;
@@ -172,8 +187,8 @@ struct CeItems {
         if (at[0] < end[0]) {
             it.side = 0;
             if constexpr (MODE == CE_PRODUCTS) {
-                const long long tiles = (long long)tiles_m[0] * tiles_n[0];
-                it.split = (int)(at[0] / tiles);
+                const int tiles = tiles_m[0] * tiles_n[0];
+                it.split = at[0] / tiles;
                 place(it, at[0] - it.split * tiles);
                 it.kb0 = it.split * num_kb[0];
                 it.kb1 = min(all_kb, it.kb0 + num_kb[0]);
@@ -253,11 +268,11 @@ struct CeRowStats {
 // One kernel for all products.  PAIR: a CTA pair works on 256 x BN tiles.
 template <int MODE, int BN, bool PAIR>
 __global__ void __launch_bounds__(kCeThreads, 1) ce_kernel(const __grid_constant__ CeParams p) {
-    using TS = TileShape<BN, PAIR>;
+    using TS = CeShape<BN, PAIR>;
     constexpr bool Q_MN = MODE == CE_PRODUCTS;  // Q's columns contiguous in memory
     constexpr bool BOTH = MODE == CE_PRODUCTS;  // side 1's P (G^T) has its rows contiguous
-    constexpr int STAGES = TS::kStages;
-    constexpr int GROUPS = STAGES / kCeBlocksPerStage;
+    constexpr int STAGES = TS::kSlots;
+    constexpr int GROUPS = TS::kGroups;
     constexpr int CG = PAIR ? 2 : 1;
     constexpr uint32_t kQBytes = Q_MN ? (uint32_t)TS::kBStage : (uint32_t)TS::kBNC * 128u;
     extern __shared__ uint8_t smem_raw[];
@@ -266,7 +281,7 @@ __global__ void __launch_bounds__(kCeThreads, 1) ce_kernel(const __grid_constant
     uint8_t* sA = smem;
     uint8_t* sB = smem + STAGES * TS::kAStage;
     uint8_t* staging = sB + STAGES * TS::kBStage;
-    uint64_t* full = reinterpret_cast<uint64_t*>(staging + TS::kStaging);
+    uint64_t* full = reinterpret_cast<uint64_t*>(staging + kCeEpiWarps * TS::kUnit);
     uint64_t* empty = full + GROUPS;
     uint64_t* tfull = empty + GROUPS;
     uint64_t* tempty = tfull + 2;
@@ -319,13 +334,13 @@ __global__ void __launch_bounds__(kCeThreads, 1) ce_kernel(const __grid_constant
         constexpr int ROLE = decltype(role)::value;
         int grp = 0;
         uint32_t phase = 0, armed = 0, armed_parity = 0;
-        const uint32_t stage_tx = (p.p_bytes + kQBytes) * (PAIR ? 2u : 1u);
         CeItems<MODE> items(p, worker, workers, TS::kBM);
         CeItem it;
         bool ok = true;
         while (ok && items.next(it)) {
             const CeSide& sd = p.side[BOTH ? it.side : 0];
             const bool p_mn = BOTH && it.side == 1;
+            const uint32_t stage_tx = (sd.p_bytes + kQBytes) * (PAIR ? 2u : 1u);
             const int m0 = it.tm * TS::kBM + (int)rank * 128;
             const int n0 = it.tn * BN + (int)rank * TS::kBNC;
             for (int kb = it.kb0; kb < it.kb1; kb += kCeBlocksPerStage) {
@@ -477,8 +492,7 @@ __global__ void __launch_bounds__(kCeThreads, 1) ce_kernel(const __grid_constant
         constexpr int kChunks = BN / 64;  // of 32 columns, per warp
         static_assert(kChunks % 2 == 0, "chunks are taken in pairs");
         const int q = warp & 3, half = (warp - 2) / 4;
-        uint8_t* stage = staging + (warp - 2) * kCeBufs * 2048;
-        uint32_t stored = 0;  // output chunks stored so far
+        uint8_t* stage = staging + (warp - 2) * TS::kUnit;
         float alpha = 1.0f;
         if constexpr (MODE == CE_PRODUCTS) alpha = __ldg(p.alpha);
         int live = 0;
@@ -514,103 +528,6 @@ __global__ void __launch_bounds__(kCeThreads, 1) ce_kernel(const __grid_constant
             const uint32_t t_row =
                 tmem_base + ((uint32_t)(q * 32) << 16) + buf * BN + half * (BN / 2);
 
-            auto finish = [&](uint32_t (&v)[32], int c) {
-                const int c0 = n0 + c * 32;
-                if constexpr (MODE == CE_LSE) {
-                    st.chunk(v, c0, p.cols);
-                } else {
-                    float y[32];
-#pragma unroll
-                    for (int j = 0; j < 32; ++j) y[j] = __uint_as_float(v[j]);
-                    if constexpr (MODE == CE_GRAD) {
-#pragma unroll
-                        for (int j = 0; j < 32; j += 2) {
-                            fma2(y[j], y[j + 1], p.to_log2, -rs.x, y[j], y[j + 1]);
-                            y[j] = pow2_gradual(y[j]);
-                            y[j + 1] = pow2_gradual(y[j + 1]);
-                        }
-                        const unsigned d = (unsigned)(target - c0);
-                        if (__any_sync(0xffffffffu, d < 32u)) {
-#pragma unroll
-                            for (int j = 0; j < 32; ++j)
-                                if (d == (unsigned)j) y[j] -= 1.0f;
-                        }
-#pragma unroll
-                        for (int j = 0; j < 32; j += 2) mul2(y + j, rs.y);
-                        if (c0 + 32 > p.cols) {  // the piece's padding columns hold zeros
-#pragma unroll
-                            for (int j = 0; j < 32; ++j)
-                                if (c0 + j >= p.cols) y[j] = 0.0f;
-                        }
-                    } else if (!planes) {
-#pragma unroll
-                        for (int j = 0; j < 32; j += 2) mul2(y + j, alpha);
-                    }
-                    // stage the 32 x 32 chunk in swizzled shared memory and store
-                    // it with one tensor copy, clipped by the map
-                    // (fp32: two of 16 columns, so that both kinds fill a buffer)
-                    if (planes) {
-#pragma unroll
-                        for (int h = 0; h < 2; ++h) {
-                            uint8_t* b = stage + (stored % kCeBufs) * 2048;
-                            if (stored >= kCeBufs && lane == 0) bulk_wait_group_read<kCeBufs - 1>();
-                            __syncwarp();
-#pragma unroll
-                            for (int k = 0; k < 4; ++k)
-                                *reinterpret_cast<float4*>(b + lane * 64 + ((k ^ ((lane >> 1) & 3)) << 4)) =
-                                    make_float4(y[16 * h + 4 * k], y[16 * h + 4 * k + 1],
-                                                y[16 * h + 4 * k + 2], y[16 * h + 4 * k + 3]);
-                            fence_proxy_async_shared();
-                            __syncwarp();
-                            if (lane == 0) {
-                                const int c1 = c0 + 16 * h;
-                                if (row0 < sd.out_rows && c1 < sd.out_cols) {
-                                    if (p.accumulate)
-                                        tma_add_3d(&sd.map_c, smem_addr(b), c1, row0, it.split);
-                                    else
-                                        tma_store_3d(&sd.map_c, smem_addr(b), c1, row0, it.split);
-                                }
-                                bulk_commit_group();
-                            }
-                            ++stored;
-                        }
-                    } else {
-                        uint8_t* b = stage + (stored % kCeBufs) * 2048;
-                        if (stored >= kCeBufs && lane == 0) bulk_wait_group_read<kCeBufs - 1>();
-                        __syncwarp();
-                        if (p.bf16)
-                            stage_row<true>(b, lane, y);
-                        else
-                            stage_row<false>(b, lane, y);
-                        fence_proxy_async_shared();
-                        __syncwarp();
-                        if (lane == 0) {
-                            if constexpr (BOTH) {
-                                // dW is not read again: its lines leave L2 first
-                                if (row0 < sd.out_rows && c0 < p.n_tma)
-                                    tma_store_2d_hint(&sd.map_c, smem_addr(b), c0, row0,
-                                                      l2_policy_evict_first());
-                            } else {
-                                tma_store_2d(&sd.map_c, smem_addr(b), c0, row0);
-                            }
-                            bulk_commit_group();
-                        }
-                        // columns the map cannot hold (all of them for an unaligned
-                        // dW): a row of the chunk per store, lane = column
-                        if (BOTH && c0 + 32 > p.n_tma && c0 < sd.out_cols) {
-                            const int col = c0 + lane;
-                            const bool mine = col >= p.n_tma && col < sd.out_cols;
-                            uint16_t* o = static_cast<uint16_t*>(p.out) + (long long)row0 * p.ldo + col;
-#pragma unroll 4
-                            for (int r = 0; r < 32; ++r)
-                                if (mine && row0 + r < sd.out_rows)
-                                    o[(long long)r * p.ldo] = *reinterpret_cast<const uint16_t*>(
-                                        b + r * 64 + (((lane >> 3) ^ ((r >> 1) & 3)) << 4) + (lane & 7) * 2);
-                        }
-                        ++stored;
-                    }
-                }
-            };
             auto release = [&]() {  // every column of this buffer is in registers
                 tc_fence_before();
                 __syncwarp();
@@ -621,24 +538,152 @@ __global__ void __launch_bounds__(kCeThreads, 1) ce_kernel(const __grid_constant
                         mbar_arrive(smem_addr(&tempty[buf]));
                 }
             };
-            // the next chunk's TMEM load runs beside this chunk's arithmetic
             uint32_t va[32], vb[32];
-            __syncwarp();
-            tmem_ld_32x32b_x32(t_row, va);
-#pragma unroll 1
-            for (int c = 0; c < kChunks; c += 2) {
-                tmem_wait_ld_regs(va);
+            if constexpr (MODE == CE_LSE) {
+                // the next chunk's TMEM load runs beside this chunk's arithmetic
                 __syncwarp();
-                tmem_ld_32x32b_x32(t_row + (c + 1) * 32, vb);
-                finish(va, c);
-                tmem_wait_ld_regs(vb);
-                if (c + 2 < kChunks) {
+                tmem_ld_32x32b_x32(t_row, va);
+#pragma unroll 1
+                for (int c = 0; c < kChunks; c += 2) {
+                    tmem_wait_ld_regs(va);
                     __syncwarp();
-                    tmem_ld_32x32b_x32(t_row + (c + 2) * 32, va);
-                } else {
-                    release();
+                    tmem_ld_32x32b_x32(t_row + (c + 1) * 32, vb);
+                    st.chunk(va, n0 + c * 32, p.cols);
+                    tmem_wait_ld_regs(vb);
+                    if (c + 2 < kChunks) {
+                        __syncwarp();
+                        tmem_ld_32x32b_x32(t_row + (c + 2) * 32, va);
+                    } else {
+                        release();
+                    }
+                    st.chunk(vb, n0 + (c + 1) * 32, p.cols);
                 }
-                finish(vb, c + 1);
+            } else {
+                // 64 columns at a time: staged in swizzled shared memory and
+                // written with one tensor store, clipped by the map.  The
+                // fence and the store's issue are most of a step's latency
+                // (500 of 1150 cycles at 32 columns), so steps are wide.
+                auto logits_to_gradient = [&](float (&y)[32], int c0) {
+#pragma unroll
+                    for (int j = 0; j < 32; j += 2) {
+                        fma2(y[j], y[j + 1], p.to_log2, -rs.x, y[j], y[j + 1]);
+                        y[j] = pow2_gradual(y[j]);
+                        y[j + 1] = pow2_gradual(y[j + 1]);
+                    }
+                    const unsigned d = (unsigned)(target - c0);
+                    if (__any_sync(0xffffffffu, d < 32u)) {
+#pragma unroll
+                        for (int j = 0; j < 32; ++j)
+                            if (d == (unsigned)j) y[j] -= 1.0f;
+                    }
+#pragma unroll
+                    for (int j = 0; j < 32; j += 2) mul2(y + j, rs.y);
+                    if (c0 + 32 > p.cols) {  // the piece's padding columns hold zeros
+#pragma unroll
+                        for (int j = 0; j < 32; ++j)
+                            if (c0 + j >= p.cols) y[j] = 0.0f;
+                    }
+                };
+                // 16 bytes of this lane's staged row
+                auto staged = [&](int k) {
+                    return reinterpret_cast<uint4*>(stage + lane * 128 + ((k ^ (lane & 7)) << 4));
+                };
+                auto stage_free = [&]() {
+                    if (lane == 0) bulk_wait_group_read<0>();
+                    __syncwarp();
+                };
+                auto stage_full = [&]() {
+                    fence_proxy_async_shared();
+                    __syncwarp();
+                };
+#pragma unroll 1
+                for (int c = 0; c < kChunks; c += 2) {
+                    const int c0 = n0 + c * 32;
+                    __syncwarp();
+                    tmem_ld_32x32b_x32(t_row + c * 32, va);
+                    tmem_ld_32x32b_x32(t_row + (c + 1) * 32, vb);
+                    tmem_wait_ld_regs(va);
+                    tmem_wait_ld_regs(vb);
+                    if (c + 2 == kChunks) release();
+                    float ya[32], yb[32];
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) {
+                        ya[j] = __uint_as_float(va[j]);
+                        yb[j] = __uint_as_float(vb[j]);
+                    }
+                    if (planes) {
+                        // 32 fp32 columns per store
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {
+                            stage_free();
+#pragma unroll
+                            for (int k = 0; k < 8; ++k) {
+                                const float* y = (h ? yb : ya) + 4 * k;
+                                *staged(k) = make_uint4(__float_as_uint(y[0]), __float_as_uint(y[1]),
+                                                        __float_as_uint(y[2]), __float_as_uint(y[3]));
+                            }
+                            stage_full();
+                            if (lane == 0) {
+                                const int c1 = c0 + 32 * h;
+                                if (row0 < sd.out_rows && c1 < sd.out_cols) {
+                                    if (p.accumulate)
+                                        tma_add_3d(&sd.map_c, smem_addr(stage), c1, row0, it.split);
+                                    else
+                                        tma_store_3d(&sd.map_c, smem_addr(stage), c1, row0, it.split);
+                                }
+                                bulk_commit_group();
+                            }
+                        }
+                        continue;
+                    }
+                    if constexpr (MODE == CE_GRAD) {
+                        logits_to_gradient(ya, c0);
+                        logits_to_gradient(yb, c0 + 32);
+                    } else {
+#pragma unroll
+                        for (int j = 0; j < 32; j += 2) {
+                            mul2(ya + j, alpha);
+                            mul2(yb + j, alpha);
+                        }
+                    }
+                    stage_free();
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) {
+                        const float* y = (k < 4 ? ya : yb) + 8 * (k & 3);
+                        *staged(k) = p.bf16 ? make_uint4(pack2t<true>(y[0], y[1]), pack2t<true>(y[2], y[3]),
+                                                         pack2t<true>(y[4], y[5]), pack2t<true>(y[6], y[7]))
+                                            : make_uint4(pack2t<false>(y[0], y[1]), pack2t<false>(y[2], y[3]),
+                                                         pack2t<false>(y[4], y[5]), pack2t<false>(y[6], y[7]));
+                    }
+                    stage_full();
+                    if (lane == 0) {
+                        if constexpr (BOTH) {
+                            // dW is not read again: its lines leave L2 first
+                            if (row0 < sd.out_rows && c0 < p.n_tma)
+                                tma_store_2d_hint(&sd.map_c, smem_addr(stage), c0, row0,
+                                                  l2_policy_evict_first());
+                        } else {
+                            tma_store_2d(&sd.map_c, smem_addr(stage), c0, row0);
+                        }
+                        bulk_commit_group();
+                    }
+                    // columns the map cannot hold (all of them for an unaligned
+                    // dW): half a row of the step per store, lane = column
+                    if (BOTH && c0 + 64 > p.n_tma && c0 < sd.out_cols) {
+                        uint16_t* o = static_cast<uint16_t*>(p.out) + (long long)row0 * p.ldo + c0;
+                        const int rows = min(32, sd.out_rows - row0);
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {
+                            const int x = 32 * h + lane;
+                            if (c0 + x < p.n_tma || c0 + x >= sd.out_cols) continue;
+#pragma unroll 8
+                            for (int r = 0; r < rows; ++r)
+                                o[(long long)r * p.ldo + x] = *reinterpret_cast<const uint16_t*>(
+                                    stage + r * 128 + (((x >> 3) ^ (r & 7)) << 4) + (x & 7) * 2);
+                        }
+                        __syncwarp();
+                    }
+                }
             }
             if constexpr (MODE == CE_LSE) {
                 if (row < p.rows) {

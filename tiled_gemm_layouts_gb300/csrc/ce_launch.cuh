@@ -11,7 +11,7 @@ namespace tg {
 
 template <int MODE, int BN, bool PAIR>
 cudaError_t launch_ce_tile(const CeParams& p, int sms, bool chained, cudaStream_t stream) {
-    using TS = TileShape<BN, PAIR>;
+    using TS = CeShape<BN, PAIR>;
     auto kern = ce_kernel<MODE, BN, PAIR>;
     static std::atomic<unsigned long long> attr_set{0};  // one bit per device
     int dev = 0;
@@ -19,7 +19,7 @@ cudaError_t launch_ce_tile(const CeParams& p, int sms, bool chained, cudaStream_
     if (e != cudaSuccess) return e;
     const unsigned long long bit = dev < 64 ? 1ull << dev : 0ull;
     if (!(attr_set.load(std::memory_order_acquire) & bit)) {
-        e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, TS::kSmemBytes);
+        e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, TS::kCeSmemBytes);
         if (e != cudaSuccess) return e;
         attr_set.fetch_or(bit, std::memory_order_release);
     }
@@ -32,7 +32,7 @@ cudaError_t launch_ce_tile(const CeParams& p, int sms, bool chained, cudaStream_
     cudaLaunchAttribute attr[2];
     lc.gridDim = dim3(PAIR ? 2 * workers : workers, 1, 1);
     lc.blockDim = dim3(kCeThreads, 1, 1);
-    lc.dynamicSmemBytes = TS::kSmemBytes;
+    lc.dynamicSmemBytes = TS::kCeSmemBytes;
     lc.stream = stream;
     if (PAIR) {
         attr[lc.numAttrs].id = cudaLaunchAttributeClusterDimension;

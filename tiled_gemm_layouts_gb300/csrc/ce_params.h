@@ -26,12 +26,12 @@ struct CeSide {
     int tiles_m, tiles_n;    // 0: this side has no work
     int group_m;             // raster: tile rows per group
     uint32_t idesc;
+    uint32_t p_bytes;        // bytes one K-block of P lands in a CTA
     int out_rows, out_cols;  // of dH's planes, or of this piece of dW
 };
 
 struct alignas(128) CeParams {
     CeSide side[2];
-    uint32_t p_bytes;        // bytes one K-block of P lands in a CTA
     int bf16;
     // Rows that count, on the device (null: all): only tile rows of logits and
     // of dH, and K-blocks of dW's contraction, that hold one are worked on.
@@ -61,6 +61,7 @@ struct alignas(128) CeParams {
 // Tile of a launch: `bn` columns; 256 rows on a CTA pair or 128 on one CTA.
 struct CeTile {
     int bn, pair;
+    int rows() const { return pair ? 256 : 128; }
 };
 
 // `chained`: the launch may be scheduled while the kernel before it in the

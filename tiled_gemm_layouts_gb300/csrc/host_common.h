@@ -74,7 +74,7 @@ bool encode_k_pairs(CUtensorMap* map, int dtype, const void* base, int64_t rows,
 bool encode_mn_atom_pairs(CUtensorMap* map, int dtype, const void* base, int64_t rows, int64_t k,
                           int64_t ld, uint32_t atoms);
 // fp32 planes x rows x cols (row stride ld elements, planes rows*ld apart),
-// box 16 columns x 32 rows, 64-byte swizzle.
+// box 32 columns x 32 rows, 128-byte swizzle.
 bool encode_f32_planes(CUtensorMap* map, const void* base, uint64_t cols, uint64_t rows,
                        uint64_t planes, int64_t ld);
 
