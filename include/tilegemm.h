@@ -285,7 +285,8 @@ int tg_pointwise(int64_t M, int64_t N, const void* X, int64_t ldx, tg_perm permX
  *     Y[r, c] = (X[r, c] - mean[r]) * rstd[r] * weight[c] + bias[c]
  *
  * X, weight, bias and Y have type `dtype`; mean and rstd are fp32 [rows] and
- * are what tg_layernorm_grad needs.  bias may be NULL (no shift).  eps >= 0.
+ * are what tg_layernorm_grad needs.  bias may be NULL (no shift).  eps >= 0,
+ * cols <= 2^30.
  * One kernel launch.  Errors as tg_pointwise's checks.
  */
 int tg_layernorm(int64_t rows, int64_t cols, const void* X, int64_t ldx, const void* weight,
@@ -317,9 +318,9 @@ int tg_layernorm_grad_workspace_size(int64_t rows, int64_t cols, tg_dtype dtype,
  *             = 0                            otherwise (an ignored token)
  *
  * H is T x D (row stride ldh), W is V x D (row stride ldw), both of type
- * `dtype`; target is [T]; loss and lse are fp32 [T].  The logits are fp32 and
- * stay on chip; the workspace holds 8 bytes per token and 128 or 256 columns
- * of the vocabulary.  Two kernel launches.
+ * `dtype`; target is [T]; loss and lse are fp32 [T]; T, V, D <= 2^30.  The
+ * logits are fp32 and stay on chip; the workspace holds 8 bytes per token and
+ * 64 or 128 columns of the vocabulary.  Two kernel launches.
  * workspace: 256-byte aligned, at least tg_linear_ce_workspace_size() bytes
  * (else TG_ERR_BUFFER).  An H or W whose rows are not 16-byte aligned is
  * copied into the workspace first.  A row whose logits hold a NaN or +inf

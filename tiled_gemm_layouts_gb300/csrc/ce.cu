@@ -267,9 +267,10 @@ __global__ void ce_scatter_kernel(const float* __restrict__ planes, int splits, 
         float y[8] = {0, 0, 0, 0, 0, 0, 0, 0};
         if (j >= 0) {
             const float* s = planes + (long long)j * ldp + c;
-            for (int k = 0; k < splits; ++k, s += plane) {
-                const float4 a = *reinterpret_cast<const float4*>(s);
-                const float4 b = *reinterpret_cast<const float4*>(s + 4);
+#pragma unroll 8
+            for (int k = 0; k < splits; ++k) {
+                const float4 a = *reinterpret_cast<const float4*>(s + k * plane);
+                const float4 b = *reinterpret_cast<const float4*>(s + k * plane + 4);
                 y[0] += a.x; y[1] += a.y; y[2] += a.z; y[3] += a.w;
                 y[4] += b.x; y[5] += b.y; y[6] += b.z; y[7] += b.w;
             }
@@ -411,7 +412,7 @@ BwdPlan backward_plan(int64_t T, int64_t V, int64_t D, const void* W, int64_t ld
 // ------------------------------------------------------ argument checks
 
 int check_sizes(int64_t T, int64_t V, int64_t D, int dtype) {
-    if (T <= 0 || V <= 0 || D <= 0 || T > kMaxDim || V > kMaxDim || D > kMaxDim)
+    if (T <= 0 || V <= 0 || D <= 0 || T > kMaxSize || V > kMaxSize || D > kMaxSize)
         return TG_ERR_INVALID_ARG;
     // tiles are counted in 32 bits
     if (cdiv(T, 128) * cdiv(V, 64) > INT_MAX || cdiv(T, 128) * cdiv(D, 64) > INT_MAX ||

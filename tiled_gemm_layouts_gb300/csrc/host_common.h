@@ -12,6 +12,8 @@
 namespace tg {
 
 constexpr int64_t kMaxDim = 2147483647LL;
+// Sizes whose kernels step past the end in 32 bits.
+constexpr int64_t kMaxSize = 1LL << 30;
 // Leading dimensions stay below the tensor-map stride limit of 2^40 bytes.
 constexpr int64_t kMaxLd = (1LL << 39) - 8;
 

@@ -892,7 +892,8 @@ cudaError_t launch_backward(const LnParams& p, const GradShape& s, cudaStream_t 
 }
 
 int check_sizes(int64_t rows, int64_t cols, int dtype) {
-    if (rows <= 0 || cols <= 0 || rows > kMaxDim || cols > kMaxDim) return TG_ERR_INVALID_ARG;
+    // (a column index plus a block's step stays within 32 bits)
+    if (rows <= 0 || cols <= 0 || rows > kMaxDim || cols > kMaxSize) return TG_ERR_INVALID_ARG;
     if (dtype != TG_F16 && dtype != TG_BF16) return TG_ERR_DTYPE;
     return TG_OK;
 }
