@@ -91,6 +91,14 @@ __device__ __forceinline__ float max_nan(float a, float b) {
     asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
     return r;
 }
+// 1 / x within an ulp.  Only a denominator below fp32's normal range would be
+// taken for zero; sqrt of the smallest fp32 is 3e-23.
+__device__ __forceinline__ float reciprocal(float x) {
+    float y;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
 // r = sqrt(x) for 8 values between `low` and `high`: with y near 1/sqrt(x),
 // s = x y is off by (x - s^2) / (2 sqrt(x)).
 __device__ __forceinline__ void roots(const float (&x)[8], float low, float high, float (&r)[8]) {
@@ -99,8 +107,8 @@ __device__ __forceinline__ void roots(const float (&x)[8], float low, float high
 #pragma unroll
         for (int k = 0; k < 8; k += 2) {
             float y0, y1;
-            asm("rsqrt.approx.f32 %0, %1;" : "=f"(y0) : "f"(x[k]));
-            asm("rsqrt.approx.f32 %0, %1;" : "=f"(y1) : "f"(x[k + 1]));
+            asm("rsqrt.approx.ftz.f32 %0, %1;" : "=f"(y0) : "f"(x[k]));
+            asm("rsqrt.approx.ftz.f32 %0, %1;" : "=f"(y1) : "f"(x[k + 1]));
             const f2 v = pair(x[k], x[k + 1]), y = pair(y0, y1), s = mul(v, y);
             const f2 root = fma(fma(mul(s, pair(-1.0f, -1.0f)), s, v), mul(y, half), s);
             r[k] = split(root).x;
@@ -290,7 +298,7 @@ __global__ void __launch_bounds__(256) adamw_kernel(const __grid_constant__ Adam
     roots(v, low, high, r);
 #pragma unroll
     for (int k = 0; k < 8; ++k)
-        w[k] = fmaf(w[k], a.keep, -__fdividef(m[k], fmaf(r[k], a.root, a.eps)) * a.step_size);
+        w[k] = fmaf(w[k], a.keep, -(m[k] * reciprocal(fmaf(r[k], a.root, a.eps))) * a.step_size);
     if (n > 0) {
         if (t.master) store8<TG_F32>(t.master, i, n, w);
         store8<PT>(t.p, i, n, w);

@@ -706,7 +706,7 @@ ln_reduce_kernel(const float* __restrict__ part, int parts, int cols, uint16_t* 
     const int c = blockIdx.x * 32 + lane;
     float a = 0.0f, b = 0.0f;
     if (c < cols)
-#pragma unroll 4
+#pragma unroll 8
         for (int r = y; r < parts; r += Y) {
             a += part[(long long)r * 2 * cols + c];
             b += part[((long long)r * 2 + 1) * cols + c];
