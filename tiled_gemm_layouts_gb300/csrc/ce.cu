@@ -441,10 +441,11 @@ void common_params(CeParams* p, int dtype, const DeviceInfo* info) {
     p->status = info->status;
 }
 
-// K-major operand: `rows` x `k`, `box` rows of it per CTA.
-bool k_major(CUtensorMap* one, CUtensorMap* two, int* use_two, int dtype, const void* base,
-             int64_t rows, int64_t k, int64_t ld, int box) {
-    *use_two = two && encode_k_pairs(two, dtype, base, rows, k, ld, (uint32_t)box);
+// K-major operand: `rows` x `k`, `box` rows of it per CTA; `two` may be null.
+bool k_major(CUtensorMap* one, CUtensorMap* two, int* pairs, int dtype, const void* base, int64_t rows,
+             int64_t k, int64_t ld, int box) {
+    const int64_t whole = k & ~int64_t(63);
+    *pairs = two && encode_k_pairs(two, dtype, base, rows, whole, ld, (uint32_t)box) ? (int)(whole / 64) : 0;
     return encode_2d(one, dtype, base, k, rows, ld, 64, (uint32_t)box);
 }
 
@@ -458,16 +459,15 @@ bool logits_side(CeParams* p, int dtype, CeTile tile, int64_t T, const void* H, 
     // nobody reads.)
     const int64_t box = h_rows >= 128 ? 128 : up(h_rows, 8);
     s.p_bytes = (uint32_t)box * 128;
-    int unused;
-    if (!k_major(&s.map_p, box == 128 ? &s.map_p2 : nullptr, box == 128 ? &s.p_2k : &unused, dtype,
-                 H, h_rows, h_cols, ldh, (int)box) ||
-        !k_major(&s.map_q, &s.map_q2, &s.q_2k, dtype, W, V, D, ldw,
-                 tile.pair ? tile.bn / 2 : tile.bn))
+    // (two K-blocks of a smaller box would not land where two stages are)
+    if (!k_major(&s.map_p, box == 128 ? &s.map_p2 : nullptr, &s.p_pairs, dtype, H, h_rows, h_cols, ldh,
+                 (int)box) ||
+        !k_major(&s.map_q, &s.map_q2, &s.q_pairs, dtype, W, V, D, ldw, tile.pair ? tile.bn / 2 : tile.bn))
         return false;
     s.num_kb = (int)cdiv(D, 64);
     s.tiles_m = (int)cdiv(T, tile.rows());
     s.tiles_n = (int)cdiv(V, tile.bn);
-    s.group_m = s.tiles_m < 16 ? s.tiles_m : 16;
+    s.group_m = std::min(s.tiles_m, 16);
     s.idesc = make_idesc(dtype, false, false, tile.bn, tile.rows());
     // Each tcgen05.mma adds 16 products to the fp32 accumulator and truncates
     // the sum: for sums of products of either sign a logit comes out smaller
@@ -485,9 +485,12 @@ bool logits_side(CeParams* p, int dtype, CeTile tile, int64_t T, const void* H, 
 bool mn_major_q(CeSide* s, int dtype, CeTile tile, const void* base, int64_t cols, int64_t k,
                 int64_t ld) {
     const int atoms = (tile.pair ? tile.bn / 2 : tile.bn) / 64;
-    s->q_3d = encode_mn_atoms(&s->map_q, dtype, base, cols, k, ld, (uint32_t)atoms);
-    s->q_2k = s->q_3d && encode_mn_atom_pairs(&s->map_q2, dtype, base, cols, k, ld, (uint32_t)atoms);
-    return s->q_3d || encode_2d(&s->map_q, dtype, base, cols, k, ld, 64, 64);
+    const int64_t whole = cols & ~int64_t(63), k_whole = k & ~int64_t(63);
+    s->q_whole = encode_mn_atoms(&s->map_q3, dtype, base, whole, k, ld, (uint32_t)atoms) ? (int)whole : 0;
+    s->q_pairs = s->q_whole && encode_mn_atom_pairs(&s->map_q2, dtype, base, whole, k_whole, ld, (uint32_t)atoms)
+                     ? (int)(k_whole / 64)
+                     : 0;
+    return encode_2d(&s->map_q, dtype, base, cols, k, ld, 64, 64);
 }
 
 }  // namespace
@@ -654,6 +657,9 @@ extern "C" int tg_linear_ce_grad(int64_t T, int64_t V, int64_t D, const void* H,
                             (long long)b.rows, tgt, lse, dloss, (int)T, (long long)V, scale2) == cudaSuccess;
     }
 
+    // Raster groups: 16 tile rows of the logits (12, 20 and 24 cost 1 to 4 % of
+    // the loss at 8192 x 4096 x 131072), 4 of dH and 8 of dW (16 of each: 3712
+    // us against 3568 at 4096 x 4096 x 65536).
     const int bm = b.products.rows();
     for (int64_t i = 0; ok && i < b.pieces; ++i) {
         const int64_t v0 = i * b.piece, cols = V - v0 < b.piece ? V - v0 : b.piece;
@@ -681,16 +687,15 @@ extern "C" int tg_linear_ce_grad(int64_t T, int64_t V, int64_t D, const void* H,
             // map fills with zeros
             // one CTA's tiles need only the rows of G that there are
             const int64_t box = b.products.pair || T >= 128 ? 128 : up(T, 8);
-            int unused;
             s.p_bytes = (uint32_t)box * 128;
-            ok = k_major(&s.map_p, box == 128 ? &s.map_p2 : nullptr, box == 128 ? &s.p_2k : &unused, dt, g,
-                         b.rows, (int64_t)p.all_kb * 64, b.piece, (int)box) &&
+            ok = k_major(&s.map_p, box == 128 ? &s.map_p2 : nullptr, &s.p_pairs, dt, g, b.rows,
+                         (int64_t)p.all_kb * 64, b.piece, (int)box) &&
                  mn_major_q(&s, dt, b.products, w, D, cols, ldw) &&
                  encode_f32_planes(&s.map_c, planes, b.ldp, T, b.splits, b.ldp);
             s.num_kb = (int)b.dh_kb;
             s.tiles_m = (int)cdiv(T, bm);
             s.tiles_n = (int)cdiv(D, b.products.bn);
-            s.group_m = s.tiles_m < 16 ? s.tiles_m : 16;
+            s.group_m = std::min(s.tiles_m, 4);
             s.idesc = make_idesc(dt, false, true, b.products.bn, bm);
             s.out_rows = (int)T;
             s.out_cols = (int)D;
@@ -704,12 +709,14 @@ extern "C" int tg_linear_ce_grad(int64_t T, int64_t V, int64_t D, const void* H,
                  mn_major_q(&s, dt, b.products, h, b.ldh, b.rows, b.ldh) &&
                  encode_2d(&s.map_c, dt, tensor ? out : g, tensor ? p.n_tma : 8, cols,
                            tensor ? lddw : b.piece, 64, 32);
-            s.p_2k = encode_mn_atom_pairs(&s.map_p2, dt, g, b.piece, b.rows, b.piece, 2);
+            s.p_pairs = encode_mn_atom_pairs(&s.map_p2, dt, g, b.piece, b.rows, b.piece, 2)
+                            ? (int)(b.rows / 64)
+                            : 0;
             s.num_kb = (int)(b.rows / 64);
             s.p_bytes = 128 * 128;
             s.tiles_m = (int)cdiv(cols, bm);
             s.tiles_n = (int)cdiv(D, b.products.bn);
-            s.group_m = s.tiles_m < 16 ? s.tiles_m : 16;
+            s.group_m = std::min(s.tiles_m, 8);
             s.idesc = make_idesc(dt, true, true, b.products.bn, bm);
             s.out_rows = (int)cols;
             s.out_cols = (int)D;

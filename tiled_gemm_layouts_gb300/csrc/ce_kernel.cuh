@@ -343,6 +343,8 @@ __global__ void __launch_bounds__(kCeThreads, 1) ce_kernel(const __grid_constant
             const uint32_t stage_tx = (sd.p_bytes + kQBytes) * (PAIR ? 2u : 1u);
             const int m0 = it.tm * TS::kBM + (int)rank * 128;
             const int n0 = it.tn * BN + (int)rank * TS::kBNC;
+            const bool whole = Q_MN && n0 + TS::kBNC <= sd.q_whole;
+            const int pairs = ROLE == 1 ? sd.p_pairs : !Q_MN || whole ? sd.q_pairs : 0;
             for (int kb = it.kb0; kb < it.kb1; kb += kCeBlocksPerStage) {
                 const int n = min(it.kb1 - kb, kCeBlocksPerStage);
                 if (!wait_bar(smem_addr(&empty[grp]), phase ^ 1, w, DEV_TIMEOUT_PRODUCER + 1)) {
@@ -378,7 +380,7 @@ __global__ void __launch_bounds__(kCeThreads, 1) ce_kernel(const __grid_constant
                 const uint32_t dst0 = ROLE == 1 ? smem_addr(sA + slot0 * TS::kAStage)
                                                 : smem_addr(sB + slot0 * TS::kBStage);
                 constexpr uint32_t kStep = ROLE == 1 ? TS::kAStage : TS::kBStage;
-                if (n == 2 && (ROLE == 1 ? sd.p_2k : sd.q_2k)) {  // both K-blocks as one box
+                if (n == 2 && kb + 2 <= pairs) {  // both K-blocks as one box
                     if constexpr (ROLE == 1) {
                         if (p_mn)
                             load4(dst0, &sd.map_p2, m0 >> 6, kb);
@@ -399,8 +401,8 @@ __global__ void __launch_bounds__(kCeThreads, 1) ce_kernel(const __grid_constant
                             else
                                 load2(dst, &sd.map_p, k0, m0);
                         } else if constexpr (Q_MN) {
-                            if (sd.q_3d) {
-                                load3(dst, &sd.map_q, 0, k0, n0 >> 6);
+                            if (whole) {
+                                load3(dst, &sd.map_q3, 0, k0, n0 >> 6);
                             } else {
 #pragma unroll
                                 for (int h = 0; h < TS::kBBoxes; ++h)

@@ -17,11 +17,13 @@ enum CeMode : int {
 
 // One tiled product P * Q^T or P * Q and where its tiles go.
 struct CeSide {
-    CUtensorMap map_p, map_q;    // one 64-deep K-block of each operand per box
-    CUtensorMap map_p2, map_q2;  // two K-blocks per box, where p_2k / q_2k
+    // One 64-deep K-block per box (MN-major Q: 64 of its columns, and all the
+    // columns of a tile in map_q3), and two K-blocks per box.  Every copy has
+    // a fixed cost, so the wide boxes are used wherever they hold whole
+    // blocks: the first p_pairs / q_pairs K-blocks, the first q_whole columns.
+    CUtensorMap map_p, map_q, map_q3, map_p2, map_q2;
     CUtensorMap map_c;           // tensor stores of the output
-    int p_2k, q_2k;
-    int q_3d;                // MN-major Q: one 3-D box per K-block (else 64-column boxes)
+    int p_pairs, q_pairs, q_whole;
     int num_kb;              // K-blocks of the contraction (or of one split of it)
     int tiles_m, tiles_n;    // 0: this side has no work
     int group_m;             // raster: tile rows per group
