@@ -16,6 +16,7 @@
 #include "../../include/tilegemm.h"
 #include "ce_launch.cuh"
 #include "host_common.h"
+#include "stage.cuh"
 
 namespace tg {
 
@@ -43,6 +44,14 @@ int64_t up(int64_t a, int64_t b) { return cdiv(a, b) * b; }
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
 // ------------------------------------------------------ small kernels
+
+// Copies of H and W, whichever a tensor map cannot describe, in one launch.
+__global__ void __launch_bounds__(256) ce_stage_kernel(const CopyJob h, const CopyJob w) {
+    allow_next_kernel();
+    const long long thread = blockIdx.x * 256LL + threadIdx.x, threads = gridDim.x * 256LL;
+    if (h.rows) copy_rows(h, thread, threads);
+    if (w.rows) copy_rows(w, thread, threads);
+}
 
 // (max in log2 units, sum of 2^(l - max)) of a set of logits.
 struct LogSum {
@@ -196,14 +205,18 @@ ce_compact_kernel(const long long* __restrict__ target, const float* __restrict_
 // Dense rows of H for the tokens that count: out[j] = H[token[j]], columns
 // [D, ldo) and the rows up to the next multiple of 256 filled with zeros.
 // HERE: the blocks compact for themselves, and the first one writes it down.
+// `w`: a copy of W, where a tensor map cannot describe it.
 template <bool HERE>
 __global__ void __launch_bounds__(kCompactThreads)
 ce_gather_kernel(const uint16_t* __restrict__ H, long long ldh, int D, CeRows r,
                  uint16_t* __restrict__ out, int ldo, long long max_rows,
                  const long long* __restrict__ target, const float* __restrict__ lse,
-                 const float* __restrict__ dloss, int T, long long V, float scale2) {
+                 const float* __restrict__ dloss, int T, long long V, float scale2, const CopyJob w) {
     __shared__ int tokens[HERE ? kCompactEverywhere : 1];
     allow_next_kernel();
+    if (w.rows)
+        copy_rows(w, blockIdx.x * (long long)kCompactThreads + threadIdx.x,
+                  (long long)gridDim.x * kCompactThreads);
     int live;
     if constexpr (HERE) {
         float ref;
@@ -230,7 +243,7 @@ ce_gather_kernel(const uint16_t* __restrict__ H, long long ldh, int D, CeRows r,
     const int vecs = ldo / 8;
     for (long long i = blockIdx.x * (long long)blockDim.x + threadIdx.x; i < rows * vecs;
          i += (long long)gridDim.x * blockDim.x) {
-        const long long j = i / vecs;
+        const long long j = row_of(i, vecs);
         const int c = (int)(i - j * vecs) * 8;
         uint4 v = make_uint4(0, 0, 0, 0);
         if (j < live && c < D) {
@@ -261,7 +274,7 @@ __global__ void ce_scatter_kernel(const float* __restrict__ planes, int splits, 
     const int vecs = (D + 7) / 8;
     for (long long i = blockIdx.x * (long long)blockDim.x + threadIdx.x; i < (long long)T * vecs;
          i += (long long)gridDim.x * blockDim.x) {
-        const long long t = i / vecs;
+        const long long t = row_of(i, vecs);
         const int c = (int)(i - t * vecs) * 8;
         const int j = r.place[t];
         float y[8] = {0, 0, 0, 0, 0, 0, 0, 0};
@@ -536,15 +549,26 @@ extern "C" int tg_linear_ce(int64_t T, int64_t V, int64_t D, const void* H, int6
 
     char* ws = static_cast<char*>(workspace);
     bool ok = true;
-    if (f.copy_h) {
-        ok = ok && launch_copy_rows(H, ldh, ws + f.h, up(D, 8), T, D, stream) == cudaSuccess;
-        H = ws + f.h;
-        ldh = up(D, 8);
-    }
-    if (f.copy_w) {
-        ok = ok && launch_copy_rows(W, ldw, ws + f.w, up(D, 8), V, D, stream) == cudaSuccess;
-        W = ws + f.w;
-        ldw = up(D, 8);
+    const bool staged = f.copy_h || f.copy_w;
+    if (staged) {
+        const int64_t wide = up(D, 8);
+        CopyJob h{static_cast<const uint16_t*>(H), ldh, reinterpret_cast<uint16_t*>(ws + f.h), wide,
+                  f.copy_h ? T : 0, D};
+        CopyJob w{static_cast<const uint16_t*>(W), ldw, reinterpret_cast<uint16_t*>(ws + f.w), wide,
+                  f.copy_w ? V : 0, D};
+        // (1216 blocks, what the SMs hold: 172 us for 23 x 1911 x 65536; 4096:
+        // 160; a block per 4 KB: 202)
+        const int64_t blocks = std::min<int64_t>(cdiv((h.rows + w.rows) * (wide / 8), 256), 4096);
+        ce_stage_kernel<<<(unsigned)blocks, 256, 0, stream>>>(h, w);
+        ok = cudaGetLastError() == cudaSuccess;
+        if (f.copy_h) {
+            H = h.dst;
+            ldh = wide;
+        }
+        if (f.copy_w) {
+            W = w.dst;
+            ldw = wide;
+        }
     }
     CeParams p;
     common_params(&p, (int)dtype, info);
@@ -552,7 +576,7 @@ extern "C" int tg_linear_ce(int64_t T, int64_t V, int64_t D, const void* H, int6
     p.target = reinterpret_cast<const long long*>(target);
     p.part = reinterpret_cast<float2*>(ws + f.part);
     p.hit = reinterpret_cast<float*>(ws + f.hit);
-    ok = ok && launch_ce(CE_LSE, p, f.tile, info->sms, false, stream) == cudaSuccess;
+    ok = ok && launch_ce(CE_LSE, p, f.tile, info->sms, staged, stream) == cudaSuccess;
     if (ok) {
         // few tokens: a block for each, so that hundreds of partial sums are
         // not one warp's serial chain (1024 of them: 6.9 us by one warp)
@@ -625,10 +649,11 @@ extern "C" int tg_linear_ce_grad(int64_t T, int64_t V, int64_t D, const void* H,
     char* ws = static_cast<char*>(workspace);
     const int dt = (int)dtype, sms = info->sms;
     bool ok = true;
+    CopyJob copy_w{static_cast<const uint16_t*>(W), ldw, reinterpret_cast<uint16_t*>(ws + b.w), up(D, 8),
+                   b.copy_w ? V : 0, D};
     if (b.copy_w) {
-        ok = launch_copy_rows(W, ldw, ws + b.w, up(D, 8), V, D, stream) == cudaSuccess;
-        W = ws + b.w;
-        ldw = up(D, 8);
+        W = copy_w.dst;
+        ldw = copy_w.ldd;
     }
     CeRows rows;
     rows.live = reinterpret_cast<int*>(ws + b.live);
@@ -643,18 +668,20 @@ extern "C" int tg_linear_ce_grad(int64_t T, int64_t V, int64_t D, const void* H,
     const float scale2 = dt == TG_F16 ? 1024.0f : 1.0f;
     const long long* tgt = reinterpret_cast<const long long*>(target);
     const bool here = T <= kCompactEverywhere;
-    const unsigned gather_blocks = (unsigned)std::min<int64_t>(cdiv(b.rows * (b.ldh / 8), kCompactThreads), sms * 2);
+    const unsigned gather_blocks = (unsigned)std::min<int64_t>(
+        cdiv(b.rows * (b.ldh / 8) + copy_w.rows * (up(D, 8) / 8), kCompactThreads), sms * 2);
     if (here) {
         ce_gather_kernel<true><<<gather_blocks, kCompactThreads, 0, stream>>>(
             static_cast<const uint16_t*>(H), ldh, (int)D, rows, h, (int)b.ldh, b.rows, tgt, lse, dloss,
-            (int)T, V, scale2);
+            (int)T, V, scale2, copy_w);
         ok = ok && cudaGetLastError() == cudaSuccess;
     } else {
         ce_compact_kernel<<<1, kCompactThreads, 0, stream>>>(tgt, lse, dloss, (int)T, V, scale2, rows);
         ok = ok && cudaGetLastError() == cudaSuccess &&
              launch_chained(ce_gather_kernel<false>, dim3(gather_blocks), kCompactThreads, stream,
                             static_cast<const uint16_t*>(H), (long long)ldh, (int)D, rows, h, (int)b.ldh,
-                            (long long)b.rows, tgt, lse, dloss, (int)T, (long long)V, scale2) == cudaSuccess;
+                            (long long)b.rows, tgt, lse, dloss, (int)T, (long long)V, scale2,
+                            copy_w) == cudaSuccess;
     }
 
     // Raster groups: 16 tile rows of the logits (12, 20 and 24 cost 1 to 4 % of
