@@ -320,7 +320,8 @@ int tg_layernorm_grad_workspace_size(int64_t rows, int64_t cols, tg_dtype dtype,
  * H is T x D (row stride ldh), W is V x D (row stride ldw), both of type
  * `dtype`; target is [T]; loss and lse are fp32 [T]; T, V, D <= 2^30.  The
  * logits are fp32 and stay on chip; the workspace holds 8 bytes per token and
- * 64 or 128 columns of the vocabulary.  Two kernel launches.
+ * 64 or 128 columns of the vocabulary.  Two kernel launches, a third where H
+ * or W has to be copied.
  * workspace: 256-byte aligned, at least tg_linear_ce_workspace_size() bytes
  * (else TG_ERR_BUFFER).  An H or W whose rows are not 16-byte aligned is
  * copied into the workspace first.  A row whose logits hold a NaN or +inf

@@ -186,11 +186,9 @@ class TileGemmError(RuntimeError):
 
 
 def _addr(x) -> int | None:
-    if x is None:
-        return None
-    if isinstance(x, int):
+    if x is None or isinstance(x, int):
         return x
-    return int(x.data_ptr())
+    return x.data_ptr()
 
 
 def _stream(s) -> int | None:

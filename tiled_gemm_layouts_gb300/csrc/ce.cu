@@ -363,8 +363,9 @@ FwdPlan forward_plan(int64_t T, int64_t V, int64_t D, const void* H, int64_t ldh
     return f;
 }
 
-// Bytes that a piece of G may take.  Each piece costs three launches, whose
-// first and last tiles leave SMs idle; a larger one costs memory only.
+// Bytes that a piece of G may take.  Each piece costs two launches, whose first
+// and last tiles leave SMs idle; a larger one costs memory only (64, 128, 256
+// and 512 MiB at 4096 x 4096 x 65536: 3783, 3674, 3673 and 3632 us).
 constexpr int64_t kPieceBytes = 512LL << 20;
 
 struct BwdPlan {
