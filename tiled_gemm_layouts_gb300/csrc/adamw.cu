@@ -13,7 +13,8 @@
 // roundings to 8 bits: sqrt(v) and the quotients by a block's scales are an
 // approximation and one correction by its fused remainder (Markstein 1990).
 // (Library quotients and roots, one byte converted at a time: 819 us for 2e8
-// elements.)
+// elements; as it is now 519 to 523, 6.1 TB/s, with 78 % of the issue slots
+// taken.  32-bit states move 28 bytes per element at 7.0 TB/s.)
 //
 // 32-bit states are two floats per element.  8-bit states are two e4m3 bytes
 // per element and, for each block of 256 elements, one fp32 scale each (a

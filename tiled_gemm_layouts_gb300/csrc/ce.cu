@@ -331,10 +331,14 @@ CeTile logits_tile(int64_t T, int64_t V) {
     return T > 128 && cdiv(T, 256) * cdiv(V, 256) >= kPairs ? CeTile{256, 1} : CeTile{128, 0};
 }
 
-// Tile of the gradients' products: the same rule on the tiles of dH and dW
-// together (128 x 512 x 4096: 25.2 us with pairs, 23.1 with single CTAs; 64 x
-// 1024 x 65536: 110 and 112).  A narrow D does not fill 256 columns.
+// Tile of the gradients' products.  For up to 128 tokens a pair would read W
+// at half the rate, for rows of dH that do not exist (with dH's contraction
+// split over all workers: 16 x 4096 x 32768 189 us with pairs and 162 with
+// single CTAs, 64 x 1024 x 65536 97 and 93, 128 x 512 x 4096 25.2 and 23.0);
+// beyond, the same rule on the tiles of dH and dW together (200 x 1024 x
+// 65536: 112 and 121).  A narrow D does not fill 256 columns.
 CeTile products_tile(int64_t T, int64_t cols, int64_t D) {
+    if (T <= 128) return CeTile{128, 0};
     const int bn = D > 128 ? 256 : 128;
     const int64_t tiles = (cdiv(T, 256) + cdiv(cols, 256)) * cdiv(D, bn);
     return tiles >= kPairs ? CeTile{bn, 1} : CeTile{128, 0};
@@ -396,7 +400,11 @@ BwdPlan backward_plan(int64_t T, int64_t V, int64_t D, const void* W, int64_t ld
     b.grad = logits_tile(T, V < b.piece ? V : b.piece);
     // A tile of dH contracts over the whole piece.  Where that is longer than
     // an equal share of all the products, split it into fp32 planes that the
-    // last kernel adds, each at least 8 K-blocks deep.
+    // last kernel adds, each at least 8 K-blocks deep.  For up to 128 tokens
+    // those planes are small beside W, which dH's workers have to read: split
+    // until every worker has a share of it, 24 K-blocks or more (8 x 856 x
+    // 54155: 87 us by the first rule, 75 by this; 128 x 300 x 20000 with
+    // shares of 12: 46.5 instead of 43.8).
     const int64_t cols = V < b.piece ? V : b.piece, kb = cdiv(cols, 64);
     b.products = products_tile(T, cols, D);
     const int64_t workers = b.products.pair ? sms / 2 : sms, bm = b.products.rows();
@@ -405,6 +413,7 @@ BwdPlan backward_plan(int64_t T, int64_t V, int64_t D, const void* W, int64_t ld
     const int64_t share = (n * std::max<int64_t>(kb, kCeTileBlocks) +
                            n_dw * std::max<int64_t>(cdiv(T, 64), kCeTileBlocks)) / workers + 1;
     int64_t splits = cdiv(kb, share);
+    if (T <= 128) splits = std::max(splits, std::min(workers / n, kb / 24));
     if (splits > kb / 8) splits = kb / 8;
     if (splits < 1) splits = 1;
     b.dh_kb = up(cdiv(kb, splits), 2);

@@ -24,10 +24,12 @@
 // the status word is set, copies and MMAs in flight are drained, TMEM is
 // freed and the kernel returns.
 //
-// What bounds it: at T = 8192, D = 4096 the tensor pipe; the epilogue's
-// 128 x 256 exponentials per tile and SM take 2048 cycles of the special
-// function unit against 16384 cycles of products, beside them.  For a few
-// tokens, reading W.
+// What bounds it: at T = 8192, D = 4096, V = 131072 the tensor pipe and the
+// power it draws (the loss 4.87 to 5.0 ms, 1760 to 1805 TFLOP/s; at 4096 x
+// 2048 x 32768, alone, 2058 TFLOP/s with the tensor pipe 96 % busy).  The
+// exponentials run beside the products: 7 % of the special function unit
+// there.  At D below about 500 the epilogue shows.  For a few tokens, reading
+// W: one token against 131072 x 4096 takes 162 us, 6.6 TB/s.
 #pragma once
 
 #include "ce_params.h"
@@ -113,8 +115,8 @@ __device__ __forceinline__ void tma_add_3d(const CUtensorMap* map, uint32_t src,
 
 // Shared memory of a launch: the ring, and 4 KB of staging per epilogue warp
 // (32 rows of 128 bytes: 64 columns of 16 bits or 32 of fp32).  More staging
-// at the price of ring slots was slower: 4 slots and 12 KB per warp took 108
-// us for 8 x 856 x 54155, 6 slots 92.
+// at the price of ring slots was slower: 4 slots and 12 KB per warp took 82
+// us for 8 x 856 x 54155, 6 slots 75.
 template <int BN, bool PAIR>
 struct CeShape : TileShape<BN, PAIR> {
     using TS = TileShape<BN, PAIR>;
@@ -598,6 +600,11 @@ __global__ void __launch_bounds__(kCeThreads, 1) ce_kernel(const __grid_constant
                     fence_proxy_async_shared();
                     __syncwarp();
                 };
+                // G's rows past the last K-block of dW's contraction are not read
+                if (MODE == CE_GRAD && row0 >= ((max(live, 1) + kBK - 1) & ~(kBK - 1))) {
+                    release();
+                    continue;
+                }
 #pragma unroll 1
                 for (int c = 0; c < kChunks; c += 2) {
                     const int c0 = n0 + c * 32;

@@ -7,11 +7,19 @@
 //
 // Both are bound by memory: every element is read once and written once.  A
 // row stays in registers between its two reductions (mean, then squared
-// differences from it: no cancellation), held by one warp up to 1024 columns
-// and by a block beyond.  The gradient's blocks walk over rows and keep their
-// columns' dw and db in fp32 registers; one partial row per block goes to the
-// workspace and a second kernel adds them in a fixed order, so results repeat
-// bit for bit.  Statistics and sums are fp32.
+// differences from it: no cancellation), held by one warp up to 512 columns
+// and by a team of up to 16 warps beyond.  Statistics and sums are fp32.
+//
+// Rows of whole 16-byte units come through a ring in shared memory: a team
+// walks over rows while bulk copies bring the next ones, so that loads never
+// wait for a reduction's barrier (16384 x 4096 in bf16: forward 46.5 us, 5.8
+// TB/s, backward 69.3 us, 5.8 TB/s; ring kernels).  Other rows are loaded by
+// element or by pair into registers, one row per team at a time, and rows too
+// long for registers are read again from L2 in chunks (wide kernels).
+//
+// The gradient's blocks walk over rows and keep their columns' dw and db in
+// fp32 registers; one partial row per block goes to the workspace and a second
+// kernel adds them in a fixed order, so results repeat bit for bit.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
