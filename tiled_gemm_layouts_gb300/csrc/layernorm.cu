@@ -13,9 +13,10 @@
 // Rows of whole 16-byte units come through a ring in shared memory: a team
 // walks over rows while bulk copies bring the next ones, so that loads never
 // wait for a reduction's barrier (16384 x 4096 in bf16: forward 46.5 us, 5.8
-// TB/s, backward 69.3 us, 5.8 TB/s; ring kernels).  Other rows are loaded by
-// element or by pair into registers, one row per team at a time, and rows too
-// long for registers are read again from L2 in chunks (wide kernels).
+// TB/s, backward 69.3 us, 5.8 TB/s).  So do long rows of other widths or
+// alignments (16384 x 4095: forward 57.7 us, backward 95.7 with its reduction).
+// Short ones are loaded by element or by pair into registers, and rows too long
+// for registers are read again from L2 in chunks (wide kernels).
 //
 // The gradient's blocks walk over rows and keep their columns' dw and db in
 // fp32 registers; one partial row per block goes to the workspace and a second
@@ -91,26 +92,29 @@ __device__ __forceinline__ void store(uint16_t* p, int left, const Pack<VEC>& v)
     }
 }
 
-// Sums of N values over the WARPS warps that share a row; every thread gets
-// them.  `buf` has room for N * WARPS floats and alternates between calls, so
-// one barrier per call is enough.
+// Sums of N values over the WARPS warps that share a row (0: the block's, up to
+// 16); every thread gets them.  `buf` has room for N * row_slots(WARPS) floats and
+// alternates between calls, so one barrier per call is enough.
+__host__ __device__ constexpr int row_slots(int warps) { return warps ? warps : 16; }
 template <int N, int WARPS>
 __device__ __forceinline__ void row_sum(float (&v)[N], float* buf) {
 #pragma unroll
     for (int o = 16; o; o >>= 1)
 #pragma unroll
         for (int k = 0; k < N; ++k) v[k] += __shfl_xor_sync(0xffffffffu, v[k], o);
-    if constexpr (WARPS > 1) {
+    if constexpr (WARPS != 1) {
+        constexpr int SLOTS = row_slots(WARPS);
         const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+        const int warps = WARPS ? WARPS : (int)blockDim.x >> 5;
         if (lane == 0)
 #pragma unroll
-            for (int k = 0; k < N; ++k) buf[k * WARPS + warp] = v[k];
+            for (int k = 0; k < N; ++k) buf[k * SLOTS + warp] = v[k];
         __syncthreads();
 #pragma unroll
         for (int k = 0; k < N; ++k) {
-            float x = lane < WARPS ? buf[k * WARPS + lane] : 0.0f;
+            float x = lane < warps ? buf[k * SLOTS + lane] : 0.0f;
 #pragma unroll
-            for (int o = WARPS / 2; o; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+            for (int o = SLOTS / 2; o; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
             v[k] = __shfl_sync(0xffffffffu, x, 0);
         }
     }
@@ -128,6 +132,7 @@ struct LnParams {
     float *mean, *rstd;
     float* part;  // gradient: [blocks][2][cols]
     int stages;   // ring: rows in flight per team
+    const uint16_t *x_end, *dy_end;  // ring: ends of x and dy
     long long timeout_cycles;
     int* status;
 };
@@ -186,11 +191,98 @@ __device__ __forceinline__ bool stage_ready(uint32_t bar, uint32_t parity, const
     return true;
 }
 
-// WARPS warps per row, NV packs of VEC elements per thread.  Rows wider than
-// that (WIDE) are read again from memory, which finds most of them in L2.
+// Rows of other widths or alignments (SHIFT).  A team walks over rows by a
+// multiple of 8, so where its rows start within 16 bytes is the same for all of
+// them, whatever the stride.  Its threads take windows of 8 columns that are
+// aligned in the *output*, whose stores are then whole; the weights are loaded
+// once, at that shift.  A stage holds the aligned 16-byte units around a row,
+// and a window is funnelled out of two of them (by 15 selects and shifts; none
+// where input and output are shifted alike).  The columns before the first
+// window and after the last, 14 at most, are taken one each by the team's last
+// threads.  (Windows over the row's ends instead, with what lies outside masked:
+// 64 us for 16384 x 4089 where whole rows of 4096 took 53; the masks and element
+// stores of two warps held up the row's barriers.)
+__host__ __device__ constexpr uint32_t stage_bytes(bool shift, int cols) {
+    return shift ? (((uint32_t)cols + 14) / 8 + 1) * 16 : (uint32_t)cols * 2;
+}
+__device__ __forceinline__ int shift_of(const uint16_t* row) {
+    return (int)(reinterpret_cast<uintptr_t>(row) & 15u) >> 1;
+}
+
+// Where a thread's columns are.
+struct Columns {
+    int front;    // columns before the first window
+    int end;      // end of the last window
+    int extra;    // the thread's single column, or -1
+};
+template <bool SHIFT>
+__device__ __forceinline__ Columns columns_of(const uint16_t* out, int cols, int tid, int width) {
+    if constexpr (!SHIFT) return {0, cols, -1};
+    Columns c;
+    c.front = min(-shift_of(out) & 7, cols);
+    c.end = c.front + ((cols - c.front) & ~7);
+    const int k = width - 1 - tid, e = k < c.front ? k : c.end + k - c.front;
+    c.extra = e < cols ? e : -1;
+    return c;
+}
+
+// The bulk copy of a row into a stage.  Units that reach past the operand's
+// end are left out, and their part of the row is stored by this thread; it
+// arrives on the stage's barrier afterwards, which hands them over.
+struct RowCopy {
+    const uint8_t* src;
+    uint32_t bytes;
+};
+__device__ __forceinline__ RowCopy row_copy(uint8_t* dst, const uint16_t* row, const uint16_t* end,
+                                            int cols) {
+    const uintptr_t at = reinterpret_cast<uintptr_t>(row), from = at & ~uintptr_t(15);
+    const uint32_t lead = (uint32_t)(at - from), need = lead + (uint32_t)cols * 2;
+    uint32_t bytes = (need + 15) & ~15u;
+    if (from + bytes > reinterpret_cast<uintptr_t>(end)) {
+        bytes = need & ~15u;
+        for (uint32_t k = max(bytes, lead); k < need; k += 2)
+            *reinterpret_cast<uint16_t*>(dst + k) = row[(k - lead) / 2];
+    }
+    return {reinterpret_cast<const uint8_t*>(from), bytes};
+}
+
+// Window `k` of a stage: 8 elements from `off` elements into unit k.
+__device__ __forceinline__ Pack<8> window(const uint8_t* stage, int k, int off) {
+    const uint4* v = reinterpret_cast<const uint4*>(stage) + k + (off >> 3);
+    const int s = off & 7;
+    uint4 a = v[0];
+    if (s) {
+        const uint4 b = v[1];
+        const bool four = s & 4, two = s & 2;
+        const uint32_t w0 = four ? a.z : a.x, w1 = four ? a.w : a.y, w2 = four ? b.x : a.z,
+                       w3 = four ? b.y : a.w, w4 = four ? b.z : b.x, w5 = four ? b.w : b.y;
+        const uint32_t v0 = two ? w1 : w0, v1 = two ? w2 : w1, v2 = two ? w3 : w2,
+                       v3 = two ? w4 : w3, v4 = two ? w5 : w4;
+        const uint32_t bits = (uint32_t)(s & 1) * 16;
+        a = make_uint4(__funnelshift_r(v0, v1, bits), __funnelshift_r(v1, v2, bits),
+                       __funnelshift_r(v2, v3, bits), __funnelshift_r(v3, v4, bits));
+    }
+    Pack<8> o;
+    *reinterpret_cast<uint4*>(&o) = a;
+    return o;
+}
+// 8 columns of the weights or the bias from `c`.
+template <bool SHIFT>
+__device__ __forceinline__ Pack<8> load_columns(const uint16_t* p, int c, int end) {
+    if constexpr (!SHIFT) return load<8, true>(p + c, end - c);
+    Pack<8> v{};
+    if (c < end)
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v.e[j] = __ldg(p + c + j);
+    return v;
+}
+
+// WARPS warps per row, NV packs of VEC elements per thread.
 constexpr int kRowsPerBlock = 4;  // rows of a block whose rows take one warp each
 constexpr int row_threads(int warps) { return 32 * (warps == 1 ? kRowsPerBlock : warps); }
 
+// A row in registers, or (WIDE) read again from memory for each pass, which
+// finds most of it in L2.
 template <bool BF, int VEC, bool WHOLE, int WARPS, int NV, bool WIDE>
 __global__ void __launch_bounds__(row_threads(WARPS), WARPS == 16 ? 2 : 1)
 ln_forward_kernel(const LnParams p) {
@@ -274,22 +366,19 @@ ln_forward_kernel(const LnParams p) {
 
 // The forward pass through the ring: teams walk over rows.
 // (1024 threads per SM with 64 registers each: 49.5 us against 47.6.)
-constexpr int kForwardThreadsPerSm = 768;  // 85 registers each
-constexpr int forward_blocks_per_sm(int warps) {
-    return row_threads(warps) >= 512 ? 1 : kForwardThreadsPerSm / row_threads(warps);
-}
-
-template <bool BF, int WARPS, int NV>
-__global__ void __launch_bounds__(row_threads(WARPS), forward_blocks_per_sm(WARPS))
+constexpr int forward_threads(int nv) { return nv == 4 ? 512 : 768; }  // per SM
+constexpr int most_threads(int warps) { return warps ? row_threads(warps) : 512; }
+template <bool BF, int WARPS, int NV, bool SHIFT>
+__global__ void __launch_bounds__(most_threads(WARPS), forward_threads(NV) / most_threads(WARPS))
 ln_forward_ring_kernel(const LnParams p) {
-    constexpr int VEC = 8, kStep = 32 * WARPS * VEC, PAIRS = VEC / 2;
-    constexpr int kTeams = WARPS == 1 ? kRowsPerBlock : 1;
+    constexpr int VEC = 8, PAIRS = VEC / 2, kTeams = WARPS == 1 ? kRowsPerBlock : 1;
     extern __shared__ __align__(128) uint8_t ring[];
-    __shared__ float buf[2][WARPS == 1 ? 1 : WARPS];
+    __shared__ float buf[2][row_slots(WARPS)];
     __shared__ uint64_t full[kTeams][kMaxStages];
     const int tid = WARPS == 1 ? threadIdx.x & 31 : threadIdx.x;
+    const int width = WARPS ? 32 * WARPS : (int)blockDim.x;  // threads of a team
     const int team = WARPS == 1 ? threadIdx.x >> 5 : 0;
-    const uint32_t bytes = (uint32_t)p.cols * 2;
+    const uint32_t bytes = stage_bytes(SHIFT, p.cols);
     uint8_t* stages = ring + (size_t)team * p.stages * bytes;
     if (threadIdx.x < kTeams * kMaxStages) mbar_init(smem_addr(&full[0][0] + threadIdx.x), 1);
     if (threadIdx.x == 0) fence_barrier_init();
@@ -297,18 +386,32 @@ ln_forward_ring_kernel(const LnParams p) {
     const long long first = (long long)blockIdx.x * kTeams + team, step = (long long)gridDim.x * kTeams;
     auto issue = [&](long long row, int st) {
         const uint32_t bar = smem_addr(&full[team][st]);
-        mbar_arrive_expect_tx(bar, bytes);
-        bulk_load(smem_addr(stages + st * bytes), p.x + row * p.ldx, bytes, bar);
+        uint8_t* dst = stages + st * bytes;
+        if constexpr (SHIFT) {
+            const RowCopy x = row_copy(dst, p.x + row * p.ldx, p.x_end, p.cols);
+            mbar_arrive_expect_tx(bar, x.bytes);
+            if (x.bytes) bulk_load(smem_addr(dst), x.src, x.bytes, bar);
+        } else {
+            mbar_arrive_expect_tx(bar, bytes);
+            bulk_load(smem_addr(dst), p.x + row * p.ldx, bytes, bar);
+        }
     };
     if (tid == 0)
         for (int st = 0; st < p.stages && first + st * step < p.rows; ++st) issue(first + st * step, st);
+    const Columns at = columns_of<SHIFT>(p.out + first * p.ldo, p.cols, tid, width);
+    const int x_shift = SHIFT ? shift_of(p.x + first * p.ldx) : 0;
     Pack<VEC> w[NV], b[NV];
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-        const int c = i * kStep + tid * VEC;
-        w[i] = load<VEC, true>(p.weight + c, p.cols - c);
+        const int c = at.front + (i * width + tid) * VEC;
+        w[i] = load_columns<SHIFT>(p.weight, c, at.end);
         b[i] = Pack<VEC>{};
-        if (p.bias) b[i] = load<VEC, true>(p.bias + c, p.cols - c);
+        if (p.bias) b[i] = load_columns<SHIFT>(p.bias, c, at.end);
+    }
+    float we = 0.0f, be = 0.0f;  // of the single column
+    if (SHIFT && at.extra >= 0) {
+        we = widen<BF>(__ldg(p.weight + at.extra));
+        if (p.bias) be = widen<BF>(__ldg(p.bias + at.extra));
     }
     int st = 0;
     uint32_t phase = 0;
@@ -317,9 +420,14 @@ ln_forward_ring_kernel(const LnParams p) {
         f2 v[NV][PAIRS], acc = pair(0.0f, 0.0f);
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
-            const int c = i * kStep + tid * VEC;
+            const int c = at.front + (i * width + tid) * VEC;
             Pack<VEC> x{};
-            if (c < p.cols) x = *reinterpret_cast<const Pack<VEC>*>(stages + st * bytes + c * 2);
+            if (c < at.end) {
+                if constexpr (SHIFT)
+                    x = window(stages + st * bytes, i * width + tid, x_shift + at.front);
+                else
+                    x = *reinterpret_cast<const Pack<VEC>*>(stages + st * bytes + c * 2);
+            }
 #pragma unroll
             for (int j = 0; j < PAIRS; ++j) {
                 v[i][j] = widen2<BF>(x.e + 2 * j);
@@ -328,6 +436,11 @@ ln_forward_ring_kernel(const LnParams p) {
         }
         float2 a = split(acc);
         float sum[1] = {a.x + a.y};
+        float ve = 0.0f;
+        if (SHIFT && at.extra >= 0) {
+            ve = widen<BF>(*reinterpret_cast<const uint16_t*>(stages + st * bytes + (x_shift + at.extra) * 2));
+            sum[0] += ve;
+        }
         row_sum<1, WARPS>(sum, buf[0]);
         // everyone has read the stage
         if constexpr (WARPS == 1) __syncwarp();
@@ -336,15 +449,21 @@ ln_forward_ring_kernel(const LnParams p) {
         const f2 minus = pair(-mean, -mean);
         acc = pair(0.0f, 0.0f);
 #pragma unroll
-        for (int i = 0; i < NV; ++i)
-            if (i * kStep + tid * VEC < p.cols)
+        for (int i = 0; i < NV; ++i) {
+            const int c = at.front + (i * width + tid) * VEC;
+            if (c < at.end)
 #pragma unroll
                 for (int j = 0; j < PAIRS; ++j) {
                     v[i][j] = add(v[i][j], minus);
                     acc = fma(v[i][j], v[i][j], acc);
                 }
+        }
         a = split(acc);
         float sq[1] = {a.x + a.y};
+        if (SHIFT && at.extra >= 0) {
+            ve -= mean;
+            sq[0] = fmaf(ve, ve, sq[0]);
+        }
         row_sum<1, WARPS>(sq, buf[1]);
         const float rstd = 1.0f / sqrtf(sq[0] / (float)p.cols + p.eps);
         if (tid == 0) {
@@ -355,8 +474,8 @@ ln_forward_ring_kernel(const LnParams p) {
         uint16_t* y = p.out + row * p.ldo;
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
-            const int c = i * kStep + tid * VEC;
-            if (c >= p.cols) continue;
+            const int c = at.front + (i * width + tid) * VEC;
+            if (c >= at.end) continue;
             Pack<VEC> o;
 #pragma unroll
             for (int j = 0; j < PAIRS; ++j) {
@@ -364,8 +483,9 @@ ln_forward_ring_kernel(const LnParams p) {
                                                       widen2<BF>(b[i].e + 2 * j)));
                 *reinterpret_cast<uint32_t*>(o.e + 2 * j) = word;
             }
-            store<VEC, true>(y + c, p.cols - c, o);
+            *reinterpret_cast<Pack<VEC>*>(y + c) = o;
         }
+        if (SHIFT && at.extra >= 0) y[at.extra] = narrow<BF>(fmaf(ve * rstd, we, be));
         if (++st == p.stages) {
             st = 0;
             phase ^= 1;
@@ -374,11 +494,13 @@ ln_forward_ring_kernel(const LnParams p) {
 }
 
 // One partial row per block: [block][2][cols]; rows that a block's warps took
-// side by side are added in the order of the warps.
+// side by side are added in the order of the warps.  `dwe`, `dbe`: of a thread's
+// single column.
 template <int VEC, int WARPS, int NV>
 __device__ __forceinline__ void write_partials(const LnParams& p, const f2 (&dw)[NV][VEC / 2],
-                                               const f2 (&db)[NV][VEC / 2]) {
-    constexpr int kStep = 32 * WARPS * VEC, PAIRS = VEC / 2;
+                                               const f2 (&db)[NV][VEC / 2], const Columns& at, float dwe,
+                                               float dbe) {
+    constexpr int PAIRS = VEC / 2;
     const int tid = WARPS == 1 ? threadIdx.x & 31 : threadIdx.x;
     const int group = WARPS == 1 ? threadIdx.x >> 5 : 0;
     if constexpr (WARPS == 1) {
@@ -393,7 +515,7 @@ __device__ __forceinline__ void write_partials(const LnParams& p, const f2 (&dw)
             float* out = p.part + ((long long)blockIdx.x * 2 + what) * p.cols;
             for (int k = threadIdx.x; k < 32 * NV * PAIRS; k += 32 * kRowsPerBlock) {
                 const int i = k / (32 * PAIRS), j = k / 32 % PAIRS, lane = k % 32;
-                const int c = i * kStep + lane * VEC + 2 * j;
+                const int c = (i * 32 + lane) * VEC + 2 * j;
                 float2 s = part[0][k];
 #pragma unroll
                 for (int y = 1; y < kRowsPerBlock; ++y) {
@@ -409,38 +531,38 @@ __device__ __forceinline__ void write_partials(const LnParams& p, const f2 (&dw)
         float* out = p.part + (long long)blockIdx.x * 2 * p.cols;
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
-            const int c = i * kStep + tid * VEC;
+            const int c = at.front + (i * (int)blockDim.x + tid) * VEC;
 #pragma unroll
             for (int j = 0; j < PAIRS; ++j) {
                 const float2 a = split(dw[i][j]), b = split(db[i][j]);
-                if (c + 2 * j < p.cols) {
+                if (c + 2 * j < at.end) {
                     out[c + 2 * j] = a.x;
                     out[p.cols + c + 2 * j] = b.x;
                 }
-                if (c + 2 * j + 1 < p.cols) {
+                if (c + 2 * j + 1 < at.end) {
                     out[c + 2 * j + 1] = a.y;
                     out[p.cols + c + 2 * j + 1] = b.y;
                 }
             }
         }
+        if (at.extra >= 0) {
+            out[at.extra] = dwe;
+            out[p.cols + at.extra] = dbe;
+        }
     }
 }
 
-// dx, and this block's partial sums of dw and db; 16 elements per thread.  Up
-// to 8192 columns (512 threads, 128 registers each) the next row's loads are
-// in flight while this row is reduced and written, and xh and g stay in
-// registers between the reduction and dx; 1024 threads have 64 registers and
-// compute those two again, with the weights from L1.
+// dx, and this block's partial sums of dw and db; 16 elements per thread, 512
+// threads per SM with 128 registers each.  The next row's loads into registers
+// are in flight while this row is reduced and written; xh and g stay in
+// registers between the reduction and dx.  (Rows of whole pairs gain nothing
+// from loading pairs: 16384 x 1500 in bf16 68 us, by elements 48.)
 constexpr int kGradThreadsPerSm = 512;
-constexpr int grad_blocks_per_sm(int warps) {
-    return row_threads(warps) >= kGradThreadsPerSm ? 1 : kGradThreadsPerSm / row_threads(warps);
-}
 
-template <bool BF, int VEC, bool WHOLE, int WARPS, int NV>
-__global__ void __launch_bounds__(row_threads(WARPS), grad_blocks_per_sm(WARPS))
+template <bool BF, int WARPS, int NV>
+__global__ void __launch_bounds__(row_threads(WARPS), kGradThreadsPerSm / row_threads(WARPS))
 ln_backward_kernel(const LnParams p) {
-    constexpr bool AHEAD = WARPS < 32;
-    constexpr int kThreads = 32 * WARPS, kStep = kThreads * VEC, PAIRS = VEC / 2;
+    constexpr int VEC = 2, kStep = 32 * WARPS * VEC, PAIRS = VEC / 2;
     constexpr int kGroups = WARPS == 1 ? kRowsPerBlock : 1;  // rows in work at once
     __shared__ float buf[2][WARPS == 1 ? 1 : 2 * WARPS];
     const int tid = WARPS == 1 ? threadIdx.x & 31 : threadIdx.x;
@@ -450,7 +572,7 @@ ln_backward_kernel(const LnParams p) {
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
         const int c = i * kStep + tid * VEC;
-        if (AHEAD) w[i] = load<VEC, WHOLE>(p.weight + c, p.cols - c);
+        w[i] = load<VEC, false>(p.weight + c, p.cols - c);
 #pragma unroll
         for (int j = 0; j < PAIRS; ++j) dw[i][j] = db[i][j] = pair(0.0f, 0.0f);
     }
@@ -465,36 +587,29 @@ ln_backward_kernel(const LnParams p) {
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
             const int c = i * kStep + tid * VEC;
-            x[i] = load<VEC, WHOLE>(px + c, p.cols - c);
-            d[i] = load<VEC, WHOLE>(pd + c, p.cols - c);
+            x[i] = load<VEC, false>(px + c, p.cols - c);
+            d[i] = load<VEC, false>(pd + c, p.cols - c);
         }
         mean = __ldg(p.mean + row);
         rstd = __ldg(p.rstd + row);
     };
     long long row = (long long)blockIdx.x * kGroups + group;
-    if (AHEAD && row < p.rows) fetch(row, nx, nd);
+    if (row < p.rows) fetch(row, nx, nd);
     int flip = 0;
     for (; row < p.rows; row += step) {
-        if (!AHEAD) fetch(row, vx, vd);
         const float r = rstd;
         // x - mean first: scaled apart, the two would cancel with their roundings
         const f2 scale = pair(r, r), minus = pair(-mean, -mean);
-        if (AHEAD) {
-#pragma unroll
-            for (int i = 0; i < NV; ++i) {
-                vx[i] = nx[i];
-                vd[i] = nd[i];
-            }
-            if (row + step < p.rows) fetch(row + step, nx, nd);
-        }
-        f2 s0 = pair(0.0f, 0.0f), s1 = s0;  // sums of g and of g xh
-        f2 g[AHEAD ? NV : 1][PAIRS], xh[AHEAD ? NV : 1][PAIRS];
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
-            if (!AHEAD) {
-                const int c = i * kStep + tid * VEC;
-                w[i] = load<VEC, WHOLE>(p.weight + c, p.cols - c);
-            }
+            vx[i] = nx[i];
+            vd[i] = nd[i];
+        }
+        if (row + step < p.rows) fetch(row + step, nx, nd);
+        f2 s0 = pair(0.0f, 0.0f), s1 = s0;  // sums of g and of g xh
+        f2 g[NV][PAIRS], xh[NV][PAIRS];
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
 #pragma unroll
             for (int j = 0; j < PAIRS; ++j) {
                 // columns past the row's end hold zeros in dy and w: they add nothing
@@ -505,10 +620,8 @@ ln_backward_kernel(const LnParams p) {
                 s1 = fma(gg, x, s1);
                 dw[i][j] = fma(d, x, dw[i][j]);
                 db[i][j] = add(db[i][j], d);
-                if (AHEAD) {
-                    xh[i][j] = x;
-                    g[i][j] = gg;
-                }
+                xh[i][j] = x;
+                g[i][j] = gg;
             }
         }
         const float2 a = split(s0), b = split(s1);
@@ -522,37 +635,33 @@ ln_backward_kernel(const LnParams p) {
         for (int i = 0; i < NV; ++i) {
             const int c = i * kStep + tid * VEC;
             if (c >= p.cols) continue;
-            if (!AHEAD) w[i] = load<VEC, WHOLE>(p.weight + c, p.cols - c);
             Pack<VEC> o;
 #pragma unroll
             for (int j = 0; j < PAIRS; ++j) {
-                const f2 x = AHEAD ? xh[i][j] : mul(add(widen2<BF>(vx[i].e + 2 * j), minus), scale);
-                const f2 gg = AHEAD ? g[i][j]
-                                    : mul(widen2<BF>(vd[i].e + 2 * j), widen2<BF>(w[i].e + 2 * j));
-                const uint32_t word = narrow2<BF>(fma(x, k2, fma(gg, scale, k1)));
+                const uint32_t word = narrow2<BF>(fma(xh[i][j], k2, fma(g[i][j], scale, k1)));
                 *reinterpret_cast<uint32_t*>(o.e + 2 * j) = word;
             }
-            store<VEC, WHOLE>(dx + c, p.cols - c, o);
+            store<VEC, false>(dx + c, p.cols - c, o);
         }
     }
-    write_partials<VEC, WARPS, NV>(p, dw, db);
+    write_partials<VEC, WARPS, NV>(p, dw, db, {0, p.cols, -1}, 0.0f, 0.0f);
 }
 
-// The same through the ring.  A row's stage is read twice, before and after
-// its reduction, by 1024 threads, whose registers hold neither the row nor xh
-// and g; it is filled again after the next row's barrier.
-template <bool BF, int WARPS, int NV>
-__global__ void __launch_bounds__(row_threads(WARPS), grad_blocks_per_sm(WARPS))
+// The same through the ring.  With 4 packs per thread, whose sums alone are 64
+// registers, a row's stage is read twice, before and after its reduction, and
+// filled again after the next row's barrier.
+template <bool BF, int WARPS, int NV, bool SHIFT>
+__global__ void __launch_bounds__(most_threads(WARPS), kGradThreadsPerSm / most_threads(WARPS))
 ln_backward_ring_kernel(const LnParams p) {
-    constexpr bool KEEP = WARPS < 32;
-    constexpr int VEC = 8, kStep = 32 * WARPS * VEC, PAIRS = VEC / 2;
-    constexpr int kTeams = WARPS == 1 ? kRowsPerBlock : 1;
+    constexpr bool KEEP = NV < 4;
+    constexpr int VEC = 8, PAIRS = VEC / 2, kTeams = WARPS == 1 ? kRowsPerBlock : 1;
     extern __shared__ __align__(128) uint8_t ring[];
-    __shared__ float buf[2][WARPS == 1 ? 1 : 2 * WARPS];
+    __shared__ float buf[2][2 * row_slots(WARPS)];
     __shared__ uint64_t full[kTeams][kMaxStages];
     const int tid = WARPS == 1 ? threadIdx.x & 31 : threadIdx.x;
+    const int width = WARPS ? 32 * WARPS : (int)blockDim.x;  // threads of a team
     const int team = WARPS == 1 ? threadIdx.x >> 5 : 0;
-    const uint32_t bytes = (uint32_t)p.cols * 2;
+    const uint32_t bytes = stage_bytes(SHIFT, p.cols);
     uint8_t* stages = ring + (size_t)team * p.stages * 2 * bytes;
     allow_next_kernel();
     if (threadIdx.x < kTeams * kMaxStages) mbar_init(smem_addr(&full[0][0] + threadIdx.x), 1);
@@ -560,19 +669,43 @@ ln_backward_ring_kernel(const LnParams p) {
     __syncthreads();
     const long long first = (long long)blockIdx.x * kTeams + team, step = (long long)gridDim.x * kTeams;
     auto issue = [&](long long row, int st) {
-        const uint32_t bar = smem_addr(&full[team][st]), dst = smem_addr(stages + st * 2 * bytes);
-        mbar_arrive_expect_tx(bar, 2 * bytes);
-        bulk_load(dst, p.x + row * p.ldx, bytes, bar);
-        bulk_load(dst + bytes, p.dy + row * p.lddy, bytes, bar);
+        const uint32_t bar = smem_addr(&full[team][st]);
+        uint8_t* dst = stages + st * 2 * bytes;
+        if constexpr (SHIFT) {
+            const RowCopy x = row_copy(dst, p.x + row * p.ldx, p.x_end, p.cols);
+            const RowCopy d = row_copy(dst + bytes, p.dy + row * p.lddy, p.dy_end, p.cols);
+            mbar_arrive_expect_tx(bar, x.bytes + d.bytes);
+            if (x.bytes) bulk_load(smem_addr(dst), x.src, x.bytes, bar);
+            if (d.bytes) bulk_load(smem_addr(dst + bytes), d.src, d.bytes, bar);
+        } else {
+            mbar_arrive_expect_tx(bar, 2 * bytes);
+            bulk_load(smem_addr(dst), p.x + row * p.ldx, bytes, bar);
+            bulk_load(smem_addr(dst + bytes), p.dy + row * p.lddy, bytes, bar);
+        }
     };
     if (tid == 0)
         for (int st = 0; st < p.stages && first + st * step < p.rows; ++st) issue(first + st * step, st);
+    const Columns at = columns_of<SHIFT>(p.out + first * p.ldo, p.cols, tid, width);
+    const int x_shift = SHIFT ? shift_of(p.x + first * p.ldx) : 0;
+    const int d_shift = SHIFT ? shift_of(p.dy + first * p.lddy) : 0;
+    // x and dy of window i of a stage
+    auto operands = [&](const uint8_t* sx, int i, int c, Pack<VEC>& vx, Pack<VEC>& vd) {
+        if constexpr (SHIFT) {
+            vx = window(sx, i * width + tid, x_shift + at.front);
+            vd = window(sx + bytes, i * width + tid, d_shift + at.front);
+        } else {
+            vx = *reinterpret_cast<const Pack<VEC>*>(sx + c * 2);
+            vd = *reinterpret_cast<const Pack<VEC>*>(sx + bytes + c * 2);
+        }
+    };
+    float we = 0.0f, dwe = 0.0f, dbe = 0.0f;  // of the single column
+    if (SHIFT && at.extra >= 0) we = widen<BF>(__ldg(p.weight + at.extra));
     f2 dw[NV][PAIRS], db[NV][PAIRS];
     Pack<VEC> w[NV];
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-        const int c = i * kStep + tid * VEC;
-        w[i] = load<VEC, true>(p.weight + c, p.cols - c);
+        const int c = at.front + (i * width + tid) * VEC;
+        w[i] = load_columns<SHIFT>(p.weight, c, at.end);
 #pragma unroll
         for (int j = 0; j < PAIRS; ++j) dw[i][j] = db[i][j] = pair(0.0f, 0.0f);
     }
@@ -598,12 +731,9 @@ ln_backward_ring_kernel(const LnParams p) {
         f2 g[KEEP ? NV : 1][PAIRS], xh[KEEP ? NV : 1][PAIRS];
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
-            const int c = i * kStep + tid * VEC;
-            Pack<VEC> vx{}, vd{};  // columns past the row's end add nothing
-            if (c < p.cols) {
-                vx = *reinterpret_cast<const Pack<VEC>*>(sx + c * 2);
-                vd = *reinterpret_cast<const Pack<VEC>*>(sx + bytes + c * 2);
-            }
+            const int c = at.front + (i * width + tid) * VEC;
+            Pack<VEC> vx{}, vd{};  // columns past the end add nothing
+            if (c < at.end) operands(sx, i, c, vx, vd);
 #pragma unroll
             for (int j = 0; j < PAIRS; ++j) {
                 const f2 d = widen2<BF>(vd.e + 2 * j);
@@ -621,6 +751,16 @@ ln_backward_ring_kernel(const LnParams p) {
         }
         const float2 a = split(s0), b = split(s1);
         float s[2] = {a.x + a.y, b.x + b.y};
+        float xe = 0.0f, ge = 0.0f;
+        if (SHIFT && at.extra >= 0) {
+            const float d = widen<BF>(*reinterpret_cast<const uint16_t*>(sx + bytes + (d_shift + at.extra) * 2));
+            xe = (widen<BF>(*reinterpret_cast<const uint16_t*>(sx + (x_shift + at.extra) * 2)) - mean) * r;
+            ge = d * we;
+            s[0] += ge;
+            s[1] = fmaf(ge, xe, s[1]);
+            dwe = fmaf(d, xe, dwe);
+            dbe += d;
+        }
         row_sum<2, WARPS>(s, buf[flip]);
         flip ^= 1;
         if constexpr (WARPS == 1) __syncwarp();
@@ -635,13 +775,10 @@ ln_backward_ring_kernel(const LnParams p) {
         uint16_t* dx = p.out + row * p.ldo;
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
-            const int c = i * kStep + tid * VEC;
-            if (c >= p.cols) continue;
+            const int c = at.front + (i * width + tid) * VEC;
+            if (c >= at.end) continue;
             Pack<VEC> o, vx, vd;
-            if (!KEEP) {
-                vx = *reinterpret_cast<const Pack<VEC>*>(sx + c * 2);
-                vd = *reinterpret_cast<const Pack<VEC>*>(sx + bytes + c * 2);
-            }
+            if (!KEEP) operands(sx, i, c, vx, vd);
 #pragma unroll
             for (int j = 0; j < PAIRS; ++j) {
                 const f2 x = KEEP ? xh[i][j] : mul(add(widen2<BF>(vx.e + 2 * j), minus), scale);
@@ -649,14 +786,15 @@ ln_backward_ring_kernel(const LnParams p) {
                 const uint32_t word = narrow2<BF>(fma(x, k2, fma(gg, scale, k1)));
                 *reinterpret_cast<uint32_t*>(o.e + 2 * j) = word;
             }
-            store<VEC, true>(dx + c, p.cols - c, o);
+            *reinterpret_cast<Pack<VEC>*>(dx + c) = o;
         }
+        if (SHIFT && at.extra >= 0) dx[at.extra] = narrow<BF>(fmaf(xe, c2, fmaf(ge, r, c1)));
         if (++st == p.stages) {
             st = 0;
             phase ^= 1;
         }
     }
-    write_partials<VEC, WARPS, NV>(p, dw, db);
+    write_partials<VEC, WARPS, NV>(p, dw, db, at, dwe, dbe);
 }
 
 // Rows too wide for registers: dx alone, one block per row.
@@ -752,31 +890,51 @@ int pack_of(int64_t cols, std::initializer_list<const void*> ptrs, std::initiali
     return 0;
 }
 
-// Row shapes: F(warps per row, packs per thread) for the first that holds
-// `cols`: up to 16 elements per thread, in packs of 8 or of 2.
-#define TG_LN_SHAPES_8(F)        \
-    if (cols <= 256) F(1, 1)     \
-    if (cols <= 512) F(1, 2)     \
-    if (cols <= 1024) F(2, 2)    \
-    if (cols <= 2048) F(4, 2)    \
-    if (cols <= 4096) F(8, 2)    \
-    if (cols <= 8192) F(16, 2)   \
-    if (cols <= 16384) F(32, 2)
-#define TG_LN_SHAPES_2(F)        \
-    if (cols <= 256) F(1, 4)     \
-    if (cols <= 512) F(1, 8)     \
-    if (cols <= 1024) F(2, 8)    \
-    if (cols <= 2048) F(4, 8)    \
-    if (cols <= 4096) F(8, 8)    \
-    if (cols <= 8192) F(16, 8)
+// How a row is held.
+struct RowShape {
+    int warps, packs, vec;  // no warps: too wide for registers
+    bool ring;
+    int rows() const { return warps == 1 ? kRowsPerBlock : 1; }  // of a block
+    int threads() const { return 32 * warps * rows(); }
+};
+// Warps for `cols` at 512 columns each: 1, 2, 4 or 8.
+int even_warps(int64_t cols) { return cols <= 512 ? 1 : cols <= 1024 ? 2 : cols <= 2048 ? 4 : 8; }
+
+// Forward.  Aligned rows go through the ring, others from 1024 columns on
+// (16000 x 1001: 22.2 us, in registers 24.7; 16384 x 255: 10.5 and 8.6).  Beyond
+// 4096 columns as few warps as hold a row with 4 packs each, so that two or
+// three rows are in work on an SM, which hides a row's barriers (8000 x 5120:
+// 33 us; 16 warps of 2 packs, one row per SM, 56; 8192: 46 and 60).
+RowShape forward_shape(int64_t cols, int vec) {
+    if (cols > 16384) return {0, 0, vec, false};
+    if (cols > 4096) return {(int)cdiv(cols, 1024), 4, vec, true};
+    const int warps = even_warps(cols);
+    if (vec == 8 || cols > 1024) return {warps, cols <= 256 ? 1 : 2, vec, true};
+    return {warps, cols <= 256 ? 4 : 8, vec, false};
+}
+// Backward.  Aligned rows go through the ring, others from 2048 columns on (16384
+// x 4095: 96 us, in registers 107; 10000 x 2047: 46 and 37).  From 8192 on with 4
+// packs per thread (4545 x 14557: 116 us; 1024 threads of 2 packs 211).
+RowShape backward_shape(int64_t cols, int vec) {
+    if (cols > 16384) return {0, 0, vec, false};
+    if (cols > 8192) return {(int)cdiv(cols, 1024), 4, vec, true};
+    if (cols > 4096) return {(int)cdiv(cols, 512), 2, vec, true};
+    const int warps = even_warps(cols);
+    if (vec == 8 || cols > 2048) return {warps, cols <= 256 ? 1 : 2, vec, true};
+    return {warps, cols <= 256 ? 4 : 8, vec, false};
+}
+// Blocks that walk over rows by a multiple of 8 (or have one row each).
+int64_t walking_blocks(int64_t need, int64_t most) {
+    return need <= most ? need : most < 8 ? 8 : most / 8 * 8;
+}
 
 // Launches a ring kernel: `operands` rows per stage, `per_sm` blocks on an SM.
 template <auto Kern>
-cudaError_t launch_ring(LnParams p, int warps, int operands, int per_sm, int64_t blocks,
+cudaError_t launch_ring(LnParams p, const RowShape& s, int operands, int per_sm, int64_t blocks,
                         cudaStream_t stream) {
     constexpr size_t kRoom = 224 * 1024;  // of an SM's shared memory
     // a block's own part: its static shared memory and the 1 KB it reserves
-    const size_t fixed = warps == 1 ? 10240 : 2048;
+    const size_t fixed = s.warps == 1 ? 10240 : 2048;
     static std::atomic<unsigned long long> attr_set{0};  // one bit per device
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
@@ -788,49 +946,59 @@ cudaError_t launch_ring(LnParams p, int warps, int operands, int per_sm, int64_t
         if (e != cudaSuccess) return e;
         attr_set.fetch_or(bit, std::memory_order_release);
     }
-    const size_t stage = (size_t)(warps == 1 ? kRowsPerBlock : 1) * operands * p.cols * 2;
+    const size_t stage = (size_t)s.rows() * operands * stage_bytes(s.vec != 8, p.cols);
     size_t stages = (kRoom / per_sm - fixed) / stage;
     if (stages > kMaxStages) stages = kMaxStages;
     p.stages = (int)stages;
-    Kern<<<(unsigned)blocks, row_threads(warps), stages * stage, stream>>>(p);
+    Kern<<<(unsigned)blocks, s.threads(), stages * stage, stream>>>(p);
     return cudaGetLastError();
 }
 
 template <bool BF>
 cudaError_t launch_forward(const LnParams& p, int vec, int sms, cudaStream_t stream) {
-    const int cols = p.cols;
-#define TG_LAUNCH(WARPS, NV, VEC, WHOLE, WIDE)                                                       \
-    {                                                                                              \
-        const long long blocks = WARPS == 1 ? cdiv(p.rows, kRowsPerBlock) : p.rows;                \
-        ln_forward_kernel<BF, VEC, WHOLE, WARPS, NV, WIDE>                                         \
-            <<<(unsigned)blocks, row_threads(WARPS), 0, stream>>>(p);                              \
-        return cudaGetLastError();                                                                 \
+    const RowShape s = forward_shape(p.cols, vec);
+    if (s.ring) {
+        const int per_sm = forward_threads(s.packs) / s.threads();
+        const int64_t blocks = walking_blocks(cdiv(p.rows, s.rows()), (int64_t)sms * per_sm);
+#define TG_RING(COND, WARPS, NV, SHIFT)                                                             \
+    if ((COND) && s.packs == NV && (vec != 8) == SHIFT)                                             \
+        return launch_ring<ln_forward_ring_kernel<BF, WARPS, NV, SHIFT>>(p, s, 1, per_sm, blocks, stream);
+        TG_RING(s.warps == 1, 1, 1, false)
+        TG_RING(s.warps == 1, 1, 2, false)
+        TG_RING(s.warps == 2, 2, 2, false)
+        TG_RING(s.warps == 4, 4, 2, false)
+        TG_RING(s.warps == 8, 8, 2, false)
+        TG_RING(true, 0, 4, false)
+        TG_RING(s.warps == 4, 4, 2, true)
+        TG_RING(s.warps == 8, 8, 2, true)
+        TG_RING(true, 0, 4, true)
+#undef TG_RING
+        return cudaErrorInvalidValue;
     }
-#define TG_FR(WARPS, NV)                                                                       \
-    {                                                                                          \
-        const int64_t need = cdiv(p.rows, WARPS == 1 ? kRowsPerBlock : 1);                     \
-        const int64_t most = (int64_t)sms * forward_blocks_per_sm(WARPS);                      \
-        return launch_ring<ln_forward_ring_kernel<BF, WARPS, NV>>(                             \
-            p, WARPS, 1, forward_blocks_per_sm(WARPS), need < most ? need : most, stream);     \
+    if (!s.warps) {
+        const dim3 grid((unsigned)p.rows);
+        if (vec == 8)
+            ln_forward_kernel<BF, 8, true, 32, 2, true><<<grid, 1024, 0, stream>>>(p);
+        else if (vec == 2)
+            ln_forward_kernel<BF, 2, true, 32, 8, true><<<grid, 1024, 0, stream>>>(p);
+        else
+            ln_forward_kernel<BF, 2, false, 32, 8, true><<<grid, 1024, 0, stream>>>(p);
+        return cudaGetLastError();
     }
-#define TG_F2(WARPS, NV) TG_LAUNCH(WARPS, NV, 2, true, false)
-#define TG_F0(WARPS, NV) TG_LAUNCH(WARPS, NV, 2, false, false)
-    if (vec == 8) {
-        TG_LN_SHAPES_8(TG_FR)
-        TG_LAUNCH(32, 2, 8, true, true)
+    const unsigned blocks = (unsigned)cdiv(p.rows, s.rows());
+#define TG_REGS(WARPS, NV)                                                                            \
+    if (s.warps == WARPS && s.packs == NV) {                                                          \
+        if (vec == 2)                                                                                 \
+            ln_forward_kernel<BF, 2, true, WARPS, NV, false><<<blocks, s.threads(), 0, stream>>>(p);  \
+        else                                                                                          \
+            ln_forward_kernel<BF, 2, false, WARPS, NV, false><<<blocks, s.threads(), 0, stream>>>(p); \
+        return cudaGetLastError();                                                                    \
     }
-    if (vec == 2) {
-        TG_LN_SHAPES_2(TG_F2)
-        if (cols <= 16384) TG_F2(16, 16)  // two rows per SM at a time
-        TG_LAUNCH(32, 8, 2, true, true)
-    }
-    TG_LN_SHAPES_2(TG_F0)
-    if (cols <= 16384) TG_F0(16, 16)
-    TG_LAUNCH(32, 8, 2, false, true)
-#undef TG_FR
-#undef TG_F2
-#undef TG_F0
-#undef TG_LAUNCH
+    TG_REGS(1, 4)
+    TG_REGS(1, 8)
+    TG_REGS(2, 8)
+#undef TG_REGS
+    return cudaErrorInvalidValue;
 }
 
 // Blocks of the gradient's kernel, each of which leaves one partial row of dw
@@ -838,75 +1006,60 @@ cudaError_t launch_forward(const LnParams& p, int vec, int sms, cudaStream_t str
 // block (a partial row is 8 bytes per column against 6 per element; four rows
 // each and two blocks: 1000 x 4096 21.5 us instead of 16.4).
 struct GradShape {
-    int warps, packs, vec;  // warps 0: the wide kernels
-    int parts;
+    RowShape row;
+    int per_sm, parts;
 };
 
 GradShape grad_shape(int64_t rows, int64_t cols, int vec, int sms) {
-    GradShape s{0, 0, vec, 0};
-#define TG_SET(WARPS, NV)              \
-    {                                  \
-        if (!s.warps) {                \
-            s.warps = WARPS;           \
-            s.packs = NV;              \
-        }                              \
+    GradShape g{backward_shape(cols, vec), 0, 0};
+    if (!g.row.warps) {
+        g.parts = (int)(rows < 64 ? rows : 64);
+        return g;
     }
-    if (vec == 8) {
-        TG_LN_SHAPES_8(TG_SET)
-    } else {
-        TG_LN_SHAPES_2(TG_SET)
-        if (cols <= 16384) TG_SET(32, 8)
-    }
-#undef TG_SET
-    if (!s.warps) {
-        s.parts = (int)(rows < 64 ? rows : 64);
-        return s;
-    }
-    const int groups = s.warps == 1 ? kRowsPerBlock : 1;
-    const int64_t steps = cdiv(rows, groups);
+    g.per_sm = kGradThreadsPerSm / g.row.threads();
+    const int64_t steps = cdiv(rows, g.row.rows());
     int64_t blocks = steps / 8;
     if (blocks < sms) blocks = sms;
-    const int64_t most = (int64_t)sms * grad_blocks_per_sm(s.warps);
+    const int64_t most = (int64_t)sms * g.per_sm;
     if (blocks > most) blocks = most;
-    if (blocks > steps) blocks = steps;
-    s.parts = (int)blocks;
-    return s;
+    g.parts = (int)walking_blocks(steps, blocks);
+    return g;
 }
 
 template <bool BF>
-cudaError_t launch_backward(const LnParams& p, const GradShape& s, cudaStream_t stream) {
-#define TG_LAUNCH(WARPS, NV, VEC, WHOLE)                                                              \
-    if (s.warps == WARPS && s.packs == NV) {                                                          \
-        ln_backward_kernel<BF, VEC, WHOLE, WARPS, NV>                                                 \
-            <<<s.parts, row_threads(WARPS), 0, stream>>>(p);                                          \
-        return cudaGetLastError();                                                                    \
-    }
-#define TG_BR(WARPS, NV)                                                                              \
-    return launch_ring<ln_backward_ring_kernel<BF, WARPS, NV>>(p, WARPS, 2, grad_blocks_per_sm(WARPS), \
-                                                               s.parts, stream);
-#define TG_B2(WARPS, NV) TG_LAUNCH(WARPS, NV, 2, true)
-#define TG_B0(WARPS, NV) TG_LAUNCH(WARPS, NV, 2, false)
-    const int cols = p.cols;
-    if (s.warps == 0) {
+cudaError_t launch_backward(const LnParams& p, const GradShape& g, cudaStream_t stream) {
+    const RowShape& s = g.row;
+    if (!s.warps) {
         ln_backward_wide_kernel<BF><<<(unsigned)p.rows, 1024, 0, stream>>>(p);
         const cudaError_t e = cudaGetLastError();
         return e != cudaSuccess ? e
                                 : launch_chained(ln_backward_wide_columns_kernel<BF>,
-                                                 dim3((unsigned)cdiv(cols, 256), s.parts), 256, stream, p);
+                                                 dim3((unsigned)cdiv(p.cols, 256), g.parts), 256, stream, p);
     }
-    if (s.vec == 8) {
-        TG_LN_SHAPES_8(TG_BR)
-    } else if (s.vec == 2) {
-        TG_LN_SHAPES_2(TG_B2)
-        TG_B2(32, 8)
-    } else {
-        TG_LN_SHAPES_2(TG_B0)
-        TG_B0(32, 8)
+#define TG_RING(COND, WARPS, NV, SHIFT)                                                              \
+    if (s.ring && (COND) && s.packs == NV && (s.vec != 8) == SHIFT)                                  \
+        return launch_ring<ln_backward_ring_kernel<BF, WARPS, NV, SHIFT>>(p, s, 2, g.per_sm, g.parts, stream);
+    TG_RING(s.warps == 1, 1, 1, false)
+    TG_RING(s.warps == 1, 1, 2, false)
+    TG_RING(s.warps == 2, 2, 2, false)
+    TG_RING(s.warps == 4, 4, 2, false)
+    TG_RING(s.warps == 8, 8, 2, false)
+    TG_RING(true, 0, 2, false)
+    TG_RING(true, 0, 4, false)
+    TG_RING(s.warps == 8, 8, 2, true)
+    TG_RING(true, 0, 2, true)
+    TG_RING(true, 0, 4, true)
+#undef TG_RING
+#define TG_REGS(WARPS, NV)                                                             \
+    if (s.warps == WARPS && s.packs == NV) {                                           \
+        ln_backward_kernel<BF, WARPS, NV><<<g.parts, s.threads(), 0, stream>>>(p);     \
+        return cudaGetLastError();                                                     \
     }
-#undef TG_BR
-#undef TG_B2
-#undef TG_B0
-#undef TG_LAUNCH
+    TG_REGS(1, 4)
+    TG_REGS(1, 8)
+    TG_REGS(2, 8)
+    TG_REGS(4, 8)
+#undef TG_REGS
     return cudaErrorInvalidValue;
 }
 
@@ -953,6 +1106,7 @@ extern "C" int tg_layernorm(int64_t rows, int64_t cols, const void* X, int64_t l
     p.cols = (int)cols;
     p.x = static_cast<const uint16_t*>(X);
     p.ldx = ldx;
+    p.x_end = p.x + (rows - 1) * ldx + cols;
     p.weight = static_cast<const uint16_t*>(weight);
     p.bias = static_cast<const uint16_t*>(bias);
     p.eps = eps;
@@ -971,7 +1125,6 @@ extern "C" int tg_layernorm(int64_t rows, int64_t cols, const void* X, int64_t l
     return TG_OK;
 }
 
-// The workspace holds the partial rows of the shape with the most of them.
 extern "C" int tg_layernorm_grad_workspace_size(int64_t rows, int64_t cols, tg_dtype dtype,
                                                 size_t* bytes) {
     int rc = check_sizes(rows, cols, (int)dtype);
@@ -980,12 +1133,8 @@ extern "C" int tg_layernorm_grad_workspace_size(int64_t rows, int64_t cols, tg_d
     int dev;
     DeviceInfo* info;
     if ((rc = current_device(&dev, &info))) return rc;
-    int64_t parts = 0;
-    for (int vec : {8, 2}) {
-        const GradShape s = grad_shape(rows, cols, vec, info->sms);
-        if (s.parts > parts) parts = s.parts;
-    }
-    *bytes = (size_t)parts * 2 * (size_t)cols * sizeof(float);
+    // (the alignment of the rows does not change their number)
+    *bytes = (size_t)grad_shape(rows, cols, 8, info->sms).parts * 2 * (size_t)cols * sizeof(float);
     return TG_OK;
 }
 
@@ -1041,8 +1190,10 @@ extern "C" int tg_layernorm_grad(int64_t rows, int64_t cols, const void* dY, int
     p.cols = (int)cols;
     p.x = static_cast<const uint16_t*>(X);
     p.ldx = ldx;
+    p.x_end = p.x + (rows - 1) * ldx + cols;
     p.dy = static_cast<const uint16_t*>(dY);
     p.lddy = lddy;
+    p.dy_end = p.dy + (rows - 1) * lddy + cols;
     p.weight = static_cast<const uint16_t*>(weight);
     p.out = static_cast<uint16_t*>(dX);
     p.ldo = lddx;
