@@ -677,7 +677,10 @@ __global__ void __launch_bounds__(kCeThreads, 1) ce_kernel(const __grid_constant
                         bulk_commit_group();
                     }
                     // columns the map cannot hold (all of them for an unaligned
-                    // dW): half a row of the step per store, lane = column
+                    // dW): half a row of the step per store, lane = column.  The
+                    // sectors that two stores share cost what they cost: 8 x 2001
+                    // x 40001 takes 108 us here where aligned rows take 60, and
+                    // 16-byte windows aligned in dW, 4 rows per store, took 125.
                     if (BOTH && c0 + 64 > p.n_tma && c0 < sd.out_cols) {
                         uint16_t* o = static_cast<uint16_t*>(p.out) + (long long)row0 * p.ldo + c0;
                         const int rows = min(32, sd.out_rows - row0);

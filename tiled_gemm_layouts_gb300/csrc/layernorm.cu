@@ -34,6 +34,7 @@
 #include "host_common.h"
 #include "packed.cuh"
 #include "ptx.cuh"
+#include "stage.cuh"
 
 namespace tg {
 namespace {
@@ -205,9 +206,6 @@ __device__ __forceinline__ bool stage_ready(uint32_t bar, uint32_t parity, const
 __host__ __device__ constexpr uint32_t stage_bytes(bool shift, int cols) {
     return shift ? (((uint32_t)cols + 14) / 8 + 1) * 16 : (uint32_t)cols * 2;
 }
-__device__ __forceinline__ int shift_of(const uint16_t* row) {
-    return (int)(reinterpret_cast<uintptr_t>(row) & 15u) >> 1;
-}
 
 // Where a thread's columns are.
 struct Columns {
@@ -251,17 +249,7 @@ __device__ __forceinline__ Pack<8> window(const uint8_t* stage, int k, int off) 
     const uint4* v = reinterpret_cast<const uint4*>(stage) + k + (off >> 3);
     const int s = off & 7;
     uint4 a = v[0];
-    if (s) {
-        const uint4 b = v[1];
-        const bool four = s & 4, two = s & 2;
-        const uint32_t w0 = four ? a.z : a.x, w1 = four ? a.w : a.y, w2 = four ? b.x : a.z,
-                       w3 = four ? b.y : a.w, w4 = four ? b.z : b.x, w5 = four ? b.w : b.y;
-        const uint32_t v0 = two ? w1 : w0, v1 = two ? w2 : w1, v2 = two ? w3 : w2,
-                       v3 = two ? w4 : w3, v4 = two ? w5 : w4;
-        const uint32_t bits = (uint32_t)(s & 1) * 16;
-        a = make_uint4(__funnelshift_r(v0, v1, bits), __funnelshift_r(v1, v2, bits),
-                       __funnelshift_r(v2, v3, bits), __funnelshift_r(v3, v4, bits));
-    }
+    if (s) a = funnel(a, v[1], s);
     Pack<8> o;
     *reinterpret_cast<uint4*>(&o) = a;
     return o;

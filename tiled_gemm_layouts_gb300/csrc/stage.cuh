@@ -8,24 +8,27 @@
 
 namespace tg {
 
-// 16 bytes from an even address, out of the aligned 16-byte words around it.
-__device__ __forceinline__ uint4 load_shifted(const uint16_t* s) {
-    const uintptr_t at = reinterpret_cast<uintptr_t>(s);
-    const uint4* base = reinterpret_cast<const uint4*>(at & ~uintptr_t(15));
-    const uint4 a = __ldg(base), b = __ldg(base + 1);
-    const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
-    const int word = (int)(at & 15u) >> 2;
-    uint32_t v[5];
-#pragma unroll
-    for (int k = 0; k < 5; ++k) {  // w[word + k] by selects
-        v[k] = w[k];
-#pragma unroll
-        for (int j = 1; j < 4; ++j)
-            if (k + j < 8) v[k] = word == j ? w[k + j] : v[k];
-    }
-    const uint32_t bits = (uint32_t)(at & 2u) * 8u;
-    return make_uint4(__funnelshift_r(v[0], v[1], bits), __funnelshift_r(v[1], v[2], bits),
-                      __funnelshift_r(v[2], v[3], bits), __funnelshift_r(v[3], v[4], bits));
+// The 8 elements that start `s` elements (0 to 7) into two 16-byte units.
+__device__ __forceinline__ uint4 funnel(uint4 a, uint4 b, int s) {
+    const bool four = s & 4, two = s & 2;
+    const uint32_t w0 = four ? a.z : a.x, w1 = four ? a.w : a.y, w2 = four ? b.x : a.z,
+                   w3 = four ? b.y : a.w, w4 = four ? b.z : b.x, w5 = four ? b.w : b.y;
+    const uint32_t v0 = two ? w1 : w0, v1 = two ? w2 : w1, v2 = two ? w3 : w2, v3 = two ? w4 : w3,
+                   v4 = two ? w5 : w4;
+    const uint32_t bits = (uint32_t)(s & 1) * 16;
+    return make_uint4(__funnelshift_r(v0, v1, bits), __funnelshift_r(v1, v2, bits),
+                      __funnelshift_r(v2, v3, bits), __funnelshift_r(v3, v4, bits));
+}
+
+// Elements between the 16-byte boundary before `p` and `p`.
+__device__ __forceinline__ int shift_of(const uint16_t* p) {
+    return (int)(reinterpret_cast<uintptr_t>(p) & 15u) >> 1;
+}
+
+// 16 bytes from an even address, out of the aligned 16-byte units around it.
+__device__ __forceinline__ uint4 load_shifted(const uint16_t* p) {
+    const uint4* base = reinterpret_cast<const uint4*>(reinterpret_cast<uintptr_t>(p) & ~uintptr_t(15));
+    return funnel(__ldg(base), __ldg(base + 1), shift_of(p));
 }
 
 // i / d for 0 <= i, 0 < d: in 32 bits where both fit (a 64-bit division is a
