@@ -25,11 +25,11 @@
 // freed and the kernel returns.
 //
 // What bounds it: at T = 8192, D = 4096, V = 131072 the tensor pipe and the
-// power it draws (the loss 4.87 to 5.0 ms, 1760 to 1805 TFLOP/s; at 4096 x
+// power it draws (the loss 4.79 to 5.0 ms, 1760 to 1840 TFLOP/s; at 4096 x
 // 2048 x 32768, alone, 2058 TFLOP/s with the tensor pipe 96 % busy).  The
 // exponentials run beside the products: 7 % of the special function unit
 // there.  At D below about 500 the epilogue shows.  For a few tokens, reading
-// W: one token against 131072 x 4096 takes 162 us, 6.6 TB/s.
+// W: one token against 131072 x 4096 takes 167 us, 6.4 TB/s.
 #pragma once
 
 #include "ce_params.h"
