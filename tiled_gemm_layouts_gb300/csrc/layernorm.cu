@@ -13,8 +13,8 @@
 // Rows of whole 16-byte units come through a ring in shared memory: a team
 // walks over rows while bulk copies bring the next ones, so that loads never
 // wait for a reduction's barrier (16384 x 4096 in bf16: forward 46.5 us, 5.8
-// TB/s, backward 69.3 us, 5.8 TB/s).  So do long rows of other widths or
-// alignments (16384 x 4095: forward 57.7 us, backward 95.7 with its reduction).
+// TB/s, backward 71 us with its reduction).  So do long rows of other widths or
+// alignments (16384 x 4095: forward 57.6 us, backward 89).
 // Short ones are loaded by element or by pair into registers, and rows too long
 // for registers are read again from L2 in chunks (wide kernels).
 //
@@ -131,7 +131,8 @@ struct LnParams {
     uint16_t* out;  // y, or dx
     long long ldo;
     float *mean, *rstd;
-    float* part;  // gradient: [blocks][2][cols]
+    float* part;  // gradient: [blocks][2][pitch]
+    int pitch;
     int stages;   // ring: rows in flight per team
     const uint16_t *x_end, *dy_end;  // ring: ends of x and dy
     long long timeout_cycles;
@@ -259,9 +260,14 @@ template <bool SHIFT>
 __device__ __forceinline__ Pack<8> load_columns(const uint16_t* p, int c, int end) {
     if constexpr (!SHIFT) return load<8, true>(p + c, end - c);
     Pack<8> v{};
-    if (c < end)
+    if (c >= end) return v;
+    const uintptr_t unit = reinterpret_cast<uintptr_t>(p + c) & ~uintptr_t(15);
+    if (unit + 32 <= reinterpret_cast<uintptr_t>(p + end)) {
+        *reinterpret_cast<uint4*>(&v) = load_shifted(p + c);
+    } else {
 #pragma unroll
         for (int j = 0; j < 8; ++j) v.e[j] = __ldg(p + c + j);
+    }
     return v;
 }
 
@@ -481,16 +487,22 @@ ln_forward_ring_kernel(const LnParams p) {
     }
 }
 
-// One partial row per block: [block][2][cols]; rows that a block's warps took
-// side by side are added in the order of the warps.  `dwe`, `dbe`: of a thread's
-// single column.
-template <int VEC, int WARPS, int NV>
+// One partial row per block: [block][2][pitch]; rows that a block's warps took
+// side by side are added in the order of the warps.  Column c is at c + lead, so
+// that windows are whole 32-byte sectors (float by float at their stride, the
+// stores of 304 blocks took 4 us of 16384 x 4096's first kernel).  `dwe`, `dbe`:
+// of a thread's single column.
+__host__ __device__ constexpr int lead_of(int front) { return 8 - front; }
+int pitch_of(int64_t cols) { return (int)(cdiv(cols + 8, 32) * 32); }  // whole lines for the sums
+template <int VEC, int WARPS, int NV, bool SHIFT>
 __device__ __forceinline__ void write_partials(const LnParams& p, const f2 (&dw)[NV][VEC / 2],
                                                const f2 (&db)[NV][VEC / 2], const Columns& at, float dwe,
                                                float dbe) {
     constexpr int PAIRS = VEC / 2;
     const int tid = WARPS == 1 ? threadIdx.x & 31 : threadIdx.x;
     const int group = WARPS == 1 ? threadIdx.x >> 5 : 0;
+    float* part_w = p.part + (long long)blockIdx.x * 2 * p.pitch + (SHIFT ? lead_of(at.front) : 0);
+    float* part_b = part_w + p.pitch;
     if constexpr (WARPS == 1) {
         __shared__ float2 part[kRowsPerBlock][32 * NV * PAIRS];
         for (int what = 0; what < 2; ++what) {
@@ -500,42 +512,40 @@ __device__ __forceinline__ void write_partials(const LnParams& p, const f2 (&dw)
                 for (int j = 0; j < PAIRS; ++j)
                     part[group][(i * PAIRS + j) * 32 + tid] = split(what ? db[i][j] : dw[i][j]);
             __syncthreads();
-            float* out = p.part + ((long long)blockIdx.x * 2 + what) * p.cols;
-            for (int k = threadIdx.x; k < 32 * NV * PAIRS; k += 32 * kRowsPerBlock) {
-                const int i = k / (32 * PAIRS), j = k / 32 % PAIRS, lane = k % 32;
-                const int c = (i * 32 + lane) * VEC + 2 * j;
+            float* out = what ? part_b : part_w;
+            for (int c = 2 * threadIdx.x; c < p.cols; c += 64 * kRowsPerBlock) {
+                const int lane = c / VEC % 32, k = (c / (32 * VEC) * PAIRS + c % VEC / 2) * 32 + lane;
                 float2 s = part[0][k];
 #pragma unroll
                 for (int y = 1; y < kRowsPerBlock; ++y) {
                     s.x += part[y][k].x;
                     s.y += part[y][k].y;
                 }
-                if (c < p.cols) out[c] = s.x;
-                if (c + 1 < p.cols) out[c + 1] = s.y;
+                *reinterpret_cast<float2*>(out + c) = s;
             }
             __syncthreads();
         }
     } else {
-        float* out = p.part + (long long)blockIdx.x * 2 * p.cols;
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
             const int c = at.front + (i * (int)blockDim.x + tid) * VEC;
+            if (c >= at.end) continue;
+            if constexpr (VEC == 2) {
+                *reinterpret_cast<float2*>(part_w + c) = split(dw[i][0]);
+                *reinterpret_cast<float2*>(part_b + c) = split(db[i][0]);
+            } else {
 #pragma unroll
-            for (int j = 0; j < PAIRS; ++j) {
-                const float2 a = split(dw[i][j]), b = split(db[i][j]);
-                if (c + 2 * j < at.end) {
-                    out[c + 2 * j] = a.x;
-                    out[p.cols + c + 2 * j] = b.x;
-                }
-                if (c + 2 * j + 1 < at.end) {
-                    out[c + 2 * j + 1] = a.y;
-                    out[p.cols + c + 2 * j + 1] = b.y;
+                for (int j = 0; j < PAIRS; j += 2) {
+                    const float2 w0 = split(dw[i][j]), w1 = split(dw[i][j + 1]);
+                    const float2 b0 = split(db[i][j]), b1 = split(db[i][j + 1]);
+                    *reinterpret_cast<float4*>(part_w + c + 2 * j) = make_float4(w0.x, w0.y, w1.x, w1.y);
+                    *reinterpret_cast<float4*>(part_b + c + 2 * j) = make_float4(b0.x, b0.y, b1.x, b1.y);
                 }
             }
         }
-        if (at.extra >= 0) {
-            out[at.extra] = dwe;
-            out[p.cols + at.extra] = dbe;
+        if (SHIFT && at.extra >= 0) {
+            part_w[at.extra] = dwe;
+            part_b[at.extra] = dbe;
         }
     }
 }
@@ -632,7 +642,7 @@ ln_backward_kernel(const LnParams p) {
             store<VEC, false>(dx + c, p.cols - c, o);
         }
     }
-    write_partials<VEC, WARPS, NV>(p, dw, db, {0, p.cols, -1}, 0.0f, 0.0f);
+    write_partials<VEC, WARPS, NV, false>(p, dw, db, {0, p.cols, -1}, 0.0f, 0.0f);
 }
 
 // The same through the ring.  With 4 packs per thread, whose sums alone are 64
@@ -782,7 +792,7 @@ ln_backward_ring_kernel(const LnParams p) {
             phase ^= 1;
         }
     }
-    write_partials<VEC, WARPS, NV>(p, dw, db, at, dwe, dbe);
+    write_partials<VEC, WARPS, NV, SHIFT>(p, dw, db, at, dwe, dbe);
 }
 
 // Rows too wide for registers: dx alone, one block per row.
@@ -823,17 +833,18 @@ __global__ void __launch_bounds__(256) ln_backward_wide_columns_kernel(const LnP
         dw = fmaf(d, xh, dw);
         db += d;
     }
-    float* part = p.part + (long long)blockIdx.y * 2 * p.cols;
+    float* part = p.part + (long long)blockIdx.y * 2 * p.pitch;
     part[c] = dw;
-    part[p.cols + c] = db;
+    part[p.pitch + c] = db;
 }
 
 // Adds the partial rows in a fixed order: 32 columns per block, Y threads
-// along the rows of each, then one over those.
+// along the rows of each, then one over those.  `shifted`: the output whose rows
+// set the partial rows' leads (block r's first row is row r), or null.
 template <bool BF, int Y>
 __global__ void __launch_bounds__(32 * Y)
-ln_reduce_kernel(const float* __restrict__ part, int parts, int cols, uint16_t* __restrict__ dw,
-                 uint16_t* __restrict__ db) {
+ln_reduce_kernel(const float* __restrict__ part, int parts, int cols, int pitch, const uint16_t* shifted,
+                 long long ldo, uint16_t* __restrict__ dw, uint16_t* __restrict__ db) {
     __shared__ float s[2][Y][32];
     wait_for_previous_kernel();
     const int lane = threadIdx.x & 31, y = threadIdx.x >> 5;
@@ -845,9 +856,10 @@ ln_reduce_kernel(const float* __restrict__ part, int parts, int cols, uint16_t* 
 #pragma unroll
             for (int k = 0; k < 8; ++k) {
                 const bool in = r + k * Y < parts;
-                const float* row = part + (long long)(r + k * Y) * 2 * cols + c;
+                const int lead = shifted ? lead_of(-shift_of(shifted + (r + k * Y) * ldo) & 7) : 0;
+                const float* row = part + (long long)(r + k * Y) * 2 * pitch + c + lead;
                 va[k] = in ? row[0] : 0.0f;
-                vb[k] = in ? row[cols] : 0.0f;
+                vb[k] = in ? row[pitch] : 0.0f;
             }
 #pragma unroll
             for (int k = 0; k < 8; ++k) {
@@ -888,8 +900,8 @@ struct RowShape {
 // Warps for `cols` at 512 columns each: 1, 2, 4 or 8.
 int even_warps(int64_t cols) { return cols <= 512 ? 1 : cols <= 1024 ? 2 : cols <= 2048 ? 4 : 8; }
 
-// Forward.  Aligned rows go through the ring, others from 1024 columns on
-// (16000 x 1001: 22.2 us, in registers 24.7; 16384 x 255: 10.5 and 8.6).  Beyond
+// Forward.  Aligned rows go through the ring, others from 768 columns on (3000
+// x 777: 7.3 us, in registers 8.3; 12909 x 697: 18.7 and 17.5).  Beyond
 // 4096 columns as few warps as hold a row with 4 packs each, so that two or
 // three rows are in work on an SM, which hides a row's barriers (8000 x 5120:
 // 33 us; 16 warps of 2 packs, one row per SM, 56; 8192: 46 and 60).
@@ -897,12 +909,12 @@ RowShape forward_shape(int64_t cols, int vec) {
     if (cols > 16384) return {0, 0, vec, false};
     if (cols > 4096) return {(int)cdiv(cols, 1024), 4, vec, true};
     const int warps = even_warps(cols);
-    if (vec == 8 || cols > 1024) return {warps, cols <= 256 ? 1 : 2, vec, true};
+    if (vec == 8 || cols > 768) return {warps, cols <= 256 ? 1 : 2, vec, true};
     return {warps, cols <= 256 ? 4 : 8, vec, false};
 }
 // Backward.  Aligned rows go through the ring, others from 2048 columns on (16384
-// x 4095: 96 us, in registers 107; 10000 x 2047: 46 and 37).  From 8192 on with 4
-// packs per thread (4545 x 14557: 116 us; 1024 threads of 2 packs 211).
+// x 4095: 89 us, in registers 107; 10000 x 2047: 41 and 37).  From 8192 on with 4
+// packs per thread (4545 x 14557: 109 us; by element, 1024 threads 211).
 RowShape backward_shape(int64_t cols, int vec) {
     if (cols > 16384) return {0, 0, vec, false};
     if (cols > 8192) return {(int)cdiv(cols, 1024), 4, vec, true};
@@ -957,6 +969,7 @@ cudaError_t launch_forward(const LnParams& p, int vec, int sms, cudaStream_t str
         TG_RING(s.warps == 4, 4, 2, false)
         TG_RING(s.warps == 8, 8, 2, false)
         TG_RING(true, 0, 4, false)
+        TG_RING(s.warps == 2, 2, 2, true)
         TG_RING(s.warps == 4, 4, 2, true)
         TG_RING(s.warps == 8, 8, 2, true)
         TG_RING(true, 0, 4, true)
@@ -1122,7 +1135,7 @@ extern "C" int tg_layernorm_grad_workspace_size(int64_t rows, int64_t cols, tg_d
     DeviceInfo* info;
     if ((rc = current_device(&dev, &info))) return rc;
     // (the alignment of the rows does not change their number)
-    *bytes = (size_t)grad_shape(rows, cols, 8, info->sms).parts * 2 * (size_t)cols * sizeof(float);
+    *bytes = (size_t)grad_shape(rows, cols, 8, info->sms).parts * 2 * (size_t)pitch_of(cols) * sizeof(float);
     return TG_OK;
 }
 
@@ -1157,7 +1170,7 @@ extern "C" int tg_layernorm_grad(int64_t rows, int64_t cols, const void* dY, int
     load_driver_entry_points();
     const int vec = pack_of(cols, {dY, X, weight, dX}, {lddy, ldx, lddx});
     const GradShape s = grad_shape(rows, cols, vec, info->sms);
-    const size_t need = (size_t)s.parts * 2 * (size_t)cols * sizeof(float);
+    const size_t need = (size_t)s.parts * 2 * (size_t)pitch_of(cols) * sizeof(float);
     if (workspace_bytes < need) return TG_ERR_BUFFER;
     const Span work = span_bytes(workspace, need);
     for (const Span& o : outs)
@@ -1188,6 +1201,7 @@ extern "C" int tg_layernorm_grad(int64_t rows, int64_t cols, const void* dY, int
     p.mean = const_cast<float*>(mean);
     p.rstd = const_cast<float*>(rstd);
     p.part = static_cast<float*>(workspace);
+    p.pitch = pitch_of(cols);
     p.timeout_cycles = watchdog_timeout();
     p.status = info->status;
     cudaError_t e = dtype == TG_BF16 ? launch_backward<true>(p, s, stream)
@@ -1197,7 +1211,8 @@ extern "C" int tg_layernorm_grad(int64_t rows, int64_t cols, const void* dY, int
         auto reduce = few ? (bf ? ln_reduce_kernel<true, 4> : ln_reduce_kernel<false, 4>)
                           : (bf ? ln_reduce_kernel<true, 32> : ln_reduce_kernel<false, 32>);
         e = launch_chained(reduce, dim3((unsigned)cdiv(cols, 32)), few ? 128 : 1024, stream, p.part, s.parts,
-                           p.cols, static_cast<uint16_t*>(dweight), static_cast<uint16_t*>(dbias));
+                           p.cols, p.pitch, s.row.ring && vec != 8 ? p.out : nullptr, p.ldo,
+                           static_cast<uint16_t*>(dweight), static_cast<uint16_t*>(dbias));
     }
     if (e != cudaSuccess) {
         cudaGetLastError();
