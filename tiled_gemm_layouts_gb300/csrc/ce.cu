@@ -10,12 +10,14 @@
 // vocabulary, CE_GRAD and CE_PRODUCTS; at the end dH's fp32 planes are
 // summed, scaled and scattered back to the tokens' rows.
 #include <algorithm>
+#include <atomic>
 #include <climits>
 #include <cstring>
 
 #include "../../include/tilegemm.h"
 #include "ce_launch.cuh"
 #include "host_common.h"
+#include "ring.cuh"
 #include "stage.cuh"
 
 namespace tg {
@@ -46,11 +48,136 @@ constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 // ------------------------------------------------------ small kernels
 
 // Copies of H and W, whichever a tensor map cannot describe, in one launch.
+// Small ones run by run; large ones through rings of bulk copies, each warp its
+// own: pieces of up to 2048 elements, several rows (with what lies between
+// them) or a part of one, out of which windows of 8 are written aligned.  The
+// columns that round a copied row up to whole windows hold anything; no tensor
+// map reaches them.  (23 x 1911 x 65536: 138 us, run by run 159, without a copy
+// 53; 500 MB moved at 5.9 TB/s.)
 __global__ void __launch_bounds__(256) ce_stage_kernel(const CopyJob h, const CopyJob w) {
     allow_next_kernel();
     const long long thread = blockIdx.x * 256LL + threadIdx.x, threads = gridDim.x * 256LL;
     if (h.rows) copy_rows(h, thread, threads);
     if (w.rows) copy_rows(w, thread, threads);
+}
+
+constexpr int kCopyWarps = 16, kCopyStages = 3, kCopyPiece = 2048;
+constexpr int kCopyStage = 33 * 128;  // the units around a piece, and one to read past it
+constexpr int kCopySmem = kCopyWarps * kCopyStages * kCopyStage;
+constexpr int64_t kRingCopyBytes = 16 << 20;  // from here on
+
+struct CopyPieces {
+    CopyJob job;
+    int per, chunks, vecs;  // rows of a piece, pieces of a row, windows of a row
+    int width;              // columns of a piece
+    long long pieces;
+};
+CopyPieces copy_pieces(const CopyJob& j) {
+    CopyPieces p{j, 1, 1, (int)cdiv(j.cols, 8), kCopyPiece, 0};
+    if (!j.rows) return p;
+    if (j.lds * 2 <= kCopyPiece) {
+        p.per = (int)(kCopyPiece / j.lds);
+    } else {
+        p.chunks = (int)cdiv(j.cols, kCopyPiece);
+        p.width = (int)up(cdiv(j.cols, p.chunks), 8);
+    }
+    p.pieces = cdiv(j.rows, p.per) * p.chunks;
+    return p;
+}
+
+__global__ void __launch_bounds__(32 * kCopyWarps, 1)
+ce_copy_kernel(const CopyPieces h, const CopyPieces w, long long timeout_cycles, int* status) {
+    extern __shared__ __align__(128) uint8_t ring[];
+    __shared__ uint64_t full[kCopyWarps][kCopyStages];
+    allow_next_kernel();
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    uint8_t* stages = ring + warp * kCopyStages * kCopyStage;
+    const long long first = blockIdx.x * (long long)kCopyWarps + warp, step = gridDim.x * (long long)kCopyWarps;
+    const long long total = h.pieces + w.pieces;
+    struct Piece {
+        long long row;  // first row, first column
+        int col, rows, n;
+        const uint16_t* src;
+    };
+    auto piece_of = [&](long long i, const CopyPieces& c) {
+        Piece p;
+        const long long g = c.chunks > 1 ? row_of(i, c.chunks) : i;
+        p.row = g * c.per;
+        p.col = (int)(i - g * c.chunks) * c.width;
+        p.rows = (int)min((long long)c.per, c.job.rows - p.row);
+        const int cols = (int)min((long long)c.width, c.job.cols - p.col);
+        p.n = (int)((p.rows - 1) * c.job.lds) + cols;
+        p.src = c.job.src + p.row * c.job.lds + p.col;
+        return p;
+    };
+    auto issue = [&](long long i, int st) {
+        const CopyPieces& c = i < h.pieces ? h : w;
+        const Piece p = piece_of(i < h.pieces ? i : i - h.pieces, c);
+        uint8_t* dst = stages + st * kCopyStage;
+        const uint32_t bar = smem_addr(&full[warp][st]);
+        const RowCopy x = row_copy(dst, p.src, c.job.src + (c.job.rows - 1) * c.job.lds + c.job.cols, p.n);
+        mbar_arrive_expect_tx(bar, x.bytes);
+        if (x.bytes) bulk_load(smem_addr(dst), x.src, x.bytes, bar);
+    };
+    if (lane == 0) {
+        for (int st = 0; st < kCopyStages; ++st) mbar_init(smem_addr(&full[warp][st]), 1);
+        fence_barrier_init();
+        for (int st = 0; st < kCopyStages && first + st * step < total; ++st) issue(first + st * step, st);
+    }
+    __syncwarp();
+    int st = 0;
+    uint32_t phase = 0;
+    for (long long i = first; i < total; i += step) {
+        const CopyPieces& c = i < h.pieces ? h : w;
+        const Piece p = piece_of(i < h.pieces ? i : i - h.pieces, c);
+        const uint8_t* stage = stages + st * kCopyStage;
+        if (!stage_ready(smem_addr(&full[warp][st]), phase, timeout_cycles, status)) return;
+        const int shift = shift_of(p.src), lds = (int)c.job.lds;
+        uint16_t* dst = c.job.dst + p.row * c.job.ldd + p.col;
+        if (c.per == 1) {
+            const int n = (p.n + 7) / 8;
+#pragma unroll 4
+            for (int k = lane; k < n; k += 32)
+                *reinterpret_cast<uint4*>(dst + k * 8) = window(stage, k, shift);
+        } else {
+            const int n = p.rows * c.vecs;
+#pragma unroll 4
+            for (int k = lane; k < n; k += 32) {
+                const int r = (uint32_t)k / (uint32_t)c.vecs, x = (k - r * c.vecs) * 8;
+                *reinterpret_cast<uint4*>(dst + r * c.job.ldd + x) = window(stage, 0, shift + r * lds + x);
+            }
+        }
+        __syncwarp();
+        if (lane == 0 && i + kCopyStages * step < total) issue(i + kCopyStages * step, st);
+        if (++st == kCopyStages) {
+            st = 0;
+            phase ^= 1;
+        }
+    }
+}
+
+cudaError_t launch_copy(const CopyJob& h, const CopyJob& w, const DeviceInfo* info, cudaStream_t stream) {
+    const long long vecs = (std::max(h.rows ? h.cols : 0, w.rows ? w.cols : 0) + 7) / 8;
+    if ((h.rows * h.cols + w.rows * w.cols) * 2 < kRingCopyBytes) {
+        // (1216 blocks, what the SMs hold: 172 us for 23 x 1911 x 65536; 4096:
+        // 160; a block per 4 KB: 202)
+        const int64_t blocks = std::min<int64_t>(cdiv((h.rows + w.rows) * vecs, 256), 4096);
+        ce_stage_kernel<<<(unsigned)blocks, 256, 0, stream>>>(h, w);
+        return cudaGetLastError();
+    }
+    static std::atomic<unsigned long long> attr_set{0};  // one bit per device
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    const unsigned long long bit = dev < 64 ? 1ull << dev : 0ull;
+    if (!(attr_set.load(std::memory_order_acquire) & bit)) {
+        e = cudaFuncSetAttribute(ce_copy_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kCopySmem);
+        if (e != cudaSuccess) return e;
+        attr_set.fetch_or(bit, std::memory_order_release);
+    }
+    ce_copy_kernel<<<(unsigned)info->sms, 32 * kCopyWarps, kCopySmem, stream>>>(
+        copy_pieces(h), copy_pieces(w), watchdog_timeout(), info->status);
+    return cudaGetLastError();
 }
 
 // (max in log2 units, sum of 2^(l - max)) of a set of logits.
@@ -566,11 +693,7 @@ extern "C" int tg_linear_ce(int64_t T, int64_t V, int64_t D, const void* H, int6
                   f.copy_h ? T : 0, D};
         CopyJob w{static_cast<const uint16_t*>(W), ldw, reinterpret_cast<uint16_t*>(ws + f.w), wide,
                   f.copy_w ? V : 0, D};
-        // (1216 blocks, what the SMs hold: 172 us for 23 x 1911 x 65536; 4096:
-        // 160; a block per 4 KB: 202)
-        const int64_t blocks = std::min<int64_t>(cdiv((h.rows + w.rows) * (wide / 8), 256), 4096);
-        ce_stage_kernel<<<(unsigned)blocks, 256, 0, stream>>>(h, w);
-        ok = cudaGetLastError() == cudaSuccess;
+        ok = launch_copy(h, w, info, stream) == cudaSuccess;
         if (f.copy_h) {
             H = h.dst;
             ldh = wide;
@@ -664,6 +787,10 @@ extern "C" int tg_linear_ce_grad(int64_t T, int64_t V, int64_t D, const void* H,
     if (b.copy_w) {
         W = copy_w.dst;
         ldw = copy_w.ldd;
+        if (V * D * 2 >= kRingCopyBytes) {  // a small copy is part of the gather below
+            ok = launch_copy(CopyJob{}, copy_w, info, stream) == cudaSuccess;
+            copy_w.rows = 0;
+        }
     }
     CeRows rows;
     rows.live = reinterpret_cast<int*>(ws + b.live);

@@ -34,6 +34,7 @@
 #include "host_common.h"
 #include "packed.cuh"
 #include "ptx.cuh"
+#include "ring.cuh"
 #include "stage.cuh"
 
 namespace tg {
@@ -169,30 +170,6 @@ __device__ __forceinline__ uint32_t narrow2(f2 a) {
 // sums, and memory's latency times its rate is about 50 KB per SM.
 constexpr int kMaxStages = 8;
 
-__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
-    asm volatile(
-        "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
-        "l"(src), "r"(bytes), "r"(bar)
-        : "memory");
-}
-
-// Bounded wait for a stage; on a timeout the status word is set, and copies
-// in flight get ample time to land before the block may end.
-__device__ __forceinline__ bool stage_ready(uint32_t bar, uint32_t parity, const LnParams& p) {
-    if (mbar_try_wait(bar, parity)) return true;
-    const long long t0 = clock64();
-    while (!mbar_try_wait_suspend(bar, parity, 200000)) {
-        if (clock64() - t0 > p.timeout_cycles) {
-            atomicCAS(p.status, 0, DEV_TIMEOUT_PRODUCER + 2);
-            const long long t1 = clock64();
-            while (clock64() - t1 < 2000000) {
-            }
-            return false;
-        }
-    }
-    return true;
-}
-
 // Rows of other widths or alignments (SHIFT).  A team walks over rows by a
 // multiple of 8, so where its rows start within 16 bytes is the same for all of
 // them, whatever the stride.  Its threads take windows of 8 columns that are
@@ -225,36 +202,6 @@ __device__ __forceinline__ Columns columns_of(const uint16_t* out, int cols, int
     return c;
 }
 
-// The bulk copy of a row into a stage.  Units that reach past the operand's
-// end are left out, and their part of the row is stored by this thread; it
-// arrives on the stage's barrier afterwards, which hands them over.
-struct RowCopy {
-    const uint8_t* src;
-    uint32_t bytes;
-};
-__device__ __forceinline__ RowCopy row_copy(uint8_t* dst, const uint16_t* row, const uint16_t* end,
-                                            int cols) {
-    const uintptr_t at = reinterpret_cast<uintptr_t>(row), from = at & ~uintptr_t(15);
-    const uint32_t lead = (uint32_t)(at - from), need = lead + (uint32_t)cols * 2;
-    uint32_t bytes = (need + 15) & ~15u;
-    if (from + bytes > reinterpret_cast<uintptr_t>(end)) {
-        bytes = need & ~15u;
-        for (uint32_t k = max(bytes, lead); k < need; k += 2)
-            *reinterpret_cast<uint16_t*>(dst + k) = row[(k - lead) / 2];
-    }
-    return {reinterpret_cast<const uint8_t*>(from), bytes};
-}
-
-// Window `k` of a stage: 8 elements from `off` elements into unit k.
-__device__ __forceinline__ Pack<8> window(const uint8_t* stage, int k, int off) {
-    const uint4* v = reinterpret_cast<const uint4*>(stage) + k + (off >> 3);
-    const int s = off & 7;
-    uint4 a = v[0];
-    if (s) a = funnel(a, v[1], s);
-    Pack<8> o;
-    *reinterpret_cast<uint4*>(&o) = a;
-    return o;
-}
 // 8 columns of the weights or the bias from `c`.
 template <bool SHIFT>
 __device__ __forceinline__ Pack<8> load_columns(const uint16_t* p, int c, int end) {
@@ -410,7 +357,7 @@ ln_forward_ring_kernel(const LnParams p) {
     int st = 0;
     uint32_t phase = 0;
     for (long long row = first; row < p.rows; row += step) {
-        if (!stage_ready(smem_addr(&full[team][st]), phase, p)) return;
+        if (!stage_ready(smem_addr(&full[team][st]), phase, p.timeout_cycles, p.status)) return;
         f2 v[NV][PAIRS], acc = pair(0.0f, 0.0f);
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
@@ -418,7 +365,8 @@ ln_forward_ring_kernel(const LnParams p) {
             Pack<VEC> x{};
             if (c < at.end) {
                 if constexpr (SHIFT)
-                    x = window(stages + st * bytes, i * width + tid, x_shift + at.front);
+                    *reinterpret_cast<uint4*>(&x) =
+                        window(stages + st * bytes, i * width + tid, x_shift + at.front);
                 else
                     x = *reinterpret_cast<const Pack<VEC>*>(stages + st * bytes + c * 2);
             }
@@ -689,8 +637,9 @@ ln_backward_ring_kernel(const LnParams p) {
     // x and dy of window i of a stage
     auto operands = [&](const uint8_t* sx, int i, int c, Pack<VEC>& vx, Pack<VEC>& vd) {
         if constexpr (SHIFT) {
-            vx = window(sx, i * width + tid, x_shift + at.front);
-            vd = window(sx + bytes, i * width + tid, d_shift + at.front);
+            *reinterpret_cast<uint4*>(&vx) = window(sx, i * width + tid, x_shift + at.front);
+            *reinterpret_cast<uint4*>(&vd) =
+                window(sx + bytes, i * width + tid, d_shift + at.front);
         } else {
             vx = *reinterpret_cast<const Pack<VEC>*>(sx + c * 2);
             vd = *reinterpret_cast<const Pack<VEC>*>(sx + bytes + c * 2);
@@ -723,7 +672,7 @@ ln_backward_ring_kernel(const LnParams p) {
         }
         // x - mean first: scaled apart, the two would cancel with their roundings
         const f2 scale = pair(r, r), minus = pair(-mean, -mean);
-        if (!stage_ready(smem_addr(&full[team][st]), phase, p)) return;
+        if (!stage_ready(smem_addr(&full[team][st]), phase, p.timeout_cycles, p.status)) return;
         const uint8_t* sx = stages + st * 2 * bytes;
         f2 s0 = pair(0.0f, 0.0f), s1 = s0;  // sums of g and of g xh
         f2 g[KEEP ? NV : 1][PAIRS], xh[KEEP ? NV : 1][PAIRS];
