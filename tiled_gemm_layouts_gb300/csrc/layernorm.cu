@@ -13,7 +13,7 @@
 // Rows of whole 16-byte units come through a ring in shared memory: a team
 // walks over rows while bulk copies bring the next ones, so that loads never
 // wait for a reduction's barrier (16384 x 4096 in bf16: forward 46.5 us, 5.8
-// TB/s, backward 71 us with its reduction).  So do long rows of other widths or
+// TB/s, backward 63 us, 6.4 TB/s, and 7 of reduction).  So do long rows of other widths or
 // alignments (16384 x 4095: forward 57.6 us, backward 89).
 // Short ones are loaded by element or by pair into registers, and rows too long
 // for registers are read again from L2 in chunks (wide kernels).
@@ -225,7 +225,7 @@ constexpr int row_threads(int warps) { return 32 * (warps == 1 ? kRowsPerBlock :
 // A row in registers, or (WIDE) read again from memory for each pass, which
 // finds most of it in L2.
 template <bool BF, int VEC, bool WHOLE, int WARPS, int NV, bool WIDE>
-__global__ void __launch_bounds__(row_threads(WARPS), WARPS == 16 ? 2 : 1)
+__global__ void __launch_bounds__(row_threads(WARPS))
 ln_forward_kernel(const LnParams p) {
     __shared__ float buf[2][WARPS == 1 ? 1 : WARPS];
     const int tid = WARPS == 1 ? threadIdx.x & 31 : threadIdx.x;
