@@ -52,3 +52,42 @@ def test_gradients_into_rows_that_start_anywhere(tg, t, v, d, dt):
         assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1]), (at_h, at_w)
     st, detail = tg.tg_debug_status()
     assert st == tg.TG_OK, hex(detail)
+
+
+# inputs: whole 16-byte units that start inside a 32-byte sector, and any address;
+# vocabularies large enough for copies of H alone, and for W's through the ring
+@pytest.mark.parametrize("t,v,d", [(100, 41000, 72), (300, 41000, 72), (5, 70001, 129), (70, 4100, 2100),
+                                   (300, 9001, 1025), (20, 70001, 500), (3, 3000, 4097)])
+def test_inputs_that_start_anywhere(tg, t, v, d):
+    dt = torch.bfloat16
+    g = torch.Generator(device="cuda").manual_seed(t + v + d)
+    values_h = torch.randn(t, d, device="cuda", generator=g).to(dt)
+    values_w = (torch.randn(v, d, device="cuda", generator=g) / d**0.5).to(dt)
+    target = torch.randint(-1, v, (t,), device="cuda", generator=g)
+    dloss = torch.rand(t, device="cuda", generator=g) / t
+
+    def run(at_h, at_w):
+        full_h, h, ldh = rows_at(t, d, *at_h, dt)
+        full_w, w, ldw = rows_at(v, d, *at_w, dt)
+        full_h.fill_(float("nan")), full_w.fill_(float("nan"))  # between the rows
+        h.copy_(values_h), w.copy_(values_w)
+        loss, lse = torch.empty(t, device="cuda"), torch.empty(t, device="cuda")
+        size = tg.tg_linear_ce_workspace_size(t, v, d, h, ldh, w, ldw, tg.TG_BF16)
+        ws = torch.full((size,), 0xFF, dtype=torch.uint8, device="cuda")
+        tg.linear_ce(t, v, d, h, ldh, w, ldw, target, loss, lse, tg.TG_BF16, ws, size)
+        dh, dw = torch.empty(t, d, dtype=dt, device="cuda"), torch.empty(v, d, dtype=dt, device="cuda")
+        size = tg.tg_linear_ce_grad_workspace_size(t, v, d, h, ldh, w, ldw, dh, d, dw, d, tg.TG_BF16)
+        ws = torch.full((size,), 0xFF, dtype=torch.uint8, device="cuda")
+        tg.linear_ce_grad(t, v, d, h, ldh, w, ldw, target, lse, dloss, dh, d, dw, d, tg.TG_BF16, ws, size)
+        torch.cuda.synchronize()
+        return loss, lse, dh, dw
+
+    pad = -d % 64
+    want = run((0, pad), (0, pad))
+    assert all(torch.isfinite(x).all() for x in want)
+    for at_h, at_w in (((0, -d % 16 + 8), (0, pad)), ((8, pad), (8, pad)), ((1, 0), (0, pad)), ((0, pad), (3, 0)),
+                       ((5, 2), (7, 1))):
+        for a, b in zip(run(at_h, at_w), want):
+            assert torch.equal(a, b), (at_h, at_w)
+    st, detail = tg.tg_debug_status()
+    assert st == tg.TG_OK, hex(detail)

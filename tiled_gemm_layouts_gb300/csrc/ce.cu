@@ -52,7 +52,7 @@ constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 // own: pieces of up to 2048 elements, several rows (with what lies between
 // them) or a part of one, out of which windows of 8 are written aligned.  The
 // columns that round a copied row up to whole windows hold anything; no tensor
-// map reaches them.  (23 x 1911 x 65536: 138 us, run by run 159, without a copy
+// map reaches them.  (23 x 1911 x 65536: 136 us, run by run 159, without a copy
 // 53; 500 MB moved at 5.9 TB/s.)
 __global__ void __launch_bounds__(256) ce_stage_kernel(const CopyJob h, const CopyJob w) {
     allow_next_kernel();
@@ -438,6 +438,12 @@ unsigned blocks_for(int64_t threads, int sms) {
 
 bool tma_rows(const void* p, int64_t ld) { return aligned16(p) && (ld * 2) % 16 == 0; }
 
+// Rows of whole 32-byte sectors.
+bool sector_rows(const void* p, int64_t ld) {
+    return ((reinterpret_cast<uintptr_t>(p) | (uintptr_t)ld * 2) & 31) == 0;
+}
+int64_t copied_ld(int64_t D) { return up(D, 64); }  // of a copy: whole lines
+
 // Places regions one after another, 256-byte aligned.
 struct Cursor {
     size_t at = 0;
@@ -481,15 +487,21 @@ struct FwdPlan {
 FwdPlan forward_plan(int64_t T, int64_t V, int64_t D, const void* H, int64_t ldh, const void* W,
                      int64_t ldw) {
     FwdPlan f;
-    f.copy_h = !tma_rows(H, ldh);
-    f.copy_w = !tma_rows(W, ldw);
     f.tile = logits_tile(T, V);
     f.tiles_n = cdiv(V, f.tile.bn);
+    // Every worker reads H again for each of its tiles, and rows that start
+    // inside a sector cost a request more per 128 bytes.  A copy of H pays from
+    // two rounds of tiles on, and not for a few rows (rows 16 bytes off in H and
+    // W: 1000 x 512 x 117936 109 us, 89 with it; 102 x 1024 x 50000 32.2, 28.9; 32 x
+    // 512 x 117936 31.6 as it is, 29.4 with aligned rows).
+    const int64_t rounds = cdiv(T, f.tile.rows()) * f.tiles_n / (f.tile.pair ? kPairs : 2 * kPairs);
+    f.copy_h = !tma_rows(H, ldh) || (T > 64 && rounds >= 2 && !sector_rows(H, ldh));
+    f.copy_w = !tma_rows(W, ldw);
     Cursor c;
     f.part = c.take((u128)T * f.tiles_n * 2 * sizeof(float2));
     f.hit = c.take((u128)T * sizeof(float));
-    f.h = c.take(f.copy_h ? (u128)T * up(D, 8) * 2 : 0);
-    f.w = c.take(f.copy_w ? (u128)V * up(D, 8) * 2 : 0);
+    f.h = c.take(f.copy_h ? (u128)T * copied_ld(D) * 2 : 0);
+    f.w = c.take(f.copy_w ? (u128)V * copied_ld(D) * 2 : 0);
     f.bytes = c.at;
     return f;
 }
@@ -554,7 +566,7 @@ BwdPlan backward_plan(int64_t T, int64_t V, int64_t D, const void* W, int64_t ld
     b.h = c.take((u128)b.rows * b.ldh * 2);
     b.g = c.take((u128)b.rows * b.piece * 2);
     b.planes = c.take((u128)b.splits * T * b.ldp * 4);
-    b.w = c.take(b.copy_w ? (u128)V * up(D, 8) * 2 : 0);
+    b.w = c.take(b.copy_w ? (u128)V * copied_ld(D) * 2 : 0);
     b.bytes = c.at;
     return b;
 }
@@ -688,7 +700,7 @@ extern "C" int tg_linear_ce(int64_t T, int64_t V, int64_t D, const void* H, int6
     bool ok = true;
     const bool staged = f.copy_h || f.copy_w;
     if (staged) {
-        const int64_t wide = up(D, 8);
+        const int64_t wide = copied_ld(D);
         CopyJob h{static_cast<const uint16_t*>(H), ldh, reinterpret_cast<uint16_t*>(ws + f.h), wide,
                   f.copy_h ? T : 0, D};
         CopyJob w{static_cast<const uint16_t*>(W), ldw, reinterpret_cast<uint16_t*>(ws + f.w), wide,
@@ -782,7 +794,7 @@ extern "C" int tg_linear_ce_grad(int64_t T, int64_t V, int64_t D, const void* H,
     char* ws = static_cast<char*>(workspace);
     const int dt = (int)dtype, sms = info->sms;
     bool ok = true;
-    CopyJob copy_w{static_cast<const uint16_t*>(W), ldw, reinterpret_cast<uint16_t*>(ws + b.w), up(D, 8),
+    CopyJob copy_w{static_cast<const uint16_t*>(W), ldw, reinterpret_cast<uint16_t*>(ws + b.w), copied_ld(D),
                    b.copy_w ? V : 0, D};
     if (b.copy_w) {
         W = copy_w.dst;

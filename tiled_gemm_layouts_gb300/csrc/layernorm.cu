@@ -13,8 +13,8 @@
 // Rows of whole 16-byte units come through a ring in shared memory: a team
 // walks over rows while bulk copies bring the next ones, so that loads never
 // wait for a reduction's barrier (16384 x 4096 in bf16: forward 46.5 us, 5.8
-// TB/s, backward 63 us, 6.4 TB/s, and 7 of reduction).  So do long rows of other widths or
-// alignments (16384 x 4095: forward 57.6 us, backward 89).
+// TB/s, backward 63 us, 6.4 TB/s, and 7 of reduction).  So do long rows of
+// other widths or alignments (16384 x 4095: forward 57.6 us, backward 89).
 // Short ones are loaded by element or by pair into registers, and rows too long
 // for registers are read again from L2 in chunks (wide kernels).
 //
@@ -438,7 +438,7 @@ ln_forward_ring_kernel(const LnParams p) {
 // One partial row per block: [block][2][pitch]; rows that a block's warps took
 // side by side are added in the order of the warps.  Column c is at c + lead, so
 // that windows are whole 32-byte sectors (float by float at their stride, the
-// stores of 304 blocks took 4 us of 16384 x 4096's first kernel).  `dwe`, `dbe`:
+// stores of 304 blocks took 7 of 16384 x 4096's 78 us).  `dwe`, `dbe`:
 // of a thread's single column.
 __host__ __device__ constexpr int lead_of(int front) { return 8 - front; }
 int pitch_of(int64_t cols) { return (int)(cdiv(cols + 8, 32) * 32); }  // whole lines for the sums
