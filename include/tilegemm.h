@@ -272,7 +272,7 @@ int tg_pointwise(int64_t M, int64_t N, const void* X, int64_t ldx, tg_perm permX
  * 1, every check before any device work, launches on `stream` only, nothing
  * allocated, no synchronisation, results that repeat bit for bit.  Rows may
  * start at any 2-byte-aligned address and strides may be any value that is at
- * least the row width; 16-byte-aligned rows are faster.  Every output's bytes
+ * least the row width; 32-byte-aligned rows are the fastest.  Every output's bytes
  * are disjoint from every other operand's.  Statistics, sums and products are
  * fp32.  Workspaces need no initialisation; calls that share one must not
  * overlap on the GPU.
@@ -324,7 +324,8 @@ int tg_layernorm_grad_workspace_size(int64_t rows, int64_t cols, tg_dtype dtype,
  * or W has to be copied.
  * workspace: 256-byte aligned, at least tg_linear_ce_workspace_size() bytes
  * (else TG_ERR_BUFFER).  An H or W whose rows are not 16-byte aligned is
- * copied into the workspace first.  A row whose logits hold a NaN or +inf
+ * copied into the workspace first, and an H whose rows are not 32-byte aligned
+ * where that is faster.  A row whose logits hold a NaN or +inf
  * has lse = NaN.  Device waits are bounded; see tg_debug_status().
  */
 int tg_linear_ce(int64_t T, int64_t V, int64_t D, const void* H, int64_t ldh, const void* W,
