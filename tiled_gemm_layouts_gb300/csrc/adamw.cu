@@ -447,9 +447,11 @@ extern "C" int tg_adamw(int64_t count, const tg_adamw_tensor* tensors, const tg_
         u128 hi;
         bool written;
     };
-    const std::unique_ptr<Mark[]> marks(new (std::nothrow) Mark[(size_t)count * 7]);
+    const std::unique_ptr<Mark[]> marks(new (std::nothrow) Mark[(size_t)count * 7 + 1]);
     if (!marks) return TG_ERR_CUDA;
     size_t used = 0;
+    const Span factor = span_bytes(o->grad_scale, 4);  // read by every block
+    if (factor.present) marks[used++] = Mark{factor.lo, factor.hi, false};
     for (int64_t k = 0; k < count; ++k) {
         if (tensors[k].numel == 0) continue;
         const Operands r = operands(tensors[k]);
@@ -469,7 +471,7 @@ extern "C" int tg_adamw(int64_t count, const tg_adamw_tensor* tensors, const tg_
     if ((rc = current_device(&dev, &info))) return rc;
     load_driver_entry_points();
     PointerChecks check{dev};
-    if ((rc = check(o->grad_scale, span_bytes(o->grad_scale, 4)))) return rc;
+    if ((rc = check(o->grad_scale, factor))) return rc;
     // operand by operand: the tensors of one list often lie side by side
     for (int i = 0; i < 7; ++i)
         for (int64_t k = 0; k < count; ++k) {
