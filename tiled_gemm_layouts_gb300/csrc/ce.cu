@@ -202,7 +202,7 @@ struct LogSum {
 // 8 warps per block.
 template <int WARPS>
 __global__ void __launch_bounds__(256)
-ce_combine_kernel(const float2* __restrict__ part, const float* __restrict__ hit,
+ce_combine_kernel(const float2* part, const float* hit,
                   const long long* __restrict__ target, int T, long long V, int tiles,
                   float* __restrict__ loss, float* __restrict__ lse) {
     wait_for_previous_kernel();
@@ -393,7 +393,7 @@ ce_gather_kernel(const uint16_t* __restrict__ H, long long ldh, int D, CeRows r,
 // dH rows: the sum of the fp32 planes' rows, scaled and rounded once; zeros
 // for tokens without a gradient.
 template <bool BF>
-__global__ void ce_scatter_kernel(const float* __restrict__ planes, int splits, long long plane,
+__global__ void ce_scatter_kernel(const float* planes, int splits, long long plane,
                                   int ldp, CeRows r, int T, int D, uint16_t* __restrict__ dH,
                                   long long ldd) {
     wait_for_previous_kernel();

@@ -160,7 +160,7 @@ struct CeItems {
             group_m[s] = p.side[s].group_m;
         }
         if (p.live) {
-            const int n = max(1, __ldg(p.live));
+            const int n = max(1, *p.live);
             tiles_m[0] = min(tiles_m[0], (n + bm - 1) / bm);
             num_kb[1] = min(num_kb[1], (n + kBK - 1) / kBK);
         }
@@ -498,9 +498,9 @@ __global__ void __launch_bounds__(kCeThreads, 1) ce_kernel(const __grid_constant
         const int q = warp & 3, half = (warp - 2) / 4;
         uint8_t* stage = staging + (warp - 2) * TS::kUnit;
         float alpha = 1.0f;
-        if constexpr (MODE == CE_PRODUCTS) alpha = __ldg(p.alpha);
+        if constexpr (MODE == CE_PRODUCTS) alpha = *p.alpha;
         int live = 0;
-        if constexpr (MODE == CE_GRAD) live = p.live ? __ldg(p.live) : p.rows;
+        if constexpr (MODE == CE_GRAD) live = p.live ? *p.live : p.rows;
         CeItems<MODE> items(p, worker, workers, TS::kBM);
         CeItem it;
         for (int i = 0; items.next(it); ++i) {
@@ -521,8 +521,8 @@ __global__ void __launch_bounds__(kCeThreads, 1) ce_kernel(const __grid_constant
                 }
             } else if constexpr (MODE == CE_GRAD) {
                 if (row < live) {
-                    rs = __ldg(p.row_scale + row);
-                    const long long t = __ldg(p.row_target + row);
+                    rs = p.row_scale[row];
+                    const long long t = p.row_target[row];
                     if (t >= p.col0 && t < p.col0 + p.cols) target = (int)(t - p.col0);
                 }
             }

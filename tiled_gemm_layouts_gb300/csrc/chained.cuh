@@ -3,7 +3,9 @@
 // be scheduled while the last blocks of the one before still run, so that a
 // launch's latency and a kernel's set-up are hidden.  Every kernel of such a
 // call waits for the end of the one before it ahead of its first access to
-// memory that any kernel of the call writes.
+// memory that any kernel of the call writes, and reads that memory with plain
+// loads: the read-only path (__ldg, const __restrict__) is for what nobody
+// writes while the kernel is resident, and its loads may move ahead of the wait.
 #pragma once
 
 #include <cuda_runtime.h>

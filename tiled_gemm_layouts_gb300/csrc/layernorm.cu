@@ -792,7 +792,7 @@ __global__ void __launch_bounds__(256) ln_backward_wide_columns_kernel(const LnP
 // set the partial rows' leads (block r's first row is row r), or null.
 template <bool BF, int Y>
 __global__ void __launch_bounds__(32 * Y)
-ln_reduce_kernel(const float* __restrict__ part, int parts, int cols, int pitch, const uint16_t* shifted,
+ln_reduce_kernel(const float* part, int parts, int cols, int pitch, const uint16_t* shifted,
                  long long ldo, uint16_t* __restrict__ dw, uint16_t* __restrict__ db) {
     __shared__ float s[2][Y][32];
     wait_for_previous_kernel();
