@@ -34,3 +34,19 @@ def test_the_guard_above_sees_the_kernels():
     for name in ("live", "alpha", "row_scale", "row_target", "part", "hit", "planes"):
         assert re.search(rf"\b{name}\b", code), name
     assert code.count("wait_for_previous_kernel();") >= 5
+
+
+def test_every_thread_that_initialises_barriers_fences():
+    """fence.mbarrier_init covers its own thread's initialisations only: it stands
+    in the block of all the initialisations of its kernel."""
+    for name in FILES:
+        code = text(name)
+        for m in re.finditer(r"fence_barrier_init\(\);", code):
+            # the innermost block around the fence holds every mbar_init of its kernel
+            before = code[:m.start()]
+            depth, at = 0, len(before)
+            while depth < 1:
+                at -= 1
+                depth += {"{": 1, "}": -1}.get(code[at], 0)
+            kernel = code[before.rfind("__global__"):m.start()]
+            assert kernel.count("mbar_init(") == code[at:m.start()].count("mbar_init(") > 0, (name, kernel[:80])

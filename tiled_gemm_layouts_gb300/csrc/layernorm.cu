@@ -321,8 +321,10 @@ ln_forward_ring_kernel(const LnParams p) {
     const int team = WARPS == 1 ? threadIdx.x >> 5 : 0;
     const uint32_t bytes = stage_bytes(SHIFT, p.cols);
     uint8_t* stages = ring + (size_t)team * p.stages * bytes;
-    if (threadIdx.x < kTeams * kMaxStages) mbar_init(smem_addr(&full[0][0] + threadIdx.x), 1);
-    if (threadIdx.x == 0) fence_barrier_init();
+    if (threadIdx.x < kTeams * kMaxStages) {
+        mbar_init(smem_addr(&full[0][0] + threadIdx.x), 1);
+        fence_barrier_init();  // of this thread's barrier
+    }
     __syncthreads();
     const long long first = (long long)blockIdx.x * kTeams + team, step = (long long)gridDim.x * kTeams;
     auto issue = [&](long long row, int st) {
@@ -610,8 +612,10 @@ ln_backward_ring_kernel(const LnParams p) {
     const uint32_t bytes = stage_bytes(SHIFT, p.cols);
     uint8_t* stages = ring + (size_t)team * p.stages * 2 * bytes;
     allow_next_kernel();
-    if (threadIdx.x < kTeams * kMaxStages) mbar_init(smem_addr(&full[0][0] + threadIdx.x), 1);
-    if (threadIdx.x == 0) fence_barrier_init();
+    if (threadIdx.x < kTeams * kMaxStages) {
+        mbar_init(smem_addr(&full[0][0] + threadIdx.x), 1);
+        fence_barrier_init();  // of this thread's barrier
+    }
     __syncthreads();
     const long long first = (long long)blockIdx.x * kTeams + team, step = (long long)gridDim.x * kTeams;
     auto issue = [&](long long row, int st) {
