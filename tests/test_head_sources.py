@@ -42,8 +42,9 @@ def test_every_thread_that_initialises_barriers_fences():
     for name in FILES:
         code = text(name)
         for m in re.finditer(r"fence_barrier_init\(\);", code):
-            # the innermost block around the fence holds every mbar_init of its kernel
             before = code[:m.start()]
+            assert before.rstrip()[-1] in "{};", (name, "a condition of the fence's own", before[-80:])
+            # the innermost block around the fence holds every mbar_init of its kernel
             depth, at = 0, len(before)
             while depth < 1:
                 at -= 1
