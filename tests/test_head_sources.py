@@ -51,3 +51,16 @@ def test_every_thread_that_initialises_barriers_fences():
                 depth += {"{": 1, "}": -1}.get(code[at], 0)
             kernel = code[before.rfind("__global__"):m.start()]
             assert kernel.count("mbar_init(") == code[at:m.start()].count("mbar_init(") > 0, (name, kernel[:80])
+
+
+def test_tensor_maps_are_prefetched_only_where_a_side_has_work():
+    """A side without work (dH or dW not asked for) has no encoded maps, and
+    prefetch.tensormap is defined on tensor maps only."""
+    code = text("ce_kernel.cuh")
+    calls = list(re.finditer(r"prefetch_tensormap\(&(.*?)\);", code))
+    assert calls
+    for m in calls:
+        side = re.match(r"(p\.side\[\w+\]|\w+)\.", m.group(1)).group(1)
+        assert re.search(re.escape(side) + r"\.tiles_m\b", code[m.start() - 200:m.start()]), m.group(0)
+    # and every side of a launch is looked at
+    assert not any("side[0]" in m.group(1) for m in calls)

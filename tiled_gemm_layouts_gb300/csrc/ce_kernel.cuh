@@ -303,8 +303,12 @@ __global__ void __launch_bounds__(kCeThreads, 1) ce_kernel(const __grid_constant
 
     allow_next_kernel();
     if (threadIdx.x == 0) {
-        prefetch_tensormap(&p.side[0].map_p);
-        prefetch_tensormap(&p.side[0].map_q);
+        // (a side without work has no maps)
+        for (const CeSide& sd : p.side) {
+            if (!sd.tiles_m) continue;
+            prefetch_tensormap(&sd.map_p);
+            prefetch_tensormap(&sd.map_q);
+        }
         for (int s = 0; s < GROUPS; ++s) {
             mbar_init(smem_addr(&full[s]), 1);
             mbar_init(smem_addr(&empty[s]), 1);
