@@ -43,7 +43,7 @@ namespace {
 int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
 int64_t up(int64_t a, int64_t b) { return cdiv(a, b) * b; }
 
-constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
+constexpr float kLn2 = 0.6931471805599453f;
 
 // ------------------------------------------------------ small kernels
 
@@ -631,13 +631,6 @@ bool logits_side(CeParams* p, int dtype, CeTile tile, int64_t T, const void* H, 
     s.tiles_n = (int)cdiv(V, tile.bn);
     s.group_m = std::min(s.tiles_m, 16);
     s.idesc = make_idesc(dtype, false, false, tile.bn, tile.rows());
-    // Each tcgen05.mma adds 16 products to the fp32 accumulator and truncates
-    // the sum: for sums of products of either sign a logit comes out smaller
-    // by a quarter of 2^-24 per addition, measured at D = 64 to 8192 in both
-    // types (0.20 to 0.36; products of one sign lose up to 1.6).  lse and the
-    // probabilities see that as a common factor, so the factor that turns
-    // logits into log2 units takes it back; at D = 4096 it is 3.8e-6.
-    p->to_log2 = (float)(1.4426950408889634 * (1.0 + 0.25 * 0x1p-24 * 4.0 * s.num_kb));
     p->rows = (int)T;
     p->cols = (int)V;
     return true;

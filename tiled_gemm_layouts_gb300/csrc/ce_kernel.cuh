@@ -48,6 +48,14 @@ constexpr int kCeThreads = 32 * (3 + kCeEpiWarps);  // producers (warps 0 and 10
 // pair's share of the memory bandwidth.
 constexpr int kCeTileBlocks = 6;
 constexpr int kCeBlocksPerStage = 2;              // K-blocks per barrier transaction
+constexpr float kLog2e = 1.4426950408889634f;     // logit -> log2 units
+// K-blocks that logits sum up in the tensor core's accumulator.  Each
+// tcgen05.mma adds 16 products to it and truncates, up to 2^-23 of the partial
+// sum each time and always towards zero.  A longer contraction (DEEP) therefore runs
+// in parts of this depth; the epilogue warps add the parts in registers, rounded
+// to nearest, while the next part's products run.
+constexpr int kCeDepth = 16;
+static_assert(kCeDepth % kCeBlocksPerStage == 0, "whole transactions");
 
 // 2^x; results below the normal range become 0 (for sums of at least 1).
 __device__ __forceinline__ float pow2(float x) {
@@ -232,13 +240,15 @@ struct CeItems {
 struct CeRowStats {
     float m, s, hit;
     int target;     // column of the target in this launch, or negative
-    float to_log2;
 
     __device__ __forceinline__ void chunk(const uint32_t (&v)[32], int c0, int cols) {
-        if (c0 >= cols) return;
         float x[32];
 #pragma unroll
         for (int j = 0; j < 32; ++j) x[j] = __uint_as_float(v[j]);
+        chunk(x, c0, cols);
+    }
+    __device__ __forceinline__ void chunk(float (&x)[32], int c0, int cols) {
+        if (c0 >= cols) return;
         if (c0 + 32 > cols) {
 #pragma unroll
             for (int j = 0; j < 32; ++j)
@@ -247,19 +257,19 @@ struct CeRowStats {
         const unsigned d = (unsigned)(target - c0);
         if (d < 32u) {
 #pragma unroll
-            for (int j = 0; j < 32; ++j) hit = d == (unsigned)j ? x[j] * to_log2 : hit;
+            for (int j = 0; j < 32; ++j) hit = d == (unsigned)j ? x[j] * kLog2e : hit;
         }
         float top[4] = {x[0], x[1], x[2], x[3]};
 #pragma unroll
         for (int j = 4; j < 32; ++j) top[j & 3] = fmaxf(top[j & 3], x[j]);
-        const float mc = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * to_log2;
+        const float mc = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * kLog2e;
         const float mn = fmaxf(m, mc);
         const float base = mn == -INFINITY ? 0.0f : mn;  // a row of -inf so far: every term is 0
         float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
         for (int j = 0; j < 32; j += 2) {
             float a, b;
-            fma2(x[j], x[j + 1], to_log2, -base, a, b);
+            fma2(x[j], x[j + 1], kLog2e, -base, a, b);
             add2(&sum[j & 2], pow2(a), pow2(b));
         }
         s = s * pow2(m - base) + ((sum[0] + sum[1]) + (sum[2] + sum[3]));
@@ -267,8 +277,9 @@ struct CeRowStats {
     }
 };
 
-// One kernel for all products.  PAIR: a CTA pair works on 256 x BN tiles.
-template <int MODE, int BN, bool PAIR>
+// One kernel for all products.  PAIR: a CTA pair works on 256 x BN tiles.  DEEP:
+// logits whose contraction is longer than kCeDepth K-blocks.
+template <int MODE, int BN, bool PAIR, bool DEEP>
 __global__ void __launch_bounds__(kCeThreads, 1) ce_kernel(const __grid_constant__ CeParams p) {
     using TS = CeShape<BN, PAIR>;
     constexpr bool Q_MN = MODE == CE_PRODUCTS;  // Q's columns contiguous in memory
@@ -276,6 +287,7 @@ __global__ void __launch_bounds__(kCeThreads, 1) ce_kernel(const __grid_constant
     constexpr int STAGES = TS::kSlots;
     constexpr int GROUPS = TS::kGroups;
     constexpr int CG = PAIR ? 2 : 1;
+    static_assert(!(DEEP && BOTH), "the gradients' products are rounded to 16 bits");
     constexpr uint32_t kQBytes = Q_MN ? (uint32_t)TS::kBStage : (uint32_t)TS::kBNC * 128u;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
@@ -445,48 +457,57 @@ __global__ void __launch_bounds__(kCeThreads, 1) ce_kernel(const __grid_constant
         constexpr uint32_t b_kstep = Q_MN ? (2048u >> 4) : (32u >> 4);
         CeItems<MODE> items(p, worker, workers, TS::kBM);
         CeItem it;
-        for (; ok && items.next(it); ++i) {
-            const int buf = i & 1;
+        while (ok && items.next(it)) {
             const bool p_mn = BOTH && it.side == 1;
             const uint32_t idesc = p.side[BOTH ? it.side : 0].idesc;
             const uint32_t a_lo0 = smem_desc_lo(smem_addr(sA), p_mn ? 8192u : 16u);
             const uint32_t a_kstep = p_mn ? (2048u >> 4) : (32u >> 4);
-            if (!wait_bar(smem_addr(&tempty[buf]), ((i >> 1) & 1) ^ 1, w, DEV_TIMEOUT_MMA + 3)) break;
-            tc_fence_after();
-            const uint32_t d_tmem = tmem_base + buf * BN;
-            for (int kb = it.kb0; kb < it.kb1; kb += kCeBlocksPerStage) {
-                const int n = min(it.kb1 - kb, kCeBlocksPerStage);
-                if (!wait_bar(smem_addr(&full[grp]), phase, w, DEV_TIMEOUT_MMA + 4)) {
+            int start = it.kb0;  // of the part
+            do {
+                const int end = DEEP ? min(it.kb1, start + kCeDepth) : it.kb1;
+                const int buf = i & 1;
+                if (!wait_bar(smem_addr(&tempty[buf]), ((i >> 1) & 1) ^ 1, w, DEV_TIMEOUT_MMA + 3)) {
                     ok = false;
                     break;
                 }
                 tc_fence_after();
+                const uint32_t d_tmem = tmem_base + buf * BN;
+                for (int kb = start; kb < end; kb += kCeBlocksPerStage) {
+                    const int n = min(end - kb, kCeBlocksPerStage);
+                    if (!wait_bar(smem_addr(&full[grp]), phase, w, DEV_TIMEOUT_MMA + 4)) {
+                        ok = false;
+                        break;
+                    }
+                    tc_fence_after();
 #pragma unroll
-                for (int j = 0; j < kCeBlocksPerStage; ++j) {
-                    if (j >= n) break;
-                    const uint32_t slot = (uint32_t)(grp * kCeBlocksPerStage + j);
-                    const uint32_t a_lo = a_lo0 + slot * (TS::kAStage >> 4);
-                    const uint32_t b_lo = b_lo0 + slot * (TS::kBStage >> 4);
+                    for (int j = 0; j < kCeBlocksPerStage; ++j) {
+                        if (j >= n) break;
+                        const uint32_t slot = (uint32_t)(grp * kCeBlocksPerStage + j);
+                        const uint32_t a_lo = a_lo0 + slot * (TS::kAStage >> 4);
+                        const uint32_t b_lo = b_lo0 + slot * (TS::kBStage >> 4);
 #pragma unroll
-                    for (int kk = 0; kk < kBK / kUmmaK; ++kk)
-                        mma_f16<CG>(d_tmem, smem_desc_join(a_lo + kk * a_kstep, d_hi),
-                                    smem_desc_join(b_lo + kk * b_kstep, d_hi), idesc,
-                                    (kb + j != it.kb0) || (kk != 0));
+                        for (int kk = 0; kk < kBK / kUmmaK; ++kk)
+                            mma_f16<CG>(d_tmem, smem_desc_join(a_lo + kk * a_kstep, d_hi),
+                                        smem_desc_join(b_lo + kk * b_kstep, d_hi), idesc,
+                                        (kb + j != start) || (kk != 0));
+                    }
+                    if constexpr (PAIR)
+                        mma_commit_pair(smem_addr(&empty[grp]), 0x3);
+                    else
+                        mma_commit(smem_addr(&empty[grp]));
+                    if (++grp == GROUPS) {
+                        grp = 0;
+                        phase ^= 1;
+                    }
                 }
+                if (!ok) break;
                 if constexpr (PAIR)
-                    mma_commit_pair(smem_addr(&empty[grp]), 0x3);
+                    mma_commit_pair(smem_addr(&tfull[buf]), 0x3);
                 else
-                    mma_commit(smem_addr(&empty[grp]));
-                if (++grp == GROUPS) {
-                    grp = 0;
-                    phase ^= 1;
-                }
-            }
-            if (!ok) break;
-            if constexpr (PAIR)
-                mma_commit_pair(smem_addr(&tfull[buf]), 0x3);
-            else
-                mma_commit(smem_addr(&tfull[buf]));
+                    mma_commit(smem_addr(&tfull[buf]));
+                ++i;
+                start = end;
+            } while (DEEP && start < it.kb1);
         }
         // nothing may still write TMEM when it is released
         if constexpr (PAIR)
@@ -508,14 +529,13 @@ __global__ void __launch_bounds__(kCeThreads, 1) ce_kernel(const __grid_constant
         CeItems<MODE> items(p, worker, workers, TS::kBM);
         CeItem it;
         for (int i = 0; items.next(it); ++i) {
-            const int buf = i & 1;
             const CeSide& sd = p.side[BOTH ? it.side : 0];
             const int row0 = it.tm * TS::kBM + (int)rank * 128 + q * 32;  // this warp's first row
             const int row = row0 + lane;
             const int n0 = it.tn * BN + half * (BN / 2);  // and first column
             const bool planes = BOTH && it.side == 0;  // fp32 output
             // what the row's epilogue needs, loaded while the products run
-            CeRowStats st{-INFINITY, 0.0f, 0.0f, -1, p.to_log2};
+            CeRowStats st{-INFINITY, 0.0f, 0.0f, -1};
             float2 rs = make_float2(0.0f, 0.0f);
             int target = -1;
             if constexpr (MODE == CE_LSE) {
@@ -530,24 +550,62 @@ __global__ void __launch_bounds__(kCeThreads, 1) ce_kernel(const __grid_constant
                     if (t >= p.col0 && t < p.col0 + p.cols) target = (int)(t - p.col0);
                 }
             }
-            const bool got = wait_bar(smem_addr(&tfull[buf]), (i >> 1) & 1, w, DEV_TIMEOUT_EPILOGUE + 4);
-            if (!__all_sync(0xffffffffu, got)) break;
-            tc_fence_after();
-            const uint32_t t_row =
-                tmem_base + ((uint32_t)(q * 32) << 16) + buf * BN + half * (BN / 2);
-
+            // G's rows past the last K-block of dW's contraction are not read
+            const bool unused = MODE == CE_GRAD && row0 >= ((max(live, 1) + kBK - 1) & ~(kBK - 1));
+            uint32_t t_row;
+            auto acquire = [&]() {  // accumulator i, this warp's columns
+                const bool got = wait_bar(smem_addr(&tfull[i & 1]), (i >> 1) & 1, w, DEV_TIMEOUT_EPILOGUE + 4);
+                tc_fence_after();
+                t_row = tmem_base + ((uint32_t)(q * 32) << 16) + (i & 1) * BN + half * (BN / 2);
+                return __all_sync(0xffffffffu, got);
+            };
             auto release = [&]() {  // every column of this buffer is in registers
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) {
                     if constexpr (PAIR)
-                        arrive_on_leader(smem_addr(&tempty[buf]));
+                        arrive_on_leader(smem_addr(&tempty[i & 1]));
                     else
-                        mbar_arrive(smem_addr(&tempty[buf]));
+                        mbar_arrive(smem_addr(&tempty[i & 1]));
                 }
             };
             uint32_t va[32], vb[32];
-            if constexpr (MODE == CE_LSE) {
+            // DEEP: the sum of the contraction's parts before the last
+            float sum[DEEP ? kChunks : 1][32];
+            auto add_chunk = [&](int c) {
+                __syncwarp();
+                tmem_ld_32x32b_x32(t_row + c * 32, va);
+                tmem_wait_ld_regs(va);
+#pragma unroll
+                for (int j = 0; j < 32; j += 2)
+                    add2(&sum[c][j], __uint_as_float(va[j]), __uint_as_float(va[j + 1]));
+            };
+            if constexpr (DEEP) {
+#pragma unroll
+                for (int c = 0; c < kChunks; ++c)
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) sum[c][j] = 0.0f;
+                bool ok = true;
+                for (int kb = it.kb0; kb + kCeDepth < it.kb1; kb += kCeDepth, ++i) {
+                    ok = acquire();
+                    if (!ok) break;
+                    if (!unused) {
+#pragma unroll
+                        for (int c = 0; c < kChunks; ++c) add_chunk(c);
+                    }
+                    release();
+                }
+                if (!ok) break;
+            }
+            if (!acquire()) break;
+            if constexpr (MODE == CE_LSE && DEEP) {
+#pragma unroll
+                for (int c = 0; c < kChunks; ++c) {
+                    add_chunk(c);
+                    if (c + 1 == kChunks) release();
+                    st.chunk(sum[c], n0 + c * 32, p.cols);
+                }
+            } else if constexpr (MODE == CE_LSE) {
                 // the next chunk's TMEM load runs beside this chunk's arithmetic
                 __syncwarp();
                 tmem_ld_32x32b_x32(t_row, va);
@@ -574,7 +632,7 @@ __global__ void __launch_bounds__(kCeThreads, 1) ce_kernel(const __grid_constant
                 auto logits_to_gradient = [&](float (&y)[32], int c0) {
 #pragma unroll
                     for (int j = 0; j < 32; j += 2) {
-                        fma2(y[j], y[j + 1], p.to_log2, -rs.x, y[j], y[j + 1]);
+                        fma2(y[j], y[j + 1], kLog2e, -rs.x, y[j], y[j + 1]);
                         y[j] = pow2_gradual(y[j]);
                         y[j + 1] = pow2_gradual(y[j + 1]);
                     }
@@ -604,26 +662,13 @@ __global__ void __launch_bounds__(kCeThreads, 1) ce_kernel(const __grid_constant
                     fence_proxy_async_shared();
                     __syncwarp();
                 };
-                // G's rows past the last K-block of dW's contraction are not read
-                if (MODE == CE_GRAD && row0 >= ((max(live, 1) + kBK - 1) & ~(kBK - 1))) {
+                if (unused) {
                     release();
                     continue;
                 }
-#pragma unroll 1
-                for (int c = 0; c < kChunks; c += 2) {
+                // the accumulator's columns from chunk c, and the next chunk's
+                auto step = [&](int c, float (&ya)[32], float (&yb)[32]) {
                     const int c0 = n0 + c * 32;
-                    __syncwarp();
-                    tmem_ld_32x32b_x32(t_row + c * 32, va);
-                    tmem_ld_32x32b_x32(t_row + (c + 1) * 32, vb);
-                    tmem_wait_ld_regs(va);
-                    tmem_wait_ld_regs(vb);
-                    if (c + 2 == kChunks) release();
-                    float ya[32], yb[32];
-#pragma unroll
-                    for (int j = 0; j < 32; ++j) {
-                        ya[j] = __uint_as_float(va[j]);
-                        yb[j] = __uint_as_float(vb[j]);
-                    }
                     if (planes) {
                         // 32 fp32 columns per store
 #pragma unroll
@@ -647,7 +692,7 @@ __global__ void __launch_bounds__(kCeThreads, 1) ce_kernel(const __grid_constant
                                 bulk_commit_group();
                             }
                         }
-                        continue;
+                        return;
                     }
                     if constexpr (MODE == CE_GRAD) {
                         logits_to_gradient(ya, c0);
@@ -698,6 +743,32 @@ __global__ void __launch_bounds__(kCeThreads, 1) ce_kernel(const __grid_constant
                                     stage + r * 128 + (((x >> 3) ^ (r & 7)) << 4) + (x & 7) * 2);
                         }
                         __syncwarp();
+                    }
+                };
+                if constexpr (DEEP) {
+#pragma unroll
+                    for (int c = 0; c < kChunks; c += 2) {
+                        add_chunk(c);
+                        add_chunk(c + 1);
+                        if (c + 2 == kChunks) release();
+                        step(c, sum[c], sum[c + 1]);
+                    }
+                } else {
+#pragma unroll 1
+                    for (int c = 0; c < kChunks; c += 2) {
+                        __syncwarp();
+                        tmem_ld_32x32b_x32(t_row + c * 32, va);
+                        tmem_ld_32x32b_x32(t_row + (c + 1) * 32, vb);
+                        tmem_wait_ld_regs(va);
+                        tmem_wait_ld_regs(vb);
+                        if (c + 2 == kChunks) release();
+                        float ya[32], yb[32];
+#pragma unroll
+                        for (int j = 0; j < 32; ++j) {
+                            ya[j] = __uint_as_float(va[j]);
+                            yb[j] = __uint_as_float(vb[j]);
+                        }
+                        step(c, ya, yb);
                     }
                 }
             }

@@ -9,10 +9,10 @@
 
 namespace tg {
 
-template <int MODE, int BN, bool PAIR>
-cudaError_t launch_ce_tile(const CeParams& p, int sms, bool chained, cudaStream_t stream) {
+template <int MODE, int BN, bool PAIR, bool DEEP>
+cudaError_t launch_ce_kernel(const CeParams& p, int sms, bool chained, cudaStream_t stream) {
     using TS = CeShape<BN, PAIR>;
-    auto kern = ce_kernel<MODE, BN, PAIR>;
+    auto kern = ce_kernel<MODE, BN, PAIR, DEEP>;
     static std::atomic<unsigned long long> attr_set{0};  // one bit per device
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
@@ -48,6 +48,13 @@ cudaError_t launch_ce_tile(const CeParams& p, int sms, bool chained, cudaStream_
     }
     lc.attrs = attr;
     return cudaLaunchKernelEx(&lc, kern, p);
+}
+
+template <int MODE, int BN, bool PAIR>
+cudaError_t launch_ce_tile(const CeParams& p, int sms, bool chained, cudaStream_t stream) {
+    if constexpr (MODE != CE_PRODUCTS)
+        if (p.side[0].num_kb > kCeDepth) return launch_ce_kernel<MODE, BN, PAIR, true>(p, sms, chained, stream);
+    return launch_ce_kernel<MODE, BN, PAIR, false>(p, sms, chained, stream);
 }
 
 template <int MODE>

@@ -38,7 +38,6 @@ struct alignas(128) CeParams {
     // Rows that count, on the device (null: all): only tile rows of logits and
     // of dH, and K-blocks of dW's contraction, that hold one are worked on.
     const int* live;
-    float to_log2;           // logit -> log2 units
     // CE_LSE and CE_GRAD
     int rows;                // T
     int cols;                // columns of the logits in this launch (a piece of V)
