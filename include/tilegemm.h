@@ -319,7 +319,9 @@ int tg_layernorm_grad_workspace_size(int64_t rows, int64_t cols, tg_dtype dtype,
  *
  * H is T x D (row stride ldh), W is V x D (row stride ldw), both of type
  * `dtype`; target is [T]; loss and lse are fp32 [T]; T, V, D <= 2^30.  The
- * logits are fp32 and stay on chip; the workspace holds 8 bytes per token and
+ * logits are fp32 and stay on chip: the tensor core sums up to 1024 products, 16 at a
+ * time with a truncation of at most 2^-23 of the sum each time, and sums of 1024
+ * are added rounded to nearest.  The workspace holds 8 bytes per token and
  * 64 or 128 columns of the vocabulary.  Two kernel launches, a third where H
  * or W has to be copied.
  * workspace: 256-byte aligned, at least tg_linear_ce_workspace_size() bytes
@@ -343,7 +345,10 @@ int tg_linear_ce_workspace_size(int64_t T, int64_t V, int64_t D, const void* H, 
  * with the lse that tg_linear_ce returned.  The logits are computed again, in
  * pieces of the vocabulary; a piece of G is rounded to `dtype` (scaled so
  * that fp16 does not underflow), both products accumulate in fp32 and are
- * rounded once.  Ignored tokens contribute nothing whatever their rows of H
+ * rounded once.  (Their accumulators run over the whole contraction, a piece of
+ * the vocabulary for dH and the tokens for dW, and truncate once per 16 products:
+ * about a quarter of 2^-24 each time for sums of either sign, 1.2e-4 after
+ * 131072 products.)  Ignored tokens contribute nothing whatever their rows of H
  * hold, and their rows of dH are zeros.  dH or dW may be NULL (not both): it
  * is then not computed.  workspace as above, of
  * tg_linear_ce_grad_workspace_size() bytes: a piece of G of at most 512 MiB

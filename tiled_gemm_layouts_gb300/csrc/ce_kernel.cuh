@@ -53,7 +53,10 @@ constexpr float kLog2e = 1.4426950408889634f;     // logit -> log2 units
 // tcgen05.mma adds 16 products to it and truncates, up to 2^-23 of the partial
 // sum each time and always towards zero.  A longer contraction (DEEP) therefore runs
 // in parts of this depth; the epilogue warps add the parts in registers, rounded
-// to nearest, while the next part's products run.
+// to nearest, while the next part's products run.  lse's error against 64 bits
+// for random operands, and the loss's time, at 8192 x 4096 x 131072: 2.7e-7,
+// 5005 us; one part 1.2e-6, 4960; parts of 8 blocks 1.4e-7, 5057 (and 777 x 1000 x
+// 50021 80 us instead of 76).  At D = 16384, where one part loses 5.3e-6, 3.0e-7.
 constexpr int kCeDepth = 16;
 static_assert(kCeDepth % kCeBlocksPerStage == 0, "whole transactions");
 
