@@ -344,7 +344,8 @@ int tg_linear_ce_workspace_size(int64_t T, int64_t V, int64_t D, const void* H, 
  *
  * with the lse that tg_linear_ce returned.  The logits are computed again, in
  * pieces of the vocabulary; a piece of G is rounded to `dtype` (scaled so
- * that fp16 does not underflow), both products accumulate in fp32 and are
+ * that fp16 keeps full precision down to probabilities of 2^-18 for every token
+ * whose |dloss| is within 2^20 of the largest), both products accumulate in fp32 and are
  * rounded once.  (Their accumulators run over the whole contraction, a piece of
  * the vocabulary for dH and the tokens for dW, and truncate once per 16 products:
  * about a quarter of 2^-24 each time for sums of either sign, 1.2e-4 after

@@ -240,8 +240,27 @@ struct CeRows {
     int* token;         // [T] compacted row -> token
     int* target;        // [T] compacted row -> target
     float2* scale;      // [T] compacted row -> (lse in log2 units, factor of G)
+    float* down;        // [T] compacted row -> what H's row is scaled by in dW's product
     int* place;         // [T] token -> compacted row, or -1
 };
+
+// fp16 ends at 2^-14 (with full precision), a probability is about 1/V, and
+// tokens may weigh very differently: G's rows are scaled by scale2, and those of
+// tokens whose |dloss| is below 2^-kEven of the largest by a power of two `up`
+// more, 2^kMostUp at most.  The scatter of dH takes it back from its row; dW sums
+// over rows of different scale, so its product reads a second copy of H whose
+// rows are scaled by 1 / up.  A token within 2^20 of the heaviest keeps full
+// precision down to probabilities of 2^-18.  (2^-kMostUp of a norm's output is
+// still exact but for elements below 2^-4, and those are off by 2^-15 at most.)  bf16
+// has fp32's range and needs none of it.
+constexpr float kScaleF16 = 16384.0f;  // fp16's largest number is four times that
+constexpr int kEven = 6, kMostUp = 10;
+// 1 / up of a token with dloss / (largest |dloss|) = x
+__device__ __forceinline__ float row_down(float x) {
+    const int e = (int)(__float_as_uint(x) >> 23 & 255u) - 127;  // 2^e <= |x| < 2^(e + 1)
+    const int up = min(max(-e - 1 - kEven, 0), kMostUp);
+    return __uint_as_float((uint32_t)(127 - up) << 23);
+}
 
 constexpr int kCompactThreads = 1024;
 // Up to this many tokens every block of the gather does the compaction for
@@ -307,21 +326,24 @@ struct CeKeep {
     CeRows r;
     const float *lse, *dloss;
     float scale2;
+    bool f16;
     const float* ref;
     __device__ __forceinline__ void operator()(int j, int t, int y) const {
         r.place[t] = j;
         r.token[j] = t;
         r.target[j] = y;
-        r.scale[j] = make_float2(lse[t] * kLog2e, dloss[t] / *ref * scale2);
+        const float x = dloss[t] / *ref, down = f16 ? row_down(x) : 1.0f;
+        r.scale[j] = make_float2(lse[t] * kLog2e, x / down * scale2);
+        r.down[j] = down;
     }
 };
 
 __global__ void __launch_bounds__(kCompactThreads)
 ce_compact_kernel(const long long* __restrict__ target, const float* __restrict__ lse,
-                  const float* __restrict__ dloss, int T, long long V, float scale2, CeRows r) {
+                  const float* __restrict__ dloss, int T, long long V, float scale2, bool f16, CeRows r) {
     allow_next_kernel();
     float ref;
-    const CeKeep keep{r, lse, dloss, scale2, &ref};
+    const CeKeep keep{r, lse, dloss, scale2, f16, &ref};
     const int live = compact(target, dloss, T, V, ref, keep, [&](int t) { r.place[t] = -1; });
     if (threadIdx.x == 0) {
         *r.live = live;
@@ -330,25 +352,27 @@ ce_compact_kernel(const long long* __restrict__ target, const float* __restrict_
 }
 
 // Dense rows of H for the tokens that count: out[j] = H[token[j]], columns
-// [D, ldo) and the rows up to the next multiple of 256 filled with zeros.
+// [D, ldo) and the rows up to the next multiple of 256 filled with zeros; and
+// the same rows scaled, out2[j] = down[j] H[token[j]], if out2 is given (fp16).
 // HERE: the blocks compact for themselves, and the first one writes it down.
 // `w`: a copy of W, where a tensor map cannot describe it.
 template <bool HERE>
 __global__ void __launch_bounds__(kCompactThreads)
 ce_gather_kernel(const uint16_t* __restrict__ H, long long ldh, int D, CeRows r,
-                 uint16_t* __restrict__ out, int ldo, long long max_rows,
+                 uint16_t* __restrict__ out, uint16_t* __restrict__ out2, int ldo, long long max_rows,
                  const long long* __restrict__ target, const float* __restrict__ lse,
-                 const float* __restrict__ dloss, int T, long long V, float scale2, const CopyJob w) {
+                 const float* __restrict__ dloss, int T, long long V, float scale2, bool f16,
+                 const CopyJob w) {
     __shared__ int tokens[HERE ? kCompactEverywhere : 1];
     allow_next_kernel();
     if (w.rows)
         copy_rows(w, blockIdx.x * (long long)kCompactThreads + threadIdx.x,
                   (long long)gridDim.x * kCompactThreads);
     int live;
+    float ref = 1.0f;
     if constexpr (HERE) {
-        float ref;
         const bool first = blockIdx.x == 0;
-        const CeKeep keep{r, lse, dloss, scale2, &ref};
+        const CeKeep keep{r, lse, dloss, scale2, f16, &ref};
         live = compact(
             target, dloss, T, V, ref,
             [&](int j, int t, int y) {
@@ -373,6 +397,7 @@ ce_gather_kernel(const uint16_t* __restrict__ H, long long ldh, int D, CeRows r,
         const long long j = row_of(i, vecs);
         const int c = (int)(i - j * vecs) * 8;
         uint4 v = make_uint4(0, 0, 0, 0);
+        float down = 1.0f;
         if (j < live && c < D) {
             const long long t = HERE ? tokens[j] : r.token[j];
             const uint16_t* s = H + t * ldh + c;
@@ -385,8 +410,16 @@ ce_gather_kernel(const uint16_t* __restrict__ H, long long ldh, int D, CeRows r,
                     if (c + k < D) e[k >> 1] |= (uint32_t)s[k] << (16 * (k & 1));
                 v = make_uint4(e[0], e[1], e[2], e[3]);
             }
+            if (out2) down = HERE ? row_down(dloss[t] / ref) : r.down[j];
         }
         *reinterpret_cast<uint4*>(out + j * ldo + c) = v;
+        if (out2) {
+            const __half2 s = __float2half2_rn(down);
+            __half2* x = reinterpret_cast<__half2*>(&v);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) x[k] = __hmul2(x[k], s);
+            *reinterpret_cast<uint4*>(out2 + j * ldo + c) = v;
+        }
     }
 }
 
@@ -414,8 +447,9 @@ __global__ void ce_scatter_kernel(const float* planes, int splits, long long pla
                 y[0] += a.x; y[1] += a.y; y[2] += a.z; y[3] += a.w;
                 y[4] += b.x; y[5] += b.y; y[6] += b.z; y[7] += b.w;
             }
+            const float back = alpha * r.down[j];
 #pragma unroll
-            for (int k = 0; k < 8; ++k) y[k] *= alpha;
+            for (int k = 0; k < 8; ++k) y[k] *= back;
         }
         uint16_t* o = dH + t * ldd + c;
         if (c + 8 <= D && (reinterpret_cast<uintptr_t>(o) & 15u) == 0) {
@@ -521,11 +555,14 @@ struct BwdPlan {
     CeTile grad, products;
     int64_t dh_kb;       // K-blocks of one split of dH's contraction
     int splits;
-    size_t live, token, target, scale, place, h, g, planes, w, bytes;
+    bool scaled_h;       // dW's product has a copy of H of its own
+    size_t live, token, target, scale, down, place, h, h2, g, planes, w, bytes;
 };
 
-BwdPlan backward_plan(int64_t T, int64_t V, int64_t D, const void* W, int64_t ldw, int sms) {
+BwdPlan backward_plan(int64_t T, int64_t V, int64_t D, const void* W, int64_t ldw, bool dw, int dtype,
+                      int sms) {
     BwdPlan b;
+    b.scaled_h = dw && dtype == TG_F16;
     b.copy_w = !tma_rows(W, ldw);
     b.rows = up(T, 256);
     b.ldh = up(D, 64);
@@ -562,8 +599,10 @@ BwdPlan backward_plan(int64_t T, int64_t V, int64_t D, const void* W, int64_t ld
     b.token = c.take((u128)T * 4);
     b.target = c.take((u128)T * 4);
     b.scale = c.take((u128)T * 8);
+    b.down = c.take((u128)T * 4);
     b.place = c.take((u128)T * 4);
     b.h = c.take((u128)b.rows * b.ldh * 2);
+    b.h2 = c.take(b.scaled_h ? (u128)b.rows * b.ldh * 2 : 0);
     b.g = c.take((u128)b.rows * b.piece * 2);
     b.planes = c.take((u128)b.splits * T * b.ldp * 4);
     b.w = c.take(b.copy_w ? (u128)V * copied_ld(D) * 2 : 0);
@@ -743,7 +782,7 @@ extern "C" int tg_linear_ce_grad_workspace_size(int64_t T, int64_t V, int64_t D,
     int dev;
     DeviceInfo* info;
     if ((rc = current_device(&dev, &info))) return rc;
-    *bytes = backward_plan(T, V, D, W, ldw, info->sms).bytes;
+    *bytes = backward_plan(T, V, D, W, ldw, dW != nullptr, (int)dtype, info->sms).bytes;
     return TG_OK;
 }
 
@@ -771,7 +810,7 @@ extern "C" int tg_linear_ce_grad(int64_t T, int64_t V, int64_t D, const void* H,
     DeviceInfo* info;
     if ((rc = current_device(&dev, &info))) return rc;
     if (!load_driver_entry_points()) return TG_ERR_CUDA;
-    const BwdPlan b = backward_plan(T, V, D, W, ldw, info->sms);
+    const BwdPlan b = backward_plan(T, V, D, W, ldw, dW != nullptr, (int)dtype, info->sms);
     if (workspace_bytes < b.bytes) return TG_ERR_BUFFER;
     const Span work = span_bytes(workspace, b.bytes);
     for (const Span& s : outs)
@@ -803,26 +842,29 @@ extern "C" int tg_linear_ce_grad(int64_t T, int64_t V, int64_t D, const void* H,
     rows.token = reinterpret_cast<int*>(ws + b.token);
     rows.target = reinterpret_cast<int*>(ws + b.target);
     rows.scale = reinterpret_cast<float2*>(ws + b.scale);
+    rows.down = reinterpret_cast<float*>(ws + b.down);
     rows.place = reinterpret_cast<int*>(ws + b.place);
     uint16_t* h = reinterpret_cast<uint16_t*>(ws + b.h);
+    uint16_t* h2 = b.scaled_h ? reinterpret_cast<uint16_t*>(ws + b.h2) : nullptr;
     uint16_t* g = reinterpret_cast<uint16_t*>(ws + b.g);
     float* planes = reinterpret_cast<float*>(ws + b.planes);
-    const float scale2 = dt == TG_F16 ? 1024.0f : 1.0f;
+    const bool f16 = dt == TG_F16;
+    const float scale2 = f16 ? kScaleF16 : 1.0f;
     const long long* tgt = reinterpret_cast<const long long*>(target);
     const bool here = T <= kCompactEverywhere;
     const unsigned gather_blocks = (unsigned)std::min<int64_t>(
         cdiv(b.rows * (b.ldh / 8) + copy_w.rows * (up(D, 8) / 8), kCompactThreads), sms * 2);
     if (here) {
         ce_gather_kernel<true><<<gather_blocks, kCompactThreads, 0, stream>>>(
-            static_cast<const uint16_t*>(H), ldh, (int)D, rows, h, (int)b.ldh, b.rows, tgt, lse, dloss,
-            (int)T, V, scale2, copy_w);
+            static_cast<const uint16_t*>(H), ldh, (int)D, rows, h, h2, (int)b.ldh, b.rows, tgt, lse, dloss,
+            (int)T, V, scale2, f16, copy_w);
         ok = ok && cudaGetLastError() == cudaSuccess;
     } else {
-        ce_compact_kernel<<<1, kCompactThreads, 0, stream>>>(tgt, lse, dloss, (int)T, V, scale2, rows);
+        ce_compact_kernel<<<1, kCompactThreads, 0, stream>>>(tgt, lse, dloss, (int)T, V, scale2, f16, rows);
         ok = ok && cudaGetLastError() == cudaSuccess &&
              launch_chained(ce_gather_kernel<false>, dim3(gather_blocks), kCompactThreads, stream,
-                            static_cast<const uint16_t*>(H), (long long)ldh, (int)D, rows, h, (int)b.ldh,
-                            (long long)b.rows, tgt, lse, dloss, (int)T, (long long)V, scale2,
+                            static_cast<const uint16_t*>(H), (long long)ldh, (int)D, rows, h, h2, (int)b.ldh,
+                            (long long)b.rows, tgt, lse, dloss, (int)T, (long long)V, scale2, f16,
                             copy_w) == cudaSuccess;
     }
 
@@ -875,7 +917,7 @@ extern "C" int tg_linear_ce_grad(int64_t T, int64_t V, int64_t D, const void* H,
             const bool tensor = tma_rows(dW, lddw) && D >= 8;
             p.n_tma = tensor ? (int)(D & ~int64_t(7)) : 0;
             ok = encode_mn_atoms(&s.map_p, dt, g, b.piece, b.rows, b.piece, 2) &&
-                 mn_major_q(&s, dt, b.products, h, b.ldh, b.rows, b.ldh) &&
+                 mn_major_q(&s, dt, b.products, h2 ? h2 : h, b.ldh, b.rows, b.ldh) &&
                  encode_2d(&s.map_c, dt, tensor ? out : g, tensor ? p.n_tma : 8, cols,
                            tensor ? lddw : b.piece, 64, 32);
             s.p_pairs = encode_mn_atom_pairs(&s.map_p2, dt, g, b.piece, b.rows, b.piece, 2)

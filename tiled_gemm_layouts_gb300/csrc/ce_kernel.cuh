@@ -13,8 +13,9 @@
 // recomputes the logits piece by piece of the vocabulary (2TVD operations,
 // where keeping them would take 2TV or 4TV bytes), writes each piece of G in
 // 16 bits, and multiplies it twice.  G is scaled so that its largest possible
-// entry is 1 (bf16) or 1024 (fp16, whose smallest normal number is 6e-5 while
-// a probability is about 1/V); the factor is applied to the fp32 products.
+// entry is 1 (bf16) or 2^14 (fp16, whose smallest normal number is 2^-14 while
+// a probability is about 1/V; rows of light tokens are scaled up further); the
+// factors are applied to the fp32 products.
 //
 // The main loop is that of the GEMM kernel: two TMA producer warps fill a
 // ring of 128B-swizzled stages, one thread issues tcgen05.mma into a
