@@ -648,6 +648,12 @@ __global__ void __launch_bounds__(kCeThreads, 1) ce_kernel(const __grid_constant
                     }
 #pragma unroll
                     for (int j = 0; j < 32; j += 2) mul2(y + j, rs.y);
+                    // no token: H's row is zeros, but W may hold infinities
+                    if (row0 + 32 > live) {
+#pragma unroll
+                        for (int j = 0; j < 32; ++j)
+                            if (row >= live) y[j] = 0.0f;
+                    }
                     if (c0 + 32 > p.cols) {  // the piece's padding columns hold zeros
 #pragma unroll
                         for (int j = 0; j < 32; ++j)
