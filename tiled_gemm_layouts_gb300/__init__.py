@@ -377,15 +377,45 @@ def linear_ce_grad(T, V, D, H, ldh, W, ldw, target, lse, dloss, dH, lddh, dW, ld
         raise TileGemmError(rc, "tg_linear_ce_grad")
 
 
+def _dense(t) -> bool:
+    """Whether a tensor's elements fill one range of memory, in any order."""
+    step = 1
+    for stride, size in sorted(zip(t.stride(), t.shape)):
+        if size != 1 and stride != step:
+            return False
+        step *= size
+    return True
+
+
+def _check_adamw_tensors(row, size, whole) -> None:
+    """The step walks over addresses: the elements of a parameter's tensors have
+    to lie one after another, in one order, and be as many as it walks over."""
+    elements, scales = ([t for t in part if hasattr(t, "stride")] for part in (row[:5], row[5:]))
+    if size == 0:
+        return
+    contiguous = all(t.is_contiguous() for t in elements)
+    alike = all(t.shape == elements[0].shape and t.stride() == elements[0].stride() and _dense(t) for t in elements)
+    if not (contiguous or alike) or not all(t.is_contiguous() for t in scales):
+        raise TileGemmError(TG_ERR_STRIDE, "make_adamw_tensors")
+    if any(t.numel() < size or (whole and t.numel() != size) for t in elements):
+        raise TileGemmError(TG_ERR_INVALID_ARG, "make_adamw_tensors")
+    if any(t.numel() < (size + 255) // 256 for t in scales):
+        raise TileGemmError(TG_ERR_BUFFER, "make_adamw_tensors")
+
+
 def make_adamw_tensors(params, grads, m, v, master=None, m_scale=None, v_scale=None, numel=None):
     """The tensor array of tg_adamw, from lists of pointers or tensors (numel:
     the params' own, where they have it).  It holds addresses only: keep the
-    tensors alive, and make it again when one of them moves."""
+    tensors alive, and make it again when one of them moves.  A parameter's
+    tensors are contiguous, or all dense with the same strides (else
+    TG_ERR_STRIDE), and of its size (TG_ERR_INVALID_ARG; scales: TG_ERR_BUFFER)."""
     n = len(params)
     lists = [params, master or [None] * n, grads, m, v, m_scale or [None] * n, v_scale or [None] * n]
     sizes = numel if numel is not None else [p.numel() for p in params]
     if any(len(x) != n for x in lists) or len(sizes) != n:
         raise TileGemmError(TG_ERR_INVALID_ARG, "make_adamw_tensors")
+    for *row, size in zip(*lists, sizes):
+        _check_adamw_tensors(row, size, numel is None)
     return (tg_adamw_tensor * n)(*[tg_adamw_tensor(*map(_addr, row), size)
                                    for *row, size in zip(*lists, sizes)])
 
