@@ -353,7 +353,9 @@ int tg_linear_ce_workspace_size(int64_t T, int64_t V, int64_t D, const void* H, 
  * hold, and their rows of dH are zeros.  dH or dW may be NULL (not both): it
  * is then not computed.  workspace as above, of
  * tg_linear_ce_grad_workspace_size() bytes: a piece of G of at most 512 MiB
- * (one 256-column strip of it at least), a dense copy of H, dH in fp32.
+ * (one 256-column strip of it at least; of 64 rows for up to 64 tokens), a dense
+ * copy of H (for dW in fp16 a scaled one too), dH in fp32 for each split of its
+ * contraction, and a copy of W whose rows are not 16-byte aligned.
  */
 int tg_linear_ce_grad(int64_t T, int64_t V, int64_t D, const void* H, int64_t ldh, const void* W,
                       int64_t ldw, const int64_t* target, const float* lse, const float* dloss,

@@ -352,7 +352,7 @@ ce_compact_kernel(const long long* __restrict__ target, const float* __restrict_
 }
 
 // Dense rows of H for the tokens that count: out[j] = H[token[j]], columns
-// [D, ldo) and the rows up to the next multiple of 256 filled with zeros; and
+// [D, ldo) and the rows up to the next multiple of 256 (max_rows at most) filled with zeros; and
 // the same rows scaled, out2[j] = down[j] H[token[j]], if out2 is given (fp16).
 // HERE: the blocks compact for themselves, and the first one writes it down.
 // `w`: a copy of W, where a tensor map cannot describe it.
@@ -547,7 +547,7 @@ constexpr int64_t kPieceBytes = 512LL << 20;
 
 struct BwdPlan {
     bool copy_w;
-    int64_t rows;        // T rounded up to whole 256-row tiles
+    int64_t rows;        // of G and of the gathered H: T rounded up to whole tiles
     int64_t ldh;         // columns of the gathered H: D rounded up to whole K-blocks
     int64_t piece;       // columns of a piece of G, a multiple of 256
     int64_t pieces;
@@ -564,7 +564,9 @@ BwdPlan backward_plan(int64_t T, int64_t V, int64_t D, const void* W, int64_t ld
     BwdPlan b;
     b.scaled_h = dw && dtype == TG_F16;
     b.copy_w = !tma_rows(W, ldw);
-    b.rows = up(T, 256);
+    // up to 128 tokens only K-blocks of dW's contraction count (rows of a 128-row
+    // tile beyond them are not stored): 16 MiB of G for one token and V = 131072
+    b.rows = up(T, T <= 128 ? 64 : 256);
     b.ldh = up(D, 64);
     const int64_t tiles_v = cdiv(V, 256);
     int64_t most = kPieceBytes / (b.rows * 512);
