@@ -267,7 +267,7 @@ constexpr int kCompactThreads = 1024;
 // itself (two passes over 12 bytes per token), which saves a launch.
 constexpr int kCompactEverywhere = 2048;
 
-// Stable compaction by one block: the largest |dloss|, then steps of 1024
+// Stable compaction by one block: the largest finite |dloss|, then steps of 1024
 // tokens; returns the number of tokens that count and, to every thread, the
 // factors.  G is scaled by 2^shift / max|dloss|: with one dloss for all tokens
 // its factor is then a power of two, and rounding G to 16 bits rounds
@@ -282,7 +282,7 @@ __device__ __forceinline__ int compact(const long long* __restrict__ target, con
     float top = 0.0f;
     for (int t = threadIdx.x; t < T; t += kCompactThreads) {
         const long long y = target[t];
-        if (y >= 0 && y < V) top = fmaxf(top, fabsf(dloss[t]));
+        if (y >= 0 && y < V && fabsf(dloss[t]) < INFINITY) top = fmaxf(top, fabsf(dloss[t]));
     }
 #pragma unroll
     for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
@@ -291,7 +291,7 @@ __device__ __forceinline__ int compact(const long long* __restrict__ target, con
     top = wmax[lane];
 #pragma unroll
     for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-    ref = top > 0.0f && top < INFINITY ? top : 1.0f;
+    ref = top > 0.0f ? top : 1.0f;
     int total = 0;
     for (int base = 0; base < T; base += kCompactThreads) {
         const int t = base + threadIdx.x;
