@@ -381,7 +381,10 @@ int tg_linear_ce_grad_workspace_size(int64_t T, int64_t V, int64_t D, const void
  * 448th of the block's largest |m| and sqrt(v); m is rounded to nearest even,
  * sqrt(v) stochastically (up with the probability of the part cut off, by
  * bits mixed from the element's index and `seed`: pass another seed each
- * step), and a root above zero never becomes zero.
+ * step; tensors of one step draw the same bits at the same index), and a root
+ * above zero never becomes zero.  A gradient that is infinite or NaN spoils its
+ * own element with 32-bit states; with 8-bit ones also the scales of its block,
+ * and with them all 256 elements from the next step on.
  * `tensors` is a host array, read during the call; a tensor of no elements is
  * skipped.  One kernel launch per 256 tensors.
  * Errors: TG_ERR_INVALID_ARG for a null pointer, a master copy of an fp32

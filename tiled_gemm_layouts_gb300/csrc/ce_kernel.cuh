@@ -26,9 +26,9 @@
 // freed and the kernel returns.
 //
 // What bounds it: at T = 8192, D = 4096, V = 131072 the tensor pipe and the
-// power it draws (the loss 4.79 to 5.0 ms, 1760 to 1840 TFLOP/s; at 4096 x
-// 2048 x 32768, alone, 2058 TFLOP/s with the tensor pipe 96 % busy).  The
-// exponentials run beside the products: 7 % of the special function unit
+// power it draws (the loss 4.74 to 5.0 ms, 1760 to 1860 TFLOP/s; at 4096 x
+// 2048 x 32768, alone, 2090 TFLOP/s with the tensor pipe 94 % busy).  The
+// exponentials run beside the products: 6 % of the special function unit
 // there.  At D below about 500 the epilogue shows.  For a few tokens, reading
 // W: one token against 131072 x 4096 takes 167 us, 6.4 TB/s.
 #pragma once
@@ -58,6 +58,8 @@ constexpr float kLog2e = 1.4426950408889634f;     // logit -> log2 units
 // for random operands, and the loss's time, at 8192 x 4096 x 131072: 2.7e-7,
 // 5005 us; one part 1.2e-6, 4960; parts of 8 blocks 1.4e-7, 5057 (and 777 x 1000 x
 // 50021 80 us instead of 76).  At D = 16384, where one part loses 5.3e-6, 3.0e-7.
+// Reading the accumulator once more per part costs the tensor pipe 1 to 3 %
+// (4096 x 2048 x 32768: 314 us, one part 306).
 constexpr int kCeDepth = 16;
 static_assert(kCeDepth % kCeBlocksPerStage == 0, "whole transactions");
 

@@ -12,11 +12,12 @@
 //
 // Rows of whole 16-byte units come through a ring in shared memory: a team
 // walks over rows while bulk copies bring the next ones, so that loads never
-// wait for a reduction's barrier (16384 x 4096 in bf16: forward 46.5 us, 5.8
-// TB/s, backward 63 us, 6.4 TB/s, and 7 of reduction).  So do long rows of
+// wait for a reduction's barrier (16384 x 4096 in bf16: forward 47.3 us, 5.7
+// TB/s, backward 62.5 us, 6.4 TB/s, and 7 of reduction).  So do long rows of
 // other widths or alignments (16384 x 4095: forward 57.6 us, backward 89).
 // Short ones are loaded by element or by pair into registers, and rows too long
-// for registers are read again from L2 in chunks (wide kernels).
+// for registers are read again from L2 in chunks (wide kernels; 2000 x 32768:
+// forward 74 us, 3.6 TB/s, backward 237 us, whose accesses are single elements).
 //
 // The gradient's blocks walk over rows and keep their columns' dw and db in
 // fp32 registers; one partial row per block goes to the workspace and a second
