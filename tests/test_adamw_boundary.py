@@ -67,10 +67,10 @@ def test_tensors_whose_elements_do_not_lie_one_after_another(tg):
         assert e.value.status == tg.TG_ERR_STRIDE, kw
 
 
-def test_tensors_of_another_size(tg):
+def test_tensors_that_are_too_small(tg):
     import torch
     for kw, code in ((dict(g=torch.zeros(6, 99)), tg.TG_ERR_INVALID_ARG), (dict(m=torch.zeros(599)), tg.TG_ERR_INVALID_ARG),
-                     (dict(v=torch.zeros(601)), tg.TG_ERR_INVALID_ARG), (dict(master=torch.zeros(1)), tg.TG_ERR_INVALID_ARG),
+                     (dict(v=torch.zeros(6, 99)), tg.TG_ERR_INVALID_ARG), (dict(master=torch.zeros(1)), tg.TG_ERR_INVALID_ARG),
                      (dict(ms=torch.zeros(2)), tg.TG_ERR_BUFFER), (dict(vs=torch.zeros(0)), tg.TG_ERR_BUFFER)):
         at, rest = lists(**kw)
         with pytest.raises(tg.TileGemmError) as e:
@@ -92,6 +92,8 @@ def test_tensors_that_may_be_given(tg):
     assert tg.make_adamw_tensors(*at, **rest)[0].numel == 120
     empty = {k: torch.zeros(0, 5) for k in ("p", "g", "m", "v", "master")}
     assert tg.make_adamw_tensors(*lists(**empty)[0])[0].numel == 0
-    # fewer elements than the tensors hold, on request
+    # states that were rounded up to whole blocks; fewer elements than the tensors hold, on request
+    at, rest = lists(m=torch.zeros(768), v=torch.zeros(768), ms=torch.zeros(4))
+    assert tg.make_adamw_tensors(*at, **rest)[0].numel == 600
     at, rest = lists()
     assert tg.make_adamw_tensors(*at, **rest, numel=[512])[0].numel == 512

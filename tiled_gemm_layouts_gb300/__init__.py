@@ -387,9 +387,9 @@ def _dense(t) -> bool:
     return True
 
 
-def _check_adamw_tensors(row, size, whole) -> None:
+def _check_adamw_tensors(row, size) -> None:
     """The step walks over addresses: the elements of a parameter's tensors have
-    to lie one after another, in one order, and be as many as it walks over."""
+    to lie one after another, in one order, and be at least as many as it walks over."""
     elements, scales = ([t for t in part if hasattr(t, "stride")] for part in (row[:5], row[5:]))
     if size == 0:
         return
@@ -397,7 +397,7 @@ def _check_adamw_tensors(row, size, whole) -> None:
     alike = all(t.shape == elements[0].shape and t.stride() == elements[0].stride() and _dense(t) for t in elements)
     if not (contiguous or alike) or not all(t.is_contiguous() for t in scales):
         raise TileGemmError(TG_ERR_STRIDE, "make_adamw_tensors")
-    if any(t.numel() < size or (whole and t.numel() != size) for t in elements):
+    if any(t.numel() < size for t in elements):
         raise TileGemmError(TG_ERR_INVALID_ARG, "make_adamw_tensors")
     if any(t.numel() < (size + 255) // 256 for t in scales):
         raise TileGemmError(TG_ERR_BUFFER, "make_adamw_tensors")
@@ -408,14 +408,14 @@ def make_adamw_tensors(params, grads, m, v, master=None, m_scale=None, v_scale=N
     the params' own, where they have it).  It holds addresses only: keep the
     tensors alive, and make it again when one of them moves.  A parameter's
     tensors are contiguous, or all dense with the same strides (else
-    TG_ERR_STRIDE), and of its size (TG_ERR_INVALID_ARG; scales: TG_ERR_BUFFER)."""
+    TG_ERR_STRIDE), and no smaller (TG_ERR_INVALID_ARG; scales: TG_ERR_BUFFER)."""
     n = len(params)
     lists = [params, master or [None] * n, grads, m, v, m_scale or [None] * n, v_scale or [None] * n]
     sizes = numel if numel is not None else [p.numel() for p in params]
     if any(len(x) != n for x in lists) or len(sizes) != n:
         raise TileGemmError(TG_ERR_INVALID_ARG, "make_adamw_tensors")
     for *row, size in zip(*lists, sizes):
-        _check_adamw_tensors(row, size, numel is None)
+        _check_adamw_tensors(row, size)
     return (tg_adamw_tensor * n)(*[tg_adamw_tensor(*map(_addr, row), size)
                                    for *row, size in zip(*lists, sizes)])
 
