@@ -64,3 +64,12 @@ def test_tensor_maps_are_prefetched_only_where_a_side_has_work():
         assert re.search(re.escape(side) + r"\.tiles_m\b", code[m.start() - 200:m.start()]), m.group(0)
     # and every side of a launch is looked at
     assert not any("side[0]" in m.group(1) for m in calls)
+
+
+def test_producers_fence_before_they_copy_what_stores_wrote():
+    """The gathered H and the copies of W are written with ordinary stores and read
+    by tensor copies in the kernel after, which belong to another proxy."""
+    code = text("ce_kernel.cuh")
+    producer = code[code.index("auto run_producer"):code.index("if (warp == 0 && lane == 0)")]
+    assert "fence_proxy_async_global();" in producer[:producer.index("items.next(it)")]
+    assert code.index("wait_for_previous_kernel();") < code.index("auto run_producer")

@@ -6,7 +6,8 @@
 // Backward: the tokens whose target lies in the vocabulary are gathered into
 // a dense copy of H first.  The others have no gradient, and a batch of
 // prompts or padded texts has many; their rows of H may hold anything, and an
-// infinity times G = 0 would put a NaN into dW.  Then, for each piece of the
+// infinity times G = 0 would put a NaN into dW.  (In fp16 dW's product has a
+// copy of its own, whose rows carry the tokens' weights.)  Then, for each piece of the
 // vocabulary, CE_GRAD and CE_PRODUCTS; at the end dH's fp32 planes are
 // summed, scaled and scattered back to the tokens' rows.
 #include <algorithm>

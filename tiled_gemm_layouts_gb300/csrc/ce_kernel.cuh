@@ -361,6 +361,7 @@ __global__ void __launch_bounds__(kCeThreads, 1) ce_kernel(const __grid_constant
         CeItems<MODE> items(p, worker, workers, TS::kBM);
         CeItem it;
         bool ok = true;
+        fence_proxy_async_global();  // H's gathered rows, copies of H and W
         while (ok && items.next(it)) {
             const CeSide& sd = p.side[BOTH ? it.side : 0];
             const bool p_mn = BOTH && it.side == 1;

@@ -19,6 +19,12 @@ __device__ __forceinline__ void allow_next_kernel() {
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }
 
+// After the wait, by a thread that issues tensor copies: what the kernels before
+// wrote with ordinary stores is visible to them.
+__device__ __forceinline__ void fence_proxy_async_global() {
+    asm volatile("fence.proxy.async.global;" ::: "memory");
+}
+
 template <class... P, class... A>
 cudaError_t launch_chained(void (*kern)(P...), dim3 grid, unsigned block, cudaStream_t stream,
                            A... args) {
