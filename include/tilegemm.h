@@ -38,7 +38,7 @@ enum {
     TG_ERR_ALIGN = 3,              /* pointer not 16-byte aligned or ld*2 not a multiple of 16 (tg_gemm),
                                       or a pointer not 2-byte aligned (every call) */
     TG_ERR_OVERLAP = 4,            /* output bytes intersect an input's bytes */
-    TG_ERR_DTYPE = 5,              /* dtype not TG_F16 / TG_BF16 (tg_adamw: nor TG_F32) */
+    TG_ERR_DTYPE = 5,              /* dtype not TG_F16 / TG_BF16 (tg_adamw, tg_route: nor TG_F32) */
     TG_ERR_UNSUPPORTED_DEVICE = 6, /* no CUDA device, or not compute capability 10.x with tcgen05 */
     TG_ERR_CUDA = 7,               /* a CUDA runtime/driver call or the launch failed */
     TG_ERR_TIMEOUT = 8,            /* a bounded device wait expired (reported by tg_debug_status) */
@@ -48,7 +48,7 @@ enum {
     TG_ERR_BUFFER = 11             /* caller's output buffer or workspace too small */
 };
 
-/* TG_F32 is a type of tg_adamw's parameters and gradients only. */
+/* TG_F32 is a type of tg_adamw's parameters and gradients and of tg_route's logits only. */
 typedef enum { TG_F16 = 0, TG_BF16 = 1, TG_F32 = 2 } tg_dtype;
 
 /* Explicit permute of an operand's storage.  A transposed input must say so;
@@ -415,6 +415,188 @@ typedef struct {
 
 int tg_adamw(int64_t count, const tg_adamw_tensor* tensors, const tg_adamw_options* options,
              cudaStream_t stream);
+
+/* ------------------------------------------------------------------------
+ * Rows that choose their weights: routing of tokens to experts, products
+ * whose rows each pick one of many matrices (with their gradients), the
+ * weighted sum of the rows that belong to a token, and low-rank adapters.
+ *
+ * As for the output head: device pointers, row strides in elements, every
+ * check before any device work, launches on `stream` only, nothing
+ * allocated, no synchronisation, results that repeat bit for bit, outputs
+ * disjoint from every other operand, sums in fp32, workspaces (256-byte
+ * aligned, TG_ERR_BUFFER if too small, no initialisation) that calls
+ * overlapping on the GPU do not share.  Indexes are int32 on the device and
+ * never checked on the host; a kernel that meets one out of range treats it as
+ * the text below says and touches no memory for it.
+ * ---------------------------------------------------------------------- */
+
+typedef enum { TG_ROUTE_SOFTMAX = 0, TG_ROUTE_SIGMOID = 1 } tg_route_score;
+
+typedef struct {
+    int score;       /* tg_route_score */
+    int k;           /* experts of a token, 1..32 and <= E * groups_kept / groups */
+    int groups;      /* groups of E / groups consecutive experts, 1..32, a divisor of E; 1: no groups */
+    int groups_kept; /* of which a token's experts come from this many, 1..groups */
+    int group_top;   /* 1 or 2: a group's key is the sum of its this many best experts' keys */
+    int renormalise; /* 0 or 1: weights divided by their sum */
+    float scale;     /* factor of the weights, finite */
+} tg_route_options;
+
+/*
+ * The k experts of each token and their weights:
+ *
+ *     s[t, e]   = softmax over e of logits[t, e], or 1 / (1 + exp(-logits[t, e]))
+ *     key[t, e] = s[t, e] + bias[e]         (without a bias: the logit)
+ *     index[t]  = the k experts with the largest keys, largest first, among
+ *                 the groups_kept groups with the largest keys
+ *     weight[t, j] = scale * s[t, index[t, j]]      (/ their sum)
+ *
+ * A group's key is the largest key of its experts (group_top = 1), or the sum
+ * of its two largest (2; without a bias of the two largest scores; of one
+ * where only one may be chosen).  Experts and groups are ranked as 64-bit
+ * arithmetic ranks them, equal ones by the lower index.  An expert whose logit is
+ * -inf or NaN is never chosen; where fewer than k may be, index is -1 and
+ * weight 0 for the rest.  Softmax weights of a row that holds a NaN or +inf
+ * are NaN (its scores, where they rank, leave the NaN out and share 1 among
+ * the +inf).
+ * logits: T rows of ld elements of type `dtype` (fp16, bf16 or fp32), E <= 1024;
+ * bias: fp32 [E], finite, or NULL; index and weight: [T, k].
+ * One kernel launch.  Errors: TG_ERR_INVALID_ARG for an option outside its
+ * range, TG_ERR_STRIDE for ld < E, TG_ERR_ALIGN for a pointer that is not a
+ * multiple of its element size.
+ */
+int tg_route(int64_t T, int64_t E, const void* logits, int64_t ld, const float* bias,
+             int32_t* index, float* weight, tg_dtype dtype, const tg_route_options* options,
+             cudaStream_t stream);
+
+/*
+ * Gradient of sum over t, j of dweight[t, j] * weight[t, j] by the logits, for
+ * the experts that tg_route chose (the choice itself has none, and a bias does
+ * not enter the weights).  dlogits: T rows of lddl elements of type `dtype`.
+ * An index outside 0..E-1 contributes nothing; an expert that is named twice
+ * contributes twice.  One kernel launch.
+ */
+int tg_route_grad(int64_t T, int64_t E, const void* logits, int64_t ld, const int32_t* index,
+                  const float* dweight, void* dlogits, int64_t lddl, tg_dtype dtype,
+                  const tg_route_options* options, cudaStream_t stream);
+
+/*
+ * Groups R rows by index: a stable counting sort.  Row i with 0 <= index[i] <
+ * G comes to place[i]; group g's rows stand at places offset[g] ..
+ * offset[g+1]-1 in ascending order, and row[place[i]] = i.  A row of any other
+ * index is in no group: its place is -1, and so is row[] from offset[G] on.
+ * index, row, place: [R]; offset: [G+1]; 1 <= R <= 2^30, 1 <= G <= 4096.
+ * place may be NULL.  One kernel launch for up to 2048 rows, else two.
+ */
+int tg_group_rows(int64_t R, int64_t G, const int32_t* index, int32_t* offset, int32_t* row,
+                  int32_t* place, void* workspace, size_t workspace_bytes, cudaStream_t stream);
+int tg_group_rows_workspace_size(int64_t R, int64_t G, size_t* bytes);
+
+/* What a grouped product's fp32 sums go through before they are rounded:
+ *
+ *     y = acc;  y += bias[g, n];  y = max(y, 0);  y = 0 where relu_of[i, n] <= 0 or is NaN
+ *
+ * each step only when it is asked for.  The last one is the gradient of a ReLU
+ * whose output relu_of is. */
+typedef struct {
+    const void* bias;    /* G rows of ld_bias elements of the product's type, or NULL */
+    int64_t ld_bias;
+    int relu;            /* 0 or 1 */
+    const void* relu_of; /* R rows of ld_relu elements, or NULL */
+    int64_t ld_relu;
+} tg_group_epilogue;
+
+/*
+ * One product per group of rows, each group with a matrix of its own:
+ *
+ *     Y[i, :] = epilogue( X[source(i), :] B[g] )       offset[g] <= i < offset[g+1]
+ *     source(i) = row[i] / per_row        (row NULL: i itself)
+ *
+ * Y has R rows of N elements; rows outside every group are left as they are.
+ * X has x_rows rows of K elements.  B[g] is K x N and starts g * stride_b
+ * elements after B: permB = TG_OP_N has its K rows of N elements ldb apart,
+ * TG_OP_T its transpose's N rows of K.  offset [G+1] ascends within 0..R (a
+ * value outside is taken for the nearest of them).  A source outside 0..x_rows-1
+ * is a row of zeros.  So with the row and offset of tg_group_rows over
+ * index[T, k], per_row = k, this is the experts' first product, without a
+ * gathered copy of X; with row NULL the second; and with the other permB the
+ * gradient by the grouped rows (for the first product's input: summed for each
+ * token by tg_combine).
+ * dtype fp16 or bf16.  As tg_gemm, 16-byte-aligned pointers and strides that
+ * are multiples of 16 bytes, else TG_ERR_ALIGN.  epi may be NULL.  R, N, K,
+ * x_rows <= 2^30, G <= 4096.  One kernel launch; waits are bounded.
+ */
+int tg_grouped_gemm(int64_t R, int64_t N, int64_t K, int64_t G, const void* X, int64_t x_rows,
+                    int64_t ldx, const int32_t* row, int64_t per_row, const void* B, int64_t ldb,
+                    int64_t stride_b, tg_perm permB, const int32_t* offset, void* Y, int64_t ldy,
+                    tg_dtype dtype, const tg_group_epilogue* epi, cudaStream_t stream);
+
+/*
+ * The gradient of tg_grouped_gemm (without epilogue) by the matrices:
+ *
+ *     dB[g] = sum over the rows i of group g of X[source(i), :]^T dY[i, :]
+ *
+ * (K x N, stored as permB, ldb and stride_b say; its transpose for TG_OP_T).
+ * Every element of every dB[g] is written; a group without rows has zeros.
+ * Arguments and errors as there.  One kernel launch.
+ */
+int tg_grouped_gemm_grad(int64_t R, int64_t N, int64_t K, int64_t G, const void* dY, int64_t lddy,
+                         const void* X, int64_t x_rows, int64_t ldx, const int32_t* row,
+                         int64_t per_row, const int32_t* offset, void* dB, int64_t lddb,
+                         int64_t stride_db, tg_perm permB, tg_dtype dtype, cudaStream_t stream);
+
+/*
+ * The weighted sum of each token's rows:
+ *
+ *     out[t, :] = sum over j < k of weight[t, j] * Y[place[t, j], :]
+ *
+ * place and weight: [T, k]; Y: y_rows rows of D elements; out: T rows.  weight
+ * may be NULL (all 1).  A place outside 0..y_rows-1 contributes nothing, whatever
+ * its weight; a token without any has a row of zeros.  k <= 1024.  Any
+ * 2-byte-aligned rows (16-byte-aligned ones are faster).  One kernel launch.
+ */
+int tg_combine(int64_t T, int64_t k, int64_t D, const void* Y, int64_t y_rows, int64_t ldy,
+               const int32_t* place, const float* weight, void* out, int64_t ldo, tg_dtype dtype,
+               cudaStream_t stream);
+
+/*
+ * Gradient of tg_combine:
+ *
+ *     dY[place[t, j], :] = weight[t, j] * dout[t, :]
+ *     dweight[t, j] = sum over d of dout[t, d] * Y[place[t, j], d]    (0 without a place)
+ *
+ * Rows of dY (y_rows of them) that no place names are left as they are; the
+ * places are different from one another (as tg_group_rows makes them: of two
+ * equal ones either may be written).  dY or dweight may be NULL (not both).
+ * weight may be NULL (all 1); Y may be NULL without dweight.  One kernel launch.
+ */
+int tg_combine_grad(int64_t T, int64_t k, int64_t D, const void* dout, int64_t lddo, const void* Y,
+                    int64_t y_rows, int64_t ldy, const int32_t* place, const float* weight, void* dY,
+                    int64_t lddy, float* dweight, tg_dtype dtype, cudaStream_t stream);
+
+/*
+ * Low-rank adapters of many requests, added to a shared projection's output in
+ * place:
+ *
+ *     Y[t, :] += scale[g] * (X[t, :] A[g]^T) B[g]^T       t = row[i], offset[g] <= i < offset[g+1]
+ *
+ * A[g]: rank rows of K elements, lda apart, g * rank * lda after A; B[g]: N rows
+ * of rank elements, ldb apart, g * N * ldb after B; scale: fp32 [G] or NULL (all
+ * 1).  X and Y have T rows; row [T] and offset [G+1] are tg_group_rows' over the
+ * adapter of each token (-1: none): rows of no adapter are left as they are.
+ * A row outside 0..T-1 is left out; the rows are different from one another.
+ * The rank-wide products are kept to about twice 16 bits' precision, and Y
+ * is rounded once.  rank <= 128; dtype fp16 or bf16; 16-byte-aligned
+ * pointers and strides (else TG_ERR_ALIGN); T, N, K <= 2^30, G <= 4096.
+ * workspace: tg_adapters_workspace_size() bytes.  Two kernel launches.
+ */
+int tg_adapters(int64_t T, int64_t N, int64_t K, int64_t rank, int64_t G, const void* X, int64_t ldx,
+                const int32_t* row, const int32_t* offset, const void* A, int64_t lda, const void* B,
+                int64_t ldb, const float* scale, void* Y, int64_t ldy, tg_dtype dtype,
+                void* workspace, size_t workspace_bytes, cudaStream_t stream);
+int tg_adapters_workspace_size(int64_t T, int64_t N, int64_t K, int64_t rank, int64_t G,
+                               tg_dtype dtype, size_t* bytes);
 
 /* Static name of a status code ("TG_OK", "TG_ERR_ALIGN", ...). */
 const char* tg_status_string(int status);

@@ -38,8 +38,9 @@ TG_ERR_POINTER = 9
 TG_ERR_LAYOUT = 10
 TG_ERR_BUFFER = 11
 
-TG_F16, TG_BF16, TG_F32 = 0, 1, 2  # TG_F32: tg_adamw only
+TG_F16, TG_BF16, TG_F32 = 0, 1, 2  # TG_F32: tg_adamw and tg_route only
 TG_OP_N, TG_OP_T = 0, 1
+TG_ROUTE_SOFTMAX, TG_ROUTE_SIGMOID = 0, 1
 
 _i64, _int, _vp, _cp = ctypes.c_int64, ctypes.c_int, ctypes.c_void_p, ctypes.c_char_p
 
@@ -59,6 +60,16 @@ class tg_adamw_options(ctypes.Structure):
                 ("eps", ctypes.c_double), ("weight_decay", ctypes.c_double), ("step", _i64),
                 ("dtype", _int), ("grad_dtype", _int), ("state_bits", _int),
                 ("seed", ctypes.c_uint32), ("grad_scale", _vp)]
+
+
+class tg_route_options(ctypes.Structure):
+    _fields_ = [("score", _int), ("k", _int), ("groups", _int), ("groups_kept", _int),
+                ("group_top", _int), ("renormalise", _int), ("scale", ctypes.c_float)]
+
+
+class tg_group_epilogue(ctypes.Structure):
+    _fields_ = [("bias", _vp), ("ld_bias", _i64), ("relu", _int), ("relu_of", _vp),
+                ("ld_relu", _i64)]
 
 
 def _sig(name, res, *args):
@@ -105,6 +116,21 @@ _sig("tg_linear_ce_grad", _int, _i64, _i64, _i64, _vp, _i64, _vp, _i64, _vp, _vp
 _sig("tg_linear_ce_grad_workspace_size", _int, _i64, _i64, _i64, _vp, _i64, _vp, _i64, _vp, _i64, _vp,
      _i64, _int, _size_p)
 _sig("tg_adamw", _int, _i64, ctypes.POINTER(tg_adamw_tensor), ctypes.POINTER(tg_adamw_options), _vp)
+_route_p, _group_epi_p = ctypes.POINTER(tg_route_options), ctypes.POINTER(tg_group_epilogue)
+_sig("tg_route", _int, _i64, _i64, _vp, _i64, _vp, _vp, _vp, _int, _route_p, _vp)
+_sig("tg_route_grad", _int, _i64, _i64, _vp, _i64, _vp, _vp, _vp, _i64, _int, _route_p, _vp)
+_sig("tg_group_rows", _int, _i64, _i64, _vp, _vp, _vp, _vp, _vp, ctypes.c_size_t, _vp)
+_sig("tg_group_rows_workspace_size", _int, _i64, _i64, _size_p)
+_sig("tg_grouped_gemm", _int, _i64, _i64, _i64, _i64, _vp, _i64, _i64, _vp, _i64, _vp, _i64, _i64, _int,
+     _vp, _vp, _i64, _int, _group_epi_p, _vp)
+_sig("tg_grouped_gemm_grad", _int, _i64, _i64, _i64, _i64, _vp, _i64, _vp, _i64, _i64, _vp, _i64, _vp,
+     _vp, _i64, _i64, _int, _int, _vp)
+_sig("tg_combine", _int, _i64, _i64, _i64, _vp, _i64, _i64, _vp, _vp, _vp, _i64, _int, _vp)
+_sig("tg_combine_grad", _int, _i64, _i64, _i64, _vp, _i64, _vp, _i64, _i64, _vp, _vp, _vp, _i64, _vp,
+     _int, _vp)
+_sig("tg_adapters", _int, _i64, _i64, _i64, _i64, _i64, _vp, _i64, _vp, _vp, _vp, _i64, _vp, _i64, _vp,
+     _vp, _i64, _int, _vp, ctypes.c_size_t, _vp)
+_sig("tg_adapters_workspace_size", _int, _i64, _i64, _i64, _i64, _i64, _int, _size_p)
 _sig("tg_debug_status", _int, ctypes.POINTER(_int))
 _sig("tg_debug_configure", _int, _i64, _i64)
 _sig("tg_probe_swizzle128", _int, _vp, _int, _i64, _vp, _vp, _vp)
@@ -436,6 +462,123 @@ def adamw(tensors, options, stream=None) -> None:
     rc = tg_adamw(tensors, options, stream)
     if rc != TG_OK:
         raise TileGemmError(rc, "tg_adamw")
+
+
+def make_route_options(k, score=TG_ROUTE_SOFTMAX, groups=1, groups_kept=1, group_top=1,
+                       renormalise=False, scale=1.0):
+    return tg_route_options(score, k, groups, groups_kept, group_top, int(renormalise), scale)
+
+
+def tg_route(T, E, logits, ld, bias, index, weight, dtype, options, stream=None) -> int:
+    return _lib.tg_route(T, E, _addr(logits), ld, _addr(bias), _addr(index), _addr(weight), dtype,
+                         ctypes.byref(options) if options is not None else None, _stream(stream))
+
+
+def route(T, E, logits, ld, bias, index, weight, dtype, options, stream=None) -> None:
+    _check(tg_route(T, E, logits, ld, bias, index, weight, dtype, options, stream), "tg_route")
+
+
+def tg_route_grad(T, E, logits, ld, index, dweight, dlogits, lddl, dtype, options,
+                  stream=None) -> int:
+    return _lib.tg_route_grad(T, E, _addr(logits), ld, _addr(index), _addr(dweight),
+                              _addr(dlogits), lddl, dtype,
+                              ctypes.byref(options) if options is not None else None,
+                              _stream(stream))
+
+
+def route_grad(T, E, logits, ld, index, dweight, dlogits, lddl, dtype, options,
+               stream=None) -> None:
+    _check(tg_route_grad(T, E, logits, ld, index, dweight, dlogits, lddl, dtype, options, stream),
+           "tg_route_grad")
+
+
+def tg_group_rows_workspace_size(R, G) -> int:
+    n = ctypes.c_size_t(0)
+    _check(_lib.tg_group_rows_workspace_size(R, G, ctypes.byref(n)), "tg_group_rows_workspace_size")
+    return n.value
+
+
+def tg_group_rows(R, G, index, offset, row, place, workspace, workspace_bytes, stream=None) -> int:
+    return _lib.tg_group_rows(R, G, _addr(index), _addr(offset), _addr(row), _addr(place),
+                              _addr(workspace), workspace_bytes, _stream(stream))
+
+
+def group_rows(R, G, index, offset, row, place, workspace, workspace_bytes, stream=None) -> None:
+    _check(tg_group_rows(R, G, index, offset, row, place, workspace, workspace_bytes, stream),
+           "tg_group_rows")
+
+
+def make_group_epilogue(bias=None, ld_bias=0, relu=False, relu_of=None, ld_relu=0):
+    return tg_group_epilogue(_addr(bias), ld_bias, int(relu), _addr(relu_of), ld_relu)
+
+
+def tg_grouped_gemm(R, N, K, G, X, x_rows, ldx, row, per_row, B, ldb, stride_b, permB, offset, Y,
+                    ldy, dtype, epi=None, stream=None) -> int:
+    return _lib.tg_grouped_gemm(R, N, K, G, _addr(X), x_rows, ldx, _addr(row), per_row, _addr(B),
+                                ldb, stride_b, permB, _addr(offset), _addr(Y), ldy, dtype,
+                                ctypes.byref(epi) if epi is not None else None, _stream(stream))
+
+
+def grouped_gemm(R, N, K, G, X, x_rows, ldx, row, per_row, B, ldb, stride_b, permB, offset, Y,
+                 ldy, dtype, epi=None, stream=None) -> None:
+    _check(tg_grouped_gemm(R, N, K, G, X, x_rows, ldx, row, per_row, B, ldb, stride_b, permB,
+                           offset, Y, ldy, dtype, epi, stream), "tg_grouped_gemm")
+
+
+def tg_grouped_gemm_grad(R, N, K, G, dY, lddy, X, x_rows, ldx, row, per_row, offset, dB, lddb,
+                         stride_db, permB, dtype, stream=None) -> int:
+    return _lib.tg_grouped_gemm_grad(R, N, K, G, _addr(dY), lddy, _addr(X), x_rows, ldx,
+                                     _addr(row), per_row, _addr(offset), _addr(dB), lddb,
+                                     stride_db, permB, dtype, _stream(stream))
+
+
+def grouped_gemm_grad(R, N, K, G, dY, lddy, X, x_rows, ldx, row, per_row, offset, dB, lddb,
+                      stride_db, permB, dtype, stream=None) -> None:
+    _check(tg_grouped_gemm_grad(R, N, K, G, dY, lddy, X, x_rows, ldx, row, per_row, offset, dB,
+                                lddb, stride_db, permB, dtype, stream), "tg_grouped_gemm_grad")
+
+
+def tg_combine(T, k, D, Y, y_rows, ldy, place, weight, out, ldo, dtype, stream=None) -> int:
+    return _lib.tg_combine(T, k, D, _addr(Y), y_rows, ldy, _addr(place), _addr(weight), _addr(out),
+                           ldo, dtype, _stream(stream))
+
+
+def combine(T, k, D, Y, y_rows, ldy, place, weight, out, ldo, dtype, stream=None) -> None:
+    _check(tg_combine(T, k, D, Y, y_rows, ldy, place, weight, out, ldo, dtype, stream),
+           "tg_combine")
+
+
+def tg_combine_grad(T, k, D, dout, lddo, Y, y_rows, ldy, place, weight, dY, lddy, dweight, dtype,
+                    stream=None) -> int:
+    return _lib.tg_combine_grad(T, k, D, _addr(dout), lddo, _addr(Y), y_rows, ldy, _addr(place),
+                                _addr(weight), _addr(dY), lddy, _addr(dweight), dtype,
+                                _stream(stream))
+
+
+def combine_grad(T, k, D, dout, lddo, Y, y_rows, ldy, place, weight, dY, lddy, dweight, dtype,
+                 stream=None) -> None:
+    _check(tg_combine_grad(T, k, D, dout, lddo, Y, y_rows, ldy, place, weight, dY, lddy, dweight,
+                           dtype, stream), "tg_combine_grad")
+
+
+def tg_adapters_workspace_size(T, N, K, rank, G, dtype) -> int:
+    n = ctypes.c_size_t(0)
+    _check(_lib.tg_adapters_workspace_size(T, N, K, rank, G, dtype, ctypes.byref(n)),
+           "tg_adapters_workspace_size")
+    return n.value
+
+
+def tg_adapters(T, N, K, rank, G, X, ldx, row, offset, A, lda, B, ldb, scale, Y, ldy, dtype,
+                workspace, workspace_bytes, stream=None) -> int:
+    return _lib.tg_adapters(T, N, K, rank, G, _addr(X), ldx, _addr(row), _addr(offset), _addr(A),
+                            lda, _addr(B), ldb, _addr(scale), _addr(Y), ldy, dtype,
+                            _addr(workspace), workspace_bytes, _stream(stream))
+
+
+def adapters(T, N, K, rank, G, X, ldx, row, offset, A, lda, B, ldb, scale, Y, ldy, dtype,
+             workspace, workspace_bytes, stream=None) -> None:
+    _check(tg_adapters(T, N, K, rank, G, X, ldx, row, offset, A, lda, B, ldb, scale, Y, ldy, dtype,
+                       workspace, workspace_bytes, stream), "tg_adapters")
 
 
 def tg_gemm_workspace_size_ex(M, N, K, A, lda, permA, B, ldb, permB, C, ldc, dtype,

@@ -1,0 +1,536 @@
+// grouped_kernel.cuh -- products in which every group of rows has a matrix of
+// its own, on sm_103a: the experts' products, their gradients, and low-rank
+// adapters.
+//
+//   GROUPED_ROWS     Y[i] = epilogue(X[source(i)] B[g])        rows i of group g
+//   GROUPED_WEIGHT   dB[g] = sum over them of X[source(i)]^T dY[i]
+//
+// The main loop is that of the GEMM kernel: TMA producers fill a ring of
+// 128B-swizzled stages, one thread issues tcgen05.mma into a double-buffered
+// fp32 accumulator in TMEM, eight epilogue warps drain it while the next
+// tile's products run; tiles of 256 x BN on a CTA pair, or 128 x BN on one CTA.
+//
+// Groups.  Only the device knows how many rows a group has.  Workers walk the
+// same list of tiles, group by group, each taking every `workers`-th: a warp
+// reads 128 groups' offsets at a time, one scan over its lanes gives their
+// first tiles, a ballot the group of a tile.  Nothing is planned by another
+// kernel or kept between calls.
+//
+// Rows by a list are gathered by the copies themselves: a gathering TMA copy
+// takes four row numbers, so the 32 lanes of the producer warp fetch the 128
+// rows of a stage, each the same four rows in every K-block, in the layout
+// that a box of 128 consecutive rows would have.  No gathered copy of X is
+// written (at 65536 rows of 4096 columns that would be 1.07 GB more traffic).
+// Rows past a group's end are not fetched at all: what is left in their part
+// of the stage only reaches accumulator rows that are not stored, so a tile of
+// one row costs one copy of 512 bytes beside the matrix's.
+//
+// In GROUPED_WEIGHT the rows are the contraction, and a group's last K-block is
+// ragged: it is fetched by row number from both operands, with numbers outside
+// the matrix for the rows that are none of the group's, which the copy fills
+// with zeros (a box would bring the next group's rows, whose infinities a zero
+// in the other operand does not undo).
+//
+// Every wait is bounded; on a timeout the status word is set, copies and MMAs
+// in flight are drained, TMEM is freed and the kernel returns.
+#pragma once
+
+#include "ce_kernel.cuh"
+#include "chained.cuh"
+#include "gemm_kernel.cuh"
+#include "grouped_params.h"
+
+namespace tg {
+
+constexpr int kGrEpiWarps = 8;   // two per TMEM lane quadrant, each with half of a tile's columns
+constexpr int kGrThreads = 32 * (3 + kGrEpiWarps);  // producers (warps 0 and 10), MMA (1), epilogue (2..9)
+
+template <int BN, bool PAIR>
+struct GroupedShape : TileShape<BN, PAIR> {
+    using TS = TileShape<BN, PAIR>;
+    static constexpr int kUnit = 4096;  // staging per epilogue warp: 32 rows of 128 bytes
+    static constexpr int kFit = (TS::kSmemLimit - 1024 - 256 - kGrEpiWarps * kUnit) / TS::kStage;
+    static constexpr int kSlots = kFit > 8 ? 8 : kFit;
+    static constexpr int kGrSmemBytes = 1024 + kSlots * TS::kStage + kGrEpiWarps * kUnit + (2 * kSlots + 5) * 8 + 16;
+    static_assert(kSlots >= 4 && kGrSmemBytes <= TS::kSmemLimit, "shared memory budget");
+};
+
+// Gathers rows r[0..3], columns c .. c+63, as four consecutive 128-byte rows.
+template <bool PAIR>
+__device__ __forceinline__ void tma_gather4(uint32_t dst, const CUtensorMap* map, uint32_t bar, int c,
+                                            const int (&r)[4]) {
+    if constexpr (PAIR)
+        asm volatile(
+            "cp.async.bulk.tensor.2d.shared::cluster.global.tile::gather4.mbarrier::complete_tx::bytes"
+            ".cta_group::2 [%0], [%1, {%3, %4, %5, %6, %7}], [%2];" ::"r"(dst),
+            "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(c), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3])
+            : "memory");
+    else
+        asm volatile(
+            "cp.async.bulk.tensor.2d.shared::cluster.global.tile::gather4.mbarrier::complete_tx::bytes"
+            " [%0], [%1, {%3, %4, %5, %6, %7}], [%2];" ::"r"(dst),
+            "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(c), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3])
+            : "memory");
+}
+
+// Source of grouped row i (counted from the group's first, lo); a number
+// outside the matrix for rows that are none of the group's cnt.
+__device__ __forceinline__ int source_row(const GroupedRows& s, int lo, int i, int cnt) {
+    if (i >= cnt) return s.count;
+    if (!s.row) return lo + i;
+    const int r = s.row[lo + i];
+    return r < 0 ? s.count : (int)((unsigned)r / (unsigned)s.per_row);
+}
+
+struct GroupedItem {
+    int g, lo, cnt;  // group, its first row, its rows
+    int tm, tn;
+};
+
+// The tiles of one worker, in order.  Called by whole warps; every lane gets
+// the same item.
+template <int MODE>
+struct GroupedItems {
+    const GroupedParams& p;
+    int lane, bm, t, step;
+    int window, base, incl;  // groups from `window`, their first tile, tiles up to this lane's last group
+    int lo[4], cnt[4];       // this lane's four groups
+    bool started;
+
+    __device__ __forceinline__ GroupedItems(const GroupedParams& params, int worker, int workers, int rows_per_tile)
+        : p(params), lane(threadIdx.x & 31), bm(rows_per_tile), t(worker), step(workers), window(-128), base(0),
+          incl(0), started(false) {}
+
+    __device__ __forceinline__ int bound(int g) const {
+        return max(0, min(p.offset[g], p.rows));
+    }
+    __device__ __forceinline__ int tiles_of(int k) const { return (cnt[k] + bm - 1) / bm * p.tiles_n; }
+    __device__ __forceinline__ void place(GroupedItem& it, int i, int tiles_m) const {
+        const int group = p.group_m * p.tiles_n;
+        const int first = i / group * p.group_m;
+        const int gm = min(tiles_m - first, p.group_m), r = i - i / group * group;
+        it.tm = first + r % gm;
+        it.tn = r / gm;
+    }
+    __device__ __forceinline__ bool next(GroupedItem& it) {
+        if constexpr (MODE == GROUPED_WEIGHT) {
+            const int per = p.tiles_m * p.tiles_n;
+            it.g = t / per;
+            if (it.g >= p.groups) return false;
+            it.lo = bound(it.g);
+            it.cnt = max(0, bound(it.g + 1) - it.lo);
+            place(it, t - it.g * per, p.tiles_m);
+            t += step;
+            return true;
+        } else {
+            while (!started || t >= base + __shfl_sync(0xffffffffu, incl, 31)) {
+                if (started) base += __shfl_sync(0xffffffffu, incl, 31);
+                started = true;
+                window += 128;
+                if (window >= p.groups) {
+                    t = 0x40000000;  // past every tile, for any further call
+                    incl = 0;
+                    window = 0x40000000;
+                    return false;
+                }
+                int end[5];
+#pragma unroll
+                for (int k = 0; k < 5; ++k) end[k] = bound(min(window + 4 * lane + k, p.groups));
+                incl = 0;
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    lo[k] = end[k];
+                    cnt[k] = max(0, end[k + 1] - end[k]);
+                    incl += tiles_of(k);
+                }
+#pragma unroll
+                for (int d = 1; d < 32; d *= 2) {
+                    const int o = __shfl_up_sync(0xffffffffu, incl, d);
+                    if (lane >= d) incl += o;
+                }
+            }
+            const int owner = __ffs(__ballot_sync(0xffffffffu, t < base + incl)) - 1;
+            // its tiles before this one, group by group
+            int i = t - base - (incl - (tiles_of(0) + tiles_of(1) + tiles_of(2) + tiles_of(3)));
+            int k = 0, first = lo[0], rows = cnt[0];
+#pragma unroll
+            for (int j = 0; j < 3; ++j)
+                if (k == j && i >= tiles_of(j)) {
+                    i -= tiles_of(j);
+                    k = j + 1;
+                    first = lo[j + 1];
+                    rows = cnt[j + 1];
+                }
+            it.g = window + 4 * owner + __shfl_sync(0xffffffffu, k, owner);
+            it.lo = __shfl_sync(0xffffffffu, first, owner);
+            it.cnt = __shfl_sync(0xffffffffu, rows, owner);
+            place(it, __shfl_sync(0xffffffffu, i, owner), (it.cnt + bm - 1) / bm);
+            t += step;
+            return true;
+        }
+    }
+};
+
+template <int MODE, int BN, bool PAIR>
+__global__ void __launch_bounds__(kGrThreads, 1) grouped_kernel(const __grid_constant__ GroupedParams p) {
+    using TS = GroupedShape<BN, PAIR>;
+    constexpr bool WEIGHT = MODE == GROUPED_WEIGHT;
+    constexpr int SLOTS = TS::kSlots;
+    constexpr int CG = PAIR ? 2 : 1;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                               ~uintptr_t(1023));
+    uint8_t* sA = smem;
+    uint8_t* sB = smem + SLOTS * TS::kAStage;
+    uint8_t* staging = sB + SLOTS * TS::kBStage;
+    uint64_t* full = reinterpret_cast<uint64_t*>(staging + kGrEpiWarps * TS::kUnit);
+    uint64_t* empty = full + SLOTS;
+    uint64_t* tfull = empty + SLOTS;
+    uint64_t* tempty = tfull + 2;
+    uint64_t* drain = tempty + 2;
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+
+    const int warp = threadIdx.x >> 5;
+    const int lane = threadIdx.x & 31;
+    const uint32_t rank = PAIR ? cluster_ctarank() : 0;
+    const bool leader = rank == 0;
+    const int worker = PAIR ? (int)(blockIdx.x >> 1) : (int)blockIdx.x;
+    const int workers = PAIR ? (int)(gridDim.x >> 1) : (int)gridDim.x;
+    const Watch w{abort_flag,
+                  PAIR ? mapa_shared(smem_addr((const void*)abort_flag), rank ^ 1u) : 0u, PAIR,
+                  p.status, p.timeout_cycles};
+
+    allow_next_kernel();
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < SLOTS; ++s) {
+            mbar_init(smem_addr(&full[s]), 1);
+            mbar_init(smem_addr(&empty[s]), 1);
+        }
+        for (int b = 0; b < 2; ++b) {
+            mbar_init(smem_addr(&tfull[b]), 1);
+            mbar_init(smem_addr(&tempty[b]), (PAIR ? 2 : 1) * kGrEpiWarps);
+        }
+        mbar_init(smem_addr(drain), 1);
+        *abort_flag = 0;
+        fence_barrier_init();
+    }
+    if (warp == 1) {
+        tmem_alloc<CG>(smem_addr(tmem_slot), TS::kTmemCols);
+        tmem_relinquish<CG>();
+    }
+    tc_fence_before();
+    if constexpr (PAIR)
+        cluster_sync();
+    else
+        __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem_base = *tmem_slot;
+    wait_for_previous_kernel();
+
+    // K-blocks of an item (a group without rows still has one, of zeros)
+    auto blocks_of = [&](const GroupedItem& it) { return WEIGHT ? max(1, (it.cnt + kBK - 1) / kBK) : p.num_kb; };
+    // rows of the tile that lie in CTA r
+    auto rows_in = [&](const GroupedItem& it, int r) { return min(128, max(0, it.cnt - it.tm * TS::kBM - 128 * r)); };
+
+    if (warp == 0 || warp == 2 + kGrEpiWarps) {
+        // -------------------------------------------------- TMA producers
+        // Warp 0 arms each slot and fetches P, the other one fetches Q into it.
+        const bool first = warp == 0;
+        int slot = 0;
+        uint32_t phase = 0, armed = 0, armed_parity = 0;
+        GroupedItems<MODE> items(p, worker, workers, TS::kBM);
+        GroupedItem it;
+        bool ok = true;
+        fence_proxy_async_global();  // low-rank rows that the kernel before stored
+        while (ok && items.next(it)) {
+            const int num_kb = blocks_of(it);
+            const GroupedRows& s = first ? p.p : p.q;
+            const uint32_t dst0 = smem_addr(first ? sA : sB);
+            constexpr uint32_t kAStep = TS::kAStage, kBStep = TS::kBStage;
+            const uint32_t step = first ? kAStep : kBStep;
+            // bytes that the two producers of every CTA bring per slot
+            uint32_t bytes;
+            if constexpr (WEIGHT) {
+                bytes = (uint32_t)(TS::kAStage + TS::kBStage) * CG;
+            } else {
+                auto rows_bytes = [&](int r) {
+                    const int n = rows_in(it, r);
+                    return s.row ? (uint32_t)((n + 3) / 4) * 512u : n ? (uint32_t)TS::kAStage : 0u;
+                };
+                bytes = rows_bytes(0) + (PAIR ? rows_bytes(1) : 0u) +
+                        (p.q_mn ? (uint32_t)TS::kBStage : (uint32_t)TS::kBNC * 128u) * CG;
+            }
+            // the rows that this lane fetches
+            int src[4], ahead[4];
+            const int mine = rows_in(it, (int)rank);
+            const int quad = WEIGHT ? lane & 15 : lane;
+            const int row0 = it.tm * TS::kBM + 128 * (int)rank;  // not WEIGHT
+            const int c0 = first ? row0 : it.tn * BN + (int)rank * TS::kBNC;  // WEIGHT: first column of P or Q
+            auto fetch_rows = [&](int i0, int (&r)[4]) {
+#pragma unroll
+                for (int k = 0; k < 4; ++k) r[k] = source_row(s, it.lo, i0 + 4 * quad + k, it.cnt);
+            };
+            if (WEIGHT)
+                fetch_rows(0, ahead);
+            else if (first && s.row)
+                fetch_rows(row0, src);
+            for (int kb = 0; kb < num_kb; ++kb) {
+                if constexpr (WEIGHT) {
+                    // the next block's row numbers are on their way while this one is awaited
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) src[k] = ahead[k];
+                    if (kb + 1 < num_kb) fetch_rows((kb + 1) * kBK, ahead);
+                }
+                const bool got = wait_bar(smem_addr(&empty[slot]), phase ^ 1, w, DEV_TIMEOUT_PRODUCER + 1);
+                if (!__all_sync(0xffffffffu, got)) {
+                    ok = false;
+                    break;
+                }
+                const uint32_t fb_local = smem_addr(&full[slot]);
+                if (first && leader && lane == 0) {
+                    mbar_arrive_expect_tx(fb_local, bytes);
+                    armed |= 1u << slot;
+                    armed_parity = (armed_parity & ~(1u << slot)) | (phase << slot);
+                }
+                const uint32_t fb = PAIR ? mapa_shared(fb_local, 0) : fb_local;
+                const uint32_t dst = dst0 + (uint32_t)slot * step;
+                auto load2 = [&](uint32_t at, const CUtensorMap* map, int x, int y) {
+                    if constexpr (PAIR)
+                        tma_load_2d_pair(at, map, fb, x, y);
+                    else
+                        tma_load_2d(at, map, fb, x, y);
+                };
+                auto load3 = [&](uint32_t at, const CUtensorMap* map, int x, int y, int z) {
+                    if constexpr (PAIR)
+                        tma_load_3d_pair(at, map, fb, x, y, z);
+                    else
+                        tma_load_3d(at, map, fb, x, y, z);
+                };
+                if constexpr (WEIGHT) {
+                    // 64 rows of the group, in atoms of 64 columns
+                    const int atoms = first ? 2 : TS::kBBoxes;
+                    if (!s.row && (kb + 1) * kBK <= it.cnt) {
+                        if (lane < atoms) load2(dst + lane * 8192, &s.box, c0 + 64 * lane, it.lo + kb * kBK);
+                    } else {
+                        for (int h = lane >> 4; h < atoms; h += 2)
+                            tma_gather4<PAIR>(dst + h * 8192 + quad * 512, &s.gather, fb, c0 + 64 * h, src);
+                    }
+                } else if (first) {
+                    const int part = kb / p.kb_wrap, x = (kb - part * p.kb_wrap) * kBK;
+                    if (s.row) {
+                        if (4 * lane < mine) tma_gather4<PAIR>(dst + lane * 512, &s.gather, fb, x, src);
+                    } else if (lane == 0 && mine > 0) {
+                        load2(dst, &s.box, x, it.lo + row0 + part * p.part_rows);
+                    }
+                } else {
+                    const int k0 = kb % p.kb_wrap * kBK;
+                    if (p.q_mn) {
+                        if (lane < TS::kBBoxes) load3(dst + lane * 8192, &p.map_q, c0 + 64 * lane, k0, it.g);
+                    } else if (lane == 0) {
+                        load3(dst, &p.map_q, k0, c0, it.g);
+                    }
+                }
+                if (++slot == SLOTS) {
+                    slot = 0;
+                    phase ^= 1;
+                }
+            }
+        }
+        if (*abort_flag && first && lane == 0) {  // no TMA write may land after the CTA exits
+            for (int q = 0; q < SLOTS; ++q)
+                if (armed & (1u << q)) drain_bar(smem_addr(&full[q]), (armed_parity >> q) & 1, w);
+        }
+    } else if (warp == 1 && leader) {
+        // ---------------------------------------------------- MMA issuer
+        int slot = 0;
+        uint32_t phase = 0;
+        bool ok = true;
+        const uint32_t d_hi = smem_desc_hi_sw128(1024);
+        const bool q_mn = WEIGHT || p.q_mn;
+        const uint32_t a_lo0 = smem_desc_lo(smem_addr(sA), WEIGHT ? 8192u : 16u);
+        const uint32_t b_lo0 = smem_desc_lo(smem_addr(sB), q_mn ? 8192u : 16u);
+        constexpr uint32_t a_kstep = WEIGHT ? (2048u >> 4) : (32u >> 4);
+        const uint32_t b_kstep = q_mn ? (2048u >> 4) : (32u >> 4);
+        GroupedItems<MODE> items(p, worker, workers, TS::kBM);
+        GroupedItem it;
+        for (int i = 0; ok && items.next(it); ++i) {
+            const int num_kb = blocks_of(it);
+            if (lane == 0) {
+                const int buf = i & 1;
+                ok = wait_bar(smem_addr(&tempty[buf]), ((i >> 1) & 1) ^ 1, w, DEV_TIMEOUT_MMA + 3);
+                tc_fence_after();
+                const uint32_t d_tmem = tmem_base + buf * BN;
+                for (int kb = 0; ok && kb < num_kb; ++kb) {
+                    ok = wait_bar(smem_addr(&full[slot]), phase, w, DEV_TIMEOUT_MMA + 4);
+                    if (!ok) break;
+                    tc_fence_after();
+                    const uint32_t a_lo = a_lo0 + (uint32_t)slot * (TS::kAStage >> 4);
+                    const uint32_t b_lo = b_lo0 + (uint32_t)slot * (TS::kBStage >> 4);
+#pragma unroll
+                    for (int kk = 0; kk < kBK / kUmmaK; ++kk)
+                        mma_f16<CG>(d_tmem, smem_desc_join(a_lo + kk * a_kstep, d_hi),
+                                    smem_desc_join(b_lo + kk * b_kstep, d_hi), p.idesc, kb != 0 || kk != 0);
+                    if constexpr (PAIR)
+                        mma_commit_pair(smem_addr(&empty[slot]), 0x3);
+                    else
+                        mma_commit(smem_addr(&empty[slot]));
+                    if (++slot == SLOTS) {
+                        slot = 0;
+                        phase ^= 1;
+                    }
+                }
+                if (ok) {
+                    if constexpr (PAIR)
+                        mma_commit_pair(smem_addr(&tfull[buf]), 0x3);
+                    else
+                        mma_commit(smem_addr(&tfull[buf]));
+                }
+            }
+            ok = __shfl_sync(0xffffffffu, (int)ok, 0) != 0;
+        }
+        if (lane == 0) {  // nothing may still write TMEM when it is released
+            if constexpr (PAIR)
+                mma_commit_pair_local(smem_addr(drain));
+            else
+                mma_commit(smem_addr(drain));
+            drain_bar(smem_addr(drain), 0, w);
+        }
+        __syncwarp();
+    } else if (warp >= 2 && warp < 2 + kGrEpiWarps) {
+        // ------------------------------------------------------ epilogue
+        // A warp of quadrant q reads TMEM lanes 32q..32q+31; thread = row.
+        constexpr int kCols = BN / 2;            // of this warp
+        constexpr int kStep = kCols < 64 ? 32 : 64;
+        constexpr int kUnits = kStep / 8;        // of 16 bytes per staged row
+        constexpr int kRowsAtOnce = 32 / kUnits; // rows that a warp stores at once
+        const int q = warp & 3, half = (warp - 2) / 4;
+        uint8_t* stage = staging + (warp - 2) * TS::kUnit;
+        // 16 bytes of a staged row: 128-byte rows, units spread over the banks
+        auto staged = [&](int r, int k) { return reinterpret_cast<uint4*>(stage + r * 128 + ((k ^ (r & 7)) << 4)); };
+        GroupedItems<MODE> items(p, worker, workers, TS::kBM);
+        GroupedItem it;
+        for (int i = 0; items.next(it); ++i) {
+            const int row0 = it.tm * TS::kBM + (int)rank * 128 + q * 32;  // this warp's first row, in its group or dB
+            const int rows = min(32, (WEIGHT ? p.m : it.cnt) - row0);
+            const int n0 = it.tn * BN + half * kCols;                     // and first column
+            const bool got = wait_bar(smem_addr(&tfull[i & 1]), (i >> 1) & 1, w, DEV_TIMEOUT_EPILOGUE + 4);
+            if (!__all_sync(0xffffffffu, got)) break;
+            tc_fence_after();
+            const uint32_t t_row = tmem_base + ((uint32_t)(q * 32) << 16) + (i & 1) * BN + half * kCols;
+            auto release = [&]() {  // every column of this buffer is in registers
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) {
+                    if constexpr (PAIR)
+                        arrive_on_leader(smem_addr(&tempty[i & 1]));
+                    else
+                        mbar_arrive(smem_addr(&tempty[i & 1]));
+                }
+            };
+            if (rows <= 0 || n0 >= p.n) {
+                release();
+                continue;
+            }
+            uint16_t* out = static_cast<uint16_t*>(p.out) +
+                            (WEIGHT ? (long long)it.g * p.out_stride + (long long)row0 * p.ldo
+                                    : (long long)(it.lo + row0) * p.ldo);
+#pragma unroll 1
+            for (int c = 0; c < kCols; c += kStep) {
+                const int c0 = n0 + c;
+                uint32_t v[kStep / 32][32];
+                __syncwarp();
+#pragma unroll
+                for (int h = 0; h < kStep / 32; ++h) tmem_ld_32x32b_x32(t_row + c + 32 * h, v[h]);
+#pragma unroll
+                for (int h = 0; h < kStep / 32; ++h) tmem_wait_ld_regs(v[h]);
+                if (c + kStep >= kCols) release();
+                if (c0 >= p.n) continue;
+                float y[kStep];
+#pragma unroll
+                for (int j = 0; j < kStep; ++j) y[j] = __uint_as_float(v[j / 32][j % 32]);
+                if (MODE == GROUPED_ROWS && p.bias) {
+                    const uint16_t* b = static_cast<const uint16_t*>(p.bias) + (long long)it.g * p.ld_bias + c0;
+#pragma unroll
+                    for (int h = 0; h < kStep / 32; ++h) {
+                        const float mine = c0 + 32 * h + lane < p.n ? to_f32(b[32 * h + lane], p.bf16) : 0.0f;
+#pragma unroll
+                        for (int j = 0; j < 32; j += 2)
+                            add2(&y[32 * h + j], __shfl_sync(0xffffffffu, mine, j), __shfl_sync(0xffffffffu, mine, j + 1));
+                    }
+                }
+                if (MODE == GROUPED_ROWS && p.relu) {
+                    // (a NaN stays one)
+#pragma unroll
+                    for (int j = 0; j < kStep; ++j) y[j] = y[j] < 0.0f ? 0.0f : y[j];
+                }
+                __syncwarp();  // the step before has been read
+#pragma unroll
+                for (int k = 0; k < kUnits; ++k) {
+                    const float* f = y + 8 * k;
+                    *staged(lane, k) = p.bf16 ? make_uint4(pack2t<true>(f[0], f[1]), pack2t<true>(f[2], f[3]),
+                                                           pack2t<true>(f[4], f[5]), pack2t<true>(f[6], f[7]))
+                                              : make_uint4(pack2t<false>(f[0], f[1]), pack2t<false>(f[2], f[3]),
+                                                           pack2t<false>(f[4], f[5]), pack2t<false>(f[6], f[7]));
+                }
+                __syncwarp();
+                // whole 16-byte units: neighbouring lanes store neighbouring units of a row
+                const int k = lane % kUnits, col = c0 + 8 * k;
+#pragma unroll
+                for (int r0 = 0; r0 < 32; r0 += kRowsAtOnce) {
+                    const int r = r0 + lane / kUnits;
+                    if (r >= rows || col >= p.n) continue;
+                    uint4 u = *staged(r, k);
+                    uint16_t* o = out + (long long)r * p.ldo + col;
+                    if (MODE == GROUPED_ROWS && p.relu_of) {
+                        const uint16_t* z = static_cast<const uint16_t*>(p.relu_of) +
+                                            (long long)(it.lo + row0 + r) * p.ld_relu + col;
+                        uint32_t* word = reinterpret_cast<uint32_t*>(&u);
+                        if (col + 8 <= p.n) {
+                            const uint4 zu = *reinterpret_cast<const uint4*>(z);
+                            const uint32_t zw[4] = {zu.x, zu.y, zu.z, zu.w};
+#pragma unroll
+                            for (int x = 0; x < 4; ++x) {
+                                if (!(to_f32((uint16_t)(zw[x] & 0xFFFFu), p.bf16) > 0.0f)) word[x] &= 0xFFFF0000u;
+                                if (!(to_f32((uint16_t)(zw[x] >> 16), p.bf16) > 0.0f)) word[x] &= 0x0000FFFFu;
+                            }
+                        } else {
+                            uint16_t* part = reinterpret_cast<uint16_t*>(&u);
+#pragma unroll
+                            for (int x = 0; x < 8; ++x)
+                                if (col + x < p.n && !(to_f32(z[x], p.bf16) > 0.0f)) part[x] = 0;
+                        }
+                    }
+                    if (col + 8 <= p.n) {
+                        *reinterpret_cast<uint4*>(o) = u;
+                    } else {
+                        const uint16_t* part = reinterpret_cast<const uint16_t*>(&u);
+#pragma unroll
+                        for (int x = 0; x < 8; ++x)
+                            if (col + x < p.n) o[x] = part[x];
+                    }
+                }
+            }
+        }
+    }
+
+    tc_fence_before();
+    __syncwarp();
+    if (*abort_flag) {
+        // copies for phases that were never armed cannot be observed: give
+        // them ample time to land
+        const long long t0 = clock64();
+        while (clock64() - t0 < 2000000) {
+        }
+    }
+    if constexpr (PAIR)
+        cluster_sync();  // no CTA leaves while its peer may still signal it
+    else
+        __syncthreads();
+    if (warp == 1) {
+        tc_fence_after();
+        tmem_dealloc<CG>(tmem_base, TS::kTmemCols);
+    }
+}
+
+}  // namespace tg

@@ -1,0 +1,71 @@
+// grouped_params.h -- what the host side hands to the grouped product kernels.
+#pragma once
+
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+#include <cstdint>
+
+namespace tg {
+
+// The launches of rows that choose their weights.
+enum GroupedMode : int {
+    GROUPED_ROWS = 0,    // Y[i] = epilogue(X[source(i)] B[g]): tiles of a group's rows
+    GROUPED_WEIGHT = 1,  // dB[g] = X^T dY over a group's rows, or its transpose
+    GROUPED_LOW = 2,     // adapters: X A^T of each row, as two 16-bit parts and a scale
+    GROUPED_ADD = 3,     // adapters: Y += scale (low B^T), rows where they stand
+};
+
+// Rows of a 16-bit matrix, one after another or by a list of rows.
+struct GroupedRows {
+    CUtensorMap box;     // whole boxes of consecutive rows (no list)
+    CUtensorMap gather;  // four rows of 64 columns, by their numbers
+    const int* row;      // [R] or null: row i itself
+    int per_row;         // source row: row[i] / per_row
+    int count;           // source rows; a row outside reads as zeros
+};
+
+struct alignas(128) GroupedParams {
+    // GROUPED_WEIGHT: P holds the product's rows, Q its columns, both along their rows' columns.
+    // Else: P is X (or the low-rank rows), and map_q the matrices: {K, N, G} or {N, K, G}.
+    GroupedRows p, q;
+    CUtensorMap map_q;
+    const int* offset;    // [groups + 1]
+    int groups, rows;     // rows: R
+    int num_kb;           // 64-deep K-blocks (not GROUPED_WEIGHT, whose rows are the depth)
+    int kb_wrap;          // K-blocks of one part of P: part k / kb_wrap starts so many parts of
+    int part_rows;        // this many rows further down, and the matrices start again
+    int tiles_m, tiles_n; // tiles_m: GROUPED_WEIGHT only
+    int group_m;          // raster: tile rows that share their columns' operand in turn
+    int m, n;             // m: rows of a dB (GROUPED_WEIGHT); n: columns of the output
+    int q_mn;             // Q's columns contiguous in memory
+    uint32_t idesc;
+    int bf16;
+    void* out;
+    long long ldo, out_stride;  // out_stride: from one dB to the next
+    const void* bias;           // [groups] rows
+    long long ld_bias;
+    int relu;
+    const void* relu_of;        // [R] rows
+    long long ld_relu;
+    const float* scale;         // GROUPED_LOW: [groups] or null
+    float* row_scale;           // [R]: written by GROUPED_LOW, read by GROUPED_ADD
+    const int* out_row;         // GROUPED_ADD: where row i of the product is added
+    int out_rows;               // of them
+    // watchdog
+    long long timeout_cycles;
+    int* status;
+};
+
+// Tile of a launch: `bn` columns; 256 rows on a CTA pair or 128 on one CTA.
+struct GroupedTile {
+    int bn, pair;
+    int rows() const { return pair ? 256 : 128; }
+};
+
+// `tiles`: the most tiles there can be.  `chained`: the launch may be
+// scheduled while the kernel before it still runs.
+cudaError_t launch_grouped(int mode, const GroupedParams& p, GroupedTile tile, long long tiles, int sms,
+                           bool chained, cudaStream_t stream);
+
+}  // namespace tg
