@@ -48,8 +48,18 @@ bool encode_stack(CUtensorMap* map, int dtype, const void* base, int64_t inner, 
 }
 
 bool encode_rows(GroupedRows* rows, int dtype, const void* base, int64_t count, int64_t cols, int64_t ld,
-                 uint32_t box_rows) {
+                 const int32_t* row, int64_t per_row, uint32_t box_rows) {
     rows->count = (int)count;
+    rows->base = base;
+    rows->ld = ld;
+    rows->cols = (int)cols;
+    rows->row = row;
+    // r / d for 0 <= r < 2^31: with d <= 2^b and m = floor(2^(31+b) / d) + 1, r m / 2^(31+b) is
+    // above r / d by less than r / 2^(31+b) < 1 / d
+    int b = 0;
+    while (((int64_t)1 << b) < per_row) ++b;
+    rows->shift = 31 + b;
+    rows->magic = (uint32_t)(((u128)1 << (31 + b)) / (u128)per_row + 1);
     return encode_2d(&rows->box, dtype, base, (uint64_t)cols, (uint64_t)count, ld, 64, box_rows) &&
            encode_2d(&rows->gather, dtype, base, (uint64_t)cols, (uint64_t)count, ld, 64, 1);
 }
@@ -154,18 +164,16 @@ extern "C" int tg_grouped_gemm(int64_t R, int64_t N, int64_t K, int64_t G, const
     for (int i = 0; i < 7; ++i)
         if ((rc = check(ptrs[i], spans[i]))) return rc;
 
-    GroupedTile tile{64, 0};
+    GroupedTile tile{64, 0, 0};
     if (R >= 128 * G)
-        tile = GroupedTile{256, 1};
+        tile = GroupedTile{256, 1, row != nullptr};
     else if (most_tiles(R, G, 128, (N + 127) / 128) >= info->sms)
-        tile = GroupedTile{128, 0};
+        tile = GroupedTile{128, 0, row && R > 16 * G};
     GroupedParams p;
     std::memset(&p, 0, sizeof(p));
     const int bnc = tile.pair ? tile.bn / 2 : tile.bn;
     p.q_mn = permB == TG_OP_N;
-    bool ok = encode_rows(&p.p, dtype, X, row ? x_rows : R, K, ldx, 128);
-    p.p.row = row;
-    p.p.per_row = (int)per_row;
+    bool ok = encode_rows(&p.p, dtype, X, row ? x_rows : R, K, ldx, row, per_row, 128);
     const int64_t stride = G > 1 ? stride_b : a.b_rows() * ldb;
     ok = ok && (p.q_mn ? encode_stack(&p.map_q, dtype, B, N, K, G, ldb, stride, 64)
                        : encode_stack(&p.map_q, dtype, B, K, N, G, ldb, stride, (uint32_t)bnc));
@@ -218,16 +226,14 @@ extern "C" int tg_grouped_gemm_grad(int64_t R, int64_t N, int64_t K, int64_t G, 
     for (int i = 0; i < 5; ++i)
         if ((rc = check(ptrs[i], spans[i]))) return rc;
 
-    GroupedTile tile{128, 0};
-    if (G * ((m + 255) / 256) * ((n + 255) / 256) >= info->sms / 2) tile = GroupedTile{256, 1};
+    GroupedTile tile{128, 0, row != nullptr};
+    if (G * ((m + 255) / 256) * ((n + 255) / 256) >= info->sms / 2) tile = GroupedTile{256, 1, row != nullptr};
     GroupedParams p;
     std::memset(&p, 0, sizeof(p));
     GroupedRows &x = permB == TG_OP_N ? p.p : p.q, &y = permB == TG_OP_N ? p.q : p.p;
-    if (!encode_rows(&x, dtype, X, row ? x_rows : R, K, ldx, 64) || !encode_rows(&y, dtype, dY, R, N, lddy, 64))
+    if (!encode_rows(&x, dtype, X, row ? x_rows : R, K, ldx, row, per_row, 64) ||
+        !encode_rows(&y, dtype, dY, R, N, lddy, nullptr, 1, 64))
         return TG_ERR_CUDA;
-    x.row = row;
-    x.per_row = (int)per_row;
-    y.per_row = 1;
     p.offset = offset;
     p.groups = (int)G;
     p.rows = (int)R;

@@ -14,8 +14,9 @@ constexpr int64_t kMaxRowGroups = 4096;
 bool encode_stack(CUtensorMap* map, int dtype, const void* base, int64_t inner, int64_t outer, int64_t groups,
                   int64_t ld, int64_t stride, uint32_t box_outer);
 
-// The maps of rows of a matrix: boxes of 64 columns x box_rows rows, and gathered rows.
+// Rows of a matrix: `row` (a list, or null), divided by per_row, and the maps of
+// boxes of 64 columns x box_rows rows and of gathered rows.
 bool encode_rows(GroupedRows* rows, int dtype, const void* base, int64_t count, int64_t cols, int64_t ld,
-                 uint32_t box_rows);
+                 const int32_t* row, int64_t per_row, uint32_t box_rows);
 
 }  // namespace tg

@@ -3,11 +3,18 @@
 
 namespace tg {
 template <>
-cudaError_t launch_grouped_mode<GROUPED_ROWS>(const GroupedParams& p, GroupedTile tile, long long tiles, int sms,
-                                              bool chained, cudaStream_t stream) {
-    if (tile.pair && tile.bn == 256) return launch_grouped_tile<GROUPED_ROWS, 256, true>(p, tiles, sms, chained, stream);
-    if (!tile.pair && tile.bn == 128) return launch_grouped_tile<GROUPED_ROWS, 128, false>(p, tiles, sms, chained, stream);
-    if (!tile.pair && tile.bn == 64) return launch_grouped_tile<GROUPED_ROWS, 64, false>(p, tiles, sms, chained, stream);
+cudaError_t launch_grouped_mode<GROUPED_ROWS>(const GroupedParams& p, GroupedTile tile, long long tiles, int sms, bool chained,
+                                              cudaStream_t stream) {
+    if (tile.bn == 256 && tile.pair && !tile.list)
+        return launch_grouped_tile<GROUPED_ROWS, 256, true, false>(p, tiles, sms, chained, stream);
+    if (tile.bn == 256 && tile.pair && tile.list)
+        return launch_grouped_tile<GROUPED_ROWS, 256, true, true>(p, tiles, sms, chained, stream);
+    if (tile.bn == 128 && !tile.pair && !tile.list)
+        return launch_grouped_tile<GROUPED_ROWS, 128, false, false>(p, tiles, sms, chained, stream);
+    if (tile.bn == 128 && !tile.pair && tile.list)
+        return launch_grouped_tile<GROUPED_ROWS, 128, false, true>(p, tiles, sms, chained, stream);
+    if (tile.bn == 64 && !tile.pair && !tile.list)
+        return launch_grouped_tile<GROUPED_ROWS, 64, false, false>(p, tiles, sms, chained, stream);
     return cudaErrorInvalidValue;
 }
 }  // namespace tg

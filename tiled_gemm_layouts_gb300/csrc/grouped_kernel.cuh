@@ -16,20 +16,21 @@
 // first tiles, a ballot the group of a tile.  Nothing is planned by another
 // kernel or kept between calls.
 //
-// Rows by a list are gathered by the copies themselves: a gathering TMA copy
-// takes four row numbers, so the 32 lanes of the producer warp fetch the 128
-// rows of a stage, each the same four rows in every K-block, in the layout
-// that a box of 128 consecutive rows would have.  No gathered copy of X is
+// Rows by a list are fetched where they stand; no gathered copy of X is
 // written (at 65536 rows of 4096 columns that would be 1.07 GB more traffic).
-// Rows past a group's end are not fetched at all: what is left in their part
-// of the stage only reaches accumulator rows that are not stored, so a tile of
-// one row costs one copy of 512 bytes beside the matrix's.
+// With LIST four warps of their own fetch them, 16 bytes per thread and
+// asynchronous copy, into the swizzled layout that a box would have.  Without LIST the producer warp uses gathering TMA copies, four
+// row numbers each.  Those take about 80 cycles of the copy engine for 512 bytes,
+// and a stage of 128 rows 2600 where its products take 512 (65536 rows, 64
+// groups, 4096 x 1024: 464 TFLOP/s, by the four warps @LIST@), so they are for tiles of
+// few rows.  Rows past a group's end are not fetched at all: what is left in
+// their part of the stage only reaches accumulator rows that are not stored, so a
+// tile of one row costs one copy of 512 bytes beside the matrix's.
 //
 // In GROUPED_WEIGHT the rows are the contraction, and a group's last K-block is
-// ragged: it is fetched by row number from both operands, with numbers outside
-// the matrix for the rows that are none of the group's, which the copy fills
-// with zeros (a box would bring the next group's rows, whose infinities a zero
-// in the other operand does not undo).
+// ragged: it is fetched by row number from both operands, with zeros for the
+// rows that are none of the group's (a box would bring the next group's rows,
+// whose infinities a zero in the other operand does not undo).
 //
 // Every wait is bounded; on a timeout the status word is set, copies and MMAs
 // in flight are drained, TMEM is freed and the kernel returns.
@@ -43,7 +44,10 @@
 namespace tg {
 
 constexpr int kGrEpiWarps = 8;   // two per TMEM lane quadrant, each with half of a tile's columns
-constexpr int kGrThreads = 32 * (3 + kGrEpiWarps);  // producers (warps 0 and 10), MMA (1), epilogue (2..9)
+constexpr int kGrWarps = 3 + kGrEpiWarps;  // producers (warps 0 and 10), MMA (1), epilogue (2..9)
+constexpr int kListWarps = 4;              // with LIST, behind them
+template <bool LIST>
+constexpr int kGrThreads = 32 * (kGrWarps + (LIST ? kListWarps : 0));
 
 template <int BN, bool PAIR>
 struct GroupedShape : TileShape<BN, PAIR> {
@@ -79,7 +83,21 @@ __device__ __forceinline__ int source_row(const GroupedRows& s, int lo, int i, i
     if (i >= cnt) return s.count;
     if (!s.row) return lo + i;
     const int r = s.row[lo + i];
-    return r < 0 ? s.count : (int)((unsigned)r / (unsigned)s.per_row);
+    return r < 0 ? s.count : (int)((uint64_t)(uint32_t)r * s.magic >> s.shift);
+}
+
+// 16 bytes, of which `bytes` are read and the rest zeros.
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src, uint32_t bytes) {
+    asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void copy16_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
+
+// Arrives on the leader CTA's barrier; what this thread knows to be written to
+// its CTA's shared memory comes before.  (A release of all memory at cluster
+// scope waits 1200 cycles here, of shared memory alone next to nothing.)
+__device__ __forceinline__ void arrive_on_leader_release(uint32_t bar) {
+    asm volatile("fence.release.sync_restrict::shared::cta.cluster;" ::: "memory");
+    arrive_on_leader(bar);
 }
 
 struct GroupedItem {
@@ -171,8 +189,8 @@ struct GroupedItems {
     }
 };
 
-template <int MODE, int BN, bool PAIR>
-__global__ void __launch_bounds__(kGrThreads, 1) grouped_kernel(const __grid_constant__ GroupedParams p) {
+template <int MODE, int BN, bool PAIR, bool LIST>
+__global__ void __launch_bounds__(kGrThreads<LIST>, 1) grouped_kernel(const __grid_constant__ GroupedParams p) {
     using TS = GroupedShape<BN, PAIR>;
     constexpr bool WEIGHT = MODE == GROUPED_WEIGHT;
     constexpr int SLOTS = TS::kSlots;
@@ -204,12 +222,12 @@ __global__ void __launch_bounds__(kGrThreads, 1) grouped_kernel(const __grid_con
     allow_next_kernel();
     if (threadIdx.x == 0) {
         for (int s = 0; s < SLOTS; ++s) {
-            mbar_init(smem_addr(&full[s]), 1);
+            mbar_init(smem_addr(&full[s]), 1 + (LIST ? CG : 0));
             mbar_init(smem_addr(&empty[s]), 1);
         }
         for (int b = 0; b < 2; ++b) {
             mbar_init(smem_addr(&tfull[b]), 1);
-            mbar_init(smem_addr(&tempty[b]), (PAIR ? 2 : 1) * kGrEpiWarps);
+            mbar_init(smem_addr(&tempty[b]), CG * kGrEpiWarps);
         }
         mbar_init(smem_addr(drain), 1);
         *abort_flag = 0;
@@ -246,17 +264,18 @@ __global__ void __launch_bounds__(kGrThreads, 1) grouped_kernel(const __grid_con
         while (ok && items.next(it)) {
             const int num_kb = blocks_of(it);
             const GroupedRows& s = first ? p.p : p.q;
+            const bool others = LIST && s.row;  // the list's warps fetch this operand
             const uint32_t dst0 = smem_addr(first ? sA : sB);
             constexpr uint32_t kAStep = TS::kAStage, kBStep = TS::kBStage;
             const uint32_t step = first ? kAStep : kBStep;
             // bytes that the two producers of every CTA bring per slot
             uint32_t bytes;
             if constexpr (WEIGHT) {
-                bytes = (uint32_t)(TS::kAStage + TS::kBStage) * CG;
+                bytes = (uint32_t)((LIST && p.p.row ? 0 : TS::kAStage) + (LIST && p.q.row ? 0 : TS::kBStage)) * CG;
             } else {
                 auto rows_bytes = [&](int r) {
                     const int n = rows_in(it, r);
-                    return s.row ? (uint32_t)((n + 3) / 4) * 512u : n ? (uint32_t)TS::kAStage : 0u;
+                    return LIST ? 0u : s.row ? (uint32_t)((n + 3) / 4) * 512u : n ? (uint32_t)TS::kAStage : 0u;
                 };
                 bytes = rows_bytes(0) + (PAIR ? rows_bytes(1) : 0u) +
                         (p.q_mn ? (uint32_t)TS::kBStage : (uint32_t)TS::kBNC * 128u) * CG;
@@ -271,12 +290,12 @@ __global__ void __launch_bounds__(kGrThreads, 1) grouped_kernel(const __grid_con
 #pragma unroll
                 for (int k = 0; k < 4; ++k) r[k] = source_row(s, it.lo, i0 + 4 * quad + k, it.cnt);
             };
-            if (WEIGHT)
+            if (WEIGHT && !others)
                 fetch_rows(0, ahead);
-            else if (first && s.row)
+            else if (!WEIGHT && first && s.row && !LIST)
                 fetch_rows(row0, src);
             for (int kb = 0; kb < num_kb; ++kb) {
-                if constexpr (WEIGHT) {
+                if (WEIGHT && !others) {
                     // the next block's row numbers are on their way while this one is awaited
 #pragma unroll
                     for (int k = 0; k < 4; ++k) src[k] = ahead[k];
@@ -307,7 +326,8 @@ __global__ void __launch_bounds__(kGrThreads, 1) grouped_kernel(const __grid_con
                     else
                         tma_load_3d(at, map, fb, x, y, z);
                 };
-                if constexpr (WEIGHT) {
+                if (others) {
+                } else if constexpr (WEIGHT) {
                     // 64 rows of the group, in atoms of 64 columns
                     const int atoms = first ? 2 : TS::kBBoxes;
                     if (!s.row && (kb + 1) * kBK <= it.cnt) {
@@ -340,6 +360,91 @@ __global__ void __launch_bounds__(kGrThreads, 1) grouped_kernel(const __grid_con
         if (*abort_flag && first && lane == 0) {  // no TMA write may land after the CTA exits
             for (int q = 0; q < SLOTS; ++q)
                 if (armed & (1u << q)) drain_bar(smem_addr(&full[q]), (armed_parity >> q) & 1, w);
+        }
+    } else if (LIST && warp >= kGrWarps) {
+        // ------------------------------------------- rows by their numbers
+        // Each warp takes every kListWarps-th stage: 1024 units of 16 bytes, lane's
+        // unit u of every kApart-th row.  16-byte unit k of 128-byte row r lies at
+        // unit k ^ (r mod 8).  Once they have landed, the warp hands what it wrote
+        // to the proxy that the MMA reads through, and arrives on the leader's
+        // barrier.  (That fence waits for every copy the thread has in flight, so
+        // stages a warp had ahead would gain nothing: with all warps on each stage
+        // and three stages ahead the products above ran at 380 TFLOP/s.)
+        constexpr int kUnitsOfRow = WEIGHT ? 16 : 8, kApart = 32 / kUnitsOfRow, kRows = WEIGHT ? 64 : 128;
+        static_assert(!WEIGHT || TS::kBNC == 128, "P's and Q's stages have one shape");
+        static_assert(SLOTS >= kListWarps, "the warps' stages are different ones");
+        const int self = warp - kGrWarps;
+        const bool is_p = !WEIGHT || p.p.row;
+        const GroupedRows& s = is_p ? p.p : p.q;
+        const int u = lane % kUnitsOfRow, q = lane / kUnitsOfRow;
+        const uint32_t dst0 = smem_addr(is_p ? sA : sB);
+        const uint32_t stage_bytes = is_p ? (uint32_t)TS::kAStage : (uint32_t)TS::kBStage;
+        // row kApart j + q: its number within eight repeats every 8 / kApart rows
+        uint32_t to[8 / kApart];
+#pragma unroll
+        for (int j = 0; j < 8 / kApart; ++j) {
+            const int r = kApart * j + q;
+            to[j] = (uint32_t)((u >> 3) * 8192 + r * 128 + (((u & 7) ^ (r & 7)) << 4));
+        }
+        const uint16_t* base = static_cast<const uint16_t*>(s.base);
+        int slot = self, wait = self;  // of this warp's next stage; stages until it is due
+        uint32_t phase = 0;
+        GroupedItems<MODE> items(p, worker, workers, TS::kBM);
+        GroupedItem it;
+        bool ok = true;
+        while (ok && items.next(it)) {
+            const int num_kb = blocks_of(it);
+            const int row0 = it.tm * TS::kBM + 128 * (int)rank;                 // not WEIGHT
+            const int c0 = is_p ? row0 : it.tn * BN + (int)rank * TS::kBNC;     // WEIGHT
+            // lane's rows of the stage: lane, lane + 32, ...
+            int src[kRows / 32], ahead[kRows / 32];
+            auto fetch_rows = [&](int i0, int (&r)[kRows / 32]) {
+#pragma unroll
+                for (int j = 0; j < kRows / 32; ++j) r[j] = source_row(s, it.lo, i0 + 32 * j + lane, it.cnt);
+            };
+            if (WEIGHT)
+                fetch_rows(wait * kBK, ahead);
+            else
+                fetch_rows(row0, src);
+            int kb = wait;
+            for (; kb < num_kb; kb += kListWarps) {
+                if constexpr (WEIGHT) {
+#pragma unroll
+                    for (int j = 0; j < kRows / 32; ++j) src[j] = ahead[j];
+                    fetch_rows((kb + kListWarps) * kBK, ahead);
+                }
+                const bool got = wait_bar(smem_addr(&empty[slot]), phase ^ 1, w, DEV_TIMEOUT_PRODUCER + 3);
+                if (!__all_sync(0xffffffffu, got)) {
+                    ok = false;
+                    break;
+                }
+                const uint32_t dst = dst0 + (uint32_t)slot * stage_bytes;
+                const int col = (WEIGHT ? c0 : kb * kBK) + 8 * u;
+                const uint32_t bytes = 2u * (uint32_t)min(8, max(0, s.cols - col));
+                const uint16_t* from = base + (bytes ? col : 0);
+#pragma unroll
+                for (int j = 0; j < kRows / kApart; ++j) {
+                    const int at = __shfl_sync(0xffffffffu, src[kApart * j / 32], (kApart * j & 31) + q);
+                    const bool there = at < s.count;
+                    copy16(dst + to[j % (8 / kApart)] + j / (8 / kApart) * 1024, from + (there ? at : 0) * s.ld,
+                           there ? bytes : 0u);
+                }
+                copy16_wait_all();
+                fence_proxy_async_shared();
+                __syncwarp();
+                if (lane == 0) {
+                    if constexpr (PAIR)
+                        arrive_on_leader_release(smem_addr(&full[slot]));
+                    else
+                        mbar_arrive(smem_addr(&full[slot]));
+                }
+                slot += kListWarps;
+                if (slot >= SLOTS) {
+                    slot -= SLOTS;
+                    phase ^= 1;
+                }
+            }
+            wait = kb - num_kb;
         }
     } else if (warp == 1 && leader) {
         // ---------------------------------------------------- MMA issuer

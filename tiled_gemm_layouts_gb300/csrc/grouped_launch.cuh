@@ -9,11 +9,11 @@
 
 namespace tg {
 
-template <int MODE, int BN, bool PAIR>
+template <int MODE, int BN, bool PAIR, bool LIST>
 cudaError_t launch_grouped_tile(const GroupedParams& p, long long tiles, int sms, bool chained,
                                 cudaStream_t stream) {
     using TS = GroupedShape<BN, PAIR>;
-    auto kern = grouped_kernel<MODE, BN, PAIR>;
+    auto kern = grouped_kernel<MODE, BN, PAIR, LIST>;
     static std::atomic<unsigned long long> attr_set{0};  // one bit per device
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
@@ -29,7 +29,7 @@ cudaError_t launch_grouped_tile(const GroupedParams& p, long long tiles, int sms
     cudaLaunchConfig_t lc = {};
     cudaLaunchAttribute attr[2];
     lc.gridDim = dim3(PAIR ? 2 * workers : workers, 1, 1);
-    lc.blockDim = dim3(kGrThreads, 1, 1);
+    lc.blockDim = dim3(kGrThreads<LIST>, 1, 1);
     lc.dynamicSmemBytes = TS::kGrSmemBytes;
     lc.stream = stream;
     if (PAIR) {

@@ -21,8 +21,12 @@ struct GroupedRows {
     CUtensorMap box;     // whole boxes of consecutive rows (no list)
     CUtensorMap gather;  // four rows of 64 columns, by their numbers
     const int* row;      // [R] or null: row i itself
-    int per_row;         // source row: row[i] / per_row
+    uint32_t magic;      // source row: row[i] / per_row = row[i] * magic >> shift
+    int shift;
     int count;           // source rows; a row outside reads as zeros
+    const void* base;    // for the list's copies
+    long long ld;
+    int cols;
 };
 
 struct alignas(128) GroupedParams {
@@ -58,8 +62,9 @@ struct alignas(128) GroupedParams {
 };
 
 // Tile of a launch: `bn` columns; 256 rows on a CTA pair or 128 on one CTA.
+// `list`: a list's rows are fetched by warps of their own, not by gathering copies.
 struct GroupedTile {
-    int bn, pair;
+    int bn, pair, list;
     int rows() const { return pair ? 256 : 128; }
 };
 
