@@ -1,17 +1,28 @@
 // adapters.cu -- low-rank adapters of many requests beside a shared projection
 // (tg_adapters).
 //
-//   u_i = x_t A_g^T   (rank values, fp32)        y_t += s_g (u_i B_g^T)
+//   u_i = x_t A_g^T   (rank values)        y_t += s_g (u_i B_g^T)
 //
 // for each grouped row i, its token t = row[i] and its group (adapter) g.
 //
-// Few rows (a decoder's batch).  Bound by latency and by reading A and B: at
-// 64 rows, each with an adapter of its own of rank 16 between 4096 columns, they
-// are 16.8 MB.  The first kernel cuts a row's columns into pieces, one per
-// block; a warp sums a piece's products for some of the rank, 16 bytes per lane
-// and load, and writes the sums by piece.  The second adds the pieces up (in
-// their order) and gives every column of y to one thread, whose row of B lies
-// beside its neighbours' in memory.  It is launched behind the first one's tail.
+// Bound by memory: x is read once, y read and written; A and B are small and
+// come out of L2 for all rows but an adapter's first.  At rank 32 and 4096
+// columns there are 170 operations per byte of x and y, a third of what the
+// legacy matrix instructions do in that time, and nothing is worth staging: an
+// mma.sync fragment is loaded from global memory as it is used.  The order of
+// the contraction is free, so lane (g, q) of a warp takes columns 8q..8q+7 of
+// rows g, g + 8, ... as one 16-byte load, and the columns of both operands meet
+// two by two in the fragments of two instructions.  Likewise the second
+// product's columns are dealt out so that a lane ends up with 8 consecutive ones
+// of y.  So every access is 16 bytes per lane, 64 consecutive ones per row.
+//
+// The first kernel takes 32 rows per block; its warps, and several blocks if
+// there are few rows, split the columns of x, and the sums are joined in shared
+// memory and (blocks) in the second kernel, always in the same order.  The
+// second kernel's operand u is split into two 16-bit parts (their sum keeps 16
+// bits of bf16, 22 of fp16), after a power of two that brings the largest of a
+// row's values near 1, so that fp16 neither overflows nor underflows; sums are
+// fp32, and y is rounded once.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -25,9 +36,14 @@
 namespace tg {
 namespace {
 
-constexpr int kLowThreads = 256;
+constexpr int kThreads = 256;
+constexpr int kWarps = kThreads / 32;
+constexpr int kRows = 32;             // per block: two fragments of 16
 constexpr int64_t kMaxRank = 128;
-constexpr int kMaxPieces = 32;
+constexpr int kRankPass = 64;         // of the rank, per block of the first kernel
+constexpr int kStepK = 64;            // columns of x per warp and step
+constexpr int kMaxSplits = 16;
+constexpr int64_t kFewRows = 64;
 
 struct AdapterParams {
     int T, G, rank, K, N;
@@ -42,8 +58,10 @@ struct AdapterParams {
     const float* scale;
     uint16_t* y;
     long long ldy;
-    int pieces, piece;  // of K, and columns (a multiple of 256) of one
-    float* part;        // [T][pieces][rank]
+    int splits, split;  // of K, and columns of one (a multiple of kStepK)
+    int pitch;          // rank rounded up to 16
+    float* low;         // [splits][T][pitch]
+    int chunk;          // columns of y per block (a multiple of 256)
 };
 
 template <bool BF>
@@ -56,6 +74,308 @@ __device__ __forceinline__ uint16_t narrow(float x) {
     if constexpr (BF) return __bfloat16_as_ushort(__float2bfloat16_rn(x));
     return __half_as_ushort(__float2half_rn(x));
 }
+template <bool BF>
+__device__ __forceinline__ uint32_t narrow2(float a, float b) {
+    return (uint32_t)narrow<BF>(a) | (uint32_t)narrow<BF>(b) << 16;
+}
+
+// c += a b, 16 x 8 x 16: lane (g, q) holds of a rows g and g + 8, of b column g,
+// of c rows g and g + 8, columns 2q and 2q + 1.
+template <bool BF>
+__device__ __forceinline__ void mma(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                    uint32_t b1) {
+    if constexpr (BF)
+        asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+                     : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+                     : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+    else
+        asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+                     : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+                     : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// Columns c .. c+7 of a row, zeros from `end` on.
+__device__ __forceinline__ uint4 load8(const uint16_t* row, int c, int end) {
+    if (c >= end) return make_uint4(0, 0, 0, 0);
+    uint4 v = *reinterpret_cast<const uint4*>(row + c);
+    if (c + 8 > end) {
+        uint32_t* w = reinterpret_cast<uint32_t*>(&v);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            if (c + 2 * j >= end) w[j] = 0;
+            if (c + 2 * j + 1 >= end) w[j] &= 0xFFFFu;
+        }
+    }
+    return v;
+}
+// And c .. c+3.
+__device__ __forceinline__ uint2 load4(const uint16_t* row, int c, int end) {
+    if (c >= end) return make_uint2(0, 0);
+    uint2 v = *reinterpret_cast<const uint2*>(row + c);
+    if (c + 4 > end) {
+        if (c + 1 >= end) v.x &= 0xFFFFu;
+        if (c + 2 >= end) v.y = 0;
+        if (c + 3 >= end) v.y &= 0xFFFFu;
+    }
+    return v;
+}
+
+// The group, and the first and number of its rows, of tile t, when every
+// group's rows are cut into tiles of kRows; g < 0 if there are fewer tiles.
+// By a whole warp, 128 groups at a time.
+struct RowTile {
+    int g, lo, rows;
+};
+__device__ __forceinline__ RowTile find_tile(const AdapterParams& p, int t, int lane) {
+    for (int window = 0; window < p.G; window += 128) {
+        int end[5], tiles[4], incl = 0;
+#pragma unroll
+        for (int k = 0; k < 5; ++k) end[k] = max(0, min(p.offset[min(window + 4 * lane + k, p.G)], p.T));
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            tiles[k] = (max(0, end[k + 1] - end[k]) + kRows - 1) / kRows;
+            incl += tiles[k];
+        }
+        const int own = incl;
+#pragma unroll
+        for (int d = 1; d < 32; d *= 2) {
+            const int o = __shfl_up_sync(0xffffffffu, incl, d);
+            if (lane >= d) incl += o;
+        }
+        const unsigned later = __ballot_sync(0xffffffffu, t < incl);
+        if (later) {
+            const int owner = __ffs(later) - 1;
+            int i = t - (incl - own), k = 0, lo = end[0], hi = end[1];
+#pragma unroll
+            for (int j = 0; j < 3; ++j)
+                if (k == j && i >= tiles[j]) {
+                    i -= tiles[j];
+                    k = j + 1;
+                    lo = end[j + 1];
+                    hi = end[j + 2];
+                }
+            RowTile r;
+            r.g = window + 4 * owner + __shfl_sync(0xffffffffu, k, owner);
+            r.lo = __shfl_sync(0xffffffffu, lo + i * kRows, owner);
+            r.rows = min(kRows, __shfl_sync(0xffffffffu, hi, owner) - r.lo);
+            return r;
+        }
+        t -= __shfl_sync(0xffffffffu, incl, 31);
+    }
+    return {-1, 0, 0};
+}
+
+// u: grid (tiles, splits of K, passes over the rank).  NT fragments of 8 of the rank.
+template <bool BF, int NT>
+__global__ void __launch_bounds__(kThreads) low_kernel(const AdapterParams p) {
+    __shared__ float joined[kWarps / 2][2][NT][4][32];
+    allow_next_kernel();
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, q = lane & 3;
+    const RowTile tile = find_tile(p, blockIdx.x, lane);
+    if (tile.g < 0) return;
+    const int r0 = blockIdx.z * kRankPass;
+    // rows g, g + 8, g + 16, g + 24 of the tile
+    const uint16_t* x[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        const int i = g + 8 * j;
+        const int t = i < tile.rows ? p.row[tile.lo + i] : -1;
+        x[j] = t >= 0 && t < p.T ? p.x + (long long)t * p.ldx : nullptr;
+    }
+    const uint16_t* a[NT];
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+        const int r = r0 + 8 * n + g;
+        a[n] = r < p.rank ? p.a + ((long long)tile.g * p.rank + r) * p.lda : nullptr;
+    }
+    float c[2][NT][4];
+#pragma unroll
+    for (int m = 0; m < 2; ++m)
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) c[m][n][j] = 0.0f;
+    const int k1 = min(p.K, (int)(blockIdx.y + 1) * p.split);
+    const bool second = tile.rows > 16;  // else its rows 16..31 are zeros
+    for (int k = blockIdx.y * p.split + warp * kStepK; k < k1; k += kWarps * kStepK) {
+        uint4 xv[2][4], av[2][NT];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const int at = k + 32 * h + 8 * q;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) xv[h][j] = x[j] ? load8(x[j], at, k1) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+            for (int n = 0; n < NT; ++n) av[h][n] = a[n] ? load8(a[n], at, k1) : make_uint4(0, 0, 0, 0);
+        }
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+                mma<BF>(c[0][n], xv[h][0].x, xv[h][1].x, xv[h][0].y, xv[h][1].y, av[h][n].x, av[h][n].y);
+                mma<BF>(c[0][n], xv[h][0].z, xv[h][1].z, xv[h][0].w, xv[h][1].w, av[h][n].z, av[h][n].w);
+                if (second) {
+                    mma<BF>(c[1][n], xv[h][2].x, xv[h][3].x, xv[h][2].y, xv[h][3].y, av[h][n].x, av[h][n].y);
+                    mma<BF>(c[1][n], xv[h][2].z, xv[h][3].z, xv[h][2].w, xv[h][3].w, av[h][n].z, av[h][n].w);
+                }
+            }
+    }
+    // the warps' sums, half of them to the other half, three times
+#pragma unroll
+    for (int half = kWarps / 2; half; half /= 2) {
+        if (warp >= half && warp < 2 * half) {
+#pragma unroll
+            for (int m = 0; m < 2; ++m)
+#pragma unroll
+                for (int n = 0; n < NT; ++n)
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) joined[warp - half][m][n][j][lane] = c[m][n][j];
+        }
+        __syncthreads();
+        if (warp < half) {
+#pragma unroll
+            for (int m = 0; m < 2; ++m)
+#pragma unroll
+                for (int n = 0; n < NT; ++n)
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) c[m][n][j] += joined[warp][m][n][j][lane];
+        }
+        __syncthreads();
+    }
+    if (warp) return;
+#pragma unroll
+    for (int m = 0; m < 2; ++m)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const int i = 16 * m + 8 * h + g;
+            if (i >= tile.rows) continue;
+            float* out = p.low + ((long long)blockIdx.y * p.T + tile.lo + i) * p.pitch + r0 + 2 * q;
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+                if (r0 + 8 * n < p.pitch) *reinterpret_cast<float2*>(out + 8 * n) = make_float2(c[m][n][2 * h], c[m][n][2 * h + 1]);
+        }
+}
+
+// y: grid (tiles, chunks of N).  KC: fragments of 16 of the rank.
+template <bool BF, int KC>
+__global__ void __launch_bounds__(kThreads) add_kernel(const AdapterParams p) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, q = lane & 3;
+    const RowTile tile = find_tile(p, blockIdx.x, lane);
+    if (tile.g < 0) return;
+    uint16_t* y[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        const int i = g + 8 * j;
+        const int t = i < tile.rows ? p.row[tile.lo + i] : -1;
+        y[j] = t >= 0 && t < p.T ? p.y + (long long)t * p.ldy : nullptr;
+    }
+    const float s = p.scale ? p.scale[tile.g] : 1.0f;
+    wait_for_previous_kernel();
+    // u of rows g, g + 8, g + 16, g + 24, columns 16 c + 4q .. + 3, as two parts
+    uint32_t hi[4][KC][2], lo[4][KC][2];
+    float factor[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        float u[KC][4], top = 0.0f;
+#pragma unroll
+        for (int c = 0; c < KC; ++c) {
+            float4 sum = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            if (g + 8 * j < tile.rows && 16 * c < p.pitch)
+                for (int k = 0; k < p.splits; ++k) {
+                    const float4 v = *reinterpret_cast<const float4*>(
+                        p.low + ((long long)k * p.T + tile.lo + g + 8 * j) * p.pitch + 16 * c + 4 * q);
+                    sum.x += v.x, sum.y += v.y, sum.z += v.z, sum.w += v.w;
+                }
+            u[c][0] = sum.x, u[c][1] = sum.y, u[c][2] = sum.z, u[c][3] = sum.w;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) top = fmaxf(top, fabsf(u[c][k]));
+        }
+        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+        // 2^-e with 2^e <= top < 2^(e+1); rows of zeros, or with an infinity, as they are
+        float down = 1.0f;
+        factor[j] = s;
+        if (top > 0x1p-100f && top < 0x1p100f) {
+            const uint32_t e = __float_as_uint(top) & 0x7F800000u;
+            down = __uint_as_float(0x7F000000u - e);
+            factor[j] = s * __uint_as_float(e);
+        }
+#pragma unroll
+        for (int c = 0; c < KC; ++c)
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                float v[2], rest[2];
+                uint16_t h[2];
+#pragma unroll
+                for (int x = 0; x < 2; ++x) {
+                    v[x] = u[c][2 * k + x] * down;
+                    h[x] = narrow<BF>(v[x]);
+                    rest[x] = v[x] - wide<BF>(h[x]);
+                    if (!(fabsf(rest[x]) < 1.0f)) rest[x] = 0.0f;  // of an infinity
+                }
+                hi[j][c][k] = (uint32_t)h[0] | (uint32_t)h[1] << 16;
+                lo[j][c][k] = narrow2<BF>(rest[0], rest[1]);
+            }
+    }
+    const bool second = tile.rows > 16;
+    const uint16_t* bg = p.b + (long long)tile.g * p.N * p.ldb;
+    const int end = min(p.N, (int)(blockIdx.y + 1) * p.chunk);
+    for (int n0 = blockIdx.y * p.chunk + warp * 32; n0 < end; n0 += kWarps * 32) {
+        const int n = n0 + 8 * q;  // this lane's columns of y
+        uint4 old[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) old[j] = y[j] ? load8(y[j], n, p.N) : make_uint4(0, 0, 0, 0);
+        // fragment f's column c is y's n0 + 8 (c / 2) + 2 f + c % 2
+        uint2 b[4][KC];
+#pragma unroll
+        for (int f = 0; f < 4; ++f) {
+            const int col = n0 + 8 * (g >> 1) + 2 * f + (g & 1);
+            const uint16_t* row = bg + (long long)col * p.ldb;
+#pragma unroll
+            for (int c = 0; c < KC; ++c) b[f][c] = col < p.N ? load4(row, 16 * c + 4 * q, p.rank) : make_uint2(0, 0);
+        }
+        float acc[2][4][4];
+#pragma unroll
+        for (int m = 0; m < 2; ++m)
+#pragma unroll
+            for (int f = 0; f < 4; ++f) {
+#pragma unroll
+                for (int j = 0; j < 4; ++j) acc[m][f][j] = 0.0f;
+                if (m && !second) continue;
+#pragma unroll
+                for (int c = 0; c < KC; ++c) {
+                    mma<BF>(acc[m][f], lo[2 * m][c][0], lo[2 * m + 1][c][0], lo[2 * m][c][1], lo[2 * m + 1][c][1], b[f][c].x, b[f][c].y);
+                    mma<BF>(acc[m][f], hi[2 * m][c][0], hi[2 * m + 1][c][0], hi[2 * m][c][1], hi[2 * m + 1][c][1], b[f][c].x, b[f][c].y);
+                }
+            }
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            if (!y[j] || n >= p.N) continue;
+            const uint32_t w[4] = {old[j].x, old[j].y, old[j].z, old[j].w};
+            uint32_t o[4];
+#pragma unroll
+            for (int f = 0; f < 4; ++f)
+                o[f] = narrow2<BF>(fmaf(factor[j], acc[j / 2][f][2 * (j & 1)], wide<BF>((uint16_t)(w[f] & 0xFFFFu))),
+                                   fmaf(factor[j], acc[j / 2][f][2 * (j & 1) + 1], wide<BF>((uint16_t)(w[f] >> 16))));
+            if (n + 8 <= p.N) {
+                *reinterpret_cast<uint4*>(y[j] + n) = make_uint4(o[0], o[1], o[2], o[3]);
+            } else {
+#pragma unroll
+                for (int x = 0; x < 8; ++x)
+                    if (n + x < p.N) y[j][n + x] = (uint16_t)(o[x / 2] >> (x & 1) * 16);
+            }
+        }
+    }
+}
+
+// ------------------------------------------------- few rows: a block per row
+//
+// A decoder's batch: bound by latency and by reading A and B (64 rows, each with
+// an adapter of its own of rank 16 between 4096 columns: 16.8 MB).  The first
+// kernel cuts a row's columns into pieces, one per block; a warp sums a piece's
+// products for some of the rank.  The second adds the pieces up and gives
+// every column of y to one thread, whose row of B lies beside its neighbours' in
+// memory.  fp32 throughout.
+
 // sum += a . b over 8 columns, those from `left` on left out
 template <bool BF>
 __device__ __forceinline__ float dot8(const uint4& a, const uint4& b, int left, float sum) {
@@ -87,18 +407,18 @@ __device__ __forceinline__ int group_of(const AdapterParams& p, int i, int lane)
 }
 
 template <bool BF>
-__global__ void __launch_bounds__(kLowThreads) low_kernel(const AdapterParams p) {
+__global__ void __launch_bounds__(kThreads) few_low_kernel(const AdapterParams p) {
     allow_next_kernel();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int i = blockIdx.y;
     const int g = group_of(p, i, lane);
     const int t = p.row[i];
     if (g < 0 || t < 0 || t >= p.T) return;
-    const int k0 = blockIdx.x * p.piece, k1 = min(p.K, k0 + p.piece);
+    const int k0 = blockIdx.x * p.split, k1 = min(p.K, k0 + p.split);
     const uint16_t* x = p.x + (long long)t * p.ldx;
     const uint16_t* a = p.a + (long long)g * p.rank * p.lda;
     constexpr int kTogether = 4;  // of the rank, so that their loads are in flight together
-    for (int r0 = warp * kTogether; r0 < p.rank; r0 += kLowThreads / 32 * kTogether) {
+    for (int r0 = warp * kTogether; r0 < p.rank; r0 += kThreads / 32 * kTogether) {
         float sum[kTogether] = {0.0f, 0.0f, 0.0f, 0.0f};
         for (int k = k0 + 8 * lane; k < k1; k += 256) {
             const uint4 xv = *reinterpret_cast<const uint4*>(x + k);
@@ -112,29 +432,29 @@ __global__ void __launch_bounds__(kLowThreads) low_kernel(const AdapterParams p)
 #pragma unroll
             for (int d = 16; d; d >>= 1) sum[j] += __shfl_xor_sync(0xffffffffu, sum[j], d);
             if (lane == 0 && r0 + j < p.rank)
-                p.part[((long long)i * p.pieces + blockIdx.x) * p.rank + r0 + j] = sum[j];
+                p.low[((long long)i * p.splits + blockIdx.x) * p.pitch + r0 + j] = sum[j];
         }
     }
 }
 
 template <bool BF>
-__global__ void __launch_bounds__(kLowThreads) add_kernel(const AdapterParams p) {
+__global__ void __launch_bounds__(kThreads) few_add_kernel(const AdapterParams p) {
     __shared__ float low[kMaxRank];
     const int i = blockIdx.y;
     const int g = group_of(p, i, threadIdx.x & 31);
     const int t = p.row[i];
     if (g < 0 || t < 0 || t >= p.T) return;
     wait_for_previous_kernel();
-    const float* part = p.part + (long long)i * p.pieces * p.rank;
-    for (int r = threadIdx.x; r < (int)kMaxRank; r += kLowThreads) {
+    const float* part = p.low + (long long)i * p.splits * p.pitch;
+    for (int r = threadIdx.x; r < (int)kMaxRank; r += kThreads) {
         float sum = 0.0f;
         if (r < p.rank)
-            for (int k = 0; k < p.pieces; ++k) sum += part[k * p.rank + r];
+            for (int k = 0; k < p.splits; ++k) sum += part[k * p.pitch + r];
         low[r] = sum;
     }
     __syncthreads();
     const float s = p.scale ? p.scale[g] : 1.0f;
-    for (int n = blockIdx.x * kLowThreads + threadIdx.x; n < p.N; n += gridDim.x * kLowThreads) {
+    for (int n = blockIdx.x * kThreads + threadIdx.x; n < p.N; n += gridDim.x * kThreads) {
         const uint16_t* b = p.b + ((long long)g * p.N + n) * p.ldb;
         uint16_t* y = p.y + (long long)t * p.ldy + n;
         float sum = 0.0f;
@@ -151,10 +471,38 @@ __global__ void __launch_bounds__(kLowThreads) add_kernel(const AdapterParams p)
     }
 }
 
-// Pieces of K: enough blocks for every SM, a multiple of 256 columns each.
-int pieces_of(int64_t T, int64_t K) {
-    const int64_t most = (K + 255) / 256, wanted = (1024 + T - 1) / T;
-    return (int)std::max<int64_t>(1, std::min<int64_t>(std::min<int64_t>(most, wanted), kMaxPieces));
+// Blocks of one row against tiles of 32 (rank 16, 4096 columns, us): 64 rows of 64
+// adapters 17 to 23, of one 15 to 15; 100 of 10 17 to 15; 512 of 512 72 to 103, of 4 52 to 17.
+bool few_rows(int64_t T, int64_t G) { return T <= kFewRows || T < 4 * G; }
+
+int64_t tiles_of(int64_t T, int64_t G) { return std::min(T, G) + T / kRows; }
+
+// Splits of K: about 1024 blocks of at least 256 columns for few rows, else about
+// 512 of at least one step of all warps.
+int splits_of(int64_t T, int64_t G, int64_t K) {
+    if (few_rows(T, G)) return (int)std::max<int64_t>(1, std::min<int64_t>((K + 255) / 256, std::min<int64_t>(kMaxSplits, 1024 / T)));
+    const int64_t most = (K + kWarps * kStepK - 1) / (kWarps * kStepK);
+    const int64_t wanted = (512 + tiles_of(T, G) - 1) / tiles_of(T, G);
+    return (int)std::max<int64_t>(1, std::min<int64_t>(std::min(most, wanted), kMaxSplits));
+}
+int64_t pitch_of(int64_t rank) { return (rank + 15) / 16 * 16; }
+
+template <bool BF>
+cudaError_t launch_low(const AdapterParams& p, dim3 grid, cudaStream_t stream) {
+    if (p.rank <= 16)
+        low_kernel<BF, 2><<<grid, kThreads, 0, stream>>>(p);
+    else if (p.rank <= 32)
+        low_kernel<BF, 4><<<grid, kThreads, 0, stream>>>(p);
+    else
+        low_kernel<BF, 8><<<grid, kThreads, 0, stream>>>(p);
+    return cudaGetLastError();
+}
+template <bool BF>
+cudaError_t launch_add(const AdapterParams& p, dim3 grid, cudaStream_t stream) {
+    if (p.rank <= 16) return launch_chained(add_kernel<BF, 1>, grid, kThreads, stream, p);
+    if (p.rank <= 32) return launch_chained(add_kernel<BF, 2>, grid, kThreads, stream, p);
+    if (p.rank <= 64) return launch_chained(add_kernel<BF, 4>, grid, kThreads, stream, p);
+    return launch_chained(add_kernel<BF, 8>, grid, kThreads, stream, p);
 }
 
 int check_sizes(int64_t T, int64_t N, int64_t K, int64_t rank, int64_t G, int dtype) {
@@ -165,8 +513,8 @@ int check_sizes(int64_t T, int64_t N, int64_t K, int64_t rank, int64_t G, int dt
     return TG_OK;
 }
 
-size_t workspace_of(int64_t T, int64_t K, int64_t rank) {
-    return (size_t)T * (size_t)pieces_of(T, K) * (size_t)rank * sizeof(float);
+size_t workspace_of(int64_t T, int64_t G, int64_t K, int64_t rank) {
+    return (size_t)T * (size_t)splits_of(T, G, K) * (size_t)pitch_of(rank) * sizeof(float);
 }
 
 }  // namespace
@@ -179,7 +527,7 @@ extern "C" int tg_adapters_workspace_size(int64_t T, int64_t N, int64_t K, int64
     const int rc = check_sizes(T, N, K, rank, G, (int)dtype);
     if (rc) return rc;
     if (!bytes) return TG_ERR_INVALID_ARG;
-    *bytes = workspace_of(T, K, rank);
+    *bytes = workspace_of(T, G, K, rank);
     return TG_OK;
 }
 
@@ -196,7 +544,7 @@ extern "C" int tg_adapters(int64_t T, int64_t N, int64_t K, int64_t rank, int64_
     if (!aligned16(X) || !aligned16(A) || !aligned16(B) || !aligned16(Y) || ldx % 8 || lda % 8 || ldb % 8 || ldy % 8 ||
         off(row, 4) || off(offset, 4) || off(scale, 4) || off(workspace, 256))
         return TG_ERR_ALIGN;
-    const size_t need = workspace_of(T, K, rank);
+    const size_t need = workspace_of(T, G, K, rank);
     if (workspace_bytes < need) return TG_ERR_BUFFER;
     // (G * rank rows of A and G * N of B, one after another)
     const void* ptrs[8] = {Y, workspace, X, A, B, row, offset, scale};
@@ -206,7 +554,6 @@ extern "C" int tg_adapters(int64_t T, int64_t N, int64_t K, int64_t rank, int64_
     for (int i = 0; i < 2; ++i)
         for (int j = i + 1; j < 8; ++j)
             if (intersects(spans[i], spans[j])) return TG_ERR_OVERLAP;
-    if (T > 65535) return TG_ERR_INVALID_ARG;
     int dev;
     DeviceInfo* info;
     if ((rc = current_device(&dev, &info))) return rc;
@@ -231,20 +578,39 @@ extern "C" int tg_adapters(int64_t T, int64_t N, int64_t K, int64_t rank, int64_
     p.scale = scale;
     p.y = static_cast<uint16_t*>(Y);
     p.ldy = ldy;
-    const int pieces = pieces_of(T, K);
-    p.piece = (int)((K + pieces * 256LL - 1) / (pieces * 256LL) * 256);
-    p.pieces = (int)((K + p.piece - 1) / p.piece);
-    p.part = static_cast<float*>(workspace);
-    const dim3 low((unsigned)p.pieces, (unsigned)T, 1);
-    const dim3 add((unsigned)std::min<int64_t>((N + kLowThreads - 1) / kLowThreads, 1024), (unsigned)T, 1);
-    if (dtype == TG_BF16)
-        low_kernel<true><<<low, kLowThreads, 0, stream>>>(p);
-    else
-        low_kernel<false><<<low, kLowThreads, 0, stream>>>(p);
-    cudaError_t e = cudaGetLastError();
-    if (e == cudaSuccess)
-        e = dtype == TG_BF16 ? launch_chained(add_kernel<true>, add, kLowThreads, stream, p)
-                             : launch_chained(add_kernel<false>, add, kLowThreads, stream, p);
+    p.splits = splits_of(T, G, K);
+    const int64_t step = few_rows(T, G) ? 256 : kStepK;
+    p.split = (int)((K + p.splits * step - 1) / (p.splits * step) * step);
+    p.splits = (int)((K + p.split - 1) / p.split);
+    p.pitch = (int)pitch_of(rank);
+    p.low = static_cast<float*>(workspace);
+    if (few_rows(T, G)) {
+        const dim3 low((unsigned)p.splits, (unsigned)T, 1);
+        const dim3 add((unsigned)std::min<int64_t>((N + kThreads - 1) / kThreads, 1024), (unsigned)T, 1);
+        if (dtype == TG_BF16)
+            few_low_kernel<true><<<low, kThreads, 0, stream>>>(p);
+        else
+            few_low_kernel<false><<<low, kThreads, 0, stream>>>(p);
+        cudaError_t e = cudaGetLastError();
+        if (e == cudaSuccess)
+            e = dtype == TG_BF16 ? launch_chained(few_add_kernel<true>, add, kThreads, stream, p)
+                                 : launch_chained(few_add_kernel<false>, add, kThreads, stream, p);
+        if (e != cudaSuccess) {
+            cudaGetLastError();
+            return TG_ERR_CUDA;
+        }
+        return TG_OK;
+    }
+    // columns of y per block: few enough for two blocks per SM, at most 1024
+    const int64_t tiles = tiles_of(T, G);
+    int64_t chunks = std::max<int64_t>((N + 1023) / 1024, std::min<int64_t>((N + 255) / 256, (2LL * info->sms + tiles - 1) / tiles));
+    p.chunk = (int)((N + chunks * 256 - 1) / (chunks * 256) * 256);
+    chunks = (N + p.chunk - 1) / p.chunk;
+    if (chunks > 65535) return TG_ERR_INVALID_ARG;
+    const dim3 low((unsigned)tiles, (unsigned)p.splits, (unsigned)((rank + kRankPass - 1) / kRankPass));
+    const dim3 add((unsigned)tiles, (unsigned)chunks, 1);
+    cudaError_t e = dtype == TG_BF16 ? launch_low<true>(p, low, stream) : launch_low<false>(p, low, stream);
+    if (e == cudaSuccess) e = dtype == TG_BF16 ? launch_add<true>(p, add, stream) : launch_add<false>(p, add, stream);
     if (e != cudaSuccess) {
         cudaGetLastError();
         return TG_ERR_CUDA;

@@ -44,12 +44,13 @@ __global__ void __launch_bounds__(kGroupThreads) count_kernel(const int* index, 
     for (int g = threadIdx.x; g < G; g += kGroupThreads) counts[(long long)blockIdx.x * G + g] = shared_counts[g];
 }
 
-// shared memory: start[G + 1] ints, then counts of 16 bits [kGroupWarps][G]
+// shared memory: start[G + 1] and earlier[G] ints, then counts of 16 bits [kGroupWarps][G]
 __global__ void __launch_bounds__(kGroupThreads) place_kernel(const int* index, int R, int G, const int* counts,
                                                               int* offset, int* row, int* place) {
     extern __shared__ int start[];
     __shared__ int warp_total[kGroupWarps];
-    uint16_t* mine = reinterpret_cast<uint16_t*>(start + G + 1);
+    int* earlier = start + G + 1;  // rows of each group in the blocks before
+    uint16_t* mine = reinterpret_cast<uint16_t*>(earlier + G);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int first = blockIdx.x * kRowsPerBlock + warp * kRowsPerWarp;
     for (int g = threadIdx.x; g < kGroupWarps * G; g += kGroupThreads) mine[g] = 0;
@@ -64,11 +65,26 @@ __global__ void __launch_bounds__(kGroupThreads) place_kernel(const int* index, 
     }
     __syncthreads();
     uint16_t* own = mine + warp * G;
-    auto peers_of = [&](int g) { return __match_any_sync(0xffffffffu, g); };
+    // lanes whose row is of the same group, from one ballot per bit of its number
+    const int bits = 32 - __clz(G);  // (so none of -1's lanes agrees with another's)
+    auto peers_of = [&](int g) {
+        unsigned peers = 0xffffffffu;
+        for (int b = 0; b < bits; ++b) {
+            const unsigned set = __ballot_sync(0xffffffffu, g >> b & 1);
+            peers &= g >> b & 1 ? set : ~set;
+        }
+        return peers;
+    };
+    // its rows' ranks among the warp's of their groups, and the warp's counts
+    const unsigned lower = (1u << lane) - 1u;
+    int rank[kSteps];
 #pragma unroll
     for (int s = 0; s < kSteps; ++s) {
         const unsigned peers = peers_of(of[s]);
-        if (of[s] >= 0 && lane == __ffs(peers) - 1) own[of[s]] += (uint16_t)__popc(peers);
+        const int before = of[s] >= 0 ? own[of[s]] : 0;
+        rank[s] = before + __popc(peers & lower);
+        __syncwarp();
+        if (of[s] >= 0 && (peers & lower) == 0) own[of[s]] = (uint16_t)(before + __popc(peers));
         __syncwarp();
     }
     __syncthreads();
@@ -83,9 +99,20 @@ __global__ void __launch_bounds__(kGroupThreads) place_kernel(const int* index, 
             before += n;
         }
         int all = before;
-        if (counts) {
+        if (counts) {  // the blocks', 32 loads in flight
             all = 0;
-            for (int b = 0; b < (int)gridDim.x; ++b) all += counts[(long long)b * G + g];
+            int ahead = 0;
+            for (int b0 = 0; b0 < (int)gridDim.x; b0 += 32) {
+                int n[32];
+#pragma unroll
+                for (int j = 0; j < 32; ++j) n[j] = b0 + j < (int)gridDim.x ? counts[(long long)(b0 + j) * G + g] : 0;
+#pragma unroll
+                for (int j = 0; j < 32; ++j) {
+                    all += n[j];
+                    if (b0 + j < (int)blockIdx.x) ahead += n[j];
+                }
+            }
+            earlier[g] = ahead;
         }
         start[g + 1] = all;
     }
@@ -117,23 +144,13 @@ __global__ void __launch_bounds__(kGroupThreads) place_kernel(const int* index, 
     __syncthreads();
     // the places this block's rows start from
     if (counts) {
-        for (int g = threadIdx.x; g < G; g += kGroupThreads) {
-            int before = 0;
-            for (int b = 0; b < (int)blockIdx.x; ++b) before += counts[(long long)b * G + g];
-            start[g] += before;
-        }
+        for (int g = threadIdx.x; g < G; g += kGroupThreads) start[g] += earlier[g];
         __syncthreads();
     }
-    unsigned lower = (1u << lane) - 1u;
 #pragma unroll
     for (int s = 0; s < kSteps; ++s) {
         const int i = first + s * 32 + lane, g = of[s];
-        const unsigned peers = peers_of(g);
-        int at = -1;
-        if (g >= 0) at = start[g] + own[g] + __popc(peers & lower);
-        __syncwarp();
-        if (g >= 0 && lane == __ffs(peers) - 1) own[g] += (uint16_t)__popc(peers);
-        __syncwarp();
+        const int at = g >= 0 ? start[g] + own[g] + rank[s] : -1;
         if (i < R) {
             if (at >= 0) row[at] = i;
             if (place) place[i] = at;
@@ -188,7 +205,7 @@ extern "C" int tg_group_rows(int64_t R, int64_t G, const int32_t* index, int32_t
         if ((rc = check(ptrs[i], spans[i]))) return rc;
     const unsigned blocks = (unsigned)blocks_of(R);
     int* counts = need ? static_cast<int*>(workspace) : nullptr;
-    const size_t shared = (size_t)(G + 1) * 4 + (size_t)kGroupWarps * G * 2;
+    const size_t shared = (size_t)(2 * G + 1) * 4 + (size_t)kGroupWarps * G * 2;
     cudaError_t e = cudaSuccess;
     if (shared > 48 * 1024)
         e = cudaFuncSetAttribute(place_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)shared);

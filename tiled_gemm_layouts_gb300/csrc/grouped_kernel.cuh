@@ -18,11 +18,11 @@
 //
 // Rows by a list are fetched where they stand; no gathered copy of X is
 // written (at 65536 rows of 4096 columns that would be 1.07 GB more traffic).
-// With LIST four warps of their own fetch them, 16 bytes per thread and
+// With LIST five warps of their own fetch them, 16 bytes per thread and
 // asynchronous copy, into the swizzled layout that a box would have.  Without LIST the producer warp uses gathering TMA copies, four
 // row numbers each.  Those take about 80 cycles of the copy engine for 512 bytes,
 // and a stage of 128 rows 2600 where its products take 512 (65536 rows, 64
-// groups, 4096 x 1024: 464 TFLOP/s, by the four warps @LIST@), so they are for tiles of
+// groups, 4096 x 1024: 464 TFLOP/s, by the five warps 1520), so they are for tiles of
 // few rows.  Rows past a group's end are not fetched at all: what is left in
 // their part of the stage only reaches accumulator rows that are not stored, so a
 // tile of one row costs one copy of 512 bytes beside the matrix's.
@@ -45,7 +45,7 @@ namespace tg {
 
 constexpr int kGrEpiWarps = 8;   // two per TMEM lane quadrant, each with half of a tile's columns
 constexpr int kGrWarps = 3 + kGrEpiWarps;  // producers (warps 0 and 10), MMA (1), epilogue (2..9)
-constexpr int kListWarps = 4;              // with LIST, behind them
+constexpr int kListWarps = 5;              // with LIST, behind them (4: 373 us where 5 take 361; 6 leave fewer registers)
 template <bool LIST>
 constexpr int kGrThreads = 32 * (kGrWarps + (LIST ? kListWarps : 0));
 
