@@ -22,7 +22,7 @@ LIB = os.path.join(HERE, "libtilegemm.so")
 CUDA_SOURCES = ["api.cu", "gemm_sm103.cu", "probes.cu", "noalloc.cu", "stage.cu", "pointwise.cu",
                 "layernorm.cu", "adamw.cu", "ce.cu", "ce_inst_lse.cu", "ce_inst_grad.cu",
                 "ce_inst_products.cu", "route.cu", "group_rows.cu", "combine.cu", "grouped.cu",
-                "grouped_inst_rows.cu", "grouped_inst_weight.cu", "adapters.cu"] + [f"gemm_inst_{i}.cu" for i in range(1, 37)]
+                "grouped_inst_rows.cu", "grouped_inst_weight.cu", "grouped_few.cu", "adapters.cu"] + [f"gemm_inst_{i}.cu" for i in range(1, 37)]
 CXX_SOURCES = ["layout.cpp", "select.cpp", "host_pipeline.cpp"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 

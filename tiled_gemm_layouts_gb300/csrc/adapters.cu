@@ -23,14 +23,12 @@
 // bits of bf16, 22 of fp16), after a power of two that brings the largest of a
 // row's values near 1, so that fp16 neither overflows nor underflows; sums are
 // fp32, and y is rounded once.
-#include <cuda_bf16.h>
-#include <cuda_fp16.h>
-
 #include <algorithm>
 #include <cstring>
 
 #include "../../include/tilegemm.h"
 #include "chained.cuh"
+#include "direct.cuh"
 #include "grouped.h"
 
 namespace tg {
@@ -64,114 +62,13 @@ struct AdapterParams {
     int chunk;          // columns of y per block (a multiple of 256)
 };
 
-template <bool BF>
-__device__ __forceinline__ float wide(uint16_t h) {
-    if constexpr (BF) return __uint_as_float((uint32_t)h << 16);
-    return __half2float(__ushort_as_half(h));
-}
-template <bool BF>
-__device__ __forceinline__ uint16_t narrow(float x) {
-    if constexpr (BF) return __bfloat16_as_ushort(__float2bfloat16_rn(x));
-    return __half_as_ushort(__float2half_rn(x));
-}
-template <bool BF>
-__device__ __forceinline__ uint32_t narrow2(float a, float b) {
-    return (uint32_t)narrow<BF>(a) | (uint32_t)narrow<BF>(b) << 16;
-}
-
-// c += a b, 16 x 8 x 16: lane (g, q) holds of a rows g and g + 8, of b column g,
-// of c rows g and g + 8, columns 2q and 2q + 1.
-template <bool BF>
-__device__ __forceinline__ void mma(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
-                                    uint32_t b1) {
-    if constexpr (BF)
-        asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
-                     : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-                     : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
-    else
-        asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
-                     : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-                     : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
-}
-
-// Columns c .. c+7 of a row, zeros from `end` on.
-__device__ __forceinline__ uint4 load8(const uint16_t* row, int c, int end) {
-    if (c >= end) return make_uint4(0, 0, 0, 0);
-    uint4 v = *reinterpret_cast<const uint4*>(row + c);
-    if (c + 8 > end) {
-        uint32_t* w = reinterpret_cast<uint32_t*>(&v);
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            if (c + 2 * j >= end) w[j] = 0;
-            if (c + 2 * j + 1 >= end) w[j] &= 0xFFFFu;
-        }
-    }
-    return v;
-}
-// And c .. c+3.
-__device__ __forceinline__ uint2 load4(const uint16_t* row, int c, int end) {
-    if (c >= end) return make_uint2(0, 0);
-    uint2 v = *reinterpret_cast<const uint2*>(row + c);
-    if (c + 4 > end) {
-        if (c + 1 >= end) v.x &= 0xFFFFu;
-        if (c + 2 >= end) v.y = 0;
-        if (c + 3 >= end) v.y &= 0xFFFFu;
-    }
-    return v;
-}
-
-// The group, and the first and number of its rows, of tile t, when every
-// group's rows are cut into tiles of kRows; g < 0 if there are fewer tiles.
-// By a whole warp, 128 groups at a time.
-struct RowTile {
-    int g, lo, rows;
-};
-__device__ __forceinline__ RowTile find_tile(const AdapterParams& p, int t, int lane) {
-    for (int window = 0; window < p.G; window += 128) {
-        int end[5], tiles[4], incl = 0;
-#pragma unroll
-        for (int k = 0; k < 5; ++k) end[k] = max(0, min(p.offset[min(window + 4 * lane + k, p.G)], p.T));
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            tiles[k] = (max(0, end[k + 1] - end[k]) + kRows - 1) / kRows;
-            incl += tiles[k];
-        }
-        const int own = incl;
-#pragma unroll
-        for (int d = 1; d < 32; d *= 2) {
-            const int o = __shfl_up_sync(0xffffffffu, incl, d);
-            if (lane >= d) incl += o;
-        }
-        const unsigned later = __ballot_sync(0xffffffffu, t < incl);
-        if (later) {
-            const int owner = __ffs(later) - 1;
-            int i = t - (incl - own), k = 0, lo = end[0], hi = end[1];
-#pragma unroll
-            for (int j = 0; j < 3; ++j)
-                if (k == j && i >= tiles[j]) {
-                    i -= tiles[j];
-                    k = j + 1;
-                    lo = end[j + 1];
-                    hi = end[j + 2];
-                }
-            RowTile r;
-            r.g = window + 4 * owner + __shfl_sync(0xffffffffu, k, owner);
-            r.lo = __shfl_sync(0xffffffffu, lo + i * kRows, owner);
-            r.rows = min(kRows, __shfl_sync(0xffffffffu, hi, owner) - r.lo);
-            return r;
-        }
-        t -= __shfl_sync(0xffffffffu, incl, 31);
-    }
-    return {-1, 0, 0};
-}
-
 // u: grid (tiles, splits of K, passes over the rank).  NT fragments of 8 of the rank.
 template <bool BF, int NT>
 __global__ void __launch_bounds__(kThreads) low_kernel(const AdapterParams p) {
     __shared__ float joined[kWarps / 2][2][NT][4][32];
     allow_next_kernel();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, q = lane & 3;
-    const RowTile tile = find_tile(p, blockIdx.x, lane);
+    const RowTile tile = find_tile<kRows>(p.offset, p.G, p.T, blockIdx.x, lane);
     if (tile.g < 0) return;
     const int r0 = blockIdx.z * kRankPass;
     // rows g, g + 8, g + 16, g + 24 of the tile
@@ -259,7 +156,7 @@ __global__ void __launch_bounds__(kThreads) low_kernel(const AdapterParams p) {
 template <bool BF, int KC>
 __global__ void __launch_bounds__(kThreads) add_kernel(const AdapterParams p) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, q = lane & 3;
-    const RowTile tile = find_tile(p, blockIdx.x, lane);
+    const RowTile tile = find_tile<kRows>(p.offset, p.G, p.T, blockIdx.x, lane);
     if (tile.g < 0) return;
     uint16_t* y[4];
 #pragma unroll

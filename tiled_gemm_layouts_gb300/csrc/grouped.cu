@@ -31,24 +31,40 @@ EncodeTiledFn encode_fn() {
     return fn;
 }
 
-}  // namespace
+bool encode(CUtensorMap* map, int dtype, int rank, const void* base, const cuuint64_t* dims, const cuuint64_t* strides,
+            const cuuint32_t* box) {
+    const cuuint32_t estr[4] = {1, 1, 1, 1};
+    EncodeTiledFn fn = encode_fn();
+    return fn &&
+           fn(map, dtype == TG_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, (cuuint32_t)rank,
+              const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
 
+// `groups` matrices of `outer` rows of `inner` elements, ld and stride elements
+// apart, in boxes of 64 x box_outer x 1.
 bool encode_stack(CUtensorMap* map, int dtype, const void* base, int64_t inner, int64_t outer, int64_t groups,
                   int64_t ld, int64_t stride, uint32_t box_outer) {
     const cuuint64_t dims[3] = {(cuuint64_t)inner, (cuuint64_t)outer, (cuuint64_t)groups};
     const cuuint64_t strides[2] = {(cuuint64_t)ld * 2, (cuuint64_t)stride * 2};
     const cuuint32_t box[3] = {64, box_outer, 1};
-    const cuuint32_t estr[3] = {1, 1, 1};
-    EncodeTiledFn encode = encode_fn();
-    return encode &&
-           encode(map, dtype == TG_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3,
-                  const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                  CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+    return encode(map, dtype, 3, base, dims, strides, box);
 }
 
+// The same in boxes of two neighbouring runs of 64: 64 x box_outer x 2 x 1.  Only
+// the whole runs of a row (`runs`, two at least).
+bool encode_stack_pairs(CUtensorMap* map, int dtype, const void* base, int64_t runs, int64_t outer, int64_t groups,
+                        int64_t ld, int64_t stride, uint32_t box_outer) {
+    const cuuint64_t dims[4] = {64, (cuuint64_t)outer, (cuuint64_t)runs, (cuuint64_t)groups};
+    const cuuint64_t strides[3] = {(cuuint64_t)ld * 2, 128, (cuuint64_t)stride * 2};
+    const cuuint32_t box[4] = {64, box_outer, 2, 1};
+    return encode(map, dtype, 4, base, dims, strides, box);
+}
+
+// Rows of a matrix: `row` (a list, or null), divided by per_row, and the maps of
+// boxes of 64 columns x 128 rows (and two of them), and of gathered rows.
 bool encode_rows(GroupedRows* rows, int dtype, const void* base, int64_t count, int64_t cols, int64_t ld,
-                 const int32_t* row, int64_t per_row, uint32_t box_rows) {
+                 const int32_t* row, int64_t per_row) {
     rows->count = (int)count;
     rows->base = base;
     rows->ld = ld;
@@ -60,15 +76,18 @@ bool encode_rows(GroupedRows* rows, int dtype, const void* base, int64_t count, 
     while (((int64_t)1 << b) < per_row) ++b;
     rows->shift = 31 + b;
     rows->magic = (uint32_t)(((u128)1 << (31 + b)) / (u128)per_row + 1);
-    return encode_2d(&rows->box, dtype, base, (uint64_t)cols, (uint64_t)count, ld, 64, box_rows) &&
-           encode_2d(&rows->gather, dtype, base, (uint64_t)cols, (uint64_t)count, ld, 64, 1);
+    rows->pairs = cols >= 128 ? (int)(cols / 64) : 0;
+    return encode_2d(&rows->box, dtype, base, (uint64_t)cols, (uint64_t)count, ld, 64, 128) &&
+           encode_2d(&rows->gather, dtype, base, (uint64_t)cols, (uint64_t)count, ld, 64, 1) &&
+           (!rows->pairs || encode_k_pairs(&rows->box2, dtype, base, count, cols / 64 * 64, ld, 128));
 }
 
-cudaError_t launch_grouped(int mode, const GroupedParams& p, GroupedTile tile, long long tiles, int sms,
-                           bool chained, cudaStream_t stream) {
+}  // namespace
+
+cudaError_t launch_grouped(int mode, const GroupedParams& p, GroupedTile tile, long long tiles, int sms, cudaStream_t stream) {
     switch (mode) {
-        case GROUPED_ROWS: return launch_grouped_mode<GROUPED_ROWS>(p, tile, tiles, sms, chained, stream);
-        case GROUPED_WEIGHT: return launch_grouped_mode<GROUPED_WEIGHT>(p, tile, tiles, sms, chained, stream);
+        case GROUPED_ROWS: return launch_grouped_mode<GROUPED_ROWS>(p, tile, tiles, sms, stream);
+        case GROUPED_WEIGHT: return launch_grouped_mode<GROUPED_WEIGHT>(p, tile, tiles, sms, stream);
     }
     return cudaErrorInvalidValue;
 }
@@ -129,6 +148,15 @@ long long most_tiles(int64_t R, int64_t G, int rows, int64_t tiles_n) {
     return (std::min(R, G) + R / rows) * tiles_n;
 }
 
+// Tiles of 16 rows (grouped_few.cu) against tiles of 128: up to two rows per group
+// that may have any, and up to 16 where the large tiles would not fill the GPU.
+// N = 2048, K = 4096, us: 64 groups, 8 rows 35 to 48, 128 rows 118 to 138, 512 rows 209
+// to 187; 8 groups, 16 rows 31 to 48, 128 rows 54 to 64, 256 rows 78 to 42.
+bool few_rows(int64_t R, int64_t N, int64_t G, int perm, int sms) {
+    const int64_t used = std::min(R, G);
+    return perm == TG_OP_T && (R <= 2 * used || (R <= 16 * used && most_tiles(R, G, 128, (N + 127) / 128) <= sms));
+}
+
 }  // namespace
 }  // namespace tg
 
@@ -164,24 +192,54 @@ extern "C" int tg_grouped_gemm(int64_t R, int64_t N, int64_t K, int64_t G, const
     for (int i = 0; i < 7; ++i)
         if ((rc = check(ptrs[i], spans[i]))) return rc;
 
+    if (few_rows(R, N, G, permB, info->sms)) {
+        FewRowsParams f = {};
+        f.offset = offset;
+        f.groups = (int)G;
+        f.rows = (int)R;
+        f.x_rows = (int)(row ? x_rows : R);
+        f.per_row = (int)per_row;
+        f.n = (int)N;
+        f.k = (int)K;
+        f.x = static_cast<const uint16_t*>(X);
+        f.ldx = ldx;
+        f.row = row;
+        f.b = static_cast<const uint16_t*>(B);
+        f.ldb = ldb;
+        f.stride_b = G > 1 ? stride_b : 0;
+        f.y = static_cast<uint16_t*>(Y);
+        f.ldy = ldy;
+        f.bias = static_cast<const uint16_t*>(bias);
+        f.ld_bias = bias ? epi->ld_bias : 0;
+        f.relu = epi ? epi->relu : 0;
+        f.relu_of = static_cast<const uint16_t*>(relu_of);
+        f.ld_relu = relu_of ? epi->ld_relu : 0;
+        if (launch_few_rows(f, dtype == TG_BF16, most_tiles(R, G, kFewTileRows, 1), stream) != cudaSuccess) {
+            cudaGetLastError();
+            return TG_ERR_CUDA;
+        }
+        return TG_OK;
+    }
     GroupedTile tile{64, 0, 0};
     if (R >= 128 * G)
         tile = GroupedTile{256, 1, row != nullptr};
     else if (most_tiles(R, G, 128, (N + 127) / 128) >= info->sms)
-        tile = GroupedTile{128, 0, row && R > 16 * G};
+        tile = GroupedTile{128, 0, row != nullptr};
     GroupedParams p;
     std::memset(&p, 0, sizeof(p));
     const int bnc = tile.pair ? tile.bn / 2 : tile.bn;
     p.q_mn = permB == TG_OP_N;
-    bool ok = encode_rows(&p.p, dtype, X, row ? x_rows : R, K, ldx, row, per_row, 128);
+    bool ok = encode_rows(&p.p, dtype, X, row ? x_rows : R, K, ldx, row, per_row);
     const int64_t stride = G > 1 ? stride_b : a.b_rows() * ldb;
-    ok = ok && (p.q_mn ? encode_stack(&p.map_q, dtype, B, N, K, G, ldb, stride, 64)
+    p.q_pairs = !p.q_mn && K >= 128 ? (int)(K / 64) : 0;
+    ok = ok && (p.q_mn ? encode_stack(&p.map_q, dtype, B, N, K, G, ldb, stride, 64u * (uint32_t)tile.blocks_rows())
                        : encode_stack(&p.map_q, dtype, B, K, N, G, ldb, stride, (uint32_t)bnc));
+    ok = ok && (!p.q_pairs || encode_stack_pairs(&p.map_q2, dtype, B, p.q_pairs, N, G, ldb, stride, (uint32_t)bnc));
     if (!ok) return TG_ERR_CUDA;
     p.offset = offset;
     p.groups = (int)G;
     p.rows = (int)R;
-    p.num_kb = p.kb_wrap = (int)((K + 63) / 64);
+    p.num_kb = (int)((K + 63) / 64);
     p.tiles_n = (int)((N + tile.bn - 1) / tile.bn);
     p.group_m = 2048 / tile.rows();
     p.n = (int)N;
@@ -196,7 +254,7 @@ extern "C" int tg_grouped_gemm(int64_t R, int64_t N, int64_t K, int64_t G, const
     p.ld_relu = relu_of ? epi->ld_relu : 0;
     p.timeout_cycles = watchdog_timeout();
     p.status = info->status;
-    if (launch_grouped(GROUPED_ROWS, p, tile, most_tiles(R, G, tile.rows(), p.tiles_n), info->sms, false, stream) != cudaSuccess) {
+    if (launch_grouped(GROUPED_ROWS, p, tile, most_tiles(R, G, tile.rows(), p.tiles_n), info->sms, stream) != cudaSuccess) {
         cudaGetLastError();
         return TG_ERR_CUDA;
     }
@@ -231,13 +289,12 @@ extern "C" int tg_grouped_gemm_grad(int64_t R, int64_t N, int64_t K, int64_t G, 
     GroupedParams p;
     std::memset(&p, 0, sizeof(p));
     GroupedRows &x = permB == TG_OP_N ? p.p : p.q, &y = permB == TG_OP_N ? p.q : p.p;
-    if (!encode_rows(&x, dtype, X, row ? x_rows : R, K, ldx, row, per_row, 64) ||
-        !encode_rows(&y, dtype, dY, R, N, lddy, nullptr, 1, 64))
+    if (!encode_rows(&x, dtype, X, row ? x_rows : R, K, ldx, row, per_row) ||
+        !encode_rows(&y, dtype, dY, R, N, lddy, nullptr, 1))
         return TG_ERR_CUDA;
     p.offset = offset;
     p.groups = (int)G;
     p.rows = (int)R;
-    p.kb_wrap = 1;
     p.tiles_m = (int)((m + tile.rows() - 1) / tile.rows());
     p.tiles_n = (int)((n + tile.bn - 1) / tile.bn);
     p.group_m = 2048 / tile.rows();
@@ -252,7 +309,7 @@ extern "C" int tg_grouped_gemm_grad(int64_t R, int64_t N, int64_t K, int64_t G, 
     p.timeout_cycles = watchdog_timeout();
     p.status = info->status;
     const long long tiles = (long long)G * p.tiles_m * p.tiles_n;
-    if (launch_grouped(GROUPED_WEIGHT, p, tile, tiles, info->sms, false, stream) != cudaSuccess) {
+    if (launch_grouped(GROUPED_WEIGHT, p, tile, tiles, info->sms, stream) != cudaSuccess) {
         cudaGetLastError();
         return TG_ERR_CUDA;
     }

@@ -9,14 +9,24 @@ namespace tg {
 
 constexpr int64_t kMaxRowGroups = 4096;
 
-// `groups` matrices of `outer` rows of `inner` elements, ld and stride elements
-// apart, in boxes of 64 x box_outer x 1 with the 128-byte swizzle.
-bool encode_stack(CUtensorMap* map, int dtype, const void* base, int64_t inner, int64_t outer, int64_t groups,
-                  int64_t ld, int64_t stride, uint32_t box_outer);
-
-// Rows of a matrix: `row` (a list, or null), divided by per_row, and the maps of
-// boxes of 64 columns x box_rows rows and of gathered rows.
-bool encode_rows(GroupedRows* rows, int dtype, const void* base, int64_t count, int64_t cols, int64_t ld,
-                 const int32_t* row, int64_t per_row, uint32_t box_rows);
+// Products of few rows per group, B by rows of its transpose (grouped_few.cu).
+constexpr int kFewTileRows = 16;
+struct FewRowsParams {
+    const int* offset;
+    int groups, rows, x_rows, per_row, n, k;
+    const uint16_t* x;
+    long long ldx;
+    const int* row;
+    const uint16_t* b;
+    long long ldb, stride_b;
+    uint16_t* y;
+    long long ldy;
+    const uint16_t* bias;
+    long long ld_bias;
+    int relu;
+    const uint16_t* relu_of;
+    long long ld_relu;
+};
+cudaError_t launch_few_rows(const FewRowsParams& p, bool bf16, long long tiles, cudaStream_t stream);
 
 }  // namespace tg

@@ -37,7 +37,6 @@
 #pragma once
 
 #include "ce_kernel.cuh"
-#include "chained.cuh"
 #include "gemm_kernel.cuh"
 #include "grouped_params.h"
 
@@ -46,17 +45,28 @@ namespace tg {
 constexpr int kGrEpiWarps = 8;   // two per TMEM lane quadrant, each with half of a tile's columns
 constexpr int kGrWarps = 3 + kGrEpiWarps;  // producers (warps 0 and 10), MMA (1), epilogue (2..9)
 constexpr int kListWarps = 5;              // with LIST, behind them (4: 373 us where 5 take 361; 6 leave fewer registers)
+// K-blocks per barrier transaction, one after the other in the ring.  Where an
+// operand's columns are contiguous, they interleave: 64 columns of all their
+// rows, then the next 64.  Two take half the copies and waits of one: the
+// gradient of 65536 rows, 64 groups, 4096 x 1024, 414 us with one, 330 with two.
+// Rows by a list for tiles of a pair come faster one by one: 361 us, 385.
+template <int MODE, bool PAIR, bool LIST>
+constexpr int kGrBlocks = MODE == GROUPED_ROWS && PAIR && LIST ? 1 : 2;
+constexpr int kGrOrder = 512;              // groups that GROUPED_WEIGHT sorts by their rows
 template <bool LIST>
 constexpr int kGrThreads = 32 * (kGrWarps + (LIST ? kListWarps : 0));
 
-template <int BN, bool PAIR>
+template <int MODE, int BN, bool PAIR, bool LIST>
 struct GroupedShape : TileShape<BN, PAIR> {
     using TS = TileShape<BN, PAIR>;
     static constexpr int kUnit = 4096;  // staging per epilogue warp: 32 rows of 128 bytes
     static constexpr int kFit = (TS::kSmemLimit - 1024 - 256 - kGrEpiWarps * kUnit) / TS::kStage;
-    static constexpr int kSlots = kFit > 8 ? 8 : kFit;
-    static constexpr int kGrSmemBytes = 1024 + kSlots * TS::kStage + kGrEpiWarps * kUnit + (2 * kSlots + 5) * 8 + 16;
-    static_assert(kSlots >= 4 && kGrSmemBytes <= TS::kSmemLimit, "shared memory budget");
+    static constexpr int kSlots = (kFit > 8 ? 8 : kFit) & ~1;
+    static constexpr int kBlocks = kGrBlocks<MODE, PAIR, LIST>;
+    static constexpr int kGroups = kSlots / kBlocks;  // of slots, a transaction each
+    static constexpr int kGrSmemBytes =
+        1024 + kSlots * TS::kStage + kGrEpiWarps * kUnit + kGrOrder * 2 + (2 * kGroups + 5) * 8 + 16;
+    static_assert(kSlots >= kListWarps && kGrSmemBytes <= TS::kSmemLimit, "shared memory budget");
 };
 
 // Gathers rows r[0..3], columns c .. c+63, as four consecutive 128-byte rows.
@@ -110,14 +120,17 @@ struct GroupedItem {
 template <int MODE>
 struct GroupedItems {
     const GroupedParams& p;
-    int lane, bm, t, step;
+    const uint16_t* order;   // GROUPED_WEIGHT: groups, the one with the most rows first, or null
+    int lane, bm, t, step;   // GROUPED_WEIGHT: t counts rounds
+    int worker;
     int window, base, incl;  // groups from `window`, their first tile, tiles up to this lane's last group
     int lo[4], cnt[4];       // this lane's four groups
     bool started;
 
-    __device__ __forceinline__ GroupedItems(const GroupedParams& params, int worker, int workers, int rows_per_tile)
-        : p(params), lane(threadIdx.x & 31), bm(rows_per_tile), t(worker), step(workers), window(-128), base(0),
-          incl(0), started(false) {}
+    __device__ __forceinline__ GroupedItems(const GroupedParams& params, const uint16_t* sorted, int self, int workers,
+                                            int rows_per_tile)
+        : p(params), order(sorted), lane(threadIdx.x & 31), bm(rows_per_tile), t(MODE == GROUPED_WEIGHT ? 0 : self),
+          step(workers), worker(self), window(-128), base(0), incl(0), started(false) {}
 
     __device__ __forceinline__ int bound(int g) const {
         return max(0, min(p.offset[g], p.rows));
@@ -132,13 +145,18 @@ struct GroupedItems {
     }
     __device__ __forceinline__ bool next(GroupedItem& it) {
         if constexpr (MODE == GROUPED_WEIGHT) {
+            // Tiles take as long as their groups have rows.  Groups come sorted, and rounds
+            // of one tile per worker alternate in direction, so that all have the same to
+            // do within about one tile (64 groups of 1024 rows give or take half, 4096 x
+            // 1024: @SORT@).
             const int per = p.tiles_m * p.tiles_n;
-            it.g = t / per;
-            if (it.g >= p.groups) return false;
+            const int i = t * step + (t & 1 ? step - 1 - worker : worker), at = i / per;
+            if (at >= p.groups) return false;
+            it.g = order ? order[at] : at;
             it.lo = bound(it.g);
             it.cnt = max(0, bound(it.g + 1) - it.lo);
-            place(it, t - it.g * per, p.tiles_m);
-            t += step;
+            place(it, i - at * per, p.tiles_m);
+            ++t;
             return true;
         } else {
             while (!started || t >= base + __shfl_sync(0xffffffffu, incl, 31)) {
@@ -191,9 +209,11 @@ struct GroupedItems {
 
 template <int MODE, int BN, bool PAIR, bool LIST>
 __global__ void __launch_bounds__(kGrThreads<LIST>, 1) grouped_kernel(const __grid_constant__ GroupedParams p) {
-    using TS = GroupedShape<BN, PAIR>;
+    using TS = GroupedShape<MODE, BN, PAIR, LIST>;
+    constexpr int BLOCKS = TS::kBlocks;
+    constexpr uint32_t kAtom = 8192u * BLOCKS;  // 64 contiguous columns of a transaction's rows
     constexpr bool WEIGHT = MODE == GROUPED_WEIGHT;
-    constexpr int SLOTS = TS::kSlots;
+    constexpr int SLOTS = TS::kSlots, GROUPS = TS::kGroups;
     constexpr int CG = PAIR ? 2 : 1;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
@@ -201,9 +221,10 @@ __global__ void __launch_bounds__(kGrThreads<LIST>, 1) grouped_kernel(const __gr
     uint8_t* sA = smem;
     uint8_t* sB = smem + SLOTS * TS::kAStage;
     uint8_t* staging = sB + SLOTS * TS::kBStage;
-    uint64_t* full = reinterpret_cast<uint64_t*>(staging + kGrEpiWarps * TS::kUnit);
-    uint64_t* empty = full + SLOTS;
-    uint64_t* tfull = empty + SLOTS;
+    uint16_t* sorted = reinterpret_cast<uint16_t*>(staging + kGrEpiWarps * TS::kUnit);
+    uint64_t* full = reinterpret_cast<uint64_t*>(sorted + kGrOrder);
+    uint64_t* empty = full + GROUPS;
+    uint64_t* tfull = empty + GROUPS;
     uint64_t* tempty = tfull + 2;
     uint64_t* drain = tempty + 2;
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
@@ -219,10 +240,9 @@ __global__ void __launch_bounds__(kGrThreads<LIST>, 1) grouped_kernel(const __gr
                   PAIR ? mapa_shared(smem_addr((const void*)abort_flag), rank ^ 1u) : 0u, PAIR,
                   p.status, p.timeout_cycles};
 
-    allow_next_kernel();
     if (threadIdx.x == 0) {
-        for (int s = 0; s < SLOTS; ++s) {
-            mbar_init(smem_addr(&full[s]), 1 + (LIST ? CG : 0));
+        for (int s = 0; s < GROUPS; ++s) {
+            mbar_init(smem_addr(&full[s]), 1 + (LIST ? CG * BLOCKS : 0));
             mbar_init(smem_addr(&empty[s]), 1);
         }
         for (int b = 0; b < 2; ++b) {
@@ -237,6 +257,19 @@ __global__ void __launch_bounds__(kGrThreads<LIST>, 1) grouped_kernel(const __gr
         tmem_alloc<CG>(smem_addr(tmem_slot), TS::kTmemCols);
         tmem_relinquish<CG>();
     }
+    const bool sort = WEIGHT && p.groups > 1 && p.groups <= kGrOrder;
+    if (sort) {  // (the staging buffers are free)
+        int* count = reinterpret_cast<int*>(staging);
+        for (int g = threadIdx.x; g < p.groups; g += kGrThreads<LIST>)
+            count[g] = min(max(p.offset[g + 1], 0), p.rows) - min(max(p.offset[g], 0), p.rows);
+        __syncthreads();
+        for (int g = threadIdx.x; g < p.groups; g += kGrThreads<LIST>) {
+            int ahead = 0;
+            for (int o = 0; o < p.groups; ++o) ahead += count[o] > count[g] || (count[o] == count[g] && o < g);
+            sorted[ahead] = (uint16_t)g;
+        }
+    }
+    const uint16_t* order = sort ? sorted : nullptr;
     tc_fence_before();
     if constexpr (PAIR)
         cluster_sync();
@@ -244,7 +277,6 @@ __global__ void __launch_bounds__(kGrThreads<LIST>, 1) grouped_kernel(const __gr
         __syncthreads();
     tc_fence_after();
     const uint32_t tmem_base = *tmem_slot;
-    wait_for_previous_kernel();
 
     // K-blocks of an item (a group without rows still has one, of zeros)
     auto blocks_of = [&](const GroupedItem& it) { return WEIGHT ? max(1, (it.cnt + kBK - 1) / kBK) : p.num_kb; };
@@ -253,22 +285,20 @@ __global__ void __launch_bounds__(kGrThreads<LIST>, 1) grouped_kernel(const __gr
 
     if (warp == 0 || warp == 2 + kGrEpiWarps) {
         // -------------------------------------------------- TMA producers
-        // Warp 0 arms each slot and fetches P, the other one fetches Q into it.
+        // Warp 0 arms each transaction and fetches P, the other one fetches Q into it.
         const bool first = warp == 0;
-        int slot = 0;
+        int grp = 0;
         uint32_t phase = 0, armed = 0, armed_parity = 0;
-        GroupedItems<MODE> items(p, worker, workers, TS::kBM);
+        GroupedItems<MODE> items(p, order, worker, workers, TS::kBM);
         GroupedItem it;
         bool ok = true;
-        fence_proxy_async_global();  // low-rank rows that the kernel before stored
+        const GroupedRows& s = first ? p.p : p.q;
+        const bool others = LIST && (WEIGHT ? s.row != nullptr : first);  // the list's warps fetch this operand
+        const uint32_t dst0 = smem_addr(first ? sA : sB), block_bytes = first ? (uint32_t)TS::kAStage : (uint32_t)TS::kBStage;
+        const int quad = WEIGHT ? lane & 15 : lane;
         while (ok && items.next(it)) {
             const int num_kb = blocks_of(it);
-            const GroupedRows& s = first ? p.p : p.q;
-            const bool others = LIST && s.row;  // the list's warps fetch this operand
-            const uint32_t dst0 = smem_addr(first ? sA : sB);
-            constexpr uint32_t kAStep = TS::kAStage, kBStep = TS::kBStage;
-            const uint32_t step = first ? kAStep : kBStep;
-            // bytes that the two producers of every CTA bring per slot
+            // bytes that the two producers of every CTA bring per K-block
             uint32_t bytes;
             if constexpr (WEIGHT) {
                 bytes = (uint32_t)((LIST && p.p.row ? 0 : TS::kAStage) + (LIST && p.q.row ? 0 : TS::kBStage)) * CG;
@@ -277,43 +307,34 @@ __global__ void __launch_bounds__(kGrThreads<LIST>, 1) grouped_kernel(const __gr
                     const int n = rows_in(it, r);
                     return LIST ? 0u : s.row ? (uint32_t)((n + 3) / 4) * 512u : n ? (uint32_t)TS::kAStage : 0u;
                 };
-                bytes = rows_bytes(0) + (PAIR ? rows_bytes(1) : 0u) +
-                        (p.q_mn ? (uint32_t)TS::kBStage : (uint32_t)TS::kBNC * 128u) * CG;
+                bytes = rows_bytes(0) + (PAIR ? rows_bytes(1) : 0u) + (p.q_mn ? 0u : (uint32_t)TS::kBStage * CG);
             }
-            // the rows that this lane fetches
-            int src[4], ahead[4];
             const int mine = rows_in(it, (int)rank);
-            const int quad = WEIGHT ? lane & 15 : lane;
-            const int row0 = it.tm * TS::kBM + 128 * (int)rank;  // not WEIGHT
+            const int row0 = it.tm * TS::kBM + 128 * (int)rank;               // not WEIGHT
             const int c0 = first ? row0 : it.tn * BN + (int)rank * TS::kBNC;  // WEIGHT: first column of P or Q
-            auto fetch_rows = [&](int i0, int (&r)[4]) {
+            int src[4];  // the rows that this lane fetches
+            auto fetch_rows = [&](int i0) {
 #pragma unroll
-                for (int k = 0; k < 4; ++k) r[k] = source_row(s, it.lo, i0 + 4 * quad + k, it.cnt);
+                for (int k = 0; k < 4; ++k) src[k] = source_row(s, it.lo, i0 + 4 * quad + k, it.cnt);
             };
-            if (WEIGHT && !others)
-                fetch_rows(0, ahead);
-            else if (!WEIGHT && first && s.row && !LIST)
-                fetch_rows(row0, src);
-            for (int kb = 0; kb < num_kb; ++kb) {
-                if (WEIGHT && !others) {
-                    // the next block's row numbers are on their way while this one is awaited
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) src[k] = ahead[k];
-                    if (kb + 1 < num_kb) fetch_rows((kb + 1) * kBK, ahead);
-                }
-                const bool got = wait_bar(smem_addr(&empty[slot]), phase ^ 1, w, DEV_TIMEOUT_PRODUCER + 1);
+            if (!WEIGHT && first && s.row && !LIST) fetch_rows(row0);
+            for (int kb = 0; kb < num_kb; kb += BLOCKS) {
+                const int n = min(BLOCKS, num_kb - kb);
+                const bool got = wait_bar(smem_addr(&empty[grp]), phase ^ 1, w, DEV_TIMEOUT_PRODUCER + 1);
                 if (!__all_sync(0xffffffffu, got)) {
                     ok = false;
                     break;
                 }
-                const uint32_t fb_local = smem_addr(&full[slot]);
+                const uint32_t fb_local = smem_addr(&full[grp]);
                 if (first && leader && lane == 0) {
-                    mbar_arrive_expect_tx(fb_local, bytes);
-                    armed |= 1u << slot;
-                    armed_parity = (armed_parity & ~(1u << slot)) | (phase << slot);
+                    // (a box of contiguous columns always holds both blocks' rows)
+                    const uint32_t whole = !WEIGHT && p.q_mn ? (uint32_t)(BLOCKS * TS::kBStage) * CG : 0u;
+                    mbar_arrive_expect_tx(fb_local, bytes * (uint32_t)n + whole);
+                    armed |= 1u << grp;
+                    armed_parity = (armed_parity & ~(1u << grp)) | (phase << grp);
                 }
                 const uint32_t fb = PAIR ? mapa_shared(fb_local, 0) : fb_local;
-                const uint32_t dst = dst0 + (uint32_t)slot * step;
+                const uint32_t dst = dst0 + (uint32_t)grp * BLOCKS * block_bytes;
                 auto load2 = [&](uint32_t at, const CUtensorMap* map, int x, int y) {
                     if constexpr (PAIR)
                         tma_load_2d_pair(at, map, fb, x, y);
@@ -326,44 +347,57 @@ __global__ void __launch_bounds__(kGrThreads<LIST>, 1) grouped_kernel(const __gr
                     else
                         tma_load_3d(at, map, fb, x, y, z);
                 };
+                auto load4 = [&](uint32_t at, const CUtensorMap* map, int y, int z, int u) {
+                    if constexpr (PAIR)
+                        tma_load_4d_pair(at, map, fb, 0, y, z, u);
+                    else
+                        tma_load_4d(at, map, fb, 0, y, z, u);
+                };
                 if (others) {
                 } else if constexpr (WEIGHT) {
-                    // 64 rows of the group, in atoms of 64 columns
+                    // rows of the group, in atoms of 64 columns
                     const int atoms = first ? 2 : TS::kBBoxes;
-                    if (!s.row && (kb + 1) * kBK <= it.cnt) {
-                        if (lane < atoms) load2(dst + lane * 8192, &s.box, c0 + 64 * lane, it.lo + kb * kBK);
+                    if ((kb + BLOCKS) * kBK <= it.cnt) {
+                        if (lane < atoms) load2(dst + lane * kAtom, &s.box, c0 + 64 * lane, it.lo + kb * kBK);
                     } else {
-                        for (int h = lane >> 4; h < atoms; h += 2)
-                            tma_gather4<PAIR>(dst + h * 8192 + quad * 512, &s.gather, fb, c0 + 64 * h, src);
+                        for (int j = 0; j < n; ++j) {
+                            fetch_rows((kb + j) * kBK);
+                            for (int h = lane >> 4; h < atoms; h += 2)
+                                tma_gather4<PAIR>(dst + h * kAtom + j * 8192 + quad * 512, &s.gather, fb, c0 + 64 * h, src);
+                        }
                     }
                 } else if (first) {
-                    const int part = kb / p.kb_wrap, x = (kb - part * p.kb_wrap) * kBK;
                     if (s.row) {
-                        if (4 * lane < mine) tma_gather4<PAIR>(dst + lane * 512, &s.gather, fb, x, src);
+                        if (4 * lane < mine)
+                            for (int j = 0; j < n; ++j)
+                                tma_gather4<PAIR>(dst + j * TS::kAStage + lane * 512, &s.gather, fb, (kb + j) * kBK, src);
                     } else if (lane == 0 && mine > 0) {
-                        load2(dst, &s.box, x, it.lo + row0 + part * p.part_rows);
+                        if (n == 2 && kb + 2 <= s.pairs)
+                            load3(dst, &s.box2, 0, it.lo + row0, kb);
+                        else
+                            for (int j = 0; j < n; ++j) load2(dst + j * TS::kAStage, &s.box, (kb + j) * kBK, it.lo + row0);
                     }
-                } else {
-                    const int k0 = kb % p.kb_wrap * kBK;
-                    if (p.q_mn) {
-                        if (lane < TS::kBBoxes) load3(dst + lane * 8192, &p.map_q, c0 + 64 * lane, k0, it.g);
-                    } else if (lane == 0) {
-                        load3(dst, &p.map_q, k0, c0, it.g);
-                    }
+                } else if (p.q_mn) {
+                    if (lane < TS::kBBoxes) load3(dst + lane * kAtom, &p.map_q, c0 + 64 * lane, kb * kBK, it.g);
+                } else if (lane == 0) {
+                    if (n == 2 && kb + 2 <= p.q_pairs)
+                        load4(dst, &p.map_q2, c0, kb, it.g);
+                    else
+                        for (int j = 0; j < n; ++j) load3(dst + j * TS::kBStage, &p.map_q, (kb + j) * kBK, c0, it.g);
                 }
-                if (++slot == SLOTS) {
-                    slot = 0;
+                if (++grp == GROUPS) {
+                    grp = 0;
                     phase ^= 1;
                 }
             }
         }
         if (*abort_flag && first && lane == 0) {  // no TMA write may land after the CTA exits
-            for (int q = 0; q < SLOTS; ++q)
+            for (int q = 0; q < GROUPS; ++q)
                 if (armed & (1u << q)) drain_bar(smem_addr(&full[q]), (armed_parity >> q) & 1, w);
         }
     } else if (LIST && warp >= kGrWarps) {
         // ------------------------------------------- rows by their numbers
-        // Each warp takes every kListWarps-th stage: 1024 units of 16 bytes, lane's
+        // Each warp takes every kListWarps-th slot: 1024 units of 16 bytes, lane's
         // unit u of every kApart-th row.  16-byte unit k of 128-byte row r lies at
         // unit k ^ (r mod 8).  Once they have landed, the warp hands what it wrote
         // to the proxy that the MMA reads through, and arrives on the leader's
@@ -372,7 +406,6 @@ __global__ void __launch_bounds__(kGrThreads<LIST>, 1) grouped_kernel(const __gr
         // and three stages ahead the products above ran at 380 TFLOP/s.)
         constexpr int kUnitsOfRow = WEIGHT ? 16 : 8, kApart = 32 / kUnitsOfRow, kRows = WEIGHT ? 64 : 128;
         static_assert(!WEIGHT || TS::kBNC == 128, "P's and Q's stages have one shape");
-        static_assert(SLOTS >= kListWarps, "the warps' stages are different ones");
         const int self = warp - kGrWarps;
         const bool is_p = !WEIGHT || p.p.row;
         const GroupedRows& s = is_p ? p.p : p.q;
@@ -384,16 +417,16 @@ __global__ void __launch_bounds__(kGrThreads<LIST>, 1) grouped_kernel(const __gr
 #pragma unroll
         for (int j = 0; j < 8 / kApart; ++j) {
             const int r = kApart * j + q;
-            to[j] = (uint32_t)((u >> 3) * 8192 + r * 128 + (((u & 7) ^ (r & 7)) << 4));
+            to[j] = (uint32_t)((u >> 3) * kAtom + r * 128 + (((u & 7) ^ (r & 7)) << 4));
         }
         const uint16_t* base = static_cast<const uint16_t*>(s.base);
-        int slot = self, wait = self;  // of this warp's next stage; stages until it is due
+        int slot = self, wait = self;  // of this warp's next K-block; K-blocks until it is due
         uint32_t phase = 0;
-        GroupedItems<MODE> items(p, worker, workers, TS::kBM);
+        GroupedItems<MODE> items(p, order, worker, workers, TS::kBM);
         GroupedItem it;
         bool ok = true;
         while (ok && items.next(it)) {
-            const int num_kb = blocks_of(it);
+            const int num_kb = blocks_of(it), all_kb = (num_kb + BLOCKS - 1) / BLOCKS * BLOCKS;
             const int row0 = it.tm * TS::kBM + 128 * (int)rank;                 // not WEIGHT
             const int c0 = is_p ? row0 : it.tn * BN + (int)rank * TS::kBNC;     // WEIGHT
             // lane's rows of the stage: lane, lane + 32, ...
@@ -407,21 +440,23 @@ __global__ void __launch_bounds__(kGrThreads<LIST>, 1) grouped_kernel(const __gr
             else
                 fetch_rows(row0, src);
             int kb = wait;
-            for (; kb < num_kb; kb += kListWarps) {
+            for (; kb < all_kb; kb += kListWarps) {
                 if constexpr (WEIGHT) {
 #pragma unroll
                     for (int j = 0; j < kRows / 32; ++j) src[j] = ahead[j];
                     fetch_rows((kb + kListWarps) * kBK, ahead);
                 }
-                const bool got = wait_bar(smem_addr(&empty[slot]), phase ^ 1, w, DEV_TIMEOUT_PRODUCER + 3);
+                const bool got = wait_bar(smem_addr(&empty[slot / BLOCKS]), phase ^ 1, w, DEV_TIMEOUT_PRODUCER + 3);
                 if (!__all_sync(0xffffffffu, got)) {
                     ok = false;
                     break;
                 }
-                const uint32_t dst = dst0 + (uint32_t)slot * stage_bytes;
+                const uint32_t dst = dst0 + (uint32_t)(slot / BLOCKS) * BLOCKS * stage_bytes +
+                                     (uint32_t)(slot % BLOCKS) * (WEIGHT ? 8192u : (uint32_t)TS::kAStage);
                 const int col = (WEIGHT ? c0 : kb * kBK) + 8 * u;
                 const uint32_t bytes = 2u * (uint32_t)min(8, max(0, s.cols - col));
                 const uint16_t* from = base + (bytes ? col : 0);
+                if (kb < num_kb) {
 #pragma unroll
                 for (int j = 0; j < kRows / kApart; ++j) {
                     const int at = __shfl_sync(0xffffffffu, src[kApart * j / 32], (kApart * j & 31) + q);
@@ -429,14 +464,15 @@ __global__ void __launch_bounds__(kGrThreads<LIST>, 1) grouped_kernel(const __gr
                     copy16(dst + to[j % (8 / kApart)] + j / (8 / kApart) * 1024, from + (there ? at : 0) * s.ld,
                            there ? bytes : 0u);
                 }
+                }
                 copy16_wait_all();
                 fence_proxy_async_shared();
                 __syncwarp();
                 if (lane == 0) {
                     if constexpr (PAIR)
-                        arrive_on_leader_release(smem_addr(&full[slot]));
+                        arrive_on_leader_release(smem_addr(&full[slot / BLOCKS]));
                     else
-                        mbar_arrive(smem_addr(&full[slot]));
+                        mbar_arrive(smem_addr(&full[slot / BLOCKS]));
                 }
                 slot += kListWarps;
                 if (slot >= SLOTS) {
@@ -444,20 +480,22 @@ __global__ void __launch_bounds__(kGrThreads<LIST>, 1) grouped_kernel(const __gr
                     phase ^= 1;
                 }
             }
-            wait = kb - num_kb;
+            wait = kb - all_kb;
         }
     } else if (warp == 1 && leader) {
         // ---------------------------------------------------- MMA issuer
-        int slot = 0;
+        int grp = 0;
         uint32_t phase = 0;
         bool ok = true;
         const uint32_t d_hi = smem_desc_hi_sw128(1024);
         const bool q_mn = WEIGHT || p.q_mn;
-        const uint32_t a_lo0 = smem_desc_lo(smem_addr(sA), WEIGHT ? 8192u : 16u);
-        const uint32_t b_lo0 = smem_desc_lo(smem_addr(sB), q_mn ? 8192u : 16u);
+        const uint32_t a_lo0 = smem_desc_lo(smem_addr(sA), WEIGHT ? kAtom : 16u);
+        const uint32_t b_lo0 = smem_desc_lo(smem_addr(sB), q_mn ? kAtom : 16u);
         constexpr uint32_t a_kstep = WEIGHT ? (2048u >> 4) : (32u >> 4);
+        constexpr uint32_t a_block = (WEIGHT ? 8192u : (uint32_t)TS::kAStage) >> 4;
         const uint32_t b_kstep = q_mn ? (2048u >> 4) : (32u >> 4);
-        GroupedItems<MODE> items(p, worker, workers, TS::kBM);
+        const uint32_t b_block = (q_mn ? 8192u : (uint32_t)TS::kBStage) >> 4;
+        GroupedItems<MODE> items(p, order, worker, workers, TS::kBM);
         GroupedItem it;
         for (int i = 0; ok && items.next(it); ++i) {
             const int num_kb = blocks_of(it);
@@ -466,22 +504,26 @@ __global__ void __launch_bounds__(kGrThreads<LIST>, 1) grouped_kernel(const __gr
                 ok = wait_bar(smem_addr(&tempty[buf]), ((i >> 1) & 1) ^ 1, w, DEV_TIMEOUT_MMA + 3);
                 tc_fence_after();
                 const uint32_t d_tmem = tmem_base + buf * BN;
-                for (int kb = 0; ok && kb < num_kb; ++kb) {
-                    ok = wait_bar(smem_addr(&full[slot]), phase, w, DEV_TIMEOUT_MMA + 4);
+                for (int kb = 0; ok && kb < num_kb; kb += BLOCKS) {
+                    ok = wait_bar(smem_addr(&full[grp]), phase, w, DEV_TIMEOUT_MMA + 4);
                     if (!ok) break;
                     tc_fence_after();
-                    const uint32_t a_lo = a_lo0 + (uint32_t)slot * (TS::kAStage >> 4);
-                    const uint32_t b_lo = b_lo0 + (uint32_t)slot * (TS::kBStage >> 4);
 #pragma unroll
-                    for (int kk = 0; kk < kBK / kUmmaK; ++kk)
-                        mma_f16<CG>(d_tmem, smem_desc_join(a_lo + kk * a_kstep, d_hi),
-                                    smem_desc_join(b_lo + kk * b_kstep, d_hi), p.idesc, kb != 0 || kk != 0);
+                    for (int j = 0; j < BLOCKS; ++j) {
+                        if (kb + j >= num_kb) break;
+                        const uint32_t a_lo = a_lo0 + (uint32_t)grp * (BLOCKS * TS::kAStage >> 4) + j * a_block;
+                        const uint32_t b_lo = b_lo0 + (uint32_t)grp * (BLOCKS * TS::kBStage >> 4) + j * b_block;
+#pragma unroll
+                        for (int kk = 0; kk < kBK / kUmmaK; ++kk)
+                            mma_f16<CG>(d_tmem, smem_desc_join(a_lo + kk * a_kstep, d_hi),
+                                        smem_desc_join(b_lo + kk * b_kstep, d_hi), p.idesc, kb + j != 0 || kk != 0);
+                    }
                     if constexpr (PAIR)
-                        mma_commit_pair(smem_addr(&empty[slot]), 0x3);
+                        mma_commit_pair(smem_addr(&empty[grp]), 0x3);
                     else
-                        mma_commit(smem_addr(&empty[slot]));
-                    if (++slot == SLOTS) {
-                        slot = 0;
+                        mma_commit(smem_addr(&empty[grp]));
+                    if (++grp == GROUPS) {
+                        grp = 0;
                         phase ^= 1;
                     }
                 }
@@ -513,7 +555,7 @@ __global__ void __launch_bounds__(kGrThreads<LIST>, 1) grouped_kernel(const __gr
         uint8_t* stage = staging + (warp - 2) * TS::kUnit;
         // 16 bytes of a staged row: 128-byte rows, units spread over the banks
         auto staged = [&](int r, int k) { return reinterpret_cast<uint4*>(stage + r * 128 + ((k ^ (r & 7)) << 4)); };
-        GroupedItems<MODE> items(p, worker, workers, TS::kBM);
+        GroupedItems<MODE> items(p, order, worker, workers, TS::kBM);
         GroupedItem it;
         for (int i = 0; items.next(it); ++i) {
             const int row0 = it.tm * TS::kBM + (int)rank * 128 + q * 32;  // this warp's first row, in its group or dB

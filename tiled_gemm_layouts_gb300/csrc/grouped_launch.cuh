@@ -10,9 +10,9 @@
 namespace tg {
 
 template <int MODE, int BN, bool PAIR, bool LIST>
-cudaError_t launch_grouped_tile(const GroupedParams& p, long long tiles, int sms, bool chained,
+cudaError_t launch_grouped_tile(const GroupedParams& p, long long tiles, int sms,
                                 cudaStream_t stream) {
-    using TS = GroupedShape<BN, PAIR>;
+    using TS = GroupedShape<MODE, BN, PAIR, LIST>;
     auto kern = grouped_kernel<MODE, BN, PAIR, LIST>;
     static std::atomic<unsigned long long> attr_set{0};  // one bit per device
     int dev = 0;
@@ -27,7 +27,7 @@ cudaError_t launch_grouped_tile(const GroupedParams& p, long long tiles, int sms
     const long long slots = PAIR ? sms / 2 : sms;
     const int workers = (int)(tiles < slots ? tiles : slots);
     cudaLaunchConfig_t lc = {};
-    cudaLaunchAttribute attr[2];
+    cudaLaunchAttribute attr[1];
     lc.gridDim = dim3(PAIR ? 2 * workers : workers, 1, 1);
     lc.blockDim = dim3(kGrThreads<LIST>, 1, 1);
     lc.dynamicSmemBytes = TS::kGrSmemBytes;
@@ -39,17 +39,11 @@ cudaError_t launch_grouped_tile(const GroupedParams& p, long long tiles, int sms
         attr[lc.numAttrs].val.clusterDim.z = 1;
         ++lc.numAttrs;
     }
-    if (chained) {
-        attr[lc.numAttrs].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-        attr[lc.numAttrs].val.programmaticStreamSerializationAllowed = 1;
-        ++lc.numAttrs;
-    }
     lc.attrs = attr;
     return cudaLaunchKernelEx(&lc, kern, p);
 }
 
 template <int MODE>
-cudaError_t launch_grouped_mode(const GroupedParams& p, GroupedTile tile, long long tiles, int sms,
-                                bool chained, cudaStream_t stream);
+cudaError_t launch_grouped_mode(const GroupedParams& p, GroupedTile tile, long long tiles, int sms, cudaStream_t stream);
 
 }  // namespace tg

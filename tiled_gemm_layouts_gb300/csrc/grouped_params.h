@@ -12,14 +12,14 @@ namespace tg {
 enum GroupedMode : int {
     GROUPED_ROWS = 0,    // Y[i] = epilogue(X[source(i)] B[g]): tiles of a group's rows
     GROUPED_WEIGHT = 1,  // dB[g] = X^T dY over a group's rows, or its transpose
-    GROUPED_LOW = 2,     // adapters: X A^T of each row, as two 16-bit parts and a scale
-    GROUPED_ADD = 3,     // adapters: Y += scale (low B^T), rows where they stand
 };
 
 // Rows of a 16-bit matrix, one after another or by a list of rows.
 struct GroupedRows {
-    CUtensorMap box;     // whole boxes of consecutive rows (no list)
+    CUtensorMap box;     // 64 columns of consecutive rows (no list)
+    CUtensorMap box2;    // GROUPED_ROWS: the same of two K-blocks, among the first `pairs`
     CUtensorMap gather;  // four rows of 64 columns, by their numbers
+    int pairs;
     const int* row;      // [R] or null: row i itself
     uint32_t magic;      // source row: row[i] / per_row = row[i] * magic >> shift
     int shift;
@@ -31,14 +31,13 @@ struct GroupedRows {
 
 struct alignas(128) GroupedParams {
     // GROUPED_WEIGHT: P holds the product's rows, Q its columns, both along their rows' columns.
-    // Else: P is X (or the low-rank rows), and map_q the matrices: {K, N, G} or {N, K, G}.
+    // Else: P is X, and map_q the matrices: {K, N, G} or {N, K, G}.
     GroupedRows p, q;
-    CUtensorMap map_q;
+    CUtensorMap map_q, map_q2;  // map_q2: two K-blocks at once, among the first q_pairs (K-major matrices)
+    int q_pairs;
     const int* offset;    // [groups + 1]
     int groups, rows;     // rows: R
     int num_kb;           // 64-deep K-blocks (not GROUPED_WEIGHT, whose rows are the depth)
-    int kb_wrap;          // K-blocks of one part of P: part k / kb_wrap starts so many parts of
-    int part_rows;        // this many rows further down, and the matrices start again
     int tiles_m, tiles_n; // tiles_m: GROUPED_WEIGHT only
     int group_m;          // raster: tile rows that share their columns' operand in turn
     int m, n;             // m: rows of a dB (GROUPED_WEIGHT); n: columns of the output
@@ -52,10 +51,6 @@ struct alignas(128) GroupedParams {
     int relu;
     const void* relu_of;        // [R] rows
     long long ld_relu;
-    const float* scale;         // GROUPED_LOW: [groups] or null
-    float* row_scale;           // [R]: written by GROUPED_LOW, read by GROUPED_ADD
-    const int* out_row;         // GROUPED_ADD: where row i of the product is added
-    int out_rows;               // of them
     // watchdog
     long long timeout_cycles;
     int* status;
@@ -66,11 +61,10 @@ struct alignas(128) GroupedParams {
 struct GroupedTile {
     int bn, pair, list;
     int rows() const { return pair ? 256 : 128; }
+    int blocks_rows() const { return pair && list ? 1 : 2; }  // K-blocks per transaction of GROUPED_ROWS
 };
 
-// `tiles`: the most tiles there can be.  `chained`: the launch may be
-// scheduled while the kernel before it still runs.
-cudaError_t launch_grouped(int mode, const GroupedParams& p, GroupedTile tile, long long tiles, int sms,
-                           bool chained, cudaStream_t stream);
+// `tiles`: the most tiles there can be.
+cudaError_t launch_grouped(int mode, const GroupedParams& p, GroupedTile tile, long long tiles, int sms, cudaStream_t stream);
 
 }  // namespace tg
