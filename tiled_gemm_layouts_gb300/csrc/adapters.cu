@@ -23,8 +23,11 @@
 // bits of bf16, 22 of fp16), after a power of two that brings the largest of a
 // row's values near 1, so that fp16 neither overflows nor underflows; sums are
 // fp32, and y is rounded once.
+#include <cooperative_groups.h>
+
 #include <algorithm>
 #include <cstring>
+#include <type_traits>
 
 #include "../../include/tilegemm.h"
 #include "chained.cuh"
@@ -71,19 +74,20 @@ __global__ void __launch_bounds__(kThreads) low_kernel(const AdapterParams p) {
     const RowTile tile = find_tile<kRows>(p.offset, p.G, p.T, blockIdx.x, lane);
     if (tile.g < 0) return;
     const int r0 = blockIdx.z * kRankPass;
-    // rows g, g + 8, g + 16, g + 24 of the tile
+    // rows g, g + 8, g + 16, g + 24 of the tile; what stands in for a row that is not
+    // there goes nowhere, and neither does what stands in for one of the rank
     const uint16_t* x[4];
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
         const int i = g + 8 * j;
         const int t = i < tile.rows ? p.row[tile.lo + i] : -1;
-        x[j] = t >= 0 && t < p.T ? p.x + (long long)t * p.ldx : nullptr;
+        x[j] = p.x + (t >= 0 && t < p.T ? (long long)t * p.ldx : 0) + 8 * q;
     }
     const uint16_t* a[NT];
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
         const int r = r0 + 8 * n + g;
-        a[n] = r < p.rank ? p.a + ((long long)tile.g * p.rank + r) * p.lda : nullptr;
+        a[n] = p.a + ((long long)tile.g * p.rank + (r < p.rank ? r : 0)) * p.lda + 8 * q;
     }
     float c[2][NT][4];
 #pragma unroll
@@ -93,28 +97,39 @@ __global__ void __launch_bounds__(kThreads) low_kernel(const AdapterParams p) {
 #pragma unroll
             for (int j = 0; j < 4; ++j) c[m][n][j] = 0.0f;
     const int k1 = min(p.K, (int)(blockIdx.y + 1) * p.split);
-    const bool second = tile.rows > 16;  // else its rows 16..31 are zeros
+    auto products = [&](int m, const uint4& x0, const uint4& x1, const uint4 (&av)[NT]) {
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+            mma<BF>(c[m][n], x0.x, x1.x, x0.y, x1.y, av[n].x, av[n].y);
+            mma<BF>(c[m][n], x0.z, x1.z, x0.w, x1.w, av[n].z, av[n].w);
+        }
+    };
+    const bool second = tile.rows > 16;  // else its rows 16..31 are none
     for (int k = blockIdx.y * p.split + warp * kStepK; k < k1; k += kWarps * kStepK) {
         uint4 xv[2][4], av[2][NT];
+        if (k + kStepK <= k1) {
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            const int at = k + 32 * h + 8 * q;
+            for (int h = 0; h < 2; ++h) {
 #pragma unroll
-            for (int j = 0; j < 4; ++j) xv[h][j] = x[j] ? load8(x[j], at, k1) : make_uint4(0, 0, 0, 0);
+                for (int j = 0; j < 4; ++j) xv[h][j] = *reinterpret_cast<const uint4*>(x[j] + k + 32 * h);
 #pragma unroll
-            for (int n = 0; n < NT; ++n) av[h][n] = a[n] ? load8(a[n], at, k1) : make_uint4(0, 0, 0, 0);
+                for (int n = 0; n < NT; ++n) av[h][n] = *reinterpret_cast<const uint4*>(a[n] + k + 32 * h);
+            }
+        } else {
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const int at = k + 32 * h;
+#pragma unroll
+                for (int j = 0; j < 4; ++j) xv[h][j] = load8(x[j] - 8 * q, at + 8 * q, k1);
+#pragma unroll
+                for (int n = 0; n < NT; ++n) av[h][n] = load8(a[n] - 8 * q, at + 8 * q, k1);
+            }
         }
 #pragma unroll
-        for (int h = 0; h < 2; ++h)
-#pragma unroll
-            for (int n = 0; n < NT; ++n) {
-                mma<BF>(c[0][n], xv[h][0].x, xv[h][1].x, xv[h][0].y, xv[h][1].y, av[h][n].x, av[h][n].y);
-                mma<BF>(c[0][n], xv[h][0].z, xv[h][1].z, xv[h][0].w, xv[h][1].w, av[h][n].z, av[h][n].w);
-                if (second) {
-                    mma<BF>(c[1][n], xv[h][2].x, xv[h][3].x, xv[h][2].y, xv[h][3].y, av[h][n].x, av[h][n].y);
-                    mma<BF>(c[1][n], xv[h][2].z, xv[h][3].z, xv[h][2].w, xv[h][3].w, av[h][n].z, av[h][n].w);
-                }
-            }
+        for (int h = 0; h < 2; ++h) {
+            products(0, xv[h][0], xv[h][1], av[h]);
+            if (second) products(1, xv[h][2], xv[h][3], av[h]);
+        }
     }
     // the warps' sums, half of them to the other half, three times
 #pragma unroll
@@ -148,12 +163,17 @@ __global__ void __launch_bounds__(kThreads) low_kernel(const AdapterParams p) {
             float* out = p.low + ((long long)blockIdx.y * p.T + tile.lo + i) * p.pitch + r0 + 2 * q;
 #pragma unroll
             for (int n = 0; n < NT; ++n)
-                if (r0 + 8 * n < p.pitch) *reinterpret_cast<float2*>(out + 8 * n) = make_float2(c[m][n][2 * h], c[m][n][2 * h + 1]);
+                if (r0 + 8 * n < p.pitch) {
+                    const int r = r0 + 8 * n + 2 * q;  // (0 from the rank on)
+                    *reinterpret_cast<float2*>(out + 8 * n) =
+                        make_float2(r < p.rank ? c[m][n][2 * h] : 0.0f, r + 1 < p.rank ? c[m][n][2 * h + 1] : 0.0f);
+                }
         }
 }
 
-// y: grid (tiles, chunks of N).  KC: fragments of 16 of the rank.
-template <bool BF, int KC>
+// y: grid (tiles, chunks of N).  KC: fragments of 16 of the rank.  TAIL: the last
+// of them is not whole.  The next 32 columns' loads run beside this 32's products.
+template <bool BF, int KC, bool TAIL>
 __global__ void __launch_bounds__(kThreads) add_kernel(const AdapterParams p) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, q = lane & 3;
     const RowTile tile = find_tile<kRows>(p.offset, p.G, p.T, blockIdx.x, lane);
@@ -165,7 +185,7 @@ __global__ void __launch_bounds__(kThreads) add_kernel(const AdapterParams p) {
         const int t = i < tile.rows ? p.row[tile.lo + i] : -1;
         y[j] = t >= 0 && t < p.T ? p.y + (long long)t * p.ldy : nullptr;
     }
-    const float s = p.scale ? p.scale[tile.g] : 1.0f;
+    const float scale = p.scale ? p.scale[tile.g] : 1.0f;
     wait_for_previous_kernel();
     // u of rows g, g + 8, g + 16, g + 24, columns 16 c + 4q .. + 3, as two parts
     uint32_t hi[4][KC][2], lo[4][KC][2];
@@ -190,11 +210,11 @@ __global__ void __launch_bounds__(kThreads) add_kernel(const AdapterParams p) {
         top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
         // 2^-e with 2^e <= top < 2^(e+1); rows of zeros, or with an infinity, as they are
         float down = 1.0f;
-        factor[j] = s;
+        factor[j] = scale;
         if (top > 0x1p-100f && top < 0x1p100f) {
             const uint32_t e = __float_as_uint(top) & 0x7F800000u;
             down = __uint_as_float(0x7F000000u - e);
-            factor[j] = s * __uint_as_float(e);
+            factor[j] = scale * __uint_as_float(e);
         }
 #pragma unroll
         for (int c = 0; c < KC; ++c)
@@ -214,45 +234,52 @@ __global__ void __launch_bounds__(kThreads) add_kernel(const AdapterParams p) {
             }
     }
     const bool second = tile.rows > 16;
-    const uint16_t* bg = p.b + (long long)tile.g * p.N * p.ldb;
     const int end = min(p.N, (int)(blockIdx.y + 1) * p.chunk);
-    for (int n0 = blockIdx.y * p.chunk + warp * 32; n0 < end; n0 += kWarps * 32) {
-        const int n = n0 + 8 * q;  // this lane's columns of y
+    // 32 columns of y from n0 on: fragment f's column c is n0 + 8 (c / 2) + 2 f + c % 2,
+    // so that this lane's are n0 + 8q .. n0 + 8q + 7
+    struct Step {
         uint4 old[4];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) old[j] = y[j] ? load8(y[j], n, p.N) : make_uint4(0, 0, 0, 0);
-        // fragment f's column c is y's n0 + 8 (c / 2) + 2 f + c % 2
         uint2 b[4][KC];
+    };
+    const uint16_t* bg = p.b + (long long)tile.g * p.N * p.ldb + 4 * q;
+    auto load = [&](Step& s, int n0) {
+        const int n = n0 + 8 * q;
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            s.old[j] = !y[j] ? make_uint4(0, 0, 0, 0) : n + 8 <= p.N ? *reinterpret_cast<const uint4*>(y[j] + n) : load8(y[j], n, p.N);
 #pragma unroll
         for (int f = 0; f < 4; ++f) {
-            const int col = n0 + 8 * (g >> 1) + 2 * f + (g & 1);
-            const uint16_t* row = bg + (long long)col * p.ldb;
+            // (a column behind the last goes nowhere)
+            const uint16_t* row = bg + (long long)min(p.N - 1, n0 + 8 * (g >> 1) + 2 * f + (g & 1)) * p.ldb;
 #pragma unroll
-            for (int c = 0; c < KC; ++c) b[f][c] = col < p.N ? load4(row, 16 * c + 4 * q, p.rank) : make_uint2(0, 0);
+            for (int c = 0; c < KC; ++c)
+                s.b[f][c] = TAIL ? load4(row - 4 * q, 16 * c + 4 * q, p.rank) : *reinterpret_cast<const uint2*>(row + 16 * c);
         }
-        float acc[2][4][4];
+    };
+    auto finish = [&](const Step& s, int n0, auto m) {
+        constexpr int M = decltype(m)::value;  // rows g + 16 M and 8 more
+        const int n = n0 + 8 * q;
+        float acc[4][4];
 #pragma unroll
-        for (int m = 0; m < 2; ++m)
+        for (int f = 0; f < 4; ++f) {
 #pragma unroll
-            for (int f = 0; f < 4; ++f) {
+            for (int j = 0; j < 4; ++j) acc[f][j] = 0.0f;
 #pragma unroll
-                for (int j = 0; j < 4; ++j) acc[m][f][j] = 0.0f;
-                if (m && !second) continue;
-#pragma unroll
-                for (int c = 0; c < KC; ++c) {
-                    mma<BF>(acc[m][f], lo[2 * m][c][0], lo[2 * m + 1][c][0], lo[2 * m][c][1], lo[2 * m + 1][c][1], b[f][c].x, b[f][c].y);
-                    mma<BF>(acc[m][f], hi[2 * m][c][0], hi[2 * m + 1][c][0], hi[2 * m][c][1], hi[2 * m + 1][c][1], b[f][c].x, b[f][c].y);
-                }
+            for (int c = 0; c < KC; ++c) {
+                mma<BF>(acc[f], lo[2 * M][c][0], lo[2 * M + 1][c][0], lo[2 * M][c][1], lo[2 * M + 1][c][1], s.b[f][c].x, s.b[f][c].y);
+                mma<BF>(acc[f], hi[2 * M][c][0], hi[2 * M + 1][c][0], hi[2 * M][c][1], hi[2 * M + 1][c][1], s.b[f][c].x, s.b[f][c].y);
             }
+        }
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            if (!y[j] || n >= p.N) continue;
-            const uint32_t w[4] = {old[j].x, old[j].y, old[j].z, old[j].w};
+        for (int h = 0; h < 2; ++h) {
+            const int j = 2 * M + h;
+            const uint32_t w[4] = {s.old[j].x, s.old[j].y, s.old[j].z, s.old[j].w};
             uint32_t o[4];
 #pragma unroll
             for (int f = 0; f < 4; ++f)
-                o[f] = narrow2<BF>(fmaf(factor[j], acc[j / 2][f][2 * (j & 1)], wide<BF>((uint16_t)(w[f] & 0xFFFFu))),
-                                   fmaf(factor[j], acc[j / 2][f][2 * (j & 1) + 1], wide<BF>((uint16_t)(w[f] >> 16))));
+                o[f] = narrow2<BF>(fmaf(factor[j], acc[f][2 * h], wide<BF>((uint16_t)(w[f] & 0xFFFFu))),
+                                   fmaf(factor[j], acc[f][2 * h + 1], wide<BF>((uint16_t)(w[f] >> 16))));
+            if (!y[j] || n >= p.N) continue;
             if (n + 8 <= p.N) {
                 *reinterpret_cast<uint4*>(y[j] + n) = make_uint4(o[0], o[1], o[2], o[3]);
             } else {
@@ -261,17 +288,34 @@ __global__ void __launch_bounds__(kThreads) add_kernel(const AdapterParams p) {
                     if (n + x < p.N) y[j][n + x] = (uint16_t)(o[x / 2] >> (x & 1) * 16);
             }
         }
+    };
+    constexpr int kAhead = kWarps * 32;
+    int n0 = blockIdx.y * p.chunk + warp * 32;
+    if (n0 >= end) return;
+    Step s, next;
+    load(s, n0);
+    for (; n0 < end; n0 += kAhead) {
+        if (KC <= 2 && n0 + kAhead < end) load(next, n0 + kAhead);
+        finish(s, n0, std::integral_constant<int, 0>{});
+        if (second) finish(s, n0, std::integral_constant<int, 1>{});
+        if (KC <= 2)
+            s = next;
+        else if (n0 + kAhead < end)
+            load(s, n0 + kAhead);
     }
 }
 
-// ------------------------------------------------- few rows: a block per row
+// ------------------------------------------- few rows: a cluster per row
 //
 // A decoder's batch: bound by latency and by reading A and B (64 rows, each with
-// an adapter of its own of rank 16 between 4096 columns: 16.8 MB).  The first
-// kernel cuts a row's columns into pieces, one per block; a warp sums a piece's
-// products for some of the rank.  The second adds the pieces up and gives
-// every column of y to one thread, whose row of B lies beside its neighbours' in
-// memory.  fp32 throughout.
+// an adapter of its own of rank 16 between 4096 columns: 16.8 MB).  The eight
+// blocks of a cluster share a row's columns; a warp sums a piece's products for some
+// of the rank, the pieces' sums meet through the cluster's shared memory, and
+// every column of y belongs to one thread, whose row of B lies beside its
+// neighbours' in memory and was asked for at the start.  fp32 throughout, one
+// launch, no workspace.  (64 rows: @CLUSTER@; as two kernels 10.3.)
+
+constexpr int kCluster = 8;
 
 // sum += a . b over 8 columns, those from `left` on left out
 template <bool BF>
@@ -304,18 +348,24 @@ __device__ __forceinline__ int group_of(const AdapterParams& p, int i, int lane)
 }
 
 template <bool BF>
-__global__ void __launch_bounds__(kThreads) few_low_kernel(const AdapterParams p) {
-    allow_next_kernel();
+__global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads) few_kernel(const __grid_constant__ AdapterParams p) {
+    __shared__ float part[kMaxRank], low[kMaxRank];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int i = blockIdx.y;
+    const int i = blockIdx.y, self = blockIdx.x;
     const int g = group_of(p, i, lane);
     const int t = p.row[i];
-    if (g < 0 || t < 0 || t >= p.T) return;
-    const int k0 = blockIdx.x * p.split, k1 = min(p.K, k0 + p.split);
+    if (g < 0 || t < 0 || t >= p.T) return;  // (every block of the cluster)
+    // this block's columns of y: their rows of B are on their way while u is computed
+    const int n0 = self * p.chunk, n1 = min(p.N, n0 + p.chunk);
+    const uint16_t* b = p.b + (long long)g * p.N * p.ldb;
+    for (int n = n0 + threadIdx.x; n < n1; n += kThreads)
+        for (int r = 0; r < p.rank; r += 64)
+            asm volatile("prefetch.global.L2 [%0];" ::"l"(b + (long long)n * p.ldb + r));
+    const int k0 = self * p.split, k1 = min(p.K, k0 + p.split);
     const uint16_t* x = p.x + (long long)t * p.ldx;
     const uint16_t* a = p.a + (long long)g * p.rank * p.lda;
     constexpr int kTogether = 4;  // of the rank, so that their loads are in flight together
-    for (int r0 = warp * kTogether; r0 < p.rank; r0 += kThreads / 32 * kTogether) {
+    for (int r0 = warp * kTogether; r0 < p.rank; r0 += kWarps * kTogether) {
         float sum[kTogether] = {0.0f, 0.0f, 0.0f, 0.0f};
         for (int k = k0 + 8 * lane; k < k1; k += 256) {
             const uint4 xv = *reinterpret_cast<const uint4*>(x + k);
@@ -328,44 +378,36 @@ __global__ void __launch_bounds__(kThreads) few_low_kernel(const AdapterParams p
         for (int j = 0; j < kTogether; ++j) {
 #pragma unroll
             for (int d = 16; d; d >>= 1) sum[j] += __shfl_xor_sync(0xffffffffu, sum[j], d);
-            if (lane == 0 && r0 + j < p.rank)
-                p.low[((long long)i * p.splits + blockIdx.x) * p.pitch + r0 + j] = sum[j];
+            if (lane == 0 && r0 + j < p.rank) part[r0 + j] = sum[j];
         }
     }
-}
-
-template <bool BF>
-__global__ void __launch_bounds__(kThreads) few_add_kernel(const AdapterParams p) {
-    __shared__ float low[kMaxRank];
-    const int i = blockIdx.y;
-    const int g = group_of(p, i, threadIdx.x & 31);
-    const int t = p.row[i];
-    if (g < 0 || t < 0 || t >= p.T) return;
-    wait_for_previous_kernel();
-    const float* part = p.low + (long long)i * p.splits * p.pitch;
+    auto cluster = cooperative_groups::this_cluster();
+    cluster.sync();
     for (int r = threadIdx.x; r < (int)kMaxRank; r += kThreads) {
         float sum = 0.0f;
         if (r < p.rank)
-            for (int k = 0; k < p.splits; ++k) sum += part[k * p.pitch + r];
+#pragma unroll
+            for (int k = 0; k < kCluster; ++k) sum += cluster.map_shared_rank(part, k)[r];
         low[r] = sum;
     }
     __syncthreads();
     const float s = p.scale ? p.scale[g] : 1.0f;
-    for (int n = blockIdx.x * kThreads + threadIdx.x; n < p.N; n += gridDim.x * kThreads) {
-        const uint16_t* b = p.b + ((long long)g * p.N + n) * p.ldb;
+    for (int n = n0 + threadIdx.x; n < n1; n += kThreads) {
+        const uint16_t* row = b + (long long)n * p.ldb;
         uint16_t* y = p.y + (long long)t * p.ldy + n;
         float sum = 0.0f;
         for (int r = 0; r < p.rank; r += 8) {
-            const uint4 v = *reinterpret_cast<const uint4*>(b + r);
+            const uint4 v = *reinterpret_cast<const uint4*>(row + r);
             const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
-                const float x = wide<BF>((uint16_t)(w[j / 2] >> ((j & 1) * 16)));
-                if (r + j < p.rank) sum = fmaf(x, low[r + j], sum);
+                const float f = wide<BF>((uint16_t)(w[j / 2] >> ((j & 1) * 16)));
+                if (r + j < p.rank) sum = fmaf(f, low[r + j], sum);
             }
         }
         *y = narrow<BF>(fmaf(s, sum, wide<BF>(*y)));
     }
+    cluster.sync();  // no block leaves while another may read its sums
 }
 
 // Blocks of one row against tiles of 32 (rank 16, 4096 columns, us): 64 rows of 64
@@ -374,10 +416,8 @@ bool few_rows(int64_t T, int64_t G) { return T <= kFewRows || T < 4 * G; }
 
 int64_t tiles_of(int64_t T, int64_t G) { return std::min(T, G) + T / kRows; }
 
-// Splits of K: about 1024 blocks of at least 256 columns for few rows, else about
-// 512 of at least one step of all warps.
+// Splits of K: about 512 blocks of at least one step of all warps.
 int splits_of(int64_t T, int64_t G, int64_t K) {
-    if (few_rows(T, G)) return (int)std::max<int64_t>(1, std::min<int64_t>((K + 255) / 256, std::min<int64_t>(kMaxSplits, 1024 / T)));
     const int64_t most = (K + kWarps * kStepK - 1) / (kWarps * kStepK);
     const int64_t wanted = (512 + tiles_of(T, G) - 1) / tiles_of(T, G);
     return (int)std::max<int64_t>(1, std::min<int64_t>(std::min(most, wanted), kMaxSplits));
@@ -396,10 +436,13 @@ cudaError_t launch_low(const AdapterParams& p, dim3 grid, cudaStream_t stream) {
 }
 template <bool BF>
 cudaError_t launch_add(const AdapterParams& p, dim3 grid, cudaStream_t stream) {
-    if (p.rank <= 16) return launch_chained(add_kernel<BF, 1>, grid, kThreads, stream, p);
-    if (p.rank <= 32) return launch_chained(add_kernel<BF, 2>, grid, kThreads, stream, p);
-    if (p.rank <= 64) return launch_chained(add_kernel<BF, 4>, grid, kThreads, stream, p);
-    return launch_chained(add_kernel<BF, 8>, grid, kThreads, stream, p);
+    // (fragments that the rank does not reach have no elements of B)
+    const bool whole = p.rank == 16 || p.rank == 32 || p.rank == 64 || p.rank == 128;
+    auto pick = [&](auto full, auto tail) { return launch_chained(whole ? full : tail, grid, kThreads, stream, p); };
+    if (p.rank <= 16) return pick(add_kernel<BF, 1, false>, add_kernel<BF, 1, true>);
+    if (p.rank <= 32) return pick(add_kernel<BF, 2, false>, add_kernel<BF, 2, true>);
+    if (p.rank <= 64) return pick(add_kernel<BF, 4, false>, add_kernel<BF, 4, true>);
+    return pick(add_kernel<BF, 8, false>, add_kernel<BF, 8, true>);
 }
 
 int check_sizes(int64_t T, int64_t N, int64_t K, int64_t rank, int64_t G, int dtype) {
@@ -411,6 +454,7 @@ int check_sizes(int64_t T, int64_t N, int64_t K, int64_t rank, int64_t G, int dt
 }
 
 size_t workspace_of(int64_t T, int64_t G, int64_t K, int64_t rank) {
+    if (few_rows(T, G)) return 0;
     return (size_t)T * (size_t)splits_of(T, G, K) * (size_t)pitch_of(rank) * sizeof(float);
 }
 
@@ -434,14 +478,16 @@ extern "C" int tg_adapters(int64_t T, int64_t N, int64_t K, int64_t rank, int64_
                            size_t workspace_bytes, cudaStream_t stream) {
     int rc = check_sizes(T, N, K, rank, G, (int)dtype);
     if (rc) return rc;
-    if (!X || !row || !offset || !A || !B || !Y || !workspace) return TG_ERR_INVALID_ARG;
+    if (!X || !row || !offset || !A || !B || !Y) return TG_ERR_INVALID_ARG;
+    const size_t need = workspace_of(T, G, K, rank);
+    if (need && !workspace) return TG_ERR_INVALID_ARG;
+    if (!need) workspace = nullptr;
     if (ldx < K || lda < K || ldb < rank || ldy < N || ldx > kMaxLd || lda > kMaxLd || ldb > kMaxLd || ldy > kMaxLd)
         return TG_ERR_STRIDE;
     auto off = [](const void* p, unsigned bytes) { return (reinterpret_cast<uintptr_t>(p) & (bytes - 1)) != 0; };
     if (!aligned16(X) || !aligned16(A) || !aligned16(B) || !aligned16(Y) || ldx % 8 || lda % 8 || ldb % 8 || ldy % 8 ||
         off(row, 4) || off(offset, 4) || off(scale, 4) || off(workspace, 256))
         return TG_ERR_ALIGN;
-    const size_t need = workspace_of(T, G, K, rank);
     if (workspace_bytes < need) return TG_ERR_BUFFER;
     // (G * rank rows of A and G * N of B, one after another)
     const void* ptrs[8] = {Y, workspace, X, A, B, row, offset, scale};
@@ -475,32 +521,25 @@ extern "C" int tg_adapters(int64_t T, int64_t N, int64_t K, int64_t rank, int64_
     p.scale = scale;
     p.y = static_cast<uint16_t*>(Y);
     p.ldy = ldy;
+    if (few_rows(T, G)) {
+        p.split = (int)((K + kCluster * 8 - 1) / (kCluster * 8) * 8);
+        p.chunk = (int)((N + kCluster - 1) / kCluster);
+        const dim3 grid(kCluster, (unsigned)T, 1);
+        if (dtype == TG_BF16)
+            few_kernel<true><<<grid, kThreads, 0, stream>>>(p);
+        else
+            few_kernel<false><<<grid, kThreads, 0, stream>>>(p);
+        if (cudaGetLastError() != cudaSuccess) return TG_ERR_CUDA;
+        return TG_OK;
+    }
     p.splits = splits_of(T, G, K);
-    const int64_t step = few_rows(T, G) ? 256 : kStepK;
-    p.split = (int)((K + p.splits * step - 1) / (p.splits * step) * step);
+    p.split = (int)((K + (int64_t)p.splits * kStepK - 1) / ((int64_t)p.splits * kStepK) * kStepK);
     p.splits = (int)((K + p.split - 1) / p.split);
     p.pitch = (int)pitch_of(rank);
     p.low = static_cast<float*>(workspace);
-    if (few_rows(T, G)) {
-        const dim3 low((unsigned)p.splits, (unsigned)T, 1);
-        const dim3 add((unsigned)std::min<int64_t>((N + kThreads - 1) / kThreads, 1024), (unsigned)T, 1);
-        if (dtype == TG_BF16)
-            few_low_kernel<true><<<low, kThreads, 0, stream>>>(p);
-        else
-            few_low_kernel<false><<<low, kThreads, 0, stream>>>(p);
-        cudaError_t e = cudaGetLastError();
-        if (e == cudaSuccess)
-            e = dtype == TG_BF16 ? launch_chained(few_add_kernel<true>, add, kThreads, stream, p)
-                                 : launch_chained(few_add_kernel<false>, add, kThreads, stream, p);
-        if (e != cudaSuccess) {
-            cudaGetLastError();
-            return TG_ERR_CUDA;
-        }
-        return TG_OK;
-    }
-    // columns of y per block: few enough for two blocks per SM, at most 1024
+    // columns of y per block: few enough for two blocks per SM, at most 2048
     const int64_t tiles = tiles_of(T, G);
-    int64_t chunks = std::max<int64_t>((N + 1023) / 1024, std::min<int64_t>((N + 255) / 256, (2LL * info->sms + tiles - 1) / tiles));
+    int64_t chunks = std::max<int64_t>((N + 2047) / 2048, std::min<int64_t>((N + 255) / 256, (2LL * info->sms + tiles - 1) / tiles));
     p.chunk = (int)((N + chunks * 256 - 1) / (chunks * 256) * 256);
     chunks = (N + p.chunk - 1) / p.chunk;
     if (chunks > 65535) return TG_ERR_INVALID_ARG;

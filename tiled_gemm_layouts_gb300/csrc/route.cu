@@ -130,10 +130,16 @@ __device__ __noinline__ RowMass row_mass(const RouteParams& p, const IN* row, in
     if (p.sigmoid) return r;
     for (int e = lane; e < p.E; e += 32) r.top = fmaxf(r.top, load_one(row + e));
     r.top = warp_fmax(r.top);
+    // (four at a time: a double operation's latency is far above its rate)
 #pragma unroll 1
-    for (int e = lane; e < p.E; e += 32) {
-        const float l = load_one(row + e);
-        if (l > -INFINITY) r.sum += l == r.top ? 1.0 : exp((double)l - r.top);  // (of +inf: the limit)
+    for (int e0 = lane; e0 < p.E; e0 += 128) {
+        double m[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const float l = e0 + 32 * j < p.E ? load_one(row + e0 + 32 * j) : -INFINITY;
+            m[j] = !(l > -INFINITY) ? 0.0 : l == r.top ? 1.0 : exp((double)l - r.top);  // (of +inf: the limit)
+        }
+        r.sum += (m[0] + m[1]) + (m[2] + m[3]);
     }
     r.sum = warp_sum(r.sum);
     return r;
@@ -213,7 +219,7 @@ __host__ __device__ inline int warp_words(int E, int C, int lanes, int k) {
 }
 
 // C: most experts of a lane.
-template <class IN, int C>
+template <class IN, int C, bool SIGMOID>
 __global__ void __launch_bounds__(32 * kWarps) route_kernel(const __grid_constant__ RouteParams p) {
     constexpr int Q = C / 4;
     extern __shared__ float4 shared_words[];
@@ -236,7 +242,7 @@ __global__ void __launch_bounds__(32 * kWarps) route_kernel(const __grid_constan
     int* chosen = candidates - 2 * tokens * p.k;
     float* chosen_key = reinterpret_cast<float*>(chosen + tokens * p.k);
     const bool by_score = p.bias || p.top == 2;  // a group's key
-    const bool scores = p.bias || (p.groups > 1 && p.top == 2) || (!p.sigmoid && !p.renorm);
+    const bool scores = p.bias || (p.groups > 1 && p.top == 2) || (!SIGMOID && !p.renorm);
     float largest_bias = 0.0f;
     if (p.bias || !p.whole) {
         for (int e = threadIdx.x; e < p.E; e += 32 * kWarps) {
@@ -260,14 +266,18 @@ __global__ void __launch_bounds__(32 * kWarps) route_kernel(const __grid_constan
     // exponential's argument x is off by 2^-24 |x| and its value by 2^-22, times
     // a slope s (1 - s); sum and quotient 2^-23), of a softmax's share (the same
     // where it is large, and a sum of up to 23 steps); and of a rounded sum of score and bias.
-    const float kScoreError = p.sigmoid ? 0x1p-21f : 0x1p-19f;
+    const float kScoreError = SIGMOID ? 0x1p-21f : 0x1p-19f;
     constexpr float kSumError = 0x1p-23f;
     auto token_max = [&](float x) {
-        for (int d = 1; d < L; d *= 2) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, d));
+#pragma unroll
+        for (int d = 1; d < 32; d *= 2)
+            if (d < L) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, d));
         return x;
     };
     auto token_sum = [&](float x) {
-        for (int d = 1; d < L; d *= 2) x += __shfl_xor_sync(0xffffffffu, x, d);
+#pragma unroll
+        for (int d = 1; d < 32; d *= 2)
+            if (d < L) x += __shfl_xor_sync(0xffffffffu, x, d);
         return x;
     };
     // a lane's run, four experts at a time
@@ -324,7 +334,7 @@ __global__ void __launch_bounds__(32 * kWarps) route_kernel(const __grid_constan
             });
         }
         spoilt = (__ballot_sync(0xffffffffu, spoilt) & of_token) != 0;
-        if (scores && !p.sigmoid) {
+        if (scores && !SIGMOID) {
             top = token_max(top);
             sum = 0.0f;
             // (of +inf: the limit)
@@ -334,10 +344,10 @@ __global__ void __launch_bounds__(32 * kWarps) route_kernel(const __grid_constan
         }
         const float inverse = 1.0f / sum;
         auto score = [&](float x) {
-            return p.sigmoid ? reciprocal(1.0f + power(-x)) : x == top ? inverse : expf(x - top) * inverse;
+            return SIGMOID ? reciprocal(1.0f + power(-x)) : x == top ? inverse : expf(x - top) * inverse;
         };
         // of one key
-        const float error = (kScoreError + kSumError) * (p.sigmoid ? 1.0f : inverse) + kSumError * largest_bias + 1e-30f;
+        const float error = (kScoreError + kSumError) * (SIGMOID ? 1.0f : inverse) + kSumError * largest_bias + 1e-30f;
         // the largest two of the lane's keys (without a bias: logits, which order as scores do)
         float one = -INFINITY, two = -INFINITY;
         auto rank = [&](float v) {
@@ -408,25 +418,39 @@ __global__ void __launch_bounds__(32 * kWarps) route_kernel(const __grid_constan
                 const int of = (__ffs(left) - 1) / (unsigned)L;
                 left &= ~((L == 32 ? 0xffffffffu : (1u << L) - 1u) << (of * L));
                 const RowMass r = row_mass<IN>(p, static_cast<const IN*>(p.logits) + (first + of < p.T ? first + of : first) * p.ld, lane);
-                // the lane's experts that may be among its group's largest, in 64 bits
-                double a = -INFINITY, b = -INFINITY;
+                // the experts that may be among their groups' largest, one per lane, in 64 bits
+                if (lane == 0) candidates[0] = 0;
+                __syncwarp();
                 if (token == of && one > -INFINITY) {
                     const float limit = (p.top == 2 ? two : one) - (p.bias ? 2.0f * error : 0.0f);
-                    int number = 0;
-                    for (int i = 0; i < n; ++i) {
-                        const float x = reinterpret_cast<const float*>(&keys[four(i >> 2, lane)])[i & 3];
-                        if (x == -INFINITY || !(x >= limit)) continue;
-                        if (++number > 4) break;
-                        const double v = wide_key(p, load_one(row + e0 + i), p.bias ? p.bias[e0 + i] : 0.0f, r);
-                        if (v > a) {
-                            b = a;
-                            a = v;
-                        } else if (v > b) {
-                            b = v;
-                        }
-                    }
-                    wide = number > 4;
+                    each([&](int q, float4 v) {
+                        const float x[4] = {v.x, v.y, v.z, v.w};
+                        for (int i = 0; i < 4; ++i)
+                            if (4 * q + i < n && x[i] > -INFINITY && x[i] >= limit) {
+                                const int at = atomicAdd(candidates, 1);
+                                if (at < 32) candidates[1 + at] = e0 + 4 * q + i;
+                            }
+                    });
                 }
+                __syncwarp();
+                const int number = candidates[0];
+                if (number > 32) {
+                    wide |= token == of;
+                    __syncwarp();
+                    continue;
+                }
+                const int e = lane < number ? candidates[1 + lane] : 0;
+                const IN* its_row = static_cast<const IN*>(p.logits) + (first + of < p.T ? first + of : first) * p.ld;
+                const double key = lane < number ? wide_key(p, load_one(its_row + e), p.bias ? p.bias[e] : 0.0f, r) : -INFINITY;
+                double a = -INFINITY, b = -INFINITY;
+                for (int o = 0; o < number; ++o) {
+                    const double v = __shfl_sync(0xffffffffu, key, o);
+                    const int its_e = __shfl_sync(0xffffffffu, e, o);
+                    if (n == 0 || its_e < e0 || its_e >= e0 + n) continue;  // another lane's
+                    b = v > a ? a : v > b ? v : b;
+                    a = v > a ? v : a;
+                }
+                __syncwarp();
                 of_group(a, b);
                 const bool now = is_kept(value_of(a, b));
                 if (token == of) kept = now;
@@ -543,12 +567,12 @@ __global__ void __launch_bounds__(32 * kWarps) route_kernel(const __grid_constan
         // weights: a lane takes every L-th of its token's
         float m = -INFINITY, total = 0.0f;
         auto form = [&](float logit) {  // a sigmoid's are exp(-m) too large, with one m for all
-            return !p.sigmoid ? expf(logit - m) : logit > 0.0f ? sigmoid(logit) : expf(logit - m) / (1.0f + expf(logit));
+            return !SIGMOID ? expf(logit - m) : logit > 0.0f ? sigmoid(logit) : expf(logit - m) / (1.0f + expf(logit));
         };
         if (p.renorm) {
             for (int j = in_token; j < found; j += L) m = fmaxf(m, load_one(row + mine[j]));
             m = token_max(m);
-            if (p.sigmoid) m = fminf(m, 0.0f);
+            if (SIGMOID) m = fminf(m, 0.0f);
             for (int j = in_token; j < found; j += L) total += form(load_one(row + mine[j]));
             total = token_sum(total);
         }
@@ -559,8 +583,8 @@ __global__ void __launch_bounds__(32 * kWarps) route_kernel(const __grid_constan
                 if (j < found) {
                     e = mine[j];
                     const float logit = load_one(row + e);
-                    w = p.renorm ? form(logit) / total : p.sigmoid ? sigmoid(logit) : expf(logit - top) / sum;
-                    if (!p.sigmoid && spoilt) w = NAN;
+                    w = p.renorm ? form(logit) / total : SIGMOID ? sigmoid(logit) : expf(logit - top) / sum;
+                    if (!SIGMOID && spoilt) w = NAN;
                 }
                 p.index[t * p.k + j] = e;
                 p.weight[t * p.k + j] = w * p.scale;
@@ -657,7 +681,7 @@ cudaError_t launch_route(const RouteParams& p, int sms, cudaStream_t stream) {
     // about as many as are resident: what a warp sets up is shared by its tokens
     const unsigned grid = (unsigned)(blocks < 6LL * sms ? blocks : 6LL * sms);
     const int bytes = 4 * (((block_words(p.E, C) + 3) & ~3) + kWarps * warp_words(p.E, C, p.lanes, p.k));
-    auto kern = route_kernel<IN, C>;
+    auto kern = p.sigmoid ? route_kernel<IN, C, true> : route_kernel<IN, C, false>;
     if (bytes > 48 * 1024) {
         const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
         if (e != cudaSuccess) return e;
@@ -719,8 +743,10 @@ RouteParams params_of(int64_t T, int64_t E, const tg_route_options& o) {
     p.kept = o.groups_kept;
     p.top = o.group_top;
     p.size = (int)(E / o.groups);
-    // runs of at most 32 experts, or of 64: then 32 lanes hold any 1024 experts in 32 groups
-    for (int most = 32; most <= 64; most *= 2) {
+    // Short runs while every token finds a warp of its own at once (one token of 256
+    // experts: @RUN@ us in runs of 8, of 32), then of at most 32 experts, or of 64: with
+    // that 32 lanes hold any 1024 experts in 32 groups.
+    for (int most = T <= 2048 ? 8 : 32; most <= 64; most *= 2) {
         p.parts = (p.size + most - 1) / most;
         if (p.groups * p.parts <= 32) break;
     }
