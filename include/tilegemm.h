@@ -589,8 +589,7 @@ int tg_combine_grad(int64_t T, int64_t k, int64_t D, const void* dout, int64_t l
  * The rank-wide products are kept to about twice 16 bits' precision, and Y
  * is rounded once.  rank <= 128; dtype fp16 or bf16; 16-byte-aligned
  * pointers and strides (else TG_ERR_ALIGN); T, N, K <= 2^30, G <= 4096.
- * workspace: tg_adapters_workspace_size() bytes (none for few rows).  One kernel
- * launch for few rows (up to 64, or fewer than four per adapter), else two.
+ * workspace: tg_adapters_workspace_size() bytes.  Two kernel launches.
  */
 int tg_adapters(int64_t T, int64_t N, int64_t K, int64_t rank, int64_t G, const void* X, int64_t ldx,
                 const int32_t* row, const int32_t* offset, const void* A, int64_t lda, const void* B,

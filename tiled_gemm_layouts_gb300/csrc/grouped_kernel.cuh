@@ -18,14 +18,16 @@
 //
 // Rows by a list are fetched where they stand; no gathered copy of X is
 // written (at 65536 rows of 4096 columns that would be 1.07 GB more traffic).
-// With LIST five warps of their own fetch them, 16 bytes per thread and
-// asynchronous copy, into the swizzled layout that a box would have.  Without LIST the producer warp uses gathering TMA copies, four
-// row numbers each.  Those take about 80 cycles of the copy engine for 512 bytes,
-// and a stage of 128 rows 2600 where its products take 512 (65536 rows, 64
-// groups, 4096 x 1024: 464 TFLOP/s, by the five warps 1520), so they are for tiles of
-// few rows.  Rows past a group's end are not fetched at all: what is left in
-// their part of the stage only reaches accumulator rows that are not stored, so a
-// tile of one row costs one copy of 512 bytes beside the matrix's.
+// With LIST three warps of their own fetch them, 16 bytes per thread and
+// asynchronous copy, into the swizzled layout that a box would have, and a fourth
+// hands them over to the MMA.  Without LIST the producer warp uses gathering TMA
+// copies, four row numbers each.  Those take about 80 cycles of the copy engine for
+// 512 bytes, and a stage of 128 rows 2600 where its products take 512 (65536 rows,
+// 64 groups, 4096 x 1024: 1184 us, by the warps 373, consecutive rows 337), so they
+// are for tiles of few rows.  Rows past a group's end are not fetched at all by
+// them: what is left in their part of the stage only reaches accumulator rows that
+// are not stored, so a tile of one row costs one copy of 512 bytes beside the
+// matrix's.
 //
 // In GROUPED_WEIGHT the rows are the contraction, and a group's last K-block is
 // ragged: it is fetched by row number from both operands, with zeros for the
@@ -44,7 +46,7 @@ namespace tg {
 
 constexpr int kGrEpiWarps = 8;   // two per TMEM lane quadrant, each with half of a tile's columns
 constexpr int kGrWarps = 3 + kGrEpiWarps;  // producers (warps 0 and 10), MMA (1), epilogue (2..9)
-constexpr int kListWarps = 5;              // with LIST, behind them (4: 373 us where 5 take 361; 6 leave fewer registers)
+constexpr int kListWarps = 3;              // with LIST, behind them, and a warp that hands over what they fetched
 // K-blocks per barrier transaction, one after the other in the ring.  Where an
 // operand's columns are contiguous, they interleave: 64 columns of all their
 // rows, then the next 64.  Two take half the copies and waits of one: the
@@ -54,7 +56,7 @@ template <int MODE, bool PAIR, bool LIST>
 constexpr int kGrBlocks = MODE == GROUPED_ROWS && PAIR && LIST ? 1 : 2;
 constexpr int kGrOrder = 512;              // groups that GROUPED_WEIGHT sorts by their rows
 template <bool LIST>
-constexpr int kGrThreads = 32 * (kGrWarps + (LIST ? kListWarps : 0));
+constexpr int kGrThreads = 32 * (kGrWarps + (LIST ? kListWarps + 1 : 0));
 
 template <int MODE, int BN, bool PAIR, bool LIST>
 struct GroupedShape : TileShape<BN, PAIR> {
@@ -65,7 +67,7 @@ struct GroupedShape : TileShape<BN, PAIR> {
     static constexpr int kBlocks = kGrBlocks<MODE, PAIR, LIST>;
     static constexpr int kGroups = kSlots / kBlocks;  // of slots, a transaction each
     static constexpr int kGrSmemBytes =
-        1024 + kSlots * TS::kStage + kGrEpiWarps * kUnit + kGrOrder * 2 + (2 * kGroups + 5) * 8 + 16;
+        1024 + kSlots * TS::kStage + kGrEpiWarps * kUnit + kGrOrder * 2 + (2 * kGroups + kSlots + 5) * 8 + 16;
     static_assert(kSlots >= kListWarps && kGrSmemBytes <= TS::kSmemLimit, "shared memory budget");
 };
 
@@ -87,18 +89,24 @@ __device__ __forceinline__ void tma_gather4(uint32_t dst, const CUtensorMap* map
             : "memory");
 }
 
+// Source of a list's row r.
+__device__ __forceinline__ int source_of(const GroupedRows& s, int r) {
+    return r < 0 ? s.count : (int)((uint64_t)(uint32_t)r * s.magic >> s.shift);
+}
 // Source of grouped row i (counted from the group's first, lo); a number
 // outside the matrix for rows that are none of the group's cnt.
 __device__ __forceinline__ int source_row(const GroupedRows& s, int lo, int i, int cnt) {
     if (i >= cnt) return s.count;
-    if (!s.row) return lo + i;
-    const int r = s.row[lo + i];
-    return r < 0 ? s.count : (int)((uint64_t)(uint32_t)r * s.magic >> s.shift);
+    return s.row ? source_of(s, s.row[lo + i]) : lo + i;
 }
 
 // 16 bytes, of which `bytes` are read and the rest zeros.
 __device__ __forceinline__ void copy16(uint32_t dst, const void* src, uint32_t bytes) {
     asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+// Arrives on the barrier once this thread's copies so far have landed.
+__device__ __forceinline__ void copy16_arrive(uint32_t bar) {
+    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
 }
 __device__ __forceinline__ void copy16_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
 
@@ -148,7 +156,7 @@ struct GroupedItems {
             // Tiles take as long as their groups have rows.  Groups come sorted, and rounds
             // of one tile per worker alternate in direction, so that all have the same to
             // do within about one tile (64 groups of 1024 rows give or take half, 4096 x
-            // 1024: @SORT@).
+            // 1024: 500 us as they come, 396 so, even groups 330).
             const int per = p.tiles_m * p.tiles_n;
             const int i = t * step + (t & 1 ? step - 1 - worker : worker), at = i / per;
             if (at >= p.groups) return false;
@@ -227,7 +235,8 @@ __global__ void __launch_bounds__(kGrThreads<LIST>, 1) grouped_kernel(const __gr
     uint64_t* tfull = empty + GROUPS;
     uint64_t* tempty = tfull + 2;
     uint64_t* drain = tempty + 2;
-    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
+    uint64_t* landed = drain + 1;  // a slot's copies by the list's warps
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(landed + SLOTS);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
 
     const int warp = threadIdx.x >> 5;
@@ -250,6 +259,7 @@ __global__ void __launch_bounds__(kGrThreads<LIST>, 1) grouped_kernel(const __gr
             mbar_init(smem_addr(&tempty[b]), CG * kGrEpiWarps);
         }
         mbar_init(smem_addr(drain), 1);
+        for (int s = 0; s < SLOTS; ++s) mbar_init(smem_addr(&landed[s]), 32);
         *abort_flag = 0;
         fence_barrier_init();
     }
@@ -395,15 +405,12 @@ __global__ void __launch_bounds__(kGrThreads<LIST>, 1) grouped_kernel(const __gr
             for (int q = 0; q < GROUPS; ++q)
                 if (armed & (1u << q)) drain_bar(smem_addr(&full[q]), (armed_parity >> q) & 1, w);
         }
-    } else if (LIST && warp >= kGrWarps) {
+    } else if (LIST && warp >= kGrWarps && warp < kGrWarps + kListWarps) {
         // ------------------------------------------- rows by their numbers
         // Each warp takes every kListWarps-th slot: 1024 units of 16 bytes, lane's
         // unit u of every kApart-th row.  16-byte unit k of 128-byte row r lies at
-        // unit k ^ (r mod 8).  Once they have landed, the warp hands what it wrote
-        // to the proxy that the MMA reads through, and arrives on the leader's
-        // barrier.  (That fence waits for every copy the thread has in flight, so
-        // stages a warp had ahead would gain nothing: with all warps on each stage
-        // and three stages ahead the products above ran at 380 TFLOP/s.)
+        // unit k ^ (r mod 8).  The copies report to the slot's own barrier, so a warp
+        // only ever waits for free slots.
         constexpr int kUnitsOfRow = WEIGHT ? 16 : 8, kApart = 32 / kUnitsOfRow, kRows = WEIGHT ? 64 : 128;
         static_assert(!WEIGHT || TS::kBNC == 128, "P's and Q's stages have one shape");
         const int self = warp - kGrWarps;
@@ -433,17 +440,19 @@ __global__ void __launch_bounds__(kGrThreads<LIST>, 1) grouped_kernel(const __gr
             int src[kRows / 32], ahead[kRows / 32];
             auto fetch_rows = [&](int i0, int (&r)[kRows / 32]) {
 #pragma unroll
-                for (int j = 0; j < kRows / 32; ++j) r[j] = source_row(s, it.lo, i0 + 32 * j + lane, it.cnt);
+                for (int j = 0; j < kRows / 32; ++j) r[j] = i0 + 32 * j + lane < it.cnt ? s.row[it.lo + i0 + 32 * j + lane] : -1;
             };
-            if (WEIGHT)
-                fetch_rows(wait * kBK, ahead);
-            else
-                fetch_rows(row0, src);
+            auto sources = [&](const int (&r)[kRows / 32]) {
+#pragma unroll
+                for (int j = 0; j < kRows / 32; ++j) src[j] = source_of(s, r[j]);
+            };
+            // (GROUPED_WEIGHT: the next block's numbers are loaded while this one's rows are)
+            fetch_rows(WEIGHT ? wait * kBK : row0, ahead);
+            if (!WEIGHT) sources(ahead);
             int kb = wait;
             for (; kb < all_kb; kb += kListWarps) {
                 if constexpr (WEIGHT) {
-#pragma unroll
-                    for (int j = 0; j < kRows / 32; ++j) src[j] = ahead[j];
+                    sources(ahead);
                     fetch_rows((kb + kListWarps) * kBK, ahead);
                 }
                 const bool got = wait_bar(smem_addr(&empty[slot / BLOCKS]), phase ^ 1, w, DEV_TIMEOUT_PRODUCER + 3);
@@ -457,23 +466,23 @@ __global__ void __launch_bounds__(kGrThreads<LIST>, 1) grouped_kernel(const __gr
                 const uint32_t bytes = 2u * (uint32_t)min(8, max(0, s.cols - col));
                 const uint16_t* from = base + (bytes ? col : 0);
                 if (kb < num_kb) {
+                    // (eight rows' numbers at a time: copies do not move past shuffles)
 #pragma unroll
-                for (int j = 0; j < kRows / kApart; ++j) {
-                    const int at = __shfl_sync(0xffffffffu, src[kApart * j / 32], (kApart * j & 31) + q);
-                    const bool there = at < s.count;
-                    copy16(dst + to[j % (8 / kApart)] + j / (8 / kApart) * 1024, from + (there ? at : 0) * s.ld,
-                           there ? bytes : 0u);
+                    for (int j0 = 0; j0 < kRows / kApart; j0 += 8) {
+                        const uint16_t* at[8];
+                        uint32_t n[8];
+#pragma unroll
+                        for (int j = 0; j < 8; ++j) {
+                            const int r = __shfl_sync(0xffffffffu, src[kApart * (j0 + j) / 32], (kApart * (j0 + j) & 31) + q);
+                            n[j] = r < s.count ? bytes : 0u;
+                            at[j] = from + (r < s.count ? r : 0) * s.ld;
+                        }
+#pragma unroll
+                        for (int j = 0; j < 8; ++j)
+                            copy16(dst + to[(j0 + j) % (8 / kApart)] + (j0 + j) / (8 / kApart) * 1024, at[j], n[j]);
+                    }
                 }
-                }
-                copy16_wait_all();
-                fence_proxy_async_shared();
-                __syncwarp();
-                if (lane == 0) {
-                    if constexpr (PAIR)
-                        arrive_on_leader_release(smem_addr(&full[slot / BLOCKS]));
-                    else
-                        mbar_arrive(smem_addr(&full[slot / BLOCKS]));
-                }
+                copy16_arrive(smem_addr(&landed[slot]));
                 slot += kListWarps;
                 if (slot >= SLOTS) {
                     slot -= SLOTS;
@@ -481,6 +490,38 @@ __global__ void __launch_bounds__(kGrThreads<LIST>, 1) grouped_kernel(const __gr
                 }
             }
             wait = kb - all_kb;
+        }
+        copy16_wait_all();
+    } else if (LIST && warp == kGrWarps + kListWarps) {
+        // ------------------------------- from the list's warps to the MMA
+        // Ordinary writes become visible to the proxy that the MMA reads through by a
+        // fence after they are known to have landed.  It is a thread of its own that
+        // passes it: the fence waits for every copy its thread has in flight, so a
+        // warp that copied and fenced had nothing in flight meanwhile (the gradient of
+        // the sizes above: 449 us with five such warps, 410 with three and this one).
+        int slot = 0;
+        uint32_t phase = 0;
+        GroupedItems<MODE> items(p, order, worker, workers, TS::kBM);
+        GroupedItem it;
+        bool ok = true;
+        while (ok && items.next(it)) {
+            const int all_kb = (blocks_of(it) + BLOCKS - 1) / BLOCKS * BLOCKS;
+            if (lane == 0) {
+                for (int kb = 0; kb < all_kb; ++kb) {
+                    ok = wait_bar(smem_addr(&landed[slot]), phase, w, DEV_TIMEOUT_PRODUCER + 4);
+                    if (!ok) break;
+                    fence_proxy_async_shared();
+                    if constexpr (PAIR)
+                        arrive_on_leader_release(smem_addr(&full[slot / BLOCKS]));
+                    else
+                        mbar_arrive(smem_addr(&full[slot / BLOCKS]));
+                    if (++slot == SLOTS) {
+                        slot = 0;
+                        phase ^= 1;
+                    }
+                }
+            }
+            ok = __shfl_sync(0xffffffffu, (int)ok, 0) != 0;
         }
     } else if (warp == 1 && leader) {
         // ---------------------------------------------------- MMA issuer

@@ -15,7 +15,7 @@
 // token with its keys 32 experts apart and integer reductions over the warp: about
 // 1100 instructions a token, 45 us; runs in registers instead of shared memory: as
 // long, for the branches that taking a key out of one of 32 registers needs.  This:
-// @ROUTE@ us.)
+// 16.)
 //
 // Which expert wins must not depend on how an exponential was rounded, so
 // the ranking is that of 64-bit arithmetic.  Doing it in 64 bits throughout would
@@ -744,7 +744,7 @@ RouteParams params_of(int64_t T, int64_t E, const tg_route_options& o) {
     p.top = o.group_top;
     p.size = (int)(E / o.groups);
     // Short runs while every token finds a warp of its own at once (one token of 256
-    // experts: @RUN@ us in runs of 8, of 32), then of at most 32 experts, or of 64: with
+    // experts: 6.8 us in runs of 8, 9.7 of 32), then of at most 32 experts, or of 64: with
     // that 32 lanes hold any 1024 experts in 32 groups.
     for (int most = T <= 2048 ? 8 : 32; most <= 64; most *= 2) {
         p.parts = (p.size + most - 1) / most;
