@@ -487,7 +487,8 @@ int tg_route_grad(int64_t T, int64_t E, const void* logits, int64_t ld, const in
  * offset[g+1]-1 in ascending order, and row[place[i]] = i.  A row of any other
  * index is in no group: its place is -1, and so is row[] from offset[G] on.
  * index, row, place: [R]; offset: [G+1]; 1 <= R <= 2^30, 1 <= G <= 4096.
- * place may be NULL.  One kernel launch for up to 2048 rows, else two.
+ * place may be NULL.  One kernel launch for up to 2048 rows, two for up to 131072,
+ * else three.
  */
 int tg_group_rows(int64_t R, int64_t G, const int32_t* index, int32_t* offset, int32_t* row,
                   int32_t* place, void* workspace, size_t workspace_bytes, cudaStream_t stream);

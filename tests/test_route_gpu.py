@@ -215,7 +215,7 @@ def group(tg, index, g, with_place=True):
 
 
 @pytest.mark.parametrize("r,g", [(1, 1), (1, 4096), (5, 3), (32, 7), (2047, 60), (2048, 256), (2049, 256), (5000, 1),
-                                 (6001, 4096), (70000, 129)])
+                                 (6001, 4096), (70000, 129), (131072, 5), (131073, 300), (400000, 64)])
 @pytest.mark.parametrize("kind", ["even", "one", "dropped", "none"])
 def test_group_rows(tg, r, g, kind):
     gen = torch.Generator(device="cuda").manual_seed(r + g)

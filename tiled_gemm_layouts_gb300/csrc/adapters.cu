@@ -407,9 +407,9 @@ extern "C" int tg_adapters(int64_t T, int64_t N, int64_t K, int64_t rank, int64_
     // columns of y per block: few enough for three blocks per SM, at most 2048
     const int64_t tiles = tiles_of(T, G);
     int64_t chunks = std::max<int64_t>((N + 2047) / 2048, std::min<int64_t>((N + 255) / 256, (3LL * info->sms + tiles - 1) / tiles));
+    chunks = std::min<int64_t>(chunks, 65535);
     p.chunk = (int)((N + chunks * 256 - 1) / (chunks * 256) * 256);
     chunks = (N + p.chunk - 1) / p.chunk;
-    if (chunks > 65535) return TG_ERR_INVALID_ARG;
     const dim3 low((unsigned)tiles, (unsigned)p.splits, (unsigned)((rank + kRankPass - 1) / kRankPass));
     const dim3 add((unsigned)tiles, (unsigned)chunks, 1);
     cudaError_t e = dtype == TG_BF16 ? launch_low<true>(p, low, stream) : launch_low<false>(p, low, stream);

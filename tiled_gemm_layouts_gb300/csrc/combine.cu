@@ -40,6 +40,7 @@ struct CombineParams {
     long long lddo;
     float* dweight;
     unsigned units;  // of VEC columns per row
+    bool narrow;     // fewer than 2^32 of them in all
 };
 
 template <bool BF>
@@ -86,7 +87,8 @@ template <bool BF, int VEC>
 __global__ void __launch_bounds__(kSumThreads) combine_kernel(const CombineParams p) {
     constexpr int W = VEC == 8 ? 4 : 1;
     const long long u = (long long)blockIdx.x * kSumThreads + threadIdx.x;
-    const long long t = u / p.units;
+    // (most often in 32 bits: a 64-bit division takes as long as the rest)
+    const long long t = p.narrow ? (long long)((unsigned)u / p.units) : u / p.units;
     if (t >= p.T) return;
     const long long c = (u - t * p.units) * VEC;
     const int* place = p.place + t * p.k;
@@ -134,7 +136,7 @@ __global__ void __launch_bounds__(32 * kGradWarps) combine_grad_kernel(const Com
     const int lane = threadIdx.x & 31;
     const long long item = (long long)blockIdx.x * kGradWarps + (threadIdx.x >> 5);
     if (item >= p.T * p.k) return;
-    const long long t = item / p.k;
+    const long long t = (unsigned)item / (unsigned)p.k;  // (T k < 2^31)
     const int at = p.place[item];
     if (at < 0 || at >= p.y_rows) {
         if (p.dweight && lane == 0) p.dweight[item] = 0.0f;
@@ -211,6 +213,7 @@ extern "C" int tg_combine(int64_t T, int64_t k, int64_t D, const void* Y, int64_
     p.units = (unsigned)(D / vec);
     const int64_t blocks = (T * (int64_t)p.units + kSumThreads - 1) / kSumThreads;
     if (blocks > kMaxDim) return TG_ERR_INVALID_ARG;
+    p.narrow = blocks < (1LL << 32) / kSumThreads;
     int dev;
     DeviceInfo* info;
     if ((rc = current_device(&dev, &info))) return rc;

@@ -9,8 +9,9 @@
 // places its rows start from.  What the blocks before hold is counted by a first
 // kernel, block by block, into the workspace; every block of the second adds
 // those counts up for itself (64 blocks x 256 groups are 64 KB, out of L2).
-// So a row's place depends on nothing but its index and number, whatever
-// order the blocks run in.  Bound by latency: two short kernels, the second's
+// (More blocks than 64 have a kernel between the two add them up, so that the
+// work stays proportional to the rows.)  So a row's place depends on nothing but
+// its index and number, whatever order the blocks run in.  Bound by latency: two short kernels, the second's
 // launch hidden behind the first (one kernel where one block holds all rows).
 #include <cuda_runtime.h>
 
@@ -28,6 +29,7 @@ constexpr int kGroupThreads = 32 * kGroupWarps;
 constexpr int kRowsPerWarp = 256;
 constexpr int kRowsPerBlock = kGroupWarps * kRowsPerWarp;
 constexpr int kMaxGroups = 4096;
+constexpr int kBlocksAdded = 64;  // that each block adds up for itself
 
 // counts[block][g]: rows of group g among the block's
 __global__ void __launch_bounds__(kGroupThreads) count_kernel(const int* index, int R, int G, int* counts) {
@@ -44,9 +46,29 @@ __global__ void __launch_bounds__(kGroupThreads) count_kernel(const int* index, 
     for (int g = threadIdx.x; g < G; g += kGroupThreads) counts[(long long)blockIdx.x * G + g] = shared_counts[g];
 }
 
+// counts[block][g] to the rows of the blocks before; all[g]: of all of them
+__global__ void __launch_bounds__(kGroupThreads) scan_kernel(int blocks, int G, int* counts, int* all) {
+    allow_next_kernel();
+    const int g = blockIdx.x * kGroupThreads + threadIdx.x;
+    if (g >= G) return;
+    wait_for_previous_kernel();
+    int run = 0;
+    for (int b0 = 0; b0 < blocks; b0 += 32) {
+        int n[32];
+#pragma unroll
+        for (int j = 0; j < 32; ++j) n[j] = b0 + j < blocks ? counts[(long long)(b0 + j) * G + g] : 0;
+#pragma unroll
+        for (int j = 0; j < 32; ++j) {
+            if (b0 + j < blocks) counts[(long long)(b0 + j) * G + g] = run;
+            run += n[j];
+        }
+    }
+    all[g] = run;
+}
+
 // shared memory: start[G + 1] and earlier[G] ints, then counts of 16 bits [kGroupWarps][G]
 __global__ void __launch_bounds__(kGroupThreads) place_kernel(const int* index, int R, int G, const int* counts,
-                                                              int* offset, int* row, int* place) {
+                                                              const int* totals, int* offset, int* row, int* place) {
     extern __shared__ int start[];
     __shared__ int warp_total[kGroupWarps];
     int* earlier = start + G + 1;  // rows of each group in the blocks before
@@ -99,7 +121,10 @@ __global__ void __launch_bounds__(kGroupThreads) place_kernel(const int* index, 
             before += n;
         }
         int all = before;
-        if (counts) {  // the blocks', 32 loads in flight
+        if (totals) {
+            all = totals[g];
+            earlier[g] = counts[(long long)blockIdx.x * G + g];
+        } else if (counts) {  // the blocks', 32 loads in flight
             all = 0;
             int ahead = 0;
             for (int b0 = 0; b0 < (int)gridDim.x; b0 += 32) {
@@ -175,7 +200,8 @@ extern "C" int tg_group_rows_workspace_size(int64_t R, int64_t G, size_t* bytes)
     const int rc = check_counts(R, G);
     if (rc) return rc;
     if (!bytes) return TG_ERR_INVALID_ARG;
-    *bytes = blocks_of(R) > 1 ? (size_t)blocks_of(R) * (size_t)G * sizeof(int) : 0;
+    const int64_t blocks = blocks_of(R);
+    *bytes = blocks > 1 ? (size_t)(blocks + (blocks > kBlocksAdded)) * (size_t)G * sizeof(int) : 0;
     return TG_OK;
 }
 
@@ -213,6 +239,10 @@ extern "C" int tg_group_rows(int64_t R, int64_t G, const int32_t* index, int32_t
         count_kernel<<<blocks, kGroupThreads, (size_t)G * 4, stream>>>(index, (int)R, (int)G, counts);
         e = cudaGetLastError();
     }
+    int* totals = blocks > (unsigned)kBlocksAdded ? counts + (size_t)blocks * (size_t)G : nullptr;
+    if (e == cudaSuccess && totals)
+        e = launch_chained(scan_kernel, dim3((unsigned)((G + kGroupThreads - 1) / kGroupThreads)), kGroupThreads, stream, (int)blocks,
+                           (int)G, counts, totals);
     if (e == cudaSuccess) {
         cudaLaunchConfig_t lc = {};
         cudaLaunchAttribute attr[1];
@@ -224,8 +254,8 @@ extern "C" int tg_group_rows(int64_t R, int64_t G, const int32_t* index, int32_t
         lc.stream = stream;
         lc.attrs = attr;
         lc.numAttrs = counts ? 1 : 0;
-        e = cudaLaunchKernelEx(&lc, place_kernel, (const int*)index, (int)R, (int)G, (const int*)counts, (int*)offset,
-                               (int*)row, (int*)place);
+        e = cudaLaunchKernelEx(&lc, place_kernel, (const int*)index, (int)R, (int)G, (const int*)counts,
+                               (const int*)totals, (int*)offset, (int*)row, (int*)place);
     }
     if (e != cudaSuccess) {
         cudaGetLastError();

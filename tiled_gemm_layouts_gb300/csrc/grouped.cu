@@ -230,7 +230,7 @@ extern "C" int tg_grouped_gemm(int64_t R, int64_t N, int64_t K, int64_t G, const
     const int bnc = tile.pair ? tile.bn / 2 : tile.bn;
     p.q_mn = permB == TG_OP_N;
     bool ok = encode_rows(&p.p, dtype, X, row ? x_rows : R, K, ldx, row, per_row);
-    const int64_t stride = G > 1 ? stride_b : a.b_rows() * ldb;
+    const int64_t stride = G > 1 ? stride_b : ldb;  // (of one matrix: none)
     p.q_pairs = !p.q_mn && K >= 128 ? (int)(K / 64) : 0;
     ok = ok && (p.q_mn ? encode_stack(&p.map_q, dtype, B, N, K, G, ldb, stride, 64u * (uint32_t)tile.blocks_rows())
                        : encode_stack(&p.map_q, dtype, B, K, N, G, ldb, stride, (uint32_t)bnc));

@@ -39,6 +39,7 @@
 #pragma once
 
 #include "ce_kernel.cuh"
+#include "direct.cuh"
 #include "gemm_kernel.cuh"
 #include "grouped_params.h"
 
@@ -193,7 +194,9 @@ struct GroupedItems {
                     if (lane >= d) incl += o;
                 }
             }
-            const int owner = __ffs(__ballot_sync(0xffffffffu, t < base + incl)) - 1;
+            const unsigned later = __ballot_sync(0xffffffffu, t < base + incl);
+            if (!later) return false;  // (more tiles than 32 bits count: offsets that do not ascend)
+            const int owner = __ffs(later) - 1;
             // its tiles before this one, group by group
             int i = t - base - (incl - (tiles_of(0) + tiles_of(1) + tiles_of(2) + tiles_of(3)));
             int k = 0, first = lo[0], rows = cnt[0];
@@ -602,6 +605,17 @@ __global__ void __launch_bounds__(kGrThreads<LIST>, 1) grouped_kernel(const __gr
             const int row0 = it.tm * TS::kBM + (int)rank * 128 + q * 32;  // this warp's first row, in its group or dB
             const int rows = min(32, (WEIGHT ? p.m : it.cnt) - row0);
             const int n0 = it.tn * BN + half * kCols;                     // and first column
+            const bool masked = MODE == GROUPED_ROWS && p.relu_of;
+            const uint16_t* mask = nullptr;  // this warp's first row
+            if (masked) {
+                // its lines are on their way while the products run: 128 bytes per lane and turn
+                mask = static_cast<const uint16_t*>(p.relu_of) + (long long)(it.lo + row0) * p.ld_relu;
+                constexpr int kLines = kCols < 64 ? 1 : kCols / 64;
+                for (int i = lane; i < 32 * kLines; i += 32) {
+                    const int r = i / kLines, c = n0 + i % kLines * 64;
+                    if (r < rows && c < p.n) asm volatile("prefetch.global.L2 [%0];" ::"l"(mask + (long long)r * p.ld_relu + c));
+                }
+            }
             const bool got = wait_bar(smem_addr(&tfull[i & 1]), (i >> 1) & 1, w, DEV_TIMEOUT_EPILOGUE + 4);
             if (!__all_sync(0xffffffffu, got)) break;
             tc_fence_after();
@@ -664,31 +678,32 @@ __global__ void __launch_bounds__(kGrThreads<LIST>, 1) grouped_kernel(const __gr
                 __syncwarp();
                 // whole 16-byte units: neighbouring lanes store neighbouring units of a row
                 const int k = lane % kUnits, col = c0 + 8 * k;
+                constexpr int kTurns = 32 / kRowsAtOnce;
+                uint4 z[kTurns];
+                if (masked) {
 #pragma unroll
-                for (int r0 = 0; r0 < 32; r0 += kRowsAtOnce) {
-                    const int r = r0 + lane / kUnits;
+                    for (int i = 0; i < kTurns; ++i) {
+                        const int r = i * kRowsAtOnce + lane / kUnits;
+                        if (r < rows && col < p.n) z[i] = load8(mask + (long long)r * p.ld_relu, col, p.n);
+                    }
+                }
+#pragma unroll
+                for (int i = 0; i < kTurns; ++i) {
+                    const int r = i * kRowsAtOnce + lane / kUnits;
                     if (r >= rows || col >= p.n) continue;
                     uint4 u = *staged(r, k);
-                    uint16_t* o = out + (long long)r * p.ldo + col;
-                    if (MODE == GROUPED_ROWS && p.relu_of) {
-                        const uint16_t* z = static_cast<const uint16_t*>(p.relu_of) +
-                                            (long long)(it.lo + row0 + r) * p.ld_relu + col;
+                    if (masked) {
                         uint32_t* word = reinterpret_cast<uint32_t*>(&u);
-                        if (col + 8 <= p.n) {
-                            const uint4 zu = *reinterpret_cast<const uint4*>(z);
-                            const uint32_t zw[4] = {zu.x, zu.y, zu.z, zu.w};
+                        const uint32_t zw[4] = {z[i].x, z[i].y, z[i].z, z[i].w};
+                        // above 0: positive, not zero, and no NaN (the largest exponent with a mantissa)
+                        const uint32_t inf = p.bf16 ? 0x7F80u : 0x7C00u;
 #pragma unroll
-                            for (int x = 0; x < 4; ++x) {
-                                if (!(to_f32((uint16_t)(zw[x] & 0xFFFFu), p.bf16) > 0.0f)) word[x] &= 0xFFFF0000u;
-                                if (!(to_f32((uint16_t)(zw[x] >> 16), p.bf16) > 0.0f)) word[x] &= 0x0000FFFFu;
-                            }
-                        } else {
-                            uint16_t* part = reinterpret_cast<uint16_t*>(&u);
-#pragma unroll
-                            for (int x = 0; x < 8; ++x)
-                                if (col + x < p.n && !(to_f32(z[x], p.bf16) > 0.0f)) part[x] = 0;
+                        for (int x = 0; x < 4; ++x) {
+                            const uint32_t low = zw[x] & 0xFFFFu, high = zw[x] >> 16;
+                            word[x] &= (low - 1u < inf ? 0xFFFFu : 0u) | (high - 1u < inf ? 0xFFFF0000u : 0u);
                         }
                     }
+                    uint16_t* o = out + (long long)r * p.ldo + col;
                     if (col + 8 <= p.n) {
                         *reinterpret_cast<uint4*>(o) = u;
                     } else {

@@ -612,7 +612,7 @@ __global__ void __launch_bounds__(32 * kWarps) route_grad_kernel(const __grid_co
         const float g = e >= 0 ? p.dweight[t * p.k + lane] * p.scale : 0.0f;
         const float logit = e >= 0 ? load_one(row + e) : -INFINITY;
         float prob[V];
-        float d, dot = 0.0f;
+        float d, dot = 0.0f, own = 0.0f;  // own: the softmax's share of this lane's expert
         if (dense) {
             float top = -INFINITY, sum = 0.0f;
 #pragma unroll
@@ -632,8 +632,8 @@ __global__ void __launch_bounds__(32 * kWarps) route_grad_kernel(const __grid_co
             const float inverse = top == -INFINITY ? 0.0f : 1.0f / sum;
 #pragma unroll
             for (int v = 0; v < V; ++v) prob[v] *= inverse;
-            const float part = e >= 0 ? g * (expf(logit - base) * inverse) : 0.0f;
-            dot = warp_sum(part);
+            own = e >= 0 ? expf(logit - base) * inverse : 0.0f;
+            dot = warp_sum(e >= 0 ? g * own : 0.0f);
             d = g;
         } else if (p.renorm) {
             float m = warp_fmax(logit);
@@ -648,22 +648,22 @@ __global__ void __launch_bounds__(32 * kWarps) route_grad_kernel(const __grid_co
         } else {
             d = e < 0 ? 0.0f : g * sigmoid(logit) * (1.0f / (1.0f + expf(logit)));
         }
-        if (e < 0) d = 0.0f;
-        float full[V];
-#pragma unroll
-        for (int v = 0; v < V; ++v) full[v] = 0.0f;
-        for (int j = 0; j < p.k; ++j) {
-            const int at = __shfl_sync(0xffffffffu, e, j);
-            const float x = __shfl_sync(0xffffffffu, d, j);
-#pragma unroll
-            for (int v = 0; v < V; ++v)
-                if (at == v * 32 + lane) full[v] += x;
-        }
+        // what is not chosen, and then what is: an expert's first lane stores its sum
 #pragma unroll
         for (int v = 0; v < V; ++v) {
             const int x = v * 32 + lane;
-            if (x < p.E) store_one(out + x, dense ? prob[v] * (full[v] - dot) : full[v]);
+            if (x < p.E) store_one(out + x, dense ? prob[v] * -dot : 0.0f);
         }
+        float sum = 0.0f;
+        bool first = e >= 0;
+        for (int j = 0; j < p.k; ++j) {
+            const int other = __shfl_sync(0xffffffffu, e, j);
+            const float x = __shfl_sync(0xffffffffu, d, j);
+            if (other == e) sum += x;
+            if (other == e && j < lane) first = false;
+        }
+        __syncwarp();  // (the stores above come before)
+        if (first) store_one(out + e, dense ? own * (sum - dot) : sum);
     }
 }
 
