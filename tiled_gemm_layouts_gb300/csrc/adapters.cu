@@ -404,9 +404,11 @@ extern "C" int tg_adapters(int64_t T, int64_t N, int64_t K, int64_t rank, int64_
     p.splits = (int)((K + p.split - 1) / p.split);
     p.pitch = (int)pitch_of(rank);
     p.low = static_cast<float*>(workspace);
-    // columns of y per block: few enough for three blocks per SM, at most 2048
+    // Columns of y per block: few enough for three blocks per SM, at most 1024, or 2048
+    // where u's fragments are many (7777 rows, us: rank 32 70 to 77, rank 64 95 to 90).
+    const int64_t most = rank <= 32 ? 1024 : 2048;
     const int64_t tiles = tiles_of(T, G);
-    int64_t chunks = std::max<int64_t>((N + 2047) / 2048, std::min<int64_t>((N + 255) / 256, (3LL * info->sms + tiles - 1) / tiles));
+    int64_t chunks = std::max<int64_t>((N + most - 1) / most, std::min<int64_t>((N + 255) / 256, (3LL * info->sms + tiles - 1) / tiles));
     chunks = std::min<int64_t>(chunks, 65535);
     p.chunk = (int)((N + chunks * 256 - 1) / (chunks * 256) * 256);
     chunks = (N + p.chunk - 1) / p.chunk;

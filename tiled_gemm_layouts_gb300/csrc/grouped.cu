@@ -214,7 +214,7 @@ extern "C" int tg_grouped_gemm(int64_t R, int64_t N, int64_t K, int64_t G, const
         f.relu = epi ? epi->relu : 0;
         f.relu_of = static_cast<const uint16_t*>(relu_of);
         f.ld_relu = relu_of ? epi->ld_relu : 0;
-        if (launch_few_rows(f, dtype == TG_BF16, most_tiles(R, G, kFewTileRows, 1), stream) != cudaSuccess) {
+        if (launch_few_rows(f, dtype == TG_BF16, most_tiles(R, G, kFewTileRows, 1), info->sms, stream) != cudaSuccess) {
             cudaGetLastError();
             return TG_ERR_CUDA;
         }

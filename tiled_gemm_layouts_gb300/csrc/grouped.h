@@ -27,6 +27,6 @@ struct FewRowsParams {
     const uint16_t* relu_of;
     long long ld_relu;
 };
-cudaError_t launch_few_rows(const FewRowsParams& p, bool bf16, long long tiles, cudaStream_t stream);
+cudaError_t launch_few_rows(const FewRowsParams& p, bool bf16, long long tiles, int sms, cudaStream_t stream);
 
 }  // namespace tg
