@@ -187,6 +187,9 @@ EXPORTED = [
     "tg_layernorm", "tg_layernorm_grad", "tg_layernorm_grad_workspace_size",
     "tg_linear_ce", "tg_linear_ce_workspace_size",
     "tg_linear_ce_grad", "tg_linear_ce_grad_workspace_size", "tg_adamw",
+    "tg_route", "tg_route_grad", "tg_group_rows", "tg_group_rows_workspace_size",
+    "tg_grouped_gemm", "tg_grouped_gemm_grad", "tg_combine", "tg_combine_grad",
+    "tg_adapters", "tg_adapters_workspace_size",
     "tg_gemm_static_ws", "tg_gemm_host", "tg_gemm_host_workspace_size",
     "tg_status_string", "tg_query_config",
     "tg_query_config_ws", "tg_query_config_for_sms",
