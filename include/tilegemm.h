@@ -498,6 +498,8 @@ int tg_group_rows_workspace_size(int64_t R, int64_t G, size_t* bytes);
  *
  *     y = acc;  y += bias[g, n];  y = max(y, 0);  y = 0 where relu_of[i, n] <= 0 or is NaN
  *
+ * (a NaN passes max(y, 0))
+ *
  * each step only when it is asked for.  The last one is the gradient of a ReLU
  * whose output relu_of is. */
 typedef struct {
@@ -554,7 +556,7 @@ int tg_grouped_gemm_grad(int64_t R, int64_t N, int64_t K, int64_t G, const void*
  *
  * place and weight: [T, k]; Y: y_rows rows of D elements; out: T rows.  weight
  * may be NULL (all 1).  A place outside 0..y_rows-1 contributes nothing, whatever
- * its weight; a token without any has a row of zeros.  k <= 1024.  Any
+ * its weight; a token without any has a row of zeros.  k <= 1024, T k < 2^31.  Any
  * 2-byte-aligned rows (16-byte-aligned ones are faster).  One kernel launch.
  */
 int tg_combine(int64_t T, int64_t k, int64_t D, const void* Y, int64_t y_rows, int64_t ldy,

@@ -26,7 +26,8 @@ def list_of(gen, r, x_rows, per_row):
 @pytest.mark.parametrize("dtype", [torch.float16, torch.bfloat16])
 @pytest.mark.parametrize("counts,n,k", [
     (SMALL, 1, 1), (SMALL, 200, 64), (FEW, 72, 100), (FEW, 129, 513), (RAGGED, 256, 64), (RAGGED, 250, 72), (LARGE, 520, 200),
-    (LARGE, 64, 65), (MANY, 100, 40), ([20000, 3], 136, 64), ([0, 0, 0], 64, 64), ([5] * 200, 1000, 24)])
+    (LARGE, 64, 65), (MANY, 100, 40), ([20000, 3], 136, 64), ([0, 0, 0], 64, 64), ([5] * 200, 1000, 24),
+    ([16, 0, 9, 17], 264, 1100), ([130] * 140, 72, 136), ([i % 3 for i in range(4096)], 8, 8)])
 @pytest.mark.parametrize("perm", [0, 1])
 @pytest.mark.parametrize("gathered", [False, True])
 def test_grouped_gemm(tg, counts, n, k, perm, gathered, dtype):
@@ -52,7 +53,7 @@ def test_grouped_gemm(tg, counts, n, k, perm, gathered, dtype):
 
 
 @pytest.mark.parametrize("dtype", [torch.float16, torch.bfloat16])
-@pytest.mark.parametrize("counts,n,k", [(FEW, 75, 64), (LARGE, 300, 64)])
+@pytest.mark.parametrize("counts,n,k", [([2, 0, 3, 1], 75, 200), (FEW, 75, 64), (LARGE, 300, 64)])
 def test_epilogue(tg, counts, n, k, dtype):
     gen = torch.Generator(device="cuda").manual_seed(4)
     g, r = len(counts), sum(counts)
@@ -89,7 +90,7 @@ def test_epilogue(tg, counts, n, k, dtype):
 @pytest.mark.parametrize("dtype", [torch.float16, torch.bfloat16])
 @pytest.mark.parametrize("counts,n,k", [
     (SMALL, 1, 1), (FEW, 72, 100), (RAGGED, 129, 65), (LARGE, 520, 200), (MANY, 40, 24), ([20000, 3], 136, 64), ([0, 0], 64, 64),
-    ([63, 64, 65] * 12, 600, 520)])
+    ([63, 64, 65] * 12, 600, 520), ([i % 5 for i in range(600)], 40, 24), ([130] * 140, 72, 136)])
 @pytest.mark.parametrize("perm", [0, 1])
 @pytest.mark.parametrize("gathered", [False, True])
 def test_grouped_gemm_grad(tg, counts, n, k, perm, gathered, dtype):

@@ -43,6 +43,11 @@ CASES = [
     (33, 40, 8, False, False, 4, 1, 1, True, 1.0),
     (50, 512, 16, False, True, 16, 3, 2, True, 1.0),
     (31, 32, 3, True, True, 32, 9, 2, True, 1.0),   # groups of one expert
+    # many tokens: longer runs of experts per lane
+    (2100, 16, 2, False, True, 1, 1, 1, True, 1.0),
+    (2100, 160, 6, True, True, 4, 2, 2, True, 1.0),
+    (2081, 64, 8, False, False, 2, 1, 2, False, 1.0),
+    (2049, 1022, 5, True, True, 14, 3, 2, False, 1.0),  # 14 groups of 73: runs of 37
 ]
 
 

@@ -253,6 +253,9 @@ __global__ void __launch_bounds__(kGrThreads<LIST>, 1) grouped_kernel(const __gr
                   p.status, p.timeout_cycles};
 
     if (threadIdx.x == 0) {
+        if (!LIST || !p.p.row) prefetch_tensormap(&p.p.box);
+        if (WEIGHT && (!LIST || !p.q.row)) prefetch_tensormap(&p.q.box);
+        if (!WEIGHT) prefetch_tensormap(p.q_pairs ? &p.map_q2 : &p.map_q);
         for (int s = 0; s < GROUPS; ++s) {
             mbar_init(smem_addr(&full[s]), 1 + (LIST ? CG * BLOCKS : 0));
             mbar_init(smem_addr(&empty[s]), 1);
