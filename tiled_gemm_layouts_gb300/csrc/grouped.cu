@@ -220,8 +220,12 @@ extern "C" int tg_grouped_gemm(int64_t R, int64_t N, int64_t K, int64_t G, const
         }
         return TG_OK;
     }
-    GroupedTile tile{64, 0, 0};
-    if (R >= 128 * G)
+    // A pair's tiles for full groups, if they are enough for all pairs; else as many
+    // columns as still leave a tile for every SM.  (Two groups of 150 rows, 1000 x 1000:
+    // 19 us by pairs, 15 by 64 columns; eight of 100, 1024 x 2048, by a list 31 by 64
+    // columns; 16 of 4096, 2048 to 192: 64 by pairs, 95 by 128 columns.)
+    GroupedTile tile{64, 0, row != nullptr};
+    if (R >= 128 * G && most_tiles(R, G, 256, (N + 255) / 256) >= info->sms / 2)
         tile = GroupedTile{256, 1, row != nullptr};
     else if (most_tiles(R, G, 128, (N + 127) / 128) >= info->sms)
         tile = GroupedTile{128, 0, row != nullptr};

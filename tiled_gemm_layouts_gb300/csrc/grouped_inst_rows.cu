@@ -15,6 +15,8 @@ cudaError_t launch_grouped_mode<GROUPED_ROWS>(const GroupedParams& p, GroupedTil
         return launch_grouped_tile<GROUPED_ROWS, 128, false, true>(p, tiles, sms, stream);
     if (tile.bn == 64 && !tile.pair && !tile.list)
         return launch_grouped_tile<GROUPED_ROWS, 64, false, false>(p, tiles, sms, stream);
+    if (tile.bn == 64 && !tile.pair && tile.list)
+        return launch_grouped_tile<GROUPED_ROWS, 64, false, true>(p, tiles, sms, stream);
     return cudaErrorInvalidValue;
 }
 }  // namespace tg

@@ -20,19 +20,18 @@
 // written (at 65536 rows of 4096 columns that would be 1.07 GB more traffic).
 // With LIST three warps of their own fetch them, 16 bytes per thread and
 // asynchronous copy, into the swizzled layout that a box would have, and a fourth
-// hands them over to the MMA.  Without LIST the producer warp uses gathering TMA
-// copies, four row numbers each.  Those take about 80 cycles of the copy engine for
-// 512 bytes, and a stage of 128 rows 2600 where its products take 512 (65536 rows,
-// 64 groups, 4096 x 1024: 1184 us, by the warps 373, consecutive rows 337), so they
-// are for tiles of few rows.  Rows past a group's end are not fetched at all by
-// them: what is left in their part of the stage only reaches accumulator rows that
-// are not stored, so a tile of one row costs one copy of 512 bytes beside the
-// matrix's.
+// hands them over to the MMA (65536 rows, 64 groups, 4096 x 1024: 373 us,
+// consecutive rows 337).  Gathering TMA copies of four rows, which would need none
+// of these, take about 80 cycles of the copy engine for 512 bytes, and a stage of 128
+// rows 2600 where its products take 512: 1184 us.  Without LIST a part of a tile
+// without rows is not fetched at all: what is left in its stage only reaches
+// accumulator rows that are not stored.
 //
 // In GROUPED_WEIGHT the rows are the contraction, and a group's last K-block is
-// ragged: it is fetched by row number from both operands, with zeros for the
-// rows that are none of the group's (a box would bring the next group's rows,
-// whose infinities a zero in the other operand does not undo).
+// ragged: it is fetched by row number from both operands (by gathering copies where
+// there is no list), with zeros for the rows that are none of the group's (a box
+// would bring the next group's rows, whose infinities a zero in the other operand
+// does not undo).
 //
 // Every wait is bounded; on a timeout the status word is set, copies and MMAs
 // in flight are drained, TMEM is freed and the kernel returns.
@@ -90,17 +89,10 @@ __device__ __forceinline__ void tma_gather4(uint32_t dst, const CUtensorMap* map
             : "memory");
 }
 
-// Source of a list's row r.
+// Source of a list's row r; a number outside the matrix for one that has none.
 __device__ __forceinline__ int source_of(const GroupedRows& s, int r) {
     return r < 0 ? s.count : (int)((uint64_t)(uint32_t)r * s.magic >> s.shift);
 }
-// Source of grouped row i (counted from the group's first, lo); a number
-// outside the matrix for rows that are none of the group's cnt.
-__device__ __forceinline__ int source_row(const GroupedRows& s, int lo, int i, int cnt) {
-    if (i >= cnt) return s.count;
-    return s.row ? source_of(s, s.row[lo + i]) : lo + i;
-}
-
 // 16 bytes, of which `bytes` are read and the rest zeros.
 __device__ __forceinline__ void copy16(uint32_t dst, const void* src, uint32_t bytes) {
     asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
@@ -311,7 +303,7 @@ __global__ void __launch_bounds__(kGrThreads<LIST>, 1) grouped_kernel(const __gr
         const GroupedRows& s = first ? p.p : p.q;
         const bool others = LIST && (WEIGHT ? s.row != nullptr : first);  // the list's warps fetch this operand
         const uint32_t dst0 = smem_addr(first ? sA : sB), block_bytes = first ? (uint32_t)TS::kAStage : (uint32_t)TS::kBStage;
-        const int quad = WEIGHT ? lane & 15 : lane;
+        const int quad = lane & 15;  // GROUPED_WEIGHT: the rows that this lane gathers
         while (ok && items.next(it)) {
             const int num_kb = blocks_of(it);
             // bytes that the two producers of every CTA bring per K-block
@@ -319,21 +311,12 @@ __global__ void __launch_bounds__(kGrThreads<LIST>, 1) grouped_kernel(const __gr
             if constexpr (WEIGHT) {
                 bytes = (uint32_t)((LIST && p.p.row ? 0 : TS::kAStage) + (LIST && p.q.row ? 0 : TS::kBStage)) * CG;
             } else {
-                auto rows_bytes = [&](int r) {
-                    const int n = rows_in(it, r);
-                    return LIST ? 0u : s.row ? (uint32_t)((n + 3) / 4) * 512u : n ? (uint32_t)TS::kAStage : 0u;
-                };
+                auto rows_bytes = [&](int r) { return !LIST && rows_in(it, r) ? (uint32_t)TS::kAStage : 0u; };
                 bytes = rows_bytes(0) + (PAIR ? rows_bytes(1) : 0u) + (p.q_mn ? 0u : (uint32_t)TS::kBStage * CG);
             }
             const int mine = rows_in(it, (int)rank);
             const int row0 = it.tm * TS::kBM + 128 * (int)rank;               // not WEIGHT
             const int c0 = first ? row0 : it.tn * BN + (int)rank * TS::kBNC;  // WEIGHT: first column of P or Q
-            int src[4];  // the rows that this lane fetches
-            auto fetch_rows = [&](int i0) {
-#pragma unroll
-                for (int k = 0; k < 4; ++k) src[k] = source_row(s, it.lo, i0 + 4 * quad + k, it.cnt);
-            };
-            if (!WEIGHT && first && s.row && !LIST) fetch_rows(row0);
             for (int kb = 0; kb < num_kb; kb += BLOCKS) {
                 const int n = min(BLOCKS, num_kb - kb);
                 const bool got = wait_bar(smem_addr(&empty[grp]), phase ^ 1, w, DEV_TIMEOUT_PRODUCER + 1);
@@ -377,17 +360,18 @@ __global__ void __launch_bounds__(kGrThreads<LIST>, 1) grouped_kernel(const __gr
                         if (lane < atoms) load2(dst + lane * kAtom, &s.box, c0 + 64 * lane, it.lo + kb * kBK);
                     } else {
                         for (int j = 0; j < n; ++j) {
-                            fetch_rows((kb + j) * kBK);
+                            int src[4];
+#pragma unroll
+                            for (int k = 0; k < 4; ++k) {
+                                const int i = (kb + j) * kBK + 4 * quad + k;
+                                src[k] = i < it.cnt ? it.lo + i : s.count;
+                            }
                             for (int h = lane >> 4; h < atoms; h += 2)
                                 tma_gather4<PAIR>(dst + h * kAtom + j * 8192 + quad * 512, &s.gather, fb, c0 + 64 * h, src);
                         }
                     }
                 } else if (first) {
-                    if (s.row) {
-                        if (4 * lane < mine)
-                            for (int j = 0; j < n; ++j)
-                                tma_gather4<PAIR>(dst + j * TS::kAStage + lane * 512, &s.gather, fb, (kb + j) * kBK, src);
-                    } else if (lane == 0 && mine > 0) {
+                    if (lane == 0 && mine > 0) {
                         if (n == 2 && kb + 2 <= s.pairs)
                             load3(dst, &s.box2, 0, it.lo + row0, kb);
                         else

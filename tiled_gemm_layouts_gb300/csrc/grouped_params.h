@@ -18,7 +18,7 @@ enum GroupedMode : int {
 struct GroupedRows {
     CUtensorMap box;     // 64 columns of consecutive rows (no list)
     CUtensorMap box2;    // GROUPED_ROWS: the same of two K-blocks, among the first `pairs`
-    CUtensorMap gather;  // four rows of 64 columns, by their numbers
+    CUtensorMap gather;  // GROUPED_WEIGHT: four rows of 64 columns, by their numbers
     int pairs;
     const int* row;      // [R] or null: row i itself
     uint32_t magic;      // source row: row[i] / per_row = row[i] * magic >> shift
@@ -57,7 +57,7 @@ struct alignas(128) GroupedParams {
 };
 
 // Tile of a launch: `bn` columns; 256 rows on a CTA pair or 128 on one CTA.
-// `list`: a list's rows are fetched by warps of their own, not by gathering copies.
+// `list`: rows by a list, fetched by warps of their own.
 struct GroupedTile {
     int bn, pair, list;
     int rows() const { return pair ? 256 : 128; }
