@@ -1,5 +1,7 @@
 """Rows and matrices that lie more than 2^31 elements apart, calls on two streams
-at once, and places that several tokens name."""
+at once and of two threads, and places that several tokens name."""
+import threading
+
 import pytest
 import torch
 
@@ -148,3 +150,44 @@ def test_two_streams_at_once(tg):
     for p, q in zip(alone, both):
         assert all(torch.equal(u, v) for u, v in zip(p[:3], q[:3]))
     assert tg.tg_debug_status()[0] == tg.TG_OK
+
+
+def test_two_threads_at_once(tg):
+    """Calls whose kernels want different amounts of shared memory beyond the default, from
+    two threads: none is refused for what the other one has set or for being its thread's
+    first, and all give what they give alone."""
+    gen = torch.Generator(device="cuda").manual_seed(7)
+    index = torch.randint(0, 4096, (2000,), generator=gen, device="cuda").int()
+    logits = torch.randn(4000, 32, generator=gen, device="cuda")
+
+    def outputs(groups, chosen):
+        ints = lambda *shape: torch.empty(*shape, dtype=torch.int32, device="cuda")
+        return ints(groups + 1), ints(2000), ints(4000, chosen), torch.empty(4000, chosen, device="cuda")
+
+    def queue(groups, chosen, out, stream=None):
+        tg.group_rows(2000, groups, index, out[0], out[1], None, None, 0, stream=stream)
+        tg.route(4000, 32, logits, 32, None, out[2], out[3], tg.TG_F32, tg.make_route_options(chosen), stream=stream)
+
+    sizes = [(4096, 32), (2100, 28)]
+    alone, both = [outputs(*s) for s in sizes], [outputs(*s) for s in sizes]
+    for s, out in zip(sizes, alone):
+        queue(*s, out)
+    torch.cuda.synchronize()
+    refused = []
+
+    def worker(s, out, stream):
+        try:
+            for _ in range(300):
+                queue(*s, out, stream)
+        except Exception as e:
+            refused.append(e)
+
+    threads = [threading.Thread(target=worker, args=(s, out, torch.cuda.Stream())) for s, out in zip(sizes, both)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    assert not refused
+    for p, q in zip(alone, both):
+        assert all(torch.equal(u, v) for u, v in zip(p, q))

@@ -31,6 +31,9 @@ constexpr int kRowsPerBlock = kGroupWarps * kRowsPerWarp;
 constexpr int kMaxGroups = 4096;
 constexpr int kBlocksAdded = 64;  // that each block adds up for itself
 
+// Shared memory of place_kernel.
+constexpr size_t place_bytes(int64_t G) { return (size_t)(2 * G + 1) * 4 + (size_t)kGroupWarps * G * 2; }
+
 // counts[block][g]: rows of group g among the block's
 __global__ void __launch_bounds__(kGroupThreads) count_kernel(const int* index, int R, int G, int* counts) {
     extern __shared__ int shared_counts[];
@@ -231,10 +234,10 @@ extern "C" int tg_group_rows(int64_t R, int64_t G, const int32_t* index, int32_t
         if ((rc = check(ptrs[i], spans[i]))) return rc;
     const unsigned blocks = (unsigned)blocks_of(R);
     int* counts = need ? static_cast<int*>(workspace) : nullptr;
-    const size_t shared = (size_t)(2 * G + 1) * 4 + (size_t)kGroupWarps * G * 2;
+    const size_t shared = place_bytes(G);
     cudaError_t e = cudaSuccess;
-    if (shared > 48 * 1024)
-        e = cudaFuncSetAttribute(place_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)shared);
+    if (shared > 48 * 1024)  // (the most of all calls: another thread's may be on its way)
+        e = cudaFuncSetAttribute(place_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)place_bytes(kMaxGroups));
     if (e == cudaSuccess && counts) {
         count_kernel<<<blocks, kGroupThreads, (size_t)G * 4, stream>>>(index, (int)R, (int)G, counts);
         e = cudaGetLastError();

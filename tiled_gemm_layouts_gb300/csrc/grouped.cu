@@ -61,8 +61,8 @@ bool encode_stack_pairs(CUtensorMap* map, int dtype, const void* base, int64_t r
     return encode(map, dtype, 4, base, dims, strides, box);
 }
 
-// Rows of a matrix: `row` (a list, or null), divided by per_row, and the maps of
-// boxes of 64 columns x 128 rows (and two of them), and of gathered rows.
+// Rows of a matrix: by `row`, a list, divided by per_row; or, without one, the maps
+// of boxes of 64 columns x 128 rows (and two of them), and of gathered rows.
 bool encode_rows(GroupedRows* rows, int dtype, const void* base, int64_t count, int64_t cols, int64_t ld,
                  const int32_t* row, int64_t per_row) {
     rows->count = (int)count;
@@ -77,6 +77,7 @@ bool encode_rows(GroupedRows* rows, int dtype, const void* base, int64_t count, 
     rows->shift = 31 + b;
     rows->magic = (uint32_t)(((u128)1 << (31 + b)) / (u128)per_row + 1);
     rows->pairs = cols >= 128 ? (int)(cols / 64) : 0;
+    if (row) return true;  // fetched without maps
     return encode_2d(&rows->box, dtype, base, (uint64_t)cols, (uint64_t)count, ld, 64, 128) &&
            encode_2d(&rows->gather, dtype, base, (uint64_t)cols, (uint64_t)count, ld, 64, 1) &&
            (!rows->pairs || encode_k_pairs(&rows->box2, dtype, base, count, cols / 64 * 64, ld, 128));

@@ -218,6 +218,10 @@ __host__ __device__ inline int warp_words(int E, int C, int lanes, int k) {
     return ((32 * C > wide ? 32 * C : wide) + 2 * (32 / lanes) * k + 33 + 3) & ~3;
 }
 
+inline int route_bytes(int E, int C, int lanes, int k) {
+    return 4 * (((block_words(E, C) + 3) & ~3) + kWarps * warp_words(E, C, lanes, k));
+}
+
 // C: most experts of a lane.
 template <class IN, int C, bool SIGMOID>
 __global__ void __launch_bounds__(32 * kWarps) route_kernel(const __grid_constant__ RouteParams p) {
@@ -680,10 +684,12 @@ cudaError_t launch_route(const RouteParams& p, int sms, cudaStream_t stream) {
     const long long per_block = (long long)kWarps * (32 / p.lanes), blocks = (p.T + per_block - 1) / per_block;
     // about as many as are resident: what a warp sets up is shared by its tokens
     const unsigned grid = (unsigned)(blocks < 6LL * sms ? blocks : 6LL * sms);
-    const int bytes = 4 * (((block_words(p.E, C) + 3) & ~3) + kWarps * warp_words(p.E, C, p.lanes, p.k));
+    const int bytes = route_bytes(p.E, C, p.lanes, p.k);
     auto kern = p.sigmoid ? route_kernel<IN, C, true> : route_kernel<IN, C, false>;
     if (bytes > 48 * 1024) {
-        const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+        // (what any call may want: another thread's may be on its way)
+        const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                                   route_bytes(kMaxExperts, C, 1, 32));
         if (e != cudaSuccess) return e;
     }
     kern<<<grid, 32 * kWarps, bytes, stream>>>(p);
