@@ -306,8 +306,8 @@ __global__ void __launch_bounds__(kThreads, KC <= 2 ? 3 : 2) add_kernel(const __
 int64_t tiles_of(int64_t T, int64_t G) { return std::min(T, G) + T / kRows; }
 
 // Splits of K: no more blocks than two on every SM, of at least one step of all
-// warps (the whole call for 7777 rows of rank 32: 76 us with 753 blocks in three splits,
-// 57 with 251, and three blocks of the second kernel on an SM instead of one).
+// warps (7777 rows of rank 32, 4096 columns: 68 us with 753 blocks in three splits, 62
+// with 251).
 int splits_of(int64_t T, int64_t G, int64_t K) {
     const int64_t most = (K + kWarps * kStepK - 1) / (kWarps * kStepK);
     const int64_t wanted = 304 / tiles_of(T, G);
@@ -415,7 +415,7 @@ extern "C" int tg_adapters(int64_t T, int64_t N, int64_t K, int64_t rank, int64_
     p.pitch = (int)pitch_of(rank);
     p.low = static_cast<float*>(workspace);
     // Columns of y per block: few enough for three blocks per SM, at most 1024, or 2048
-    // where u's fragments are many (7777 rows, us: rank 32 70 to 77, rank 64 95 to 90).
+    // where u's fragments are many (7777 rows, us, 1024 to 2048: rank 32 62 to 70, rank 64 93 to 89).
     const int64_t most = rank <= 32 ? 1024 : 2048;
     const int64_t tiles = tiles_of(T, G);
     int64_t chunks = std::max<int64_t>((N + most - 1) / most, std::min<int64_t>((N + 255) / 256, (3LL * info->sms + tiles - 1) / tiles));

@@ -149,13 +149,14 @@ long long most_tiles(int64_t R, int64_t G, int rows, int64_t tiles_n) {
     return (std::min(R, G) + R / rows) * tiles_n;
 }
 
-// Tiles of 16 rows (grouped_few.cu) against tiles of 128: up to two rows per group
+// Tiles of 16 rows (grouped_few.cu) against tiles of 128: up to four rows per group
 // that may have any, and up to 16 where the large tiles would not fill the GPU.
-// N = 2048, K = 4096, us: 64 groups, 8 rows 35 to 48, 128 rows 118 to 138, 512 rows 209
-// to 187; 8 groups, 16 rows 31 to 48, 128 rows 54 to 64, 256 rows 78 to 42.
+// N = 2048, K = 4096, us: 64 groups, 8 rows 31 to 50, 128 rows 119 to 138, 256 rows 158
+// to 166, 512 rows 199 to 189; 8 groups, 16 rows 31 to 50, 128 rows 44 to 52, 256 rows
+// 68 to 42.
 bool few_rows(int64_t R, int64_t N, int64_t G, int perm, int sms) {
     const int64_t used = std::min(R, G);
-    return perm == TG_OP_T && (R <= 2 * used || (R <= 16 * used && most_tiles(R, G, 128, (N + 127) / 128) <= sms));
+    return perm == TG_OP_T && (R <= 4 * used || (R <= 16 * used && most_tiles(R, G, 128, (N + 127) / 128) <= sms));
 }
 
 }  // namespace

@@ -7,7 +7,7 @@
 // the matrix in flight, 64 KB per SM; the sums are joined in shared memory, always
 // in the same order.  The matrix fragments are loaded as they are used: nothing is
 // gained by staging what is read once.  One row through 8 matrices of 2048 x 4096
-// (134 MB): 27 us, 5.0 TB/s; the tiles of 128 rows take 43, waiting for one
+// (134 MB): 27 us, 5.0 TB/s; the tiles of 128 rows take 46, waiting for one
 // 8 KB copy after another.
 #include "direct.cuh"
 #include "grouped.h"
