@@ -189,12 +189,14 @@ __global__ void __launch_bounds__(kThreads, KC <= 2 ? 3 : 2) add_kernel(const __
         const int t = i < tile.rows ? p.row[tile.lo + i] : -1;
         y[j] = t >= 0 && t < p.T ? p.y + (long long)t * p.ldy : nullptr;
     }
-    // (y's columns are brought to L2 ahead, the first ones before the wait and each pass's
-    // next ones in the loop below: 58 us without, 51)
+    // y's columns are brought to L2 ahead, the first ones before the wait and each pass's
+    // next ones in the loop below, but not for ranks up to 16, whose passes are too short
+    // for it.  (30000 rows, us without and with: rank 16 158 and 163, 32 211 and 178,
+    // 128 518 and 468.)
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
         const int n = blockIdx.y * p.chunk + warp * 32 + 8 * q;
-        if (y[j] && n < p.N) asm volatile("prefetch.global.L2 [%0];" ::"l"(y[j] + n));
+        if (KC > 1 && y[j] && n < p.N) asm volatile("prefetch.global.L2 [%0];" ::"l"(y[j] + n));
     }
     wait_for_previous_kernel();
     if (warp < 4) {
@@ -253,7 +255,7 @@ __global__ void __launch_bounds__(kThreads, KC <= 2 ? 3 : 2) add_kernel(const __
         const int n = n0 + 8 * q;
 #pragma unroll
         for (int j = 0; j < 4; ++j)
-            if (y[j] && n + kWarps * 32 < end) asm volatile("prefetch.global.L2 [%0];" ::"l"(y[j] + n + kWarps * 32));
+            if (KC > 1 && y[j] && n + kWarps * 32 < end) asm volatile("prefetch.global.L2 [%0];" ::"l"(y[j] + n + kWarps * 32));
         uint4 old[4];
 #pragma unroll
         for (int j = 0; j < 4; ++j)
