@@ -25,7 +25,7 @@
 // fp32, and y is rounded once.
 //
 // 6677 rows with one of 8 adapters of rank 32, 4096 columns: 51 us, 3.2 TB/s; the
-// second kernel takes two thirds of it.  64 rows, each with an adapter of its own of
+// second kernel takes half of it.  64 rows, each with an adapter of its own of
 // rank 16: 10 us, most of it two launches.  (There, a block or a cluster of blocks
 // per row, without matrix instructions, took 10 to 17 us and for fewer adapters more.)
 #include <algorithm>
