@@ -195,8 +195,15 @@ int check_pointer(const void* p, const Span& s, int dev, Span* inside) {
     if (!g_range) return TG_ERR_POINTER;
     CUdeviceptr base = 0;
     size_t size = 0;
-    if (g_range(&base, &size, reinterpret_cast<CUdeviceptr>(p)) != CUDA_SUCCESS)
+    CUresult r = g_range(&base, &size, reinterpret_cast<CUdeviceptr>(p));
+    // A thread's first use of CUDA: unlike the runtime's query above, the driver's
+    // wants a current context.  (One that the thread has made current stays.)
+    if (r == CUDA_ERROR_INVALID_CONTEXT && cudaSetDevice(dev) == cudaSuccess)
+        r = g_range(&base, &size, reinterpret_cast<CUdeviceptr>(p));
+    if (r != CUDA_SUCCESS) {
+        cudaGetLastError();
         return TG_ERR_POINTER;
+    }
     if ((u128)s.lo < (u128)base || s.hi > (u128)base + size) return TG_ERR_POINTER;
     if (inside) {
         inside->present = true;

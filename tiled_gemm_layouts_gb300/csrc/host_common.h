@@ -61,9 +61,6 @@ struct PointerChecks {
     Span last = {};
     int operator()(const void* p, const Span& s) {
         if (s.present && last.present && last.lo <= s.lo && s.hi <= last.hi) return 0;
-        if (check_pointer(p, s, dev, &last) == 0) return 0;
-        // (a thread's first call: the driver's range query wants the device's context current)
-        if (cudaSetDevice(dev) != cudaSuccess) cudaGetLastError();
         return check_pointer(p, s, dev, &last);
     }
 };
