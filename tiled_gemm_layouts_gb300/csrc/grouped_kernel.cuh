@@ -55,6 +55,10 @@ constexpr int kListWarps = 3;              // with LIST, behind them, and a warp
 template <int MODE, bool PAIR, bool LIST>
 constexpr int kGrBlocks = MODE == GROUPED_ROWS && PAIR && LIST ? 1 : 2;
 constexpr int kGrOrder = 512;              // groups that GROUPED_WEIGHT sorts by their rows
+// What a K-block adds to the epilogue's time limit.  Its wait covers a tile's whole
+// contraction, of up to 2^24 K-blocks, which at 250 to 900 cycles each may take longer than
+// one limit; all other waits are for single K-blocks or a tile's output.
+constexpr long long kGrBlockCycles = 8192;
 template <bool LIST>
 constexpr int kGrThreads = 32 * (kGrWarps + (LIST ? kListWarps + 1 : 0));
 
@@ -603,7 +607,9 @@ __global__ void __launch_bounds__(kGrThreads<LIST>, 1) grouped_kernel(const __gr
                     if (r < rows && c < p.n) asm volatile("prefetch.global.L2 [%0];" ::"l"(mask + (long long)r * p.ld_relu + c));
                 }
             }
-            const bool got = wait_bar(smem_addr(&tfull[i & 1]), (i >> 1) & 1, w, DEV_TIMEOUT_EPILOGUE + 4);
+            Watch whole = w;
+            whole.timeout += blocks_of(it) * kGrBlockCycles;
+            const bool got = wait_bar(smem_addr(&tfull[i & 1]), (i >> 1) & 1, whole, DEV_TIMEOUT_EPILOGUE + 4);
             if (!__all_sync(0xffffffffu, got)) break;
             tc_fence_after();
             const uint32_t t_row = tmem_base + ((uint32_t)(q * 32) << 16) + (i & 1) * BN + half * kCols;
