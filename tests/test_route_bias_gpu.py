@@ -1,0 +1,34 @@
+"""Balance biases near the ends of fp32: experts and groups that are all but shut out or forced."""
+import pytest
+import torch
+
+from rows_reference import assert_within, code, route
+
+pytestmark = pytest.mark.gpu
+
+LOWEST = torch.finfo(torch.float32).min
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("sigmoid", [False, True])
+@pytest.mark.parametrize("top", [1, 2])
+@pytest.mark.parametrize("t,size", [(5, 4), (5, 24), (3000, 8)])
+@pytest.mark.parametrize("of_group", [
+    [-3.0e38, -2.5e38, -2.0e38, 0.0],          # sums of two are below fp32's range
+    [2.0e38, 2.5e38, 3.0e38, 2.2e38],          # and above it
+    [LOWEST, LOWEST, LOWEST, LOWEST],
+    [LOWEST, 0.0, LOWEST, -0.5],
+    [-3.0e38, 3.0e38, 2.9e38, -2.9e38]])
+def test_groups_of_large_biases(tg, of_group, t, size, top, sigmoid, dtype):
+    gen = torch.Generator(device="cuda").manual_seed(size)
+    e, k = 4 * size, 6
+    logits = torch.randn(t, e, generator=gen, device="cuda").to(dtype)
+    bias = torch.tensor(of_group, device="cuda").repeat_interleave(size)
+    index, weight = torch.empty(t, k, dtype=torch.int32, device="cuda"), torch.empty(t, k, device="cuda")
+    tg.route(t, e, logits, e, bias, index, weight, code(tg, dtype),
+             tg.make_route_options(k, tg.TG_ROUTE_SIGMOID if sigmoid else tg.TG_ROUTE_SOFTMAX, 4, 2, top, True))
+    some = slice(0, t, max(1, t // 40))
+    want_index, want = route(logits[some], bias, k, sigmoid, 4, 2, top, True, 1.0)
+    assert torch.equal(index[some], want_index)
+    # an exponential, a quotient and a sum of six, each within 2^-22
+    assert_within(weight[some], want, 2.0**-19 * want, "weight")

@@ -404,7 +404,8 @@ __global__ void __launch_bounds__(32 * kWarps) route_kernel(const __grid_constan
             kept = is_kept(value);
             // the least of those kept and the best of those not are what decides
             const float least = -token_max(kept && n > 0 ? -value : -INFINITY), best = token_max(kept || n == 0 ? -INFINITY : value);
-            bool near = by_score && least - best <= 4.0f * error;  // (no number if nothing is left in them)
+            // (no number if nothing is left in them; of two keys this large, fp32 may not hold the sum)
+            bool near = by_score && (least - best <= 4.0f * error || (p.top == 2 && largest_bias > 0x1p126f));
             if (by_two_scores && __any_sync(0xffffffffu, near)) {
                 // groups with the same two logits are equal in any arithmetic
                 bool different = false;
