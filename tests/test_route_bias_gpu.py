@@ -32,3 +32,13 @@ def test_groups_of_large_biases(tg, of_group, t, size, top, sigmoid, dtype):
     assert torch.equal(index[some], want_index)
     # an exponential, a quotient and a sum of six, each within 2^-22
     assert_within(weight[some], want, 2.0**-19 * want, "weight")
+
+
+def test_an_infinite_logit_is_above_the_largest_finite_one(tg):
+    """Groups ranked by their largest logits, which are keys themselves."""
+    logits = torch.zeros(3, 8, device="cuda")
+    logits[:, 1], logits[0, 6], logits[1, 6] = torch.finfo(torch.float32).max, float("inf"), 1.0
+    index, weight = torch.empty(3, 2, dtype=torch.int32, device="cuda"), torch.empty(3, 2, device="cuda")
+    tg.route(3, 8, logits, 8, None, index, weight, tg.TG_F32, tg.make_route_options(2, tg.TG_ROUTE_SIGMOID, 2, 1, 1))
+    assert index.tolist() == [[6, 4], [1, 0], [1, 0]]
+    assert weight.tolist() == [[1.0, 0.5], [1.0, 0.5], [1.0, 0.5]]

@@ -33,6 +33,7 @@
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
+#include <cfloat>
 #include <cmath>
 
 #include "../../include/tilegemm.h"
@@ -391,8 +392,10 @@ __global__ void __launch_bounds__(32 * kWarps) route_kernel(const __grid_constan
             of_group(one, two);
             auto value_of = [&](auto a, auto b) { return p.top == 2 && b > -INFINITY ? a + b : a; };
             const bool by_two_scores = !p.bias && p.top == 2;
-            const float value = !by_two_scores || one == -INFINITY ? value_of(one, two)
-                                                                   : value_of(score(one), two == -INFINITY ? two : score(two));
+            float value = !by_two_scores || one == -INFINITY ? value_of(one, two)
+                                                             : value_of(score(one), two == -INFINITY ? two : score(two));
+            // (the sum of two finite keys may lie outside fp32's range; a group without any keeps -inf)
+            if (fabsf(one) < INFINITY) value = fmaxf(fminf(value, FLT_MAX), -FLT_MAX);
             auto is_kept = [&](auto value) {
                 int ahead = 0;  // groups that come before this lane's
                 for (int o = 0; o < p.groups; ++o) {
@@ -404,8 +407,7 @@ __global__ void __launch_bounds__(32 * kWarps) route_kernel(const __grid_constan
             kept = is_kept(value);
             // the least of those kept and the best of those not are what decides
             const float least = -token_max(kept && n > 0 ? -value : -INFINITY), best = token_max(kept || n == 0 ? -INFINITY : value);
-            // (no number if nothing is left in them; of two keys this large, fp32 may not hold the sum)
-            bool near = by_score && (least - best <= 4.0f * error || (p.top == 2 && largest_bias > 0x1p126f));
+            bool near = by_score && least - best <= 4.0f * error;  // (no number if nothing is left in them)
             if (by_two_scores && __any_sync(0xffffffffu, near)) {
                 // groups with the same two logits are equal in any arithmetic
                 bool different = false;
