@@ -428,7 +428,9 @@ int tg_adamw(int64_t count, const tg_adamw_tensor* tensors, const tg_adamw_optio
  * aligned, TG_ERR_BUFFER if too small, no initialisation) that calls
  * overlapping on the GPU do not share.  Indexes are int32 on the device and
  * never checked on the host; a kernel that meets one out of range treats it as
- * the text below says and touches no memory for it.
+ * the text below says and touches no memory for it.  Where rows have to start on
+ * 16 bytes, the last 16 of a row may be read whole: up to 14 bytes behind its last
+ * element, of the same 16-byte unit, which no result depends on.
  * ---------------------------------------------------------------------- */
 
 typedef enum { TG_ROUTE_SOFTMAX = 0, TG_ROUTE_SIGMOID = 1 } tg_route_score;
@@ -638,7 +640,8 @@ int tg_debug_status(int* detail);
 
 /*
  * Watchdog settings for later launches on this process: the wait limit in
- * SM clock cycles (0 restores the default of 4e9, about two seconds) and a
+ * SM clock cycles (0 restores the default of 4e9, about two seconds; a wait
+ * of a grouped product's epilogue has 8192 more per 64 of the contraction) and a
  * test hook: the producer skips arming k-block `skip_kblock` (counted across
  * the CTA's tiles; -1 = off) so a wait provably expires.
  */

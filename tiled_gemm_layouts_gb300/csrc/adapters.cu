@@ -24,7 +24,7 @@
 // row's values near 1, so that fp16 neither overflows nor underflows; sums are
 // fp32, and y is rounded once.
 //
-// 6677 rows with one of 8 adapters of rank 32, 4096 columns: 51 us, 3.2 TB/s; the
+// 6677 rows with one of 8 adapters of rank 32, 4096 columns: 51 us, 3.3 TB/s; the
 // second kernel takes half of it.  64 rows, each with an adapter of its own of
 // rank 16: 10 us, most of it two launches.  (There, a block or a cluster of blocks
 // per row, without matrix instructions, took 10 to 17 us and for fewer adapters more.)
@@ -46,6 +46,9 @@ constexpr int64_t kMaxRank = 128;
 constexpr int kRankPass = 64;         // of the rank, per block of the first kernel
 constexpr int kStepK = 64;            // columns of x per warp and step
 constexpr int kMaxSplits = 16;
+// Blocks of the first kernel beyond which splits gain nothing: two on each of a GB300's 152
+// SMs.  A constant, since the workspace, whose size follows from it, is asked for without a device.
+constexpr int kLowBlocks = 2 * 152;
 
 struct AdapterParams {
     int T, G, rank, K, N;
@@ -312,7 +315,7 @@ int64_t tiles_of(int64_t T, int64_t G) { return std::min(T, G) + T / kRows; }
 // with 251).
 int splits_of(int64_t T, int64_t G, int64_t K) {
     const int64_t most = (K + kWarps * kStepK - 1) / (kWarps * kStepK);
-    const int64_t wanted = 304 / tiles_of(T, G);
+    const int64_t wanted = kLowBlocks / tiles_of(T, G);
     return (int)std::max<int64_t>(1, std::min<int64_t>(std::min(most, wanted), kMaxSplits));
 }
 int64_t pitch_of(int64_t rank) { return (rank + 15) / 16 * 16; }

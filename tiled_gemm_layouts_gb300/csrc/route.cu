@@ -4,8 +4,9 @@
 //   s_e = softmax(l)_e or 1 / (1 + exp(-l_e));   key_e = s_e + b_e, or l_e without a bias
 //   the k largest keys among the experts of the best groups;   w_j = c s_j (/ their sum)
 //
-// Bound by instructions: 16384 tokens of 256 experts are 8 MB, 1.2 us.  So
-// as little as possible is done across lanes.  A token has as many lanes as its
+// Bound by the latency of its chains of instructions: 16384 tokens of 256 experts are
+// 8 MB, 1.2 us, and take 18 to 22, with half of the issue slots used and 1.12 rounds of
+// blocks (14592 tokens, one round: 17).  So as little as possible is done across lanes.  A token has as many lanes as its
 // experts, in runs of at most 32 (64 where that makes too many) of one group each,
 // need, rounded up to a power of two, and a warp 32 / lanes tokens.  A lane's keys lie
 // in shared memory, four by four; registers hold a maximum per four.  A group's
@@ -14,8 +15,7 @@
 // shuffles, and, if it was its own, one read and one write of four.  (A warp per
 // token with its keys 32 experts apart and integer reductions over the warp: about
 // 1100 instructions a token, 45 us; runs in registers instead of shared memory: as
-// long, for the branches that taking a key out of one of 32 registers needs.  This:
-// 16.)
+// long, for the branches that taking a key out of one of 32 registers needs.)
 //
 // Which expert wins must not depend on how an exponential was rounded, so
 // the ranking is that of 64-bit arithmetic.  Doing it in 64 bits throughout would
